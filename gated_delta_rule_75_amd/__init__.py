@@ -20,6 +20,8 @@ __all__ = [
     "chunk_fwd", "chunk_fwd_workspace_size", "chunk_fwd_workspace_min", "chunk_fwd_checkpointed",
     "chunk_fwd_fused", "chunk_fwd_noalloc", "kcp_scan", "kcp_workspace_size", "kcp_workspace_min", "decode_step",
     "decode_step_fused", "decode_replay",
+    "linattn_fwd", "linattn_fwd_workspace_size", "linattn_bwd", "linattn_bwd_workspace_size",
+    "linattn_decode_step", "rope", "rope_frequencies", "norm_fwd", "norm_bwd", "norm_bwd_workspace_size",
     "KDA_BF16", "KDA_F32",
 ]
 
@@ -36,7 +38,10 @@ SYMBOLS = ("kda_version", "kda_status_string", "kda_chunk_fwd_workspace_size",
            "kda_chunk_fwd_workspace_min", "kda_chunk_fwd", "kda_chunk_fwd_checkpointed",
            "kda_kcp_workspace_size", "kda_kcp_workspace_min", "kda_kcp_scan",
            "kda_decode_step", "kda_decode_replay", "kda_chunk_fwd_fused", "kda_decode_step_fused",
-           "kda_chunk_fwd_noalloc", "kda_noalloc_scratch_bytes")
+           "kda_chunk_fwd_noalloc", "kda_noalloc_scratch_bytes",
+           "kda_linattn_fwd", "kda_linattn_fwd_workspace_size", "kda_linattn_bwd",
+           "kda_linattn_bwd_workspace_size", "kda_linattn_decode_step", "kda_rope",
+           "kda_rope_frequencies", "kda_norm_fwd", "kda_norm_bwd", "kda_norm_bwd_workspace_size")
 
 
 class KDAError(RuntimeError):
@@ -93,6 +98,27 @@ def lib() -> ctypes.CDLL:
     L.kda_decode_step_fused.restype = i
     L.kda_decode_replay.argtypes = [i, i, i, i, i, i, f, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     L.kda_decode_replay.restype = i
+    lin = [i, i, i, i, i, f, i, i64, vp, vp, i64, vp, i64, vp, i64, vp, i]
+    L.kda_linattn_fwd.argtypes = lin + [vp, vp, vp, vp, sz, vp]
+    L.kda_linattn_fwd.restype = i
+    L.kda_linattn_bwd.argtypes = lin + [vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.kda_linattn_bwd.restype = i
+    for fn in (L.kda_linattn_fwd_workspace_size, L.kda_linattn_bwd_workspace_size):
+        fn.argtypes = [i, i, i, i, i, i, i64]
+        fn.restype = sz
+    L.kda_linattn_decode_step.argtypes = [i, i, i, i, i, i, f, vp, i64, vp, i64, vp, i64, vp, i, vp, vp, vp]
+    L.kda_linattn_decode_step.restype = i
+    d = ctypes.c_double
+    L.kda_rope_frequencies.argtypes = [i, d, i, d, d, d, d, vp, ctypes.POINTER(f)]
+    L.kda_rope_frequencies.restype = i
+    L.kda_rope.argtypes = [i, i64, i, i, i, i, i, i, f, vp, vp, vp, i64, vp, i64, vp, i64, vp, i64, vp]
+    L.kda_rope.restype = i
+    L.kda_norm_fwd.argtypes = [i, i, i64, i, i, f, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.kda_norm_fwd.restype = i
+    L.kda_norm_bwd.argtypes = [i, i, i64, i, i, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.kda_norm_bwd.restype = i
+    L.kda_norm_bwd_workspace_size.argtypes = [i, i64, i, i]
+    L.kda_norm_bwd_workspace_size.restype = sz
     _lib = L
     return L
 
@@ -433,3 +459,8 @@ def decode_replay(q, k, v, g, beta, state, accepted=None, z=None, scale: float =
                                  _stream(dev))
     _check("kda_decode_replay", st)
     return y
+
+
+from .layer import (linattn_bwd, linattn_bwd_workspace_size, linattn_decode_step, linattn_fwd,  # noqa: E402
+                    linattn_fwd_workspace_size, norm_bwd, norm_bwd_workspace_size, norm_fwd, rope,
+                    rope_frequencies)

@@ -17,7 +17,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libkda.so")
-SOURCES = ["api.cpp", "decode.hip", "chunk_prep.hip", "chunk_state.hip", "kcp.hip"]
+SOURCES = ["api.cpp", "decode.hip", "chunk_prep.hip", "chunk_state.hip", "kcp.hip",
+           "linattn.hip", "layer_api.cpp", "norm.hip", "rope.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -30,11 +31,13 @@ COMMON = [
 ]
 
 
-# MFMA results in ordinary VGPRs: the scan and preparation kernels scale and
+# MFMA results in ordinary VGPRs: the scan, preparation and linear-attention
+# kernels scale and
 # convert accumulators with VALU instructions, which cannot read AGPRs
 PER_SOURCE = {
     "chunk_state.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "chunk_prep.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    "linattn.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
 }
 
 

@@ -115,4 +115,114 @@ hipError_t launch_kcp_scan(int H, int dk, int dv, int nseg, const float* pairs,
                            const float* initial_state, float* starts, float* group_pairs,
                            float* group_starts, hipStream_t stream);
 
+struct RopeArgs {
+    int dtype;  // 0 bf16, 1 fp32
+    int64_t T;
+    int Hq, Hk, d, rot;
+    bool half;                 // pairs (i, i + rot/2), else (2i, 2i + 1)
+    bool inverse;
+    float mscale;
+    const int32_t* positions;  // [T]
+    const double* inv_freq;    // [rot / 2]
+    const void *q, *k;         // rows of heads at a token stride (elements)
+    int64_t q_stride, k_stride;
+    void *q_out, *k_out;
+    int64_t qo_stride, ko_stride;
+    void* stream;
+};
+hipError_t launch_rope(const RopeArgs& a);
+
+// The gated norm (dy NULL) or its gradient over rows [T, H, D].
+struct NormArgs {
+    int dtype;
+    int64_t T;
+    int H, D;
+    float eps;
+    int rms;
+    const void *x, *z;
+    const float *weight, *bias;
+    void* y;
+    float *mean, *rstd;     // written by the norm, read by its gradient
+    const void* dy;
+    void *dx, *dz;
+    float *dweight, *dbias;
+    float *dwp, *dbp;       // partial rows [slots, D]
+    int64_t slots;          // rows walked side by side, a multiple of H
+    void* stream;
+};
+hipError_t launch_norm(const NormArgs& a);
+
+// Rows of one operand: [T, heads, D] at a token stride; `share` value heads
+// read one head.
+struct LinRows {
+    const void* p;
+    int64_t stride;
+    int share;
+};
+
+struct LinArgs {
+    int H, num_seqs;
+    int64_t T_total;
+    const int32_t* cu_seqlens;
+    int64_t L;                  // tokens of a block, a multiple of 64
+    int nblocks;                // a bound on the blocks of all sequences
+    const float* g;
+    bool g_per_token;           // [T, H], else [H]
+    LinRows q, k, v, x;
+    float p_scale, s_scale, u_scale;
+    const float* initial;       // one state a sequence, where states is NULL
+    float* states;              // [nblocks, H]: entering states (written by the state pass)
+    float* decays;              // [nblocks, H]
+    bool transposed;            // the stored states are the transposes
+    bool last_state;            // state pass: the last block too
+    bool reverse;
+    bool pairs;
+    float* final;
+    void* out;                  // [T, H, D]
+    bool out_f32;
+    float* sums;                // [H, T]
+    void* stream;
+};
+
+struct LinCarry {
+    float* states;
+    const float* decays;
+    const float* initial;
+    float* after;
+    int reverse;
+};
+
+struct LinCall {
+    LinArgs args;               // sizes, offsets, decays, stream
+    int dtype, dk, dv;
+    float scale;
+    LinRows q, k, v, dy;
+    const float* initial_state;
+    float* final_state;
+    void* y;
+    float *states, *decays;     // NULL: one block a sequence
+    // gradient
+    const float* d_final_state;
+    float* d_initial_state;
+    void *dq, *dk_out, *dv_out;
+    float* dg;
+    float *rstates, *rdecays, *s_end, *sums_a, *sums_b, *dg_tokens;
+    void* share_buf;
+};
+hipError_t launch_linattn_fwd(const LinCall& c);
+hipError_t launch_linattn_bwd(const LinCall& c);
+
+struct LinDecodeArgs {
+    int dtype;
+    int N, H, dk, dv;
+    float scale;
+    LinRows q, k, v;
+    const float* g;
+    bool g_per_token;
+    float* state;
+    void* y;
+    void* stream;
+};
+hipError_t launch_linattn_decode(const LinDecodeArgs& a);
+
 }  // namespace kda

@@ -1,0 +1,955 @@
+// Linear attention with a decay for each head, by chunks of 64 tokens.
+//
+// One kernel computes, for operand rows q_i, k_i (DK channels), v_i (DV) and
+// log-decays g_i, the causal form of
+//   S_i = exp(g_i) S_{i-1} + u k_i v_i^T,       o_i = S_i^T q_i
+// and, with G the sum of g inside the chunk, does so chunk by chunk:
+//   P_ij = p exp(G_i - G_j) q_i.k_j  (j <= i, else 0)
+//   O    = P V + s exp(G_i) Q S_in
+//   S    = exp(G_63) S_in + u sum_j exp(G_63 - G_j) k_j v_j^T
+// The prompt is (p, s, u) = (scale, scale, 1) on (q, k, v).  Its gradient is
+// three more runs of the same form:
+//   dq: rows (dy, v, k), state S^T, first token to last
+//   dv: rows (k, q, dy), state R,   last to first
+//   dk: rows (v, dy, q), state R^T, last to first
+// where R is the gradient of the state.  Run backwards, the decay between a
+// token and the one handled before it is the later token's, so the local
+// decays are g shifted by one.
+//
+// Every exponent is a difference of sums that is at most 0: sums are kept in
+// fp64 (one wave, a scan over lanes) and enter as a quotient against the start
+// of a 16-token tile, or inside a tile as integer and fraction, so that a decay
+// of any strength leaves the small ones behind it exact.
+//
+// A workgroup of four waves owns a (block of tokens, head); each wave owns
+// DV / 4 columns of the fp32 state in its MFMA accumulators.  The accumulator
+// layout (lane l: rows 4 (l / 16) + r of column l % 16) is a B operand as it
+// stands when the contraction runs in the order 16a + 4g + r, 16(a + 1) + 4g + r,
+// so the state never leaves the registers; the other operand is read from LDS
+// in that order, and the token-contracted operands by transposing LDS reads.
+// Rows are kept in LDS in 16-byte pieces, piece index xor row, against bank
+// conflicts.
+#include <type_traits>
+
+#include "launch.h"
+#include "vec.h"
+
+namespace kda {
+
+namespace {
+
+constexpr int C = 64;               // tokens of a chunk
+constexpr float kFloor = -200.f;    // exp(-200) is 0 in fp32 with room for any factor: g is held above it
+
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ s16x4_t lds_tr(const __bf16* p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)p);
+}
+
+// Eight consecutive contraction steps of a lane and the product of a 16 x 32
+// by a 32 x 16 tile.  fp32: eight 16x16x4 products, step e of every lane group
+// at a time.
+template <typename T> struct Frag8;
+template <> struct Frag8<__bf16> {
+    bf16x8_t v;
+    __device__ __forceinline__ float get(int i) const { return (float)v[i]; }
+    __device__ __forceinline__ void set(int i, float x) { v[i] = (__bf16)x; }
+};
+template <> struct Frag8<float> {
+    float v[8];
+    __device__ __forceinline__ float get(int i) const { return v[i]; }
+    __device__ __forceinline__ void set(int i, float x) { v[i] = x; }
+};
+__device__ __forceinline__ f32x4_t mma(const Frag8<__bf16>& a, const Frag8<__bf16>& b, f32x4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, b.v, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4_t mma(const Frag8<float>& a, const Frag8<float>& b, f32x4_t c) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[e], b.v[e], c, 0, 0, 0);
+    return c;
+}
+
+// A tile of rows of D elements in LDS, 16-byte pieces swizzled by the row.
+template <typename T, int D>
+struct Tile {
+    static constexpr int EP = 16 / (int)sizeof(T);        // elements of a piece
+    static constexpr int PIECES = D / EP;
+    static constexpr int MASK = PIECES < 16 ? PIECES - 1 : 15;
+    static __device__ __forceinline__ int off(int row, int col) {
+        return row * D + (((col / EP) ^ (row & MASK)) * EP) + col % EP;
+    }
+    // rows row0 + l % 16, contraction 32 s + {0, 16} + 4 g + (0..3)
+    static __device__ __forceinline__ Frag8<T> rows(const T* t, int row0, int s, int lane) {
+        const int row = row0 + (lane & 15), k = 32 * s + 4 * (lane >> 4);
+        Frag8<T> f;
+        if constexpr (sizeof(T) == 2) {
+            const bf16x4_t a = *reinterpret_cast<const bf16x4_t*>(t + off(row, k));
+            const bf16x4_t b = *reinterpret_cast<const bf16x4_t*>(t + off(row, k + 16));
+            f.v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+        } else {
+            const f32x4_t a = *reinterpret_cast<const f32x4_t*>(t + off(row, k));
+            const f32x4_t b = *reinterpret_cast<const f32x4_t*>(t + off(row, k + 16));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f.v[i] = a[i];
+                f.v[4 + i] = b[i];
+            }
+        }
+        return f;
+    }
+    // columns col0 + l % 16, contraction over rows 32 s + {0, 16} + 4 g + (0..3)
+    static __device__ __forceinline__ Frag8<T> cols(const T* t, int col0, int s, int lane) {
+        Frag8<T> f;
+        if constexpr (sizeof(T) == 2) {
+            // a transposing read takes 4 rows x 16 columns from 16 lanes: lane
+            // i of them points at row i / 4, columns 4 (i % 4)
+            const int row = 32 * s + 4 * (lane >> 4) + ((lane & 15) >> 2), col = col0 + 4 * (lane & 3);
+            const s16x4_t a = lds_tr(t + off(row, col));
+            const s16x4_t b = lds_tr(t + off(row + 16, col));
+            const bf16x4_t x = __builtin_bit_cast(bf16x4_t, a), y = __builtin_bit_cast(bf16x4_t, b);
+            f.v = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+        } else {
+            const int row = 32 * s + 4 * (lane >> 4), col = col0 + (lane & 15);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f.v[i] = t[off(row + i, col)];
+                f.v[4 + i] = t[off(row + 16 + i, col)];
+            }
+        }
+        return f;
+    }
+};
+
+// The block of tokens of a workgroup: block j of sequence n.  A sequence has
+// max(1, ceil(len / L)) blocks, numbered across the sequences in order.
+struct Block {
+    int n, j;            // sequence, block in it (n < 0: no such block)
+    int nb;              // blocks of the sequence
+    int64_t begin;       // the sequence's first token
+    int64_t start;       // the block's first token
+    int cnt;             // tokens of the block
+};
+
+__device__ __forceinline__ int64_t seq_at(const LinArgs& a, int n) {
+    if (!a.cu_seqlens) return n == 0 ? 0 : a.T_total;
+    int64_t x = a.cu_seqlens[n];
+    return x < 0 ? 0 : x > a.T_total ? a.T_total : x;
+}
+
+__device__ __forceinline__ int blocks_of(int64_t len, int64_t L) {
+    return len <= L ? 1 : (int)((len + L - 1) / L);
+}
+
+__device__ __forceinline__ int wave_incl_sum(int x, int lane) {
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+        const int y = __shfl_up(x, d);
+        if (lane >= d) x += y;
+    }
+    return x;
+}
+
+// Every wave finds the block itself, 64 sequences at a time.
+__device__ __forceinline__ Block find_block(const LinArgs& a, int b) {
+    const int lane = threadIdx.x & 63;
+    Block r;
+    r.n = -1;
+    int before = 0;
+    for (int n0 = 0; n0 < a.num_seqs; n0 += kWave) {
+        const int n = n0 + lane;
+        int64_t s = 0, e = 0;
+        int nb = 0;
+        if (n < a.num_seqs) {
+            s = seq_at(a, n);
+            e = seq_at(a, n + 1);
+            if (e < s) e = s;
+            nb = blocks_of(e - s, a.L);
+        }
+        const int incl = wave_incl_sum(nb, lane);
+        const int total = __shfl(incl, kWave - 1);
+        if (b < before + total) {
+            const uint64_t m = __ballot(before + incl > b);
+            const int src = __ffsll((unsigned long long)m) - 1;
+            r.n = n0 + src;
+            r.nb = __shfl(nb, src);
+            r.j = b - before - (__shfl(incl, src) - r.nb);
+            const int64_t sb = ((int64_t)__shfl((int)(s >> 32), src) << 32) | (uint32_t)__shfl((int)s, src);
+            const int64_t eb = ((int64_t)__shfl((int)(e >> 32), src) << 32) | (uint32_t)__shfl((int)e, src);
+            r.begin = sb;
+            r.start = sb + (int64_t)r.j * a.L;
+            const int64_t left = eb - r.start;
+            r.cnt = (int)(left < a.L ? left : a.L);
+            break;
+        }
+        before += total;
+    }
+    auto uni = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
+    auto uni64 = [&](int64_t x) { return ((int64_t)uni((int)(x >> 32)) << 32) | (uint32_t)uni((int)x); };
+    r.n = uni(r.n);
+    if (r.n < 0) return r;
+    r.j = uni(r.j);
+    r.nb = uni(r.nb);
+    r.cnt = uni(r.cnt);
+    r.begin = uni64(r.begin);
+    r.start = uni64(r.start);
+    return r;
+}
+
+// Index of sequence n's first block.
+__device__ __forceinline__ int first_block(const LinArgs& a, int n) {
+    const int lane = threadIdx.x & 63;
+    int sum = 0;
+    for (int m = lane; m < n; m += kWave) {
+        const int64_t len = seq_at(a, m + 1) - seq_at(a, m);
+        sum += blocks_of(len, a.L);
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+    return sum;
+}
+
+// Decay tables of a chunk, one token a lane.
+struct Tables {
+    float frac[C];      // log2 sum G = whole + frac
+    int whole[C];
+    float tile[C];      // exp2(G_i - G at the start of i's 16-token tile)
+    float upto[3][C];   // exp2(G at the start of tile t + 1 - G_j), j before it
+    float in[C];        // exp2(G_i)
+    float out[C];       // exp2(G_63 - G_j)
+    float row[4][C];    // partial sums of the waves (decay gradient)
+    float total;
+};
+
+__device__ __forceinline__ double shfl_d(double x, int src) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __shfl((int)(uint32_t)u, src), hi = __shfl((int)(uint32_t)(u >> 32), src);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+__device__ __forceinline__ double decay_scan(float g, int lane) {
+    double x = (double)(g < kFloor ? kFloor : g) * 1.4426950408889634074;
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+        const double y = shfl_d(x, lane - d < 0 ? 0 : lane - d);
+        if (lane >= d) x += y;
+    }
+    return x;
+}
+
+__device__ __forceinline__ void write_tables(Tables* t, double G, int lane) {
+    const double w = floor(G);
+    t->frac[lane] = (float)(G - w);
+    t->whole[lane] = (int)w;
+    const double r1 = shfl_d(G, 15), r2 = shfl_d(G, 31), r3 = shfl_d(G, 47), end = shfl_d(G, 63);
+    const double mine = lane < 16 ? 0.0 : lane < 32 ? r1 : lane < 48 ? r2 : r3;
+    t->tile[lane] = exp2_fast((float)(G - mine));
+    t->upto[0][lane] = exp2_fast((float)(r1 - G));   // read for j < 16 (t + 1) only
+    t->upto[1][lane] = exp2_fast((float)(r2 - G));
+    t->upto[2][lane] = exp2_fast((float)(r3 - G));
+    t->in[lane] = exp2_fast((float)G);
+    t->out[lane] = exp2_fast((float)(end - G));
+    if (lane == 0) t->total = exp2_fast((float)end);
+}
+
+enum : int { kOut = 0, kState = 1, kGrad = 2 };
+
+// Bytes of LDS: row tiles of q, k, v (and the extra rows), P, the tables.
+template <typename T, int DK, int DV, int MODE>
+constexpr int lds_bytes() {
+    const int rows = MODE == kState ? DK + DV : MODE == kOut ? 2 * DK + DV : 2 * DK + 2 * DV;
+    return C * rows * (int)sizeof(T) + (MODE == kState ? 0 : C * C * (int)sizeof(T)) + (int)sizeof(Tables);
+}
+
+// Tokens of a block in the order they are handled: chunk boundaries lie at the
+// same tokens in both directions, so backwards the first rows may be empty.
+struct Rows {
+    int64_t start;
+    int cnt, rows;   // tokens; rows, a multiple of 64
+    bool rev;
+    __device__ __forceinline__ bool has(int m) const { return rev ? m >= rows - cnt : m < cnt; }
+    __device__ __forceinline__ int64_t token(int m) const { return rev ? start + (rows - 1 - m) : start + m; }
+};
+
+// A thread's share of a tile's global rows, in 16-byte pieces.
+template <typename T, int D>
+struct Stage {
+    static constexpr int EP = 16 / (int)sizeof(T), PIECES = D / EP, N = C * PIECES / 256;
+    f32x4_t r[N];
+    // the chunk's rows m0 .. (zeros where there is no token)
+    __device__ __forceinline__ void load(const LinRows& x, int h, const Rows& rows, int m0) {
+        const T* base = (const T*)x.p + (int64_t)(h / x.share) * D;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int p = threadIdx.x + 256 * i, m = m0 + p / PIECES;
+            f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+            if (rows.has(m)) v = *reinterpret_cast<const f32x4_t*>(base + rows.token(m) * x.stride + (p % PIECES) * EP);
+            r[i] = v;
+        }
+    }
+    __device__ __forceinline__ void put(T* t) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int p = threadIdx.x + 256 * i;
+            *reinterpret_cast<f32x4_t*>(t + Tile<T, D>::off(p / PIECES, (p % PIECES) * EP)) = r[i];
+        }
+    }
+};
+
+// x as a sum of NS values of type T, the largest first.
+template <typename T, int NS>
+__device__ __forceinline__ void split(float x, Frag8<T> (&f)[NS], int e) {
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+        f[s].set(e, x);
+        x -= f[s].get(e);
+    }
+}
+
+// MODE kState: the block's own state from zero (a.states) and its decay
+// (a.decays); kOut: outputs, from the entering state; kGrad: outputs, and for
+// the decay's gradient the products of extra rows x_i with the part of o_i that
+// comes from the entering state, plus (a.pairs) those of pairs inside a chunk.
+//
+// Roundings of bf16 inputs: P and the entering state are rounded once to bf16
+// as operands (the state three ways in kGrad, whose sums are fp32 outputs); the
+// update's exp(G_63 - G_j) v_j enters as a sum of three bf16 values, so that
+// the state keeps its 24 bits.
+template <typename T, int DK, int DV, int MODE>
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(LinArgs a) {
+    constexpr bool kBf = sizeof(T) == 2;
+    constexpr int NT = DV / 64;             // 16-column tiles of a wave
+    constexpr int KT = DK / 16;             // 16-row tiles of the state
+    constexpr int NU = kBf ? 3 : 1;         // parts of an update operand
+    constexpr int NS = kBf && MODE == kGrad ? 3 : 1;   // parts of the state as an operand
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    T* sk = reinterpret_cast<T*>(smem);                 // [C][DK]
+    T* sv = sk + C * DK;                                // [C][DV]
+    T* sq = sv + C * DV;                                // [C][DK]
+    T* sx = sq + (MODE == kState ? 0 : C * DK);         // [C][DV]
+    T* sp = sx + (MODE == kGrad ? C * DV : 0);          // [C][C]
+    Tables* tb = reinterpret_cast<Tables*>(sp + (MODE == kState ? 0 : C * C));
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lr = lane & 15, lg = lane >> 4;
+    const int b = blockIdx.x / a.H, h = blockIdx.x % a.H;
+    const Block bl = find_block(a, b);
+    if (bl.n < 0) return;
+    const bool rev = a.reverse;
+    const bool first = rev ? bl.j == bl.nb - 1 : bl.j == 0;         // no block is handled before it
+    const bool last = rev ? bl.j == 0 : bl.j == bl.nb - 1;
+    if (MODE == kState && last && !a.last_state) return;
+    const int cnt = bl.cnt;
+    const Rows rows{bl.start, cnt, (cnt + C - 1) / C * C, rev};
+    const int wcol = wave * (DV / 4);
+
+    f32x4_t S[KT][NT];
+    {
+        const float* s0 = nullptr;
+        if (MODE != kState) {
+            if (a.states) s0 = a.states + ((int64_t)b * a.H + h) * DK * DV;
+            else if (a.initial) s0 = a.initial + ((int64_t)bl.n * a.H + h) * DK * DV;
+        }
+#pragma unroll
+        for (int i = 0; i < KT; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                f32x4_t x = {0.f, 0.f, 0.f, 0.f};
+                if (s0) {
+                    const int row = 16 * i + 4 * lg, col = wcol + 16 * n + lr;
+                    if (a.transposed) {
+                        x = *reinterpret_cast<const f32x4_t*>(s0 + (int64_t)col * DK + row);
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) x[r] = s0[(int64_t)(row + r) * DV + col];
+                    }
+                }
+                S[i][n] = x;
+            }
+    }
+
+    Stage<T, DK> rq, rk;
+    Stage<T, DV> rv, rx;
+    float gl = 0.f;      // this lane's local log-decay of the staged chunk (wave 0)
+    double sum_total = 0.0;
+    auto fetch = [&](int m0) {
+        rk.load(a.k, h, rows, m0);
+        rv.load(a.v, h, rows, m0);
+        if constexpr (MODE != kState) rq.load(a.q, h, rows, m0);
+        if constexpr (MODE == kGrad) rx.load(a.x, h, rows, m0);
+        if (wave == 0) {
+            const int m = m0 + lane;
+            gl = 0.f;
+            // backwards: the token after it, and none behind the sequence's last
+            const int64_t tok = rows.token(m) + (rev ? 1 : 0);
+            if (rows.has(m) && !(rev && first && tok == bl.start + cnt)) gl = a.g[a.g_per_token ? tok * a.H + h : h];
+        }
+    };
+    if (cnt > 0) fetch(0);
+    for (int m0 = 0; m0 < rows.rows; m0 += C) {
+        __syncthreads();                       // the chunk before is no longer read
+        rk.put(sk);
+        rv.put(sv);
+        if constexpr (MODE != kState) rq.put(sq);
+        if constexpr (MODE == kGrad) rx.put(sx);
+        if (wave == 0) {
+            const double G = decay_scan(gl, lane);
+            write_tables(tb, G, lane);
+            if (MODE == kState) sum_total += shfl_d(G, 63);
+        }
+        if (m0 + C < rows.rows) fetch(m0 + C);
+        __syncthreads();
+
+        f32x4_t acc[4][NT];
+        if constexpr (MODE != kState) {
+            // P, transposed tiles (rows j, columns i): a lane holds 4 consecutive
+            // j of one i.  Waves take 3, 3, 2 and 2 of the 10 tiles on or below
+            // the diagonal; two tiles above it are read as zeros.
+            float rowsum = 0.f;
+            (void)rowsum;
+            auto ptile = [&](int ti, int tj) {
+                f32x4_t c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int s = 0; s < DK / 32; ++s)
+                    c = mma(Tile<T, DK>::rows(sk, 16 * tj, s, lane), Tile<T, DK>::rows(sq, 16 * ti, s, lane), c);
+                const int i = 16 * ti + lr, j = 16 * tj + 4 * lg;
+                f32x4_t w;
+                if (ti == tj) {
+                    const float fi = tb->frac[i];
+                    const int wi = tb->whole[i];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float e = exp2_fast(fi - tb->frac[j + r]);
+                        w[r] = j + r <= i ? __builtin_amdgcn_ldexpf(e, wi - tb->whole[j + r]) : 0.f;
+                    }
+                } else {
+                    const float ei = tb->tile[i];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) w[r] = ei * tb->upto[ti - 1][j + r];
+                }
+                float p[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) p[r] = j + r <= i ? c[r] * w[r] * a.p_scale : 0.f;
+                store_vec<T, 4>(sp + Tile<T, C>::off(i, j), p);
+                if constexpr (MODE == kGrad) {
+                    if (a.pairs) {
+                        // weight of each pair i > j in the decay's gradient
+                        f32x4_t d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int s = 0; s < DV / 32; ++s)
+                            d = mma(Tile<T, DV>::rows(sv, 16 * tj, s, lane), Tile<T, DV>::rows(sx, 16 * ti, s, lane), d);
+                        float sum = 0.f;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const float e = j + r < i ? p[r] * d[r] : 0.f;
+                            sum += e;
+                            const float col = row16_sum(e);
+                            if (lr == 0) atomicAdd(&tb->row[wave][j + r], -col);
+                        }
+                        sum += __shfl_xor(sum, 16);
+                        sum += __shfl_xor(sum, 32);
+                        if (lg == 0) atomicAdd(&tb->row[wave][i], sum);
+                    }
+                }
+            };
+            auto pzero = [&](int ti, int tj) {
+                const float z[4] = {0.f, 0.f, 0.f, 0.f};
+                store_vec<T, 4>(sp + Tile<T, C>::off(16 * ti + lr, 16 * tj + 4 * lg), z);
+            };
+            if constexpr (MODE == kGrad) tb->row[wave][lane] = 0.f;
+            if (wave == 0) {
+                ptile(0, 0);
+                ptile(1, 0);
+                ptile(1, 1);
+            } else if (wave == 1) {
+                ptile(2, 0);
+                ptile(2, 1);
+                ptile(2, 2);
+            } else if (wave == 2) {
+                ptile(3, 0);
+                ptile(3, 1);
+                pzero(0, 1);
+            } else {
+                ptile(3, 2);
+                ptile(3, 3);
+                pzero(2, 3);
+            }
+            // the entering state's part, this wave's columns
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) acc[t][n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < DK / 32; ++s) {
+                Frag8<T> fs[NT][NS];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        split<T, NS>(S[2 * s][n][r], fs[n], r);
+                        split<T, NS>(S[2 * s + 1][n][r], fs[n], 4 + r);
+                    }
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const Frag8<T> fq = Tile<T, DK>::rows(sq, 16 * t, s, lane);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int p = NS - 1; p >= 0; --p) acc[t][n] = mma(fq, fs[n][p], acc[t][n]);
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                float dot[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int i = 16 * t + 4 * lg + r;
+                    const float e = tb->in[i] * a.s_scale;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        acc[t][n][r] *= e;
+                        if constexpr (MODE == kGrad)
+                            dot[r] += acc[t][n][r] * to_f32(sx[Tile<T, DV>::off(i, wcol + 16 * n + lr)]);
+                    }
+                    if constexpr (MODE == kGrad) {
+                        dot[r] = row16_sum(dot[r]);
+                        if (lr == 0) atomicAdd(&tb->row[wave][i], dot[r]);
+                    }
+                }
+            }
+            __syncthreads();                   // P is whole
+            if constexpr (MODE == kGrad) {
+                if (tid < C && rows.has(m0 + tid)) {
+                    a.sums[(int64_t)h * a.T_total + rows.token(m0 + tid)] =
+                        (tb->row[0][tid] + tb->row[1][tid]) + (tb->row[2][tid] + tb->row[3][tid]);
+                }
+            }
+        }
+        const float total = tb->total;
+#pragma unroll
+        for (int i = 0; i < KT; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) S[i][n] *= total;
+#pragma unroll
+        for (int s = 0; s < C / 32; ++s) {
+            Frag8<T> fv[NT], fu[NT][NU];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                fv[n] = Tile<T, DV>::cols(sv, wcol + 16 * n, s, lane);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    split<T, NU>(fv[n].get(r) * (tb->out[32 * s + 4 * lg + r] * a.u_scale), fu[n], r);
+                    split<T, NU>(fv[n].get(4 + r) * (tb->out[32 * s + 16 + 4 * lg + r] * a.u_scale), fu[n], 4 + r);
+                }
+            }
+            if constexpr (MODE != kState) {
+#pragma unroll
+                for (int t = 2 * s; t < 4; ++t) {
+                    const Frag8<T> fp = Tile<T, C>::rows(sp, 16 * t, s, lane);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) acc[t][n] = mma(fp, fv[n], acc[t][n]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < KT; ++i) {
+                const Frag8<T> fk = Tile<T, DK>::cols(sk, 16 * i, s, lane);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int p = NU - 1; p >= 0; --p) S[i][n] = mma(fk, fu[n][p], S[i][n]);
+            }
+        }
+        if constexpr (MODE != kState) {
+            // outputs: straight from the accumulators (rows of 16 columns)
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int m = m0 + 16 * t + 4 * lg + r;
+                    if (!rows.has(m)) continue;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const int64_t at = (rows.token(m) * a.H + h) * DV + wcol + 16 * n + lr;
+                        if (a.out_f32) static_cast<float*>(a.out)[at] = acc[t][n][r];
+                        else gstore(static_cast<T*>(a.out) + at, acc[t][n][r]);
+                    }
+                }
+        }
+    }
+
+    float* dst = nullptr;
+    float f = 1.f;
+    if (MODE == kState) {
+        dst = a.states + ((int64_t)b * a.H + h) * DK * DV;
+        if (tid == 0) a.decays[(int64_t)b * a.H + h] = exp2_fast((float)sum_total);
+    } else if (last && a.final) {
+        dst = a.final + ((int64_t)bl.n * a.H + h) * DK * DV;
+        // backwards: the first token's own decay is still to come
+        if (rev && cnt > 0) {
+            const float g = a.g[a.g_per_token ? bl.begin * a.H + h : h];
+            f = expf(g < kFloor ? kFloor : g);
+        }
+    }
+    if (dst) {
+#pragma unroll
+        for (int i = 0; i < KT; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    dst[(int64_t)(16 * i + 4 * lg + r) * DV + wcol + 16 * n + lr] = S[i][n][r] * f;
+    }
+}
+
+// Entering states of every block from the blocks' own ones, in place:
+// S_{j+1} = decay_j S_j + U_j, S_0 the sequence's (or 0); backwards from the
+// last block for the state's gradient.  blockIdx.z: which of the two arrays.
+// after (one state a sequence and head) gets the state behind the last block.
+__global__ __launch_bounds__(256) void linattn_carry_kernel(LinArgs a, LinCarry c0, LinCarry c1) {
+    const LinCarry c = blockIdx.z ? c1 : c0;
+    const int n = blockIdx.y / a.H, h = blockIdx.y % a.H;
+    const int b0 = first_block(a, n);
+    const int nb = blocks_of(seq_at(a, n + 1) - seq_at(a, n), a.L);
+    const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, size = (int64_t)gridDim.x * 1024;
+    f32x4_t s = {0.f, 0.f, 0.f, 0.f};
+    if (c.initial) s = *reinterpret_cast<const f32x4_t*>(c.initial + ((int64_t)n * a.H + h) * size + e);
+    for (int i = 0; i < nb; ++i) {
+        const int64_t at = (int64_t)(b0 + (c.reverse ? nb - 1 - i : i)) * a.H + h;
+        float* p = c.states + at * size + e;
+        if (i + 1 < nb || c.after) {
+            const f32x4_t u = *reinterpret_cast<const f32x4_t*>(p);
+            const float d = c.decays[at];
+            *reinterpret_cast<f32x4_t*>(p) = s;
+            s = s * d + u;
+        } else {
+            *reinterpret_cast<f32x4_t*>(p) = s;
+        }
+    }
+    if (c.after) *reinterpret_cast<f32x4_t*>(c.after + ((int64_t)n * a.H + h) * size + e) = s;
+}
+
+// The decay's gradient of a (block, head): dg_t = sum_{s >= t} (A_s - B_s) + E,
+// A and B the two kGrad runs' sums of the block's tokens, E what crosses the
+// block's end: the product of the state there with its gradient.
+__global__ __launch_bounds__(256) void linattn_dg_kernel(LinArgs a, int size, const float* S, const float* R,
+                                                         const float* s_end, const float* r_end, const float* A,
+                                                         const float* B, float* dg) {
+    __shared__ double part[4];
+    __shared__ double carry;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int b = blockIdx.x / a.H, h = blockIdx.x % a.H;
+    const Block bl = find_block(a, b);
+    if (bl.n < 0) return;
+    const bool last = bl.j == bl.nb - 1;
+    double e = 0.0;
+    const float *x = nullptr, *y = nullptr;
+    if (!last) {
+        x = S + ((int64_t)(b + 1) * a.H + h) * size;
+        y = R + ((int64_t)b * a.H + h) * size;
+    } else if (r_end) {
+        x = s_end + ((int64_t)bl.n * a.H + h) * size;
+        y = r_end + ((int64_t)bl.n * a.H + h) * size;
+    }
+    if (x) {
+        float f = 0.f;
+        for (int i = tid * 4; i < size; i += 1024) {
+            const f32x4_t u = *reinterpret_cast<const f32x4_t*>(x + i), v = *reinterpret_cast<const f32x4_t*>(y + i);
+            f += (u[0] * v[0] + u[1] * v[1]) + (u[2] * v[2] + u[3] * v[3]);
+        }
+        e = f;
+#pragma unroll
+        for (int d = 32; d > 0; d >>= 1) e += shfl_d(e, lane ^ d);
+    }
+    if (lane == 0) part[wave] = e;
+    __syncthreads();
+    if (tid == 0) {
+        double s = (part[0] + part[1]) + (part[2] + part[3]);
+        if (!last) {
+            const float g = a.g[a.g_per_token ? (bl.start + bl.cnt) * a.H + h : h];
+            s *= exp((double)(g < kFloor ? kFloor : g));
+        }
+        carry = s;
+    }
+    __syncthreads();
+    // from the block's end, 256 tokens at a time
+    for (int m0 = 0; m0 < bl.cnt; m0 += 256) {
+        const int m = m0 + tid;
+        const int64_t tok = bl.start + bl.cnt - 1 - m;
+        double d = 0.0;
+        if (m < bl.cnt) d = (double)A[(int64_t)h * a.T_total + tok] - (double)B[(int64_t)h * a.T_total + tok];
+#pragma unroll
+        for (int k = 1; k < kWave; k <<= 1) {
+            const double o = shfl_d(d, lane - k < 0 ? 0 : lane - k);
+            if (lane >= k) d += o;
+        }
+        if (lane == 63) part[wave] = d;
+        __syncthreads();
+        double before = carry;
+        for (int w = 0; w < wave; ++w) before += part[w];
+        const double v = before + d;
+        __syncthreads();
+        if (tid == 255) carry = v;
+        if (m < bl.cnt) dg[tok * a.H + h] = (float)v;
+        __syncthreads();
+    }
+}
+
+// dg of a decay that all tokens of a head share: the sum over tokens, one
+// workgroup a head, in a fixed order.
+__global__ __launch_bounds__(256) void linattn_dg_sum_kernel(int64_t T, int H, const float* dg, float* out) {
+    __shared__ double part[256];
+    const int h = blockIdx.x, tid = threadIdx.x;
+    double s = 0.0;
+    for (int64_t t = tid; t < T; t += 256) s += (double)dg[t * H + h];
+    part[tid] = s;
+    __syncthreads();
+    for (int d = 128; d > 0; d >>= 1) {
+        if (tid < d) part[tid] += part[tid + d];
+        __syncthreads();
+    }
+    if (tid == 0) out[h] = (float)part[0];
+}
+
+// Sum over the value heads that share a key head: fp32 [T, H, D] to [T, H / r, D].
+template <typename T>
+__global__ __launch_bounds__(256) void linattn_share_kernel(int64_t n, int r, int D, const float* src, T* dst) {
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= n) return;
+    const int64_t row = i / D;
+    const float* p = src + row * r * D + i % D;
+    f32x4_t s = *reinterpret_cast<const f32x4_t*>(p);
+    for (int j = 1; j < r; ++j) s += *reinterpret_cast<const f32x4_t*>(p + (int64_t)j * D);
+    const float o[4] = {s[0], s[1], s[2], s[3]};
+    store_vec<T, 4>(dst + i, o);
+}
+
+template <typename T, int DK, int DV, int MODE>
+hipError_t launch_t(const LinArgs& a) {
+    constexpr int lds = lds_bytes<T, DK, DV, MODE>();
+    static_assert(lds <= 160 * 1024, "LDS");
+    const void* kern = reinterpret_cast<const void*>(&linattn_kernel<T, DK, DV, MODE>);
+    hipError_t e = ensure_lds_limit(kern, lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((linattn_kernel<T, DK, DV, MODE>), dim3((unsigned)(a.nblocks * a.H)), dim3(256), lds,
+                       (hipStream_t)a.stream, a);
+    return hipGetLastError();
+}
+
+template <typename T, int MODE>
+hipError_t launch_m(const LinArgs& a, int dk, int dv) {
+    if (dk == 64) return dv == 64 ? launch_t<T, 64, 64, MODE>(a) : launch_t<T, 64, 128, MODE>(a);
+    return dv == 64 ? launch_t<T, 128, 64, MODE>(a) : launch_t<T, 128, 128, MODE>(a);
+}
+
+template <typename T>
+hipError_t launch_k(const LinArgs& a, int dk, int dv, int mode) {
+    if (mode == kState) return launch_m<T, kState>(a, dk, dv);
+    return mode == kOut ? launch_m<T, kOut>(a, dk, dv) : launch_m<T, kGrad>(a, dk, dv);
+}
+
+hipError_t launch_core(const LinArgs& a, int dtype, int dk, int dv, int mode) {
+    return dtype == 0 ? launch_k<__bf16>(a, dk, dv, mode) : launch_k<float>(a, dk, dv, mode);
+}
+
+}  // namespace
+
+hipError_t launch_linattn_fwd(const LinCall& c) {
+    LinArgs a = c.args;
+    a.q = c.q;
+    a.k = c.k;
+    a.v = c.v;
+    a.p_scale = a.s_scale = c.scale;
+    a.u_scale = 1.f;
+    if (c.states) {
+        // several blocks a sequence: their own states, the carry, then all outputs at once
+        LinArgs s = a;
+        s.states = c.states;
+        s.decays = c.decays;
+        hipError_t e = launch_core(s, c.dtype, c.dk, c.dv, kState);
+        if (e != hipSuccess) return e;
+        const LinCarry f{c.states, c.decays, c.initial_state, nullptr, 0};
+        hipLaunchKernelGGL(linattn_carry_kernel, dim3((unsigned)(c.dk * c.dv / 1024), (unsigned)(a.num_seqs * a.H), 1),
+                           dim3(256), 0, (hipStream_t)a.stream, a, f, f);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        a.states = c.states;
+    } else {
+        a.initial = c.initial_state;
+    }
+    a.final = c.final_state;
+    a.out = c.y;
+    return launch_core(a, c.dtype, c.dk, c.dv, kOut);
+}
+
+hipError_t launch_linattn_bwd(const LinCall& c) {
+    LinArgs a = c.args;
+    a.p_scale = c.scale;
+    hipError_t e;
+    // the blocks' own states, of the recurrence and of its gradient
+    LinArgs s = a;
+    s.k = c.k;
+    s.v = c.v;
+    s.u_scale = 1.f;
+    s.states = c.states;
+    s.decays = c.decays;
+    s.last_state = c.d_final_state != nullptr;
+    if ((e = launch_core(s, c.dtype, c.dk, c.dv, kState)) != hipSuccess) return e;
+    s.k = c.q;
+    s.v = c.dy;
+    s.u_scale = c.scale;
+    s.states = c.rstates;
+    s.decays = c.rdecays;
+    s.last_state = false;
+    s.reverse = true;
+    if ((e = launch_core(s, c.dtype, c.dk, c.dv, kState)) != hipSuccess) return e;
+    const LinCarry f{c.states, c.decays, c.initial_state, c.d_final_state ? c.s_end : nullptr, 0};
+    const LinCarry r{c.rstates, c.rdecays, c.d_final_state, nullptr, 1};
+    hipLaunchKernelGGL(linattn_carry_kernel, dim3((unsigned)(c.dk * c.dv / 1024), (unsigned)(a.num_seqs * a.H), 2),
+                       dim3(256), 0, (hipStream_t)a.stream, a, f, r);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+
+    const bool shared = c.k.share > 1;
+    // dq, and the pairs' and entering state's part of dg
+    LinArgs x = a;
+    x.q = c.dy;
+    x.k = c.v;
+    x.v = c.k;
+    x.x = c.q;
+    x.s_scale = c.scale;
+    x.u_scale = 1.f;
+    x.states = c.states;
+    x.transposed = true;
+    x.pairs = true;
+    x.sums = c.sums_a;
+    x.out = shared ? c.share_buf : c.dq;
+    x.out_f32 = shared;
+    if ((e = launch_core(x, c.dtype, c.dv, c.dk, kGrad)) != hipSuccess) return e;
+    auto share = [&](void* dst) -> hipError_t {
+        const int64_t n = a.T_total * (a.H / c.k.share) * c.dk;
+        if (n == 0) return hipSuccess;
+        const dim3 grid((unsigned)((n / 4 + 255) / 256));
+        if (c.dtype == 0)
+            hipLaunchKernelGGL(linattn_share_kernel<__bf16>, grid, dim3(256), 0, (hipStream_t)a.stream, n, c.k.share,
+                               c.dk, (const float*)c.share_buf, (__bf16*)dst);
+        else
+            hipLaunchKernelGGL(linattn_share_kernel<float>, grid, dim3(256), 0, (hipStream_t)a.stream, n, c.k.share,
+                               c.dk, (const float*)c.share_buf, (float*)dst);
+        return hipGetLastError();
+    };
+    if (shared && (e = share(c.dq)) != hipSuccess) return e;
+    // dk
+    x.q = c.v;
+    x.k = c.dy;
+    x.v = c.q;
+    x.x = c.k;
+    x.s_scale = 1.f;
+    x.u_scale = c.scale;
+    x.states = c.rstates;
+    x.pairs = false;
+    x.reverse = true;
+    x.sums = c.sums_b;
+    x.out = shared ? c.share_buf : c.dk_out;
+    if ((e = launch_core(x, c.dtype, c.dv, c.dk, kGrad)) != hipSuccess) return e;
+    if (shared && (e = share(c.dk_out)) != hipSuccess) return e;
+    // dv and the gradient of the initial state
+    x = a;
+    x.q = c.k;
+    x.k = c.q;
+    x.v = c.dy;
+    x.s_scale = 1.f;
+    x.u_scale = c.scale;
+    x.states = c.rstates;
+    x.reverse = true;
+    x.final = c.d_initial_state;
+    x.out = c.dv_out;
+    if ((e = launch_core(x, c.dtype, c.dk, c.dv, kOut)) != hipSuccess) return e;
+    // dg
+    if (c.dg) {
+        float* per_token = a.g_per_token ? c.dg : c.dg_tokens;
+        hipLaunchKernelGGL(linattn_dg_kernel, dim3((unsigned)(a.nblocks * a.H)), dim3(256), 0, (hipStream_t)a.stream, a,
+                           c.dk * c.dv, c.states, c.rstates, c.s_end, c.d_final_state, c.sums_a, c.sums_b, per_token);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        if (!a.g_per_token) {
+            hipLaunchKernelGGL(linattn_dg_sum_kernel, dim3((unsigned)a.H), dim3(256), 0, (hipStream_t)a.stream,
+                               a.T_total, a.H, per_token, c.dg);
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+        }
+    }
+    return hipSuccess;
+}
+
+// One token a request against the resident fp32 state [N, H, dk, dv], updated
+// in place: S <- exp(g) S + k v^T, y = scale S^T q.  Unlike the delta rule,
+// nothing is reduced before the write, so a thread writes each piece as soon as
+// it has it, and columns are independent: a workgroup takes COLS columns of a
+// (request, head).  Bound by the state's two crossings of memory; narrow column
+// slices only to spread few states over the CUs.
+namespace {
+
+template <typename T, int DK, int COLS>
+__global__ __launch_bounds__(256) void linattn_decode_kernel(LinDecodeArgs a) {
+    constexpr int CG = COLS / 4, RG = 256 / CG, RPT = DK / RG;
+    static_assert(RG * CG == 256 && RPT * RG == DK, "decode tiling");
+    __shared__ float s_k[DK], s_q[DK];
+    __shared__ float s_o[RG][COLS + 4];
+    const int tid = threadIdx.x, cg = tid % CG, rg = tid / CG;
+    const int slices = a.dv / COLS;
+    const int nh = blockIdx.x / slices, col0 = (blockIdx.x % slices) * COLS;
+    const int n = nh / a.H, h = nh % a.H;
+    float* st = a.state + (int64_t)nh * DK * a.dv + col0 + 4 * cg;
+    f32x4_t S[RPT];
+#pragma unroll
+    for (int r = 0; r < RPT; ++r) S[r] = *reinterpret_cast<const f32x4_t*>(st + (int64_t)(r * RG + rg) * a.dv);
+    const T* q = (const T*)a.q.p + (int64_t)n * a.q.stride + (int64_t)(h / a.q.share) * DK;
+    const T* k = (const T*)a.k.p + (int64_t)n * a.k.stride + (int64_t)(h / a.k.share) * DK;
+    const T* v = (const T*)a.v.p + (int64_t)n * a.v.stride + (int64_t)h * a.dv + col0 + 4 * cg;
+    for (int c = tid; c < DK; c += 256) {
+        s_k[c] = gload(k + c);
+        s_q[c] = gload(q + c);
+    }
+    float vv[4];
+    load_vec<T, 4>(v, vv);
+    const f32x4_t v4 = {vv[0], vv[1], vv[2], vv[3]};
+    const float decay = expf(a.g[a.g_per_token ? nh : h]);
+    __syncthreads();
+    f32x4_t o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int r = 0; r < RPT; ++r) {
+        const int row = r * RG + rg;
+        const f32x4_t x = S[r] * decay + s_k[row] * v4;
+        o += s_q[row] * x;
+        __builtin_nontemporal_store(x, reinterpret_cast<f32x4_t*>(st + (int64_t)row * a.dv));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s_o[rg][4 * cg + i] = o[i];
+    __syncthreads();
+    if (tid < COLS) {
+        float x = 0.f;
+#pragma unroll
+        for (int r = 0; r < RG; ++r) x += s_o[r][tid];
+        gstore((T*)a.y + (int64_t)nh * a.dv + col0 + tid, a.scale * x);
+    }
+}
+
+template <typename T, int DK, int COLS>
+hipError_t decode_t(const LinDecodeArgs& a) {
+    hipLaunchKernelGGL((linattn_decode_kernel<T, DK, COLS>), dim3((unsigned)((int64_t)a.N * a.H * (a.dv / COLS))),
+                       dim3(256), 0, (hipStream_t)a.stream, a);
+    return hipGetLastError();
+}
+
+template <typename T, int DK>
+hipError_t decode_c(const LinDecodeArgs& a) {
+    if (a.N * (int64_t)a.H < 512) return decode_t<T, DK, 16>(a);
+    return a.dv == 64 ? decode_t<T, DK, 64>(a) : decode_t<T, DK, 128>(a);
+}
+
+}  // namespace
+
+hipError_t launch_linattn_decode(const LinDecodeArgs& a) {
+    if (a.N == 0) return hipSuccess;
+    if (a.dtype == 0) return a.dk == 64 ? decode_c<__bf16, 64>(a) : decode_c<__bf16, 128>(a);
+    return a.dk == 64 ? decode_c<float, 64>(a) : decode_c<float, 128>(a);
+}
+
+}  // namespace kda

@@ -1,0 +1,268 @@
+// Norm of a mixer's output rows with the output gate, and its gradient.
+//
+// Row r = (token t, head h), D elements, weight and bias of the row's head:
+//   m = mean(x) (layer) or 0 (rms);  rstd = (mean((x - m)^2) + eps)^-1/2
+//   h = (x - m) rstd;  n = h w + b;  y = n sigmoid(z)
+// and with d = dy sigmoid(z):
+//   dw = sum_t d h;  db = sum_t d;  dz = dy n sigmoid(z) (1 - sigmoid(z))
+//   e = d w;  dx = rstd (e - h mean(e h) - [layer: mean(e)])
+// All of it in fp32 from the stored values, one rounding at each output.
+//
+// Both passes are bound by memory: a row stays in the registers of LANES
+// threads (16, 64, 256 or 1024, so that a thread holds 16 elements at most),
+// which read it once; the centred sum of squares is a second pass over
+// registers, so no cancellation.  The gradient's workgroups walk rows s, s + S,
+// s + 2S, ... (S a multiple of H: the head, and with it a thread's weight
+// columns, never change), keep dw and db in registers, and write one partial
+// row each; a second kernel adds the partials in a fixed order.
+#include "launch.h"
+#include "vec.h"
+
+namespace kda {
+
+namespace {
+
+// A thread's NV runs of VEC columns of a row of D: columns (j LANES + lane) VEC.
+template <int VEC, int LANES, int NV>
+struct Cols {
+    int lane, D;
+    __device__ __forceinline__ int at(int j) const { return (j * LANES + lane) * VEC; }
+    __device__ __forceinline__ bool in(int j) const { return at(j) < D; }
+};
+
+template <typename T, int VEC, int LANES, int NV>
+__global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_fwd_kernel(
+    int64_t rows, int H, int D, float eps, int rms, const T* __restrict__ x, const float* __restrict__ w,
+    const float* __restrict__ b, const T* __restrict__ z, T* __restrict__ y, float* __restrict__ mean,
+    float* __restrict__ rstd) {
+    constexpr int RPB = LANES < 256 ? 256 / LANES : 1;   // rows of a workgroup
+    __shared__ float part[2][LANES > 64 ? LANES / 64 : 1];
+    const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / LANES;
+    if (LANES <= 64 && row >= rows) return;              // no barrier below for these
+    const Cols<VEC, LANES, NV> c{(int)(threadIdx.x % LANES), D};
+    const int64_t base = row * D, wb = (int64_t)(row % H) * D;
+    float v[NV][VEC];
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        if (c.in(j)) {
+            load_vec<T, VEC>(x + base + c.at(j), v[j]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[j][i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) s += v[j][i];
+    }
+    float m = 0.f;
+    if (!rms) m = lanes_sum<LANES>(s, part[0]) / (float)D;
+    float q = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+        if (c.in(j)) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) q += (v[j][i] - m) * (v[j][i] - m);
+        }
+    q = lanes_sum<LANES>(q, part[1]);
+    const float r = 1.f / sqrtf(q / (float)D + eps);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        if (!c.in(j)) continue;
+        float wv[VEC], o[VEC];
+        load_vec<float, VEC>(w + wb + c.at(j), wv);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) o[i] = (v[j][i] - m) * r * wv[i];
+        if (b) {
+            float bv[VEC];
+            load_vec<float, VEC>(b + wb + c.at(j), bv);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) o[i] += bv[i];
+        }
+        if (z) {
+            float zv[VEC];
+            load_vec<T, VEC>(z + base + c.at(j), zv);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) o[i] *= sigmoid(zv[i]);
+        }
+        store_vec<T, VEC>(y + base + c.at(j), o);
+    }
+    if (c.lane == 0) {
+        if (mean) mean[row] = m;
+        if (rstd) rstd[row] = r;
+    }
+}
+
+template <typename T, int VEC, int LANES, int NV>
+__global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_bwd_kernel(
+    int64_t rows, int64_t S, int H, int D, const T* __restrict__ x, const float* __restrict__ w,
+    const float* __restrict__ b, const T* __restrict__ z, const float* __restrict__ mean,
+    const float* __restrict__ rstd, const T* __restrict__ dy, T* __restrict__ dx, T* __restrict__ dz,
+    float* __restrict__ dwp, float* __restrict__ dbp) {
+    constexpr int RPB = LANES < 256 ? 256 / LANES : 1;
+    __shared__ float part[2][2][LANES > 64 ? LANES / 64 : 1];
+    const int64_t slot = (int64_t)blockIdx.x * RPB + threadIdx.x / LANES;
+    if (slot >= S) return;   // whole lane groups (a whole workgroup where LANES > 64)
+    const Cols<VEC, LANES, NV> c{(int)(threadIdx.x % LANES), D};
+    const int64_t wb = (int64_t)(slot % H) * D;
+    float wv[NV][VEC], bv[NV][VEC], aw[NV][VEC], ab[NV][VEC];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) wv[j][i] = bv[j][i] = aw[j][i] = ab[j][i] = 0.f;
+        if (c.in(j)) {
+            load_vec<float, VEC>(w + wb + c.at(j), wv[j]);
+            if (b) load_vec<float, VEC>(b + wb + c.at(j), bv[j]);
+        }
+    }
+    int par = 0;
+    for (int64_t row = slot; row < rows; row += S, par ^= 1) {
+        const int64_t base = row * D;
+        const float m = mean ? mean[row] : 0.f, r = rstd[row];
+        float h[NV][VEC], d[NV][VEC];
+        float se = 0.f, seh = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if (!c.in(j)) {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) h[j][i] = d[j][i] = 0.f;
+                continue;
+            }
+            load_vec<T, VEC>(x + base + c.at(j), h[j]);
+            load_vec<T, VEC>(dy + base + c.at(j), d[j]);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) h[j][i] = (h[j][i] - m) * r;
+            if (z) {
+                float zv[VEC], o[VEC];
+                load_vec<T, VEC>(z + base + c.at(j), zv);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const float s = sigmoid(zv[i]), ds = d[j][i] * s;
+                    o[i] = ds * (h[j][i] * wv[j][i] + bv[j][i]) * sigmoid(-zv[i]);   // 1 - s without cancellation
+                    d[j][i] = ds;
+                }
+                store_vec<T, VEC>(dz + base + c.at(j), o);
+            }
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                aw[j][i] += d[j][i] * h[j][i];
+                ab[j][i] += d[j][i];
+                d[j][i] *= wv[j][i];
+                se += d[j][i];
+                seh += d[j][i] * h[j][i];
+            }
+        }
+        // two buffers in turn: a row's sums are read before the barrier of the next row's
+        seh = lanes_sum<LANES>(seh, part[par][0]) / (float)D;
+        se = mean ? lanes_sum<LANES>(se, part[par][1]) / (float)D : 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if (!c.in(j)) continue;
+            float o[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) o[i] = r * (d[j][i] - h[j][i] * seh - se);
+            store_vec<T, VEC>(dx + base + c.at(j), o);
+        }
+    }
+    const int64_t pb = slot * D;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        if (!c.in(j)) continue;
+        store_vec<float, VEC>(dwp + pb + c.at(j), aw[j]);
+        if (dbp) store_vec<float, VEC>(dbp + pb + c.at(j), ab[j]);
+    }
+}
+
+// dw[c] = sum over P partial rows of HD columns, in a fixed order: 16 threads
+// take every 16th partial of a column, then their sums are added.
+__global__ __launch_bounds__(256) void norm_reduce_kernel(int64_t P, int64_t HD, const float* __restrict__ dwp,
+                                                          const float* __restrict__ dbp, float* __restrict__ dw,
+                                                          float* __restrict__ db) {
+    __shared__ float s[16][17];
+    const float* src = blockIdx.y ? dbp : dwp;
+    float* dst = blockIdx.y ? db : dw;
+    const int cx = threadIdx.x & 15, py = threadIdx.x >> 4;
+    const int64_t col = (int64_t)blockIdx.x * 16 + cx;
+    float a = 0.f;
+    if (col < HD)
+        for (int64_t p = py; p < P; p += 16) a += src[p * HD + col];
+    s[py][cx] = a;
+    __syncthreads();
+    if (py == 0 && col < HD) {
+        a = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) a += s[i][cx];
+        dst[col] = a;
+    }
+}
+
+template <typename T, int VEC, int LANES, int NV>
+hipError_t launch_t(const NormArgs& a) {
+    constexpr int RPB = LANES < 256 ? 256 / LANES : 1, NT = LANES < 256 ? 256 : LANES;
+    const int64_t rows = a.T * a.H;
+    if (!a.dy) {
+        hipLaunchKernelGGL((norm_fwd_kernel<T, VEC, LANES, NV>), dim3((unsigned)((rows + RPB - 1) / RPB)), dim3(NT), 0,
+                           (hipStream_t)a.stream, rows, a.H, a.D, a.eps, a.rms, (const T*)a.x, a.weight, a.bias,
+                           (const T*)a.z, (T*)a.y, a.mean, a.rstd);
+    } else {
+        hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, LANES, NV>), dim3((unsigned)((a.slots + RPB - 1) / RPB)), dim3(NT),
+                           0, (hipStream_t)a.stream, rows, a.slots, a.H, a.D, (const T*)a.x, a.weight, a.bias,
+                           (const T*)a.z, a.mean, a.rstd, (const T*)a.dy, (T*)a.dx, (T*)a.dz, a.dwp, a.dbp);
+    }
+    return hipGetLastError();
+}
+
+// The narrowest lane group that holds a row with at most 16 elements a thread.
+template <typename T, int VEC>
+hipError_t launch_v(const NormArgs& a) {
+    const int n = (a.D + VEC - 1) / VEC;   // runs of a row
+    if (n <= 16) return launch_t<T, VEC, 16, 1>(a);
+    if (n <= 64) return launch_t<T, VEC, 64, 1>(a);
+    if (n <= 128) return launch_t<T, VEC, 64, 2>(a);
+    if constexpr (VEC <= 4) {
+        if (n <= 256) return launch_t<T, VEC, 64, 4>(a);
+    } else {
+        if (n <= 256) return launch_t<T, VEC, 256, 1>(a);
+    }
+    if (n <= 512) return launch_t<T, VEC, 256, 2>(a);
+    if constexpr (VEC == 1) {
+        if (n <= 1024) return launch_t<T, VEC, 256, 4>(a);
+        if (n <= 2048) return launch_t<T, VEC, 256, 8>(a);
+        if (n <= 4096) return launch_t<T, VEC, 256, 16>(a);
+        if (n <= 8192) return launch_t<T, VEC, 1024, 8>(a);
+        return launch_t<T, VEC, 1024, 16>(a);
+    } else if constexpr (VEC == 4) {
+        if (n <= 1024) return launch_t<T, VEC, 256, 4>(a);
+        if (n <= 2048) return launch_t<T, VEC, 1024, 2>(a);
+        return launch_t<T, VEC, 1024, 4>(a);
+    } else {
+        if (n <= 1024) return launch_t<T, VEC, 1024, 1>(a);
+        return launch_t<T, VEC, 1024, 2>(a);
+    }
+}
+
+bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+template <typename T>
+hipError_t launch_d(const NormArgs& a) {
+    const bool vec = a.D % kVec16<T> == 0 && al16(a.x) && al16(a.weight) && al16(a.bias) && al16(a.z) && al16(a.y) &&
+                     al16(a.dy) && al16(a.dx) && al16(a.dz);
+    return vec ? launch_v<T, kVec16<T>>(a) : launch_v<T, 1>(a);
+}
+
+}  // namespace
+
+hipError_t launch_norm(const NormArgs& a) {
+    if (a.T > 0) {
+        const hipError_t e = a.dtype == 0 ? launch_d<__bf16>(a) : launch_d<float>(a);
+        if (e != hipSuccess) return e;
+    }
+    if (a.dweight) {
+        const int64_t HD = (int64_t)a.H * a.D;
+        hipLaunchKernelGGL(norm_reduce_kernel, dim3((unsigned)((HD + 15) / 16), a.dbias ? 2 : 1), dim3(256), 0,
+                           (hipStream_t)a.stream, a.T > 0 ? a.slots / a.H : 0, HD, a.dwp, a.dbp, a.dweight, a.dbias);
+        return hipGetLastError();
+    }
+    return hipSuccess;
+}
+
+}  // namespace kda

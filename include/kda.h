@@ -333,6 +333,172 @@ kda_status kda_decode_replay(kda_dtype dt, int N, int Td, int H, int dk, int dv,
                              const float* beta, const void* z, const int32_t* accepted,
                              float* state, void* y, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The operators around the recurrence: linear attention with one decay for
+ * each head (no delta rule), rotary positions for queries and keys, and the
+ * norm of a mixer's output with its gate.  Same conventions as above; the
+ * prompt form and the single-token form come with the gradients that training
+ * needs.
+ *
+ * Rows q, k, v of these calls need not be packed: a `stride` (elements, at
+ * least heads * d) leads from token to token, so that they can be slices of one
+ * projection's output; the heads of a token are contiguous.  Outputs, states
+ * and gradients are contiguous.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * kda_linattn_fwd -- per sequence and value head h
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T,      y_t = scale * S_t^T q_t
+ * over packed sequences, by chunks of 64 tokens.
+ *
+ *   H, Hk            value heads and key heads; Hk divides H, and value heads
+ *                    h with equal h / (H / Hk) share a key head's q and k.
+ *   dk, dv           64 or 128 each.
+ *   num_seqs, T_total, cu_seqlens   as kda_chunk_fwd (num_seqs * H <= 65535).
+ *                    Sequences may be empty: their state passes through.
+ *   q, k             [T_total, Hk, dk] in dtype dt, v [T_total, H, dv].
+ *                    16-byte aligned, strides multiples of 16 bytes, finite.
+ *   g                fp32 natural log of the decay, <= 0: [T_total, H]
+ *                    (g_per_token != 0) or one for each head [H].  Below -200
+ *                    it counts as -200: the factor is 0 in fp32, so -INFINITY
+ *                    starts the head's state anew at that token.
+ *   initial_state, final_state   fp32 [num_seqs, H, dk, dv] or NULL, as
+ *                    kda_chunk_fwd; they may be the same buffer.
+ *   y                [T_total, H, dv] in dtype dt; must not overlap inputs.
+ *   workspace        at least kda_linattn_fwd_workspace_size bytes for the same
+ *                    sizes, 256-byte aligned (0 bytes and NULL do where
+ *                    T_total <= 256).  Sequences are cut into blocks of tokens
+ *                    that run side by side; it holds the blocks' states.
+ */
+size_t kda_linattn_fwd_workspace_size(kda_dtype dt, int H, int Hk, int dk, int dv, int num_seqs, int64_t T_total);
+kda_status kda_linattn_fwd(kda_dtype dt, int H, int Hk, int dk, int dv, float scale, int num_seqs, int64_t T_total,
+                           const int32_t* cu_seqlens, const void* q, int64_t q_stride, const void* k,
+                           int64_t k_stride, const void* v, int64_t v_stride, const float* g, int g_per_token,
+                           const float* initial_state, float* final_state, void* y, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
+ * kda_linattn_bwd -- the gradient of kda_linattn_fwd for given gradients of y
+ * and of the final state, recomputing the states (nothing is kept from the
+ * forward call).
+ *
+ *   dy               [T_total, H, dv] in dtype dt, contiguous.
+ *   d_final_state    fp32 [num_seqs, H, dk, dv], or NULL (zeros).
+ *   dq, dk_out       [T_total, Hk, dk] in dtype dt, summed over the value heads
+ *                    that share a key head (in fp32, rounded once).
+ *   dv_out           [T_total, H, dv] in dtype dt.
+ *   dg               fp32, [T_total, H] or [H] (summed over all tokens) as g.
+ *                    Where g is below -200 the gradient is taken at -200.
+ *   d_initial_state  fp32 [num_seqs, H, dk, dv] or NULL.
+ *   workspace        at least kda_linattn_bwd_workspace_size bytes, 256-byte
+ *                    aligned.
+ *   all other arguments: as kda_linattn_fwd.
+ */
+size_t kda_linattn_bwd_workspace_size(kda_dtype dt, int H, int Hk, int dk, int dv, int num_seqs, int64_t T_total);
+kda_status kda_linattn_bwd(kda_dtype dt, int H, int Hk, int dk, int dv, float scale, int num_seqs, int64_t T_total,
+                           const int32_t* cu_seqlens, const void* q, int64_t q_stride, const void* k,
+                           int64_t k_stride, const void* v, int64_t v_stride, const float* g, int g_per_token,
+                           const float* initial_state, const void* dy, const float* d_final_state, void* dq,
+                           void* dk_out, void* dv_out, float* dg, float* d_initial_state, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
+ * kda_linattn_decode_step -- one token for each of N requests against resident
+ * states: q, k [N, Hk, dk], v [N, H, dv] (strides as above), g [N, H] or [H],
+ * state fp32 [N, H, dk, dv] updated in place, y [N, H, dv] in dtype dt.
+ */
+kda_status kda_linattn_decode_step(kda_dtype dt, int N, int H, int Hk, int dk, int dv, float scale, const void* q,
+                                   int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                   int64_t v_stride, const float* g, int g_per_token, float* state, void* y,
+                                   void* stream);
+
+typedef enum {
+    KDA_ROPE_HALF = 0,         /* pairs (i, i + rot / 2) */
+    KDA_ROPE_INTERLEAVED = 1   /* pairs (2 i, 2 i + 1) */
+} kda_rope_layout;
+
+typedef enum {
+    KDA_ROPE_PLAIN = 0,    /* base^(-2 i / rot) */
+    KDA_ROPE_LINEAR = 1,   /* the same divided by factor (positions pressed together) */
+    KDA_ROPE_NTK = 2,      /* base * factor^(rot / (rot - 2)) as the base (rot > 2) */
+    KDA_ROPE_YARN = 3      /* slow pairs divided by factor, fast ones kept, a ramp between */
+} kda_rope_scaling;
+
+/*
+ * kda_rope_frequencies -- host only: the rot / 2 angles a position (radians, in
+ * fp64) and the factor on cosines and sines for a context stretched `factor`
+ * times beyond trained_len.  factor is read for the three scaled forms,
+ * trained_len, beta_fast and beta_slow (turns over the trained length where the
+ * ramp begins and ends; usually 32 and 1) for KDA_ROPE_YARN only, whose factor
+ * on cosines and sines is 0.1 ln(factor) + 1 (else 1).  inv_freq is host
+ * memory; the caller copies it to the device for kda_rope.
+ */
+kda_status kda_rope_frequencies(int rot, double base, kda_rope_scaling scaling, double factor, double trained_len,
+                                double beta_fast, double beta_slow, double* inv_freq, float* mscale);
+
+/*
+ * kda_rope -- turns the pairs of the first `rot` channels of every head of q
+ * and k by positions[t] * inv_freq[pair]; channels from rot on are copied.
+ *
+ *   T, Hq, Hk, d     tokens, query and key heads (Hk may be 0: no k), channels
+ *                    of a head (<= 1024).
+ *   inverse          0: turn.  Otherwise turn back, also times mscale: the
+ *                    gradient of the turn.
+ *   positions        device int32 [T], any values.
+ *   inv_freq         device fp64 [rot / 2].  Angles are formed in fp64.
+ *   q, k             [T, heads, d] in dtype dt at token strides; q_out, k_out
+ *                    likewise.  An output may be its own input (same pointer
+ *                    and stride); other overlaps are not allowed.  16-byte
+ *                    aligned rows with d and rot / 2 multiples of 16 bytes run
+ *                    fastest; any element alignment works.
+ */
+kda_status kda_rope(kda_dtype dt, int64_t T, int Hq, int Hk, int d, int rot, kda_rope_layout layout, int inverse,
+                    float mscale, const int32_t* positions, const double* inv_freq, const void* q, int64_t q_stride,
+                    const void* k, int64_t k_stride, void* q_out, int64_t q_out_stride, void* k_out,
+                    int64_t k_out_stride, void* stream);
+
+typedef enum {
+    KDA_NORM_LAYER = 0,   /* mean and variance */
+    KDA_NORM_RMS = 1      /* mean square only */
+} kda_norm_kind;
+
+/*
+ * kda_norm_fwd -- normalises every row x[t, h, :] of D elements and gates it:
+ *     h = (x - m) rstd,   rstd = 1 / sqrt(mean((x - m)^2) + eps)
+ *     y = (h * weight[h, :] + bias[h, :]) * sigmoid(z)
+ * with m the row's mean (KDA_NORM_LAYER) or 0 (KDA_NORM_RMS).  H = 1 with D the
+ * model's width is the ordinary norm; H heads of D = dv is the norm between a
+ * mixer's output and its gate.
+ *
+ *   x, z, y          [T, H, D] in dtype dt, contiguous; z NULL: no gate.  y may
+ *                    be x or z.
+ *   weight, bias     fp32 [H, D]; bias may be NULL.
+ *   mean, rstd       fp32 [T, H], each NULL or written (mean only for
+ *                    KDA_NORM_LAYER): what the gradient needs.
+ *   D                1 to 16384 (else KDA_ERR_UNSUPPORTED).
+ */
+kda_status kda_norm_fwd(kda_dtype dt, kda_norm_kind kind, int64_t T, int H, int D, float eps, const void* x,
+                        const float* weight, const float* bias, const void* z, void* y, float* mean, float* rstd,
+                        void* stream);
+
+/*
+ * kda_norm_bwd -- the gradient of kda_norm_fwd.
+ *
+ *   mean, rstd       as written by kda_norm_fwd (mean NULL for KDA_NORM_RMS).
+ *   dy, dx           [T, H, D] in dtype dt.
+ *   dweight, dbias   fp32 [H, D], sums over the T tokens (in a fixed order;
+ *                    zeros where T is 0); dbias may be NULL.
+ *   dz               [T, H, D] in dtype dt, given exactly where z is.
+ *                    dx and dz must not overlap any input or each other.
+ *   workspace        at least kda_norm_bwd_workspace_size bytes, 256-byte
+ *                    aligned: partial sums of dweight and dbias.
+ */
+size_t kda_norm_bwd_workspace_size(kda_dtype dt, int64_t T, int H, int D);
+kda_status kda_norm_bwd(kda_dtype dt, kda_norm_kind kind, int64_t T, int H, int D, const void* x, const float* weight,
+                        const float* bias, const void* z, const float* mean, const float* rstd, const void* dy,
+                        void* dx, float* dweight, float* dbias, void* dz, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
 #ifdef __cplusplus
 }
 #endif
