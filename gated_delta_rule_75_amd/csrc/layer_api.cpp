@@ -19,19 +19,23 @@ kda_status from_hip(hipError_t e) { return e == hipSuccess ? KDA_OK : KDA_ERR_HI
 
 bool head_ok(int d) { return d == 64 || d == 128; }
 
+// A chunk of 64 tokens is addressed with 32 bits.
+constexpr int64_t kMaxStride = int64_t(1) << 23;
+
 // Rows of heads x d elements at a token stride, moved in 16-byte pieces.
 bool rows_ok(kda_dtype dt, const void* p, int64_t stride, int heads, int d) {
-    return aligned(p, 16) && stride >= (int64_t)heads * d && stride % (int64_t)(16 / elt(dt)) == 0;
+    return aligned(p, 16) && stride >= (int64_t)heads * d && stride <= kMaxStride && stride % (int64_t)(16 / elt(dt)) == 0;
 }
 
 // Tokens of a block.  Sequences longer than a block are cut, and their blocks
 // run side by side from states that a first pass over k and v builds (about half
 // the call's reads again): worth it where uncut sequences leave CUs without
-// work, so a block is an even share of the tokens for 512 workgroups (two a
-// CU), and never less than `least`.
+// work.  512 workgroups (two a CU) run at once, and the ones behind them would
+// take a second round: so the blocks of one long sequence are as many as that
+// holds, and no shorter than `least`.
 int64_t block_len(int H, int64_t T, int64_t least, int64_t most) {
-    int64_t L = (T * H + 511) / 512;
-    L = (L + 63) / 64 * 64;
+    const int64_t n = H < 512 ? 512 / H : 1;
+    int64_t L = ((T + n - 1) / n + 63) / 64 * 64;
     if (L < least) L = least;
     if (L > most) L = most;
     const int64_t all = T < 64 ? 64 : (T + 63) / 64 * 64;

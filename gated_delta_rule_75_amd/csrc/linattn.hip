@@ -210,7 +210,7 @@ __device__ __forceinline__ int first_block(const LinArgs& a, int n) {
 }
 
 // Decay tables of a chunk, one token a lane.
-struct Tables {
+struct __attribute__((aligned(16))) Tables {
     float frac[C];      // log2 sum G = whole + frac
     int whole[C];
     float tile[C];      // exp2(G_i - G at the start of i's 16-token tile)
@@ -227,13 +227,31 @@ __device__ __forceinline__ double shfl_d(double x, int src) {
     return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 
-__device__ __forceinline__ double decay_scan(float g, int lane) {
+// x moved by a DPP pattern, zero where it has no source.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_d(double x) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const unsigned lo = __builtin_amdgcn_update_dpp(0, (int)(unsigned)u, CTRL, ROWS, 0xF, ROWS == 0xF);
+    const unsigned hi = __builtin_amdgcn_update_dpp(0, (int)(unsigned)(u >> 32), CTRL, ROWS, 0xF, ROWS == 0xF);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ double lane_d(double x, int lane) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const unsigned lo = __builtin_amdgcn_readlane((int)(unsigned)u, lane);
+    const unsigned hi = __builtin_amdgcn_readlane((int)(unsigned)(u >> 32), lane);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+// Inclusive sum over the wave: shifts within rows of 16 lanes, then the last
+// lane of a row into the rows behind it.
+__device__ __forceinline__ double decay_scan(float g) {
     double x = (double)(g < kFloor ? kFloor : g) * 1.4426950408889634074;
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-        const double y = shfl_d(x, lane - d < 0 ? 0 : lane - d);
-        if (lane >= d) x += y;
-    }
+    x += dpp_d<0x111, 0xF>(x);
+    x += dpp_d<0x112, 0xF>(x);
+    x += dpp_d<0x114, 0xF>(x);
+    x += dpp_d<0x118, 0xF>(x);
+    x += dpp_d<0x142, 0xA>(x);
+    x += dpp_d<0x143, 0xC>(x);
     return x;
 }
 
@@ -241,7 +259,7 @@ __device__ __forceinline__ void write_tables(Tables* t, double G, int lane) {
     const double w = floor(G);
     t->frac[lane] = (float)(G - w);
     t->whole[lane] = (int)w;
-    const double r1 = shfl_d(G, 15), r2 = shfl_d(G, 31), r3 = shfl_d(G, 47), end = shfl_d(G, 63);
+    const double r1 = lane_d(G, 15), r2 = lane_d(G, 31), r3 = lane_d(G, 47), end = lane_d(G, 63);
     const double mine = lane < 16 ? 0.0 : lane < 32 ? r1 : lane < 48 ? r2 : r3;
     t->tile[lane] = exp2_fast((float)(G - mine));
     t->upto[0][lane] = exp2_fast((float)(r1 - G));   // read for j < 16 (t + 1) only
@@ -269,42 +287,88 @@ struct Rows {
     bool rev;
     __device__ __forceinline__ bool has(int m) const { return rev ? m >= rows - cnt : m < cnt; }
     __device__ __forceinline__ int64_t token(int m) const { return rev ? start + (rows - 1 - m) : start + m; }
+    // lowest token of the chunk of rows m0 .. m0 + 63, and its tokens
+    __device__ __forceinline__ int low(int m0) const { return rev ? rows - C - m0 : m0; }
+    __device__ __forceinline__ int tokens(int m0) const { return cnt - low(m0) < C ? cnt - low(m0) : C; }
 };
 
-// A thread's share of a tile's global rows, in 16-byte pieces.
+typedef unsigned u32x4_t __attribute__((ext_vector_type(4)));
+
+// A thread's share of a tile's global rows, in 16-byte pieces.  Buffer loads
+// whose bound is the chunk's last token: rows behind it read as zeros, and a
+// thread's offset into a chunk is the same for every chunk.
 template <typename T, int D>
 struct Stage {
-    static constexpr int EP = 16 / (int)sizeof(T), PIECES = D / EP, N = C * PIECES / 256;
-    f32x4_t r[N];
-    // the chunk's rows m0 .. (zeros where there is no token)
+    static constexpr int EP = 16 / (int)sizeof(T), PIECES = D / EP, N = C * PIECES / 256, RPI = 256 / PIECES;
+    u32x4_t r[N];
     __device__ __forceinline__ void load(const LinRows& x, int h, const Rows& rows, int m0) {
-        const T* base = (const T*)x.p + (int64_t)(h / x.share) * D;
+        const int row = threadIdx.x / PIECES, nt = rows.tokens(m0);
+        const unsigned step = (unsigned)x.stride * (unsigned)sizeof(T);
+        const T* base = (const T*)x.p + (rows.start + rows.low(m0)) * x.stride + (int64_t)(h / x.share) * D;
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(base), 0,
+                                                            (unsigned)(nt - 1) * step + D * (unsigned)sizeof(T), 0x00027000);
+        const unsigned at = (unsigned)(rows.rev ? (RPI - 1 - row) : row) * step + (threadIdx.x % PIECES) * 16u;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int p = threadIdx.x + 256 * i, m = m0 + p / PIECES;
-            f32x4_t v = {0.f, 0.f, 0.f, 0.f};
-            if (rows.has(m)) v = *reinterpret_cast<const f32x4_t*>(base + rows.token(m) * x.stride + (p % PIECES) * EP);
-            r[i] = v;
-        }
+        for (int i = 0; i < N; ++i)
+            r[i] = __builtin_amdgcn_raw_buffer_load_b128(
+                rsrc, at, (unsigned)((rows.rev ? N - 1 - i : i) * RPI) * step, 0);
     }
     __device__ __forceinline__ void put(T* t) const {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int p = threadIdx.x + 256 * i;
-            *reinterpret_cast<f32x4_t*>(t + Tile<T, D>::off(p / PIECES, (p % PIECES) * EP)) = r[i];
+            const int row = threadIdx.x / PIECES + RPI * i;
+            *reinterpret_cast<u32x4_t*>(t + Tile<T, D>::off(row, (threadIdx.x % PIECES) * EP)) = r[i];
         }
     }
 };
 
-// x as a sum of NS values of type T, the largest first.
-template <typename T, int NS>
-__device__ __forceinline__ void split(float x, Frag8<T> (&f)[NS], int e) {
-#pragma unroll
-    for (int s = 0; s < NS; ++s) {
-        f[s].set(e, x);
-        x -= f[s].get(e);
-    }
+// Eight values as a sum of NS operands of type T.  One: rounded to nearest.
+// Three bf16: the leading 8 bits, the next 8 and the rest, by cutting; exact.
+__device__ __forceinline__ unsigned cvt2(float a, float b) {
+    return __builtin_bit_cast(unsigned, __builtin_convertvector((f32x2_t{a, b}), bf16x2_t));
 }
+template <int NS>
+__device__ __forceinline__ void split(const float (&x)[8], Frag8<__bf16> (&f)[NS]) {
+    static_assert(NS == 1 || NS == 3, "parts");
+    u32x4_t p[NS];
+    if constexpr (NS == 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[0][i] = cvt2(x[2 * i], x[2 * i + 1]);
+    } else {
+        unsigned y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = __builtin_bit_cast(unsigned, x[i]);
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[s][i] = __builtin_amdgcn_perm(y[2 * i + 1], y[2 * i], 0x07060302);
+            if (s + 1 < NS) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    y[i] = __builtin_bit_cast(unsigned, __builtin_bit_cast(float, y[i]) -
+                                                            __builtin_bit_cast(float, y[i] & 0xffff0000u));
+            }
+        }
+    }
+#pragma unroll
+    for (int s = 0; s < NS; ++s) f[s].v = __builtin_bit_cast(bf16x8_t, p[s]);
+}
+__device__ __forceinline__ void split(const float (&x)[8], Frag8<float> (&f)[1]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[0].v[i] = x[i];
+}
+template <typename T>
+__device__ __forceinline__ void store4(T* p, const f32x4_t& x) {
+    if constexpr (sizeof(T) == 2)
+        *reinterpret_cast<uint2*>(p) = make_uint2(cvt2(x[0], x[1]), cvt2(x[2], x[3]));
+    else
+        *reinterpret_cast<f32x4_t*>(p) = x;
+}
+__device__ __forceinline__ f32x4_t load4(const __bf16* p) {
+    const bf16x4_t v = *reinterpret_cast<const bf16x4_t*>(p);
+    return f32x4_t{(float)v[0], (float)v[1], (float)v[2], (float)v[3]};
+}
+__device__ __forceinline__ f32x4_t load4(const float* p) { return *reinterpret_cast<const f32x4_t*>(p); }
 
 // MODE kState: the block's own state from zero (a.states) and its decay
 // (a.decays); kOut: outputs, from the entering state; kGrad: outputs, and for
@@ -387,26 +451,27 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
     };
     if (cnt > 0) fetch(0);
     for (int m0 = 0; m0 < rows.rows; m0 += C) {
+        double G = 0.0;
+        if (wave == 0) G = decay_scan(gl);
         __syncthreads();                       // the chunk before is no longer read
         rk.put(sk);
         rv.put(sv);
         if constexpr (MODE != kState) rq.put(sq);
         if constexpr (MODE == kGrad) rx.put(sx);
         if (wave == 0) {
-            const double G = decay_scan(gl, lane);
             write_tables(tb, G, lane);
-            if (MODE == kState) sum_total += shfl_d(G, 63);
+            if (MODE == kState) sum_total += lane_d(G, 63);
         }
         if (m0 + C < rows.rows) fetch(m0 + C);
         __syncthreads();
 
+        // outputs, transposed tiles: a lane holds 4 consecutive columns of row
+        // 16 t + l % 16
         f32x4_t acc[4][NT];
         if constexpr (MODE != kState) {
             // P, transposed tiles (rows j, columns i): a lane holds 4 consecutive
             // j of one i.  Waves take 3, 3, 2 and 2 of the 10 tiles on or below
             // the diagonal; two tiles above it are read as zeros.
-            float rowsum = 0.f;
-            (void)rowsum;
             auto ptile = [&](int ti, int tj) {
                 f32x4_t c = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -420,17 +485,15 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const float e = exp2_fast(fi - tb->frac[j + r]);
-                        w[r] = j + r <= i ? __builtin_amdgcn_ldexpf(e, wi - tb->whole[j + r]) : 0.f;
+                        w[r] = __builtin_amdgcn_ldexpf(e, wi - tb->whole[j + r]);
                     }
                 } else {
-                    const float ei = tb->tile[i];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) w[r] = ei * tb->upto[ti - 1][j + r];
+                    w = *reinterpret_cast<const f32x4_t*>(&tb->upto[ti - 1][j]) * tb->tile[i];
                 }
-                float p[4];
+                f32x4_t p;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) p[r] = j + r <= i ? c[r] * w[r] * a.p_scale : 0.f;
-                store_vec<T, 4>(sp + Tile<T, C>::off(i, j), p);
+                for (int r = 0; r < 4; ++r) p[r] = ti != tj || j + r <= i ? c[r] * w[r] * a.p_scale : 0.f;
+                store4<T>(sp + Tile<T, C>::off(i, j), p);
                 if constexpr (MODE == kGrad) {
                     if (a.pairs) {
                         // weight of each pair i > j in the decay's gradient
@@ -453,8 +516,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
                 }
             };
             auto pzero = [&](int ti, int tj) {
-                const float z[4] = {0.f, 0.f, 0.f, 0.f};
-                store_vec<T, 4>(sp + Tile<T, C>::off(16 * ti + lr, 16 * tj + 4 * lg), z);
+                store4<T>(sp + Tile<T, C>::off(16 * ti + lr, 16 * tj + 4 * lg), f32x4_t{0.f, 0.f, 0.f, 0.f});
             };
             if constexpr (MODE == kGrad) tb->row[wave][lane] = 0.f;
             if (wave == 0) {
@@ -483,38 +545,42 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
             for (int s = 0; s < DK / 32; ++s) {
                 Frag8<T> fs[NT][NS];
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NT; ++n) {
+                    float x[8];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        split<T, NS>(S[2 * s][n][r], fs[n], r);
-                        split<T, NS>(S[2 * s + 1][n][r], fs[n], 4 + r);
+                        x[r] = S[2 * s][n][r];
+                        x[4 + r] = S[2 * s + 1][n][r];
                     }
+                    split(x, fs[n]);
+                }
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     const Frag8<T> fq = Tile<T, DK>::rows(sq, 16 * t, s, lane);
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int p = NS - 1; p >= 0; --p) acc[t][n] = mma(fq, fs[n][p], acc[t][n]);
+                        for (int p = NS - 1; p >= 0; --p) acc[t][n] = mma(fs[n][p], fq, acc[t][n]);
                 }
             }
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                float dot[4] = {0.f, 0.f, 0.f, 0.f};
+                const int i = 16 * t + lr;
+                const float e = tb->in[i] * a.s_scale;
+                float dot = 0.f;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int i = 16 * t + 4 * lg + r;
-                    const float e = tb->in[i] * a.s_scale;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        acc[t][n][r] *= e;
-                        if constexpr (MODE == kGrad)
-                            dot[r] += acc[t][n][r] * to_f32(sx[Tile<T, DV>::off(i, wcol + 16 * n + lr)]);
-                    }
+                for (int n = 0; n < NT; ++n) {
+                    acc[t][n] *= e;
                     if constexpr (MODE == kGrad) {
-                        dot[r] = row16_sum(dot[r]);
-                        if (lr == 0) atomicAdd(&tb->row[wave][i], dot[r]);
+                        const f32x4_t x = load4(sx + Tile<T, DV>::off(i, wcol + 16 * n + 4 * lg));
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) dot += acc[t][n][r] * x[r];
                     }
+                }
+                if constexpr (MODE == kGrad) {
+                    dot += __shfl_xor(dot, 16);
+                    dot += __shfl_xor(dot, 32);
+                    if (lg == 0) atomicAdd(&tb->row[wave][i], dot);
                 }
             }
             __syncthreads();                   // P is whole
@@ -533,21 +599,25 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
 #pragma unroll
         for (int s = 0; s < C / 32; ++s) {
             Frag8<T> fv[NT], fu[NT][NU];
+            const f32x4_t e0 = *reinterpret_cast<const f32x4_t*>(&tb->out[32 * s + 4 * lg]) * a.u_scale;
+            const f32x4_t e1 = *reinterpret_cast<const f32x4_t*>(&tb->out[32 * s + 16 + 4 * lg]) * a.u_scale;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 fv[n] = Tile<T, DV>::cols(sv, wcol + 16 * n, s, lane);
+                float x[8];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    split<T, NU>(fv[n].get(r) * (tb->out[32 * s + 4 * lg + r] * a.u_scale), fu[n], r);
-                    split<T, NU>(fv[n].get(4 + r) * (tb->out[32 * s + 16 + 4 * lg + r] * a.u_scale), fu[n], 4 + r);
+                    x[r] = fv[n].get(r) * e0[r];
+                    x[4 + r] = fv[n].get(4 + r) * e1[r];
                 }
+                split(x, fu[n]);
             }
             if constexpr (MODE != kState) {
 #pragma unroll
                 for (int t = 2 * s; t < 4; ++t) {
                     const Frag8<T> fp = Tile<T, C>::rows(sp, 16 * t, s, lane);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) acc[t][n] = mma(fp, fv[n], acc[t][n]);
+                    for (int n = 0; n < NT; ++n) acc[t][n] = mma(fv[n], fp, acc[t][n]);
                 }
             }
 #pragma unroll
@@ -560,20 +630,17 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
             }
         }
         if constexpr (MODE != kState) {
-            // outputs: straight from the accumulators (rows of 16 columns)
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+            for (int t = 0; t < 4; ++t) {
+                const int m = m0 + 16 * t + lr;
+                if (!rows.has(m)) continue;
+                const int64_t at = (rows.token(m) * a.H + h) * DV + wcol + 4 * lg;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int m = m0 + 16 * t + 4 * lg + r;
-                    if (!rows.has(m)) continue;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const int64_t at = (rows.token(m) * a.H + h) * DV + wcol + 16 * n + lr;
-                        if (a.out_f32) static_cast<float*>(a.out)[at] = acc[t][n][r];
-                        else gstore(static_cast<T*>(a.out) + at, acc[t][n][r]);
-                    }
+                for (int n = 0; n < NT; ++n) {
+                    if (MODE == kGrad && a.out_f32) store4<float>(static_cast<float*>(a.out) + at + 16 * n, acc[t][n]);
+                    else store4<T>(static_cast<T*>(a.out) + at + 16 * n, acc[t][n]);
                 }
+            }
         }
     }
 

@@ -357,7 +357,8 @@ kda_status kda_decode_replay(kda_dtype dt, int N, int Td, int H, int dk, int dv,
  *   num_seqs, T_total, cu_seqlens   as kda_chunk_fwd (num_seqs * H <= 65535).
  *                    Sequences may be empty: their state passes through.
  *   q, k             [T_total, Hk, dk] in dtype dt, v [T_total, H, dv].
- *                    16-byte aligned, strides multiples of 16 bytes, finite.
+ *                    16-byte aligned, strides multiples of 16 bytes (at most
+ *                    2^23 elements), finite.
  *   g                fp32 natural log of the decay, <= 0: [T_total, H]
  *                    (g_per_token != 0) or one for each head [H].  Below -200
  *                    it counts as -200: the factor is 0 in fp32, so -INFINITY
