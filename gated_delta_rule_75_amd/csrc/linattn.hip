@@ -75,9 +75,16 @@ template <typename T, int D>
 struct Tile {
     static constexpr int EP = 16 / (int)sizeof(T);        // elements of a piece
     static constexpr int PIECES = D / EP;
-    static constexpr int MASK = PIECES < 16 ? PIECES - 1 : 15;
+    // Which piece xor: 16 rows of one piece, and the rows and 16 columns of a
+    // transposing (bf16) or plain (fp32) column read, then each touch every bank
+    // once.  (bf16 rows of 128 bytes share a line of banks in twos.)
+    static __device__ __forceinline__ int swz(int row) {
+        if constexpr (sizeof(T) == 4) return row & 15;
+        if constexpr (PIECES == 16) return ((row << 1) | ((row >> 3) & 1)) & 15;
+        return (row & 6) | ((row >> 3) & 1);   // rows in twos: bits 3 2 1 turned to 2 1 3
+    }
     static __device__ __forceinline__ int off(int row, int col) {
-        return row * D + (((col / EP) ^ (row & MASK)) * EP) + col % EP;
+        return row * D + (((col / EP) ^ swz(row)) * EP) + col % EP;
     }
     // rows row0 + l % 16, contraction 32 s + {0, 16} + 4 g + (0..3)
     static __device__ __forceinline__ Frag8<T> rows(const T* t, int row0, int s, int lane) {
@@ -120,6 +127,12 @@ struct Tile {
         return f;
     }
 };
+
+// The same value in every lane, as a scalar.
+__device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uni64(int64_t x) {
+    return ((int64_t)uni((int)(x >> 32)) << 32) | (uint32_t)uni((int)x);
+}
 
 // The block of tokens of a workgroup: block j of sequence n.  A sequence has
 // max(1, ceil(len / L)) blocks, numbered across the sequences in order.
@@ -184,8 +197,6 @@ __device__ __forceinline__ Block find_block(const LinArgs& a, int b) {
         }
         before += total;
     }
-    auto uni = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
-    auto uni64 = [&](int64_t x) { return ((int64_t)uni((int)(x >> 32)) << 32) | (uint32_t)uni((int)x); };
     r.n = uni(r.n);
     if (r.n < 0) return r;
     r.j = uni(r.j);
@@ -218,6 +229,7 @@ struct __attribute__((aligned(16))) Tables {
     float in[C];        // exp2(G_i)
     float out[C];       // exp2(G_63 - G_j)
     float row[4][C];    // partial sums of the waves (decay gradient)
+    float g[2][C];      // log-decays of the next two chunks
     float total;
 };
 
@@ -255,27 +267,32 @@ __device__ __forceinline__ double decay_scan(float g) {
     return x;
 }
 
-__device__ __forceinline__ void write_tables(Tables* t, double G, int lane) {
+// valid: the lane has a token.  The others, behind the last token or (backwards)
+// before the first one, get weight 0 in every product that is kept.
+__device__ __forceinline__ void write_tables(Tables* t, double G, int lane, bool valid, bool rev) {
     const double w = floor(G);
     t->frac[lane] = (float)(G - w);
-    t->whole[lane] = (int)w;
+    t->whole[lane] = valid ? (int)w : rev ? 1 << 20 : -(1 << 20);
     const double r1 = lane_d(G, 15), r2 = lane_d(G, 31), r3 = lane_d(G, 47), end = lane_d(G, 63);
     const double mine = lane < 16 ? 0.0 : lane < 32 ? r1 : lane < 48 ? r2 : r3;
-    t->tile[lane] = exp2_fast((float)(G - mine));
-    t->upto[0][lane] = exp2_fast((float)(r1 - G));   // read for j < 16 (t + 1) only
-    t->upto[1][lane] = exp2_fast((float)(r2 - G));
-    t->upto[2][lane] = exp2_fast((float)(r3 - G));
+    t->tile[lane] = valid ? exp2_fast((float)(G - mine)) : 0.f;
+    t->upto[0][lane] = valid ? exp2_fast((float)(r1 - G)) : 0.f;   // read for j < 16 (t + 1) only
+    t->upto[1][lane] = valid ? exp2_fast((float)(r2 - G)) : 0.f;
+    t->upto[2][lane] = valid ? exp2_fast((float)(r3 - G)) : 0.f;
     t->in[lane] = exp2_fast((float)G);
-    t->out[lane] = exp2_fast((float)(end - G));
+    t->out[lane] = valid ? exp2_fast((float)(end - G)) : 0.f;
     if (lane == 0) t->total = exp2_fast((float)end);
 }
 
 enum : int { kOut = 0, kState = 1, kGrad = 2 };
 
-// Bytes of LDS: row tiles of q, k, v (and the extra rows), P, the tables.
+// Buffers of the k rows: two where the LDS of two workgroups a CU allows it.
+template <int MODE> constexpr int kbufs() { return MODE == kGrad ? 1 : 2; }
+
+// Bytes of LDS: row tiles of k, v, q (and the extra rows), P, the tables.
 template <typename T, int DK, int DV, int MODE>
 constexpr int lds_bytes() {
-    const int rows = MODE == kState ? DK + DV : MODE == kOut ? 2 * DK + DV : 2 * DK + 2 * DV;
+    const int rows = kbufs<MODE>() * DK + DV + (MODE == kState ? 0 : DK) + (MODE == kGrad ? DV : 0);
     return C * rows * (int)sizeof(T) + (MODE == kState ? 0 : C * C * (int)sizeof(T)) + (int)sizeof(Tables);
 }
 
@@ -293,34 +310,44 @@ struct Rows {
 };
 
 typedef unsigned u32x4_t __attribute__((ext_vector_type(4)));
+typedef unsigned u32x2_t __attribute__((ext_vector_type(2)));
 
-// A thread's share of a tile's global rows, in 16-byte pieces.  Buffer loads
-// whose bound is the chunk's last token: rows behind it read as zeros, and a
-// thread's offset into a chunk is the same for every chunk.
+// 16 (or 4) bytes a lane from global memory straight to LDS address lds + 16
+// (4) lane.  As assembly: the compiler makes every later LDS read of the wave
+// wait for a copy that it knows of, and here the copy is for the next chunk;
+// the waits are the kernel's own.  (No register is written; the first s_nop
+// covers scalars that a vector instruction has just produced.)
+__device__ __forceinline__ unsigned lds_addr(const void* p) {
+    return (unsigned)(uintptr_t)(__attribute__((address_space(3))) const char*)p;
+}
+__device__ __forceinline__ void copy16(unsigned lds, const void* base, unsigned off) {
+    asm volatile("s_nop 4\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :: "s"(lds), "v"(off), "s"(base) : "memory", "m0");
+}
+__device__ __forceinline__ void copy4(unsigned lds, const void* addr) {
+    asm volatile("s_nop 4\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+                 :: "s"(lds), "v"(addr) : "memory", "m0");
+}
+
+// The copy of a chunk's rows into a tile by the workgroup's four waves.  A
+// wave's copy is 1 KiB of LDS in order, so the swizzle is on the source side.
+// Rows without a token take the last token's: the tables give them no weight.
 template <typename T, int D>
-struct Stage {
-    static constexpr int EP = 16 / (int)sizeof(T), PIECES = D / EP, N = C * PIECES / 256, RPI = 256 / PIECES;
-    u32x4_t r[N];
-    __device__ __forceinline__ void load(const LinRows& x, int h, const Rows& rows, int m0) {
-        const int row = threadIdx.x / PIECES, nt = rows.tokens(m0);
-        const unsigned step = (unsigned)x.stride * (unsigned)sizeof(T);
-        const T* base = (const T*)x.p + (rows.start + rows.low(m0)) * x.stride + (int64_t)(h / x.share) * D;
-        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(base), 0,
-                                                            (unsigned)(nt - 1) * step + D * (unsigned)sizeof(T), 0x00027000);
-        const unsigned at = (unsigned)(rows.rev ? (RPI - 1 - row) : row) * step + (threadIdx.x % PIECES) * 16u;
+__device__ __forceinline__ void copy_tile(T* t, const LinRows& x, int h, const Rows& rows, int m0, int wave, int lane) {
+    constexpr int PIECES = Tile<T, D>::PIECES, RPW = 64 / PIECES, N = C / (4 * RPW);
+    const int top = rows.tokens(m0) - 1;
+    const unsigned step = (unsigned)x.stride * (unsigned)sizeof(T);
+    const T* base = (const T*)x.p + (rows.start + rows.low(m0)) * x.stride + (int64_t)(h / x.share) * D;
+    const void* ub = reinterpret_cast<const void*>(uni64(reinterpret_cast<int64_t>(base)));
+    const unsigned lds = uni(lds_addr(t) + wave * 1024);
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            r[i] = __builtin_amdgcn_raw_buffer_load_b128(
-                rsrc, at, (unsigned)((rows.rev ? N - 1 - i : i) * RPI) * step, 0);
+    for (int i = 0; i < N; ++i) {
+        const int row = (i * 4 + wave) * RPW + lane / PIECES;
+        const int tok = rows.rev ? C - 1 - row : row;
+        copy16(lds + i * 4096, ub,
+               (unsigned)(tok < top ? tok : top) * step + (unsigned)((lane % PIECES) ^ Tile<T, D>::swz(row)) * 16u);
     }
-    __device__ __forceinline__ void put(T* t) const {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int row = threadIdx.x / PIECES + RPI * i;
-            *reinterpret_cast<u32x4_t*>(t + Tile<T, D>::off(row, (threadIdx.x % PIECES) * EP)) = r[i];
-        }
-    }
-};
+}
 
 // Eight values as a sum of NS operands of type T.  One: rounded to nearest.
 // Three bf16: the leading 8 bits, the next 8 and the rest, by cutting; exact.
@@ -387,15 +414,16 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
     constexpr int NU = kBf ? 3 : 1;         // parts of an update operand
     constexpr int NS = kBf && MODE == kGrad ? 3 : 1;   // parts of the state as an operand
     extern __shared__ __attribute__((aligned(16))) char smem[];
-    T* sk = reinterpret_cast<T*>(smem);                 // [C][DK]
-    T* sv = sk + C * DK;                                // [C][DV]
-    T* sq = sv + C * DV;                                // [C][DK]
-    T* sx = sq + (MODE == kState ? 0 : C * DK);         // [C][DV]
-    T* sp = sx + (MODE == kGrad ? C * DV : 0);          // [C][C]
-    Tables* tb = reinterpret_cast<Tables*>(sp + (MODE == kState ? 0 : C * C));
+    constexpr int KB = kbufs<MODE>();
+    T* const skb = reinterpret_cast<T*>(smem);          // [KB][C][DK]
+    T* const sv = skb + KB * C * DK;                    // [C][DV]
+    T* const sq = sv + C * DV;                          // [C][DK]
+    T* const sx = sq + (MODE == kState ? 0 : C * DK);   // [C][DV]
+    T* const sp = sx + (MODE == kGrad ? C * DV : 0);    // [C][C]
+    Tables* const tb = reinterpret_cast<Tables*>(sp + (MODE == kState ? 0 : C * C));
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int lr = lane & 15, lg = lane >> 4;
+    const int tid = threadIdx.x, lane0 = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int lane = lane0, lr = lane & 15, lg = lane >> 4;
     const int b = blockIdx.x / a.H, h = blockIdx.x % a.H;
     const Block bl = find_block(a, b);
     if (bl.n < 0) return;
@@ -432,38 +460,70 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
             }
     }
 
-    Stage<T, DK> rq, rk;
-    Stage<T, DV> rv, rx;
-    float gl = 0.f;      // this lane's local log-decay of the staged chunk (wave 0)
     double sum_total = 0.0;
-    auto fetch = [&](int m0) {
-        rk.load(a.k, h, rows, m0);
-        rv.load(a.v, h, rows, m0);
-        if constexpr (MODE != kState) rq.load(a.q, h, rows, m0);
-        if constexpr (MODE == kGrad) rx.load(a.x, h, rows, m0);
-        if (wave == 0) {
-            const int m = m0 + lane;
-            gl = 0.f;
-            // backwards: the token after it, and none behind the sequence's last
-            const int64_t tok = rows.token(m) + (rev ? 1 : 0);
-            if (rows.has(m) && !(rev && first && tok == bl.start + cnt)) gl = a.g[a.g_per_token ? tok * a.H + h : h];
-        }
+    // The log-decay of local row m goes to tb->g (wave 0), two chunks ahead.
+    auto fetch_g = [&](int m0) {
+        int64_t tok = rows.token(m0 + lane) + (rev ? 1 : 0);   // backwards: the token after it
+        tok = tok < 0 ? 0 : tok >= a.T_total ? a.T_total - 1 : tok;
+        copy4(uni(lds_addr(tb->g[(m0 / C) & 1])), a.g + (a.g_per_token ? tok * a.H + h : h));
     };
-    if (cnt > 0) fetch(0);
-    for (int m0 = 0; m0 < rows.rows; m0 += C) {
-        double G = 0.0;
-        if (wave == 0) G = decay_scan(gl);
-        __syncthreads();                       // the chunk before is no longer read
-        rk.put(sk);
-        rv.put(sv);
-        if constexpr (MODE != kState) rq.put(sq);
-        if constexpr (MODE == kGrad) rx.put(sx);
+    auto fetch_k = [&](int m0) {
+        copy_tile<T, DK>(skb + (KB == 2 ? ((m0 / C) & 1) * C * DK : 0), a.k, h, rows, m0, wave, lane);
+    };
+    auto fetch_rest = [&](int m0) {
+        copy_tile<T, DV>(sv, a.v, h, rows, m0, wave, lane);
+        if constexpr (MODE != kState) copy_tile<T, DK>(sq, a.q, h, rows, m0, wave, lane);
+        if constexpr (MODE == kGrad) copy_tile<T, DV>(sx, a.x, h, rows, m0, wave, lane);
+    };
+    auto tables = [&](int m0) {
+        const int m = m0 + lane;
+        const bool valid = rows.has(m);
+        // backwards nothing decays before the sequence's last token
+        const float g = valid && !(rev && first && rows.token(m) == bl.start + cnt - 1) ? tb->g[(m0 / C) & 1][lane] : 0.f;
+        const double G = decay_scan(g);
+        write_tables(tb, G, lane, valid, rev);
+        if (MODE == kState) sum_total += lane_d(G, 63);
+    };
+    // Stores of a wave and chunk, the youngest of its memory operations where
+    // the copies are waited for.
+    constexpr int NST = MODE == kOut ? 4 * NT : 0;
+    if (cnt > 0) {
         if (wave == 0) {
-            write_tables(tb, G, lane);
-            if (MODE == kState) sum_total += lane_d(G, 63);
+            fetch_g(0);
+            if (C < rows.rows) fetch_g(C);
         }
-        if (m0 + C < rows.rows) fetch(m0 + C);
-        __syncthreads();
+        fetch_k(0);
+        fetch_rest(0);
+        wait_vmcnt<0>();
+        if (wave == 0) tables(0);
+    }
+    for (int m0 = 0; m0 < rows.rows; m0 += C) {
+        // LDS addresses are formed anew in each chunk (a few dozen operations):
+        // kept across the loop they cost registers that spill
+        lane = lane0;
+        asm volatile("" : "+v"(lane));
+        lr = lane & 15;
+        lg = lane >> 4;
+        // A: this chunk's copies and tables are there; the chunk before is read
+        if (m0 > 0) wait_vmcnt<NST>();
+        barrier_keep_loads();
+        const T* const sk = skb + (KB == 2 ? ((m0 / C) & 1) * C * DK : 0);
+        const bool more = m0 + C < rows.rows;
+        if (wave == 0 && m0 + 2 * C < rows.rows) fetch_g(m0 + 2 * C);
+        if (KB == 2 && more) fetch_k(m0 + C);
+
+        // v's columns of this wave and the factors of the update, before v is
+        // overwritten
+        Frag8<T> fv[2][NT];
+        f32x4_t eo[2][2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) fv[s][n] = Tile<T, DV>::cols(sv, wcol + 16 * n, s, lane);
+            eo[s][0] = *reinterpret_cast<const f32x4_t*>(&tb->out[32 * s + 4 * lg]) * a.u_scale;
+            eo[s][1] = *reinterpret_cast<const f32x4_t*>(&tb->out[32 * s + 16 + 4 * lg]) * a.u_scale;
+        }
+        const float total = tb->total;
 
         // outputs, transposed tiles: a lane holds 4 consecutive columns of row
         // 16 t + l % 16
@@ -583,7 +643,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
                     if (lg == 0) atomicAdd(&tb->row[wave][i], dot);
                 }
             }
-            __syncthreads();                   // P is whole
+            // B: P is whole; v, q, x and the tables are read
+            barrier_keep_loads();
             if constexpr (MODE == kGrad) {
                 if (tid < C && rows.has(m0 + tid)) {
                     a.sums[(int64_t)h * a.T_total + rows.token(m0 + tid)] =
@@ -591,24 +652,25 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
                 }
             }
         }
-        const float total = tb->total;
+        if constexpr (MODE == kState) barrier_keep_loads();
+        if (more) {
+            fetch_rest(m0 + C);
+            if (wave == 0) tables(m0 + C);
+        }
 #pragma unroll
         for (int i = 0; i < KT; ++i)
 #pragma unroll
             for (int n = 0; n < NT; ++n) S[i][n] *= total;
 #pragma unroll
         for (int s = 0; s < C / 32; ++s) {
-            Frag8<T> fv[NT], fu[NT][NU];
-            const f32x4_t e0 = *reinterpret_cast<const f32x4_t*>(&tb->out[32 * s + 4 * lg]) * a.u_scale;
-            const f32x4_t e1 = *reinterpret_cast<const f32x4_t*>(&tb->out[32 * s + 16 + 4 * lg]) * a.u_scale;
+            Frag8<T> fu[NT][NU];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                fv[n] = Tile<T, DV>::cols(sv, wcol + 16 * n, s, lane);
                 float x[8];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    x[r] = fv[n].get(r) * e0[r];
-                    x[4 + r] = fv[n].get(4 + r) * e1[r];
+                    x[r] = fv[s][n].get(r) * eo[s][0][r];
+                    x[4 + r] = fv[s][n].get(4 + r) * eo[s][1][r];
                 }
                 split(x, fu[n]);
             }
@@ -617,7 +679,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
                 for (int t = 2 * s; t < 4; ++t) {
                     const Frag8<T> fp = Tile<T, C>::rows(sp, 16 * t, s, lane);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) acc[t][n] = mma(fv[n], fp, acc[t][n]);
+                    for (int n = 0; n < NT; ++n) acc[t][n] = mma(fv[s][n], fp, acc[t][n]);
                 }
             }
 #pragma unroll
@@ -630,17 +692,33 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
             }
         }
         if constexpr (MODE != kState) {
+            // buffer stores: the same number in every chunk, rows without a
+            // token lie behind the bound and are dropped
+            const bool wide = MODE == kGrad && a.out_f32;
+            const int es = wide ? 4 : (int)sizeof(T);
+            const unsigned step = (unsigned)(a.H * DV) * es;
+            char* base = static_cast<char*>(a.out) + ((rows.start + rows.low(m0)) * a.H + h) * DV * es;
+            const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
+                reinterpret_cast<void*>(uni64(reinterpret_cast<int64_t>(base))), 0,
+                uni((unsigned)(rows.tokens(m0) - 1) * step + DV * es), 0x00027000);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                const int m = m0 + 16 * t + lr;
-                if (!rows.has(m)) continue;
-                const int64_t at = (rows.token(m) * a.H + h) * DV + wcol + 4 * lg;
+                const int row = 16 * t + lr;
+                const unsigned at = (unsigned)(rev ? C - 1 - row : row) * step + (unsigned)((wcol + 4 * lg) * es);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    if (MODE == kGrad && a.out_f32) store4<float>(static_cast<float*>(a.out) + at + 16 * n, acc[t][n]);
-                    else store4<T>(static_cast<T*>(a.out) + at + 16 * n, acc[t][n]);
+                    if (sizeof(T) == 4 || wide) {
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc[t][n]), rsrc, at + 16 * n * 4, 0, 0);
+                    } else {
+                        const u32x2_t p = {cvt2(acc[t][n][0], acc[t][n][1]), cvt2(acc[t][n][2], acc[t][n][3])};
+                        __builtin_amdgcn_raw_buffer_store_b64(p, rsrc, at + 16 * n * 2, 0, 0);
+                    }
                 }
             }
+        }
+        if (KB == 1 && more) {
+            barrier_keep_loads();   // k is read
+            fetch_k(m0 + C);
         }
     }
 
