@@ -228,9 +228,13 @@ struct __attribute__((aligned(16))) Tables {
     float upto[3][C];   // exp2(G at the start of tile t + 1 - G_j), j before it
     float in[C];        // exp2(G_i)
     float out[C];       // exp2(G_63 - G_j)
-    float row[4][C];    // partial sums of the waves (decay gradient)
-    float g[2][C];      // log-decays of the next two chunks
     float total;
+};
+// beside the two tables: log-decays of two chunks, and partial sums of the
+// waves for the decay's gradient
+struct __attribute__((aligned(16))) Scratch {
+    float g[2][C];
+    float row[4][C];
 };
 
 __device__ __forceinline__ double shfl_d(double x, int src) {
@@ -286,16 +290,6 @@ __device__ __forceinline__ void write_tables(Tables* t, double G, int lane, bool
 
 enum : int { kOut = 0, kState = 1, kGrad = 2 };
 
-// Buffers of the k rows: two where the LDS of two workgroups a CU allows it.
-template <int MODE> constexpr int kbufs() { return MODE == kGrad ? 1 : 2; }
-
-// Bytes of LDS: row tiles of k, v, q (and the extra rows), P, the tables.
-template <typename T, int DK, int DV, int MODE>
-constexpr int lds_bytes() {
-    const int rows = kbufs<MODE>() * DK + DV + (MODE == kState ? 0 : DK) + (MODE == kGrad ? DV : 0);
-    return C * rows * (int)sizeof(T) + (MODE == kState ? 0 : C * C * (int)sizeof(T)) + (int)sizeof(Tables);
-}
-
 // Tokens of a block in the order they are handled: chunk boundaries lie at the
 // same tokens in both directions, so backwards the first rows may be empty.
 struct Rows {
@@ -338,15 +332,99 @@ __device__ __forceinline__ void copy_tile(T* t, const LinRows& x, int h, const R
     const int top = rows.tokens(m0) - 1;
     const unsigned step = (unsigned)x.stride * (unsigned)sizeof(T);
     const T* base = (const T*)x.p + (rows.start + rows.low(m0)) * x.stride + (int64_t)(h / x.share) * D;
-    const void* ub = reinterpret_cast<const void*>(uni64(reinterpret_cast<int64_t>(base)));
+    const int64_t ub = uni64(reinterpret_cast<int64_t>(base));
     const unsigned lds = uni(lds_addr(t) + wave * 1024);
+    const int row0 = wave * RPW + lane / PIECES;
+    if (top == C - 1) {
+        const unsigned off = (unsigned)(rows.rev ? 4 * RPW - 1 - row0 : row0) * step;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int row = (i * 4 + wave) * RPW + lane / PIECES;
-        const int tok = rows.rev ? C - 1 - row : row;
-        copy16(lds + i * 4096, ub,
-               (unsigned)(tok < top ? tok : top) * step + (unsigned)((lane % PIECES) ^ Tile<T, D>::swz(row)) * 16u);
+        for (int i = 0; i < N; ++i)
+            copy16(lds + i * 4096, reinterpret_cast<const void*>(ub + (int64_t)((rows.rev ? N - 1 - i : i) * 4 * RPW) * step),
+                   off + (unsigned)((lane % PIECES) ^ Tile<T, D>::swz(4 * RPW * i + row0)) * 16u);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int row = i * 4 * RPW + row0;
+            const int tok = rows.rev ? C - 1 - row : row;
+            copy16(lds + i * 4096, reinterpret_cast<const void*>(ub),
+                   (unsigned)(tok < top ? tok : top) * step + (unsigned)((lane % PIECES) ^ Tile<T, D>::swz(row)) * 16u);
+        }
     }
+}
+
+// A wave's columns of the v rows (SW of them): to registers a chunk ahead, then
+// 32 tokens at a time through LDS of the wave's own, where the transposing reads
+// take them.  No other wave waits for them, and P's tiles of the wave take their
+// place once they are read.
+template <typename T, int SW>
+struct Slice {
+    static constexpr int EP = 16 / (int)sizeof(T), PIECES = SW / EP, RPI = 64 / PIECES, N = C / RPI, HALF = N / 2;
+    static constexpr int SIZE = 32 * SW > 3 * 256 ? 32 * SW : 3 * 256;   // elements: half the rows, or three tiles of P
+    static_assert(N % 2 == 0, "two halves");
+    u32x4_t r[N];
+    static __device__ __forceinline__ int off(int row, int col) {
+        // conflict-free for SW = 32 in bf16: rows r and r + 4 in different pieces
+        const int x = PIECES >= 4 ? ((row >> 2) & 1) * (PIECES / 2) : 0;
+        return row * SW + (((col / EP) ^ x) * EP) + col % EP;
+    }
+    __device__ __forceinline__ void load(const LinRows& x, int h, int D, int col0, const Rows& rows, int m0, int lane) {
+        const unsigned step = (unsigned)x.stride * (unsigned)sizeof(T);
+        const T* base = (const T*)x.p + (rows.start + rows.low(m0)) * x.stride + (int64_t)(h / x.share) * D + col0;
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
+            reinterpret_cast<void*>(uni64(reinterpret_cast<int64_t>(base))), 0,
+            uni((unsigned)(rows.tokens(m0) - 1) * step + SW * (unsigned)sizeof(T)), 0x00027000);
+        const int row = lane / PIECES;
+        const unsigned at = (unsigned)(rows.rev ? RPI - 1 - row : row) * step + (lane % PIECES) * 16u;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            r[i] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, at, (unsigned)((rows.rev ? N - 1 - i : i) * RPI) * step, 0);
+    }
+    // tokens 32 s .. of the wave's columns as operands
+    template <int NT>
+    __device__ __forceinline__ void cols(T* t, int s, int lane, Frag8<T> (&f)[NT]) const {
+#pragma unroll
+        for (int i = 0; i < HALF; ++i)
+            *reinterpret_cast<u32x4_t*>(t + off(i * RPI + lane / PIECES, (lane % PIECES) * EP)) = r[s * HALF + i];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            if constexpr (sizeof(T) == 2) {
+                const int row = 4 * (lane >> 4) + ((lane & 15) >> 2), col = 16 * n + 4 * (lane & 3);
+                const bf16x4_t x = __builtin_bit_cast(bf16x4_t, lds_tr(t + off(row, col)));
+                const bf16x4_t y = __builtin_bit_cast(bf16x4_t, lds_tr(t + off(row + 16, col)));
+                f[n].v = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+            } else {
+                const int row = 4 * (lane >> 4), col = 16 * n + (lane & 15);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    f[n].v[i] = t[off(row + i, col)];
+                    f[n].v[4 + i] = t[off(row + 16 + i, col)];
+                }
+            }
+        }
+    }
+};
+
+// P, 16 x 16 tiles of their own: rows of 16 elements, 4 at a time.  Tile
+// (ti, tj) is the slot-th of wave `owner`.
+struct PSlot { int owner, slot; };
+__device__ __forceinline__ constexpr PSlot p_slot(int ti, int tj) {
+    return ti == 0 ? (tj == 0 ? PSlot{0, 0} : PSlot{2, 2}) : ti == 1 ? PSlot{0, 1 + tj}
+         : ti == 2 ? (tj < 3 ? PSlot{1, tj} : PSlot{3, 2}) : tj < 2 ? PSlot{2, tj} : PSlot{3, tj - 2};
+}
+template <typename T>
+__device__ __forceinline__ int p_off(int i, int j4) {   // row, run of 4 columns
+    return i * 16 + (sizeof(T) == 2 ? (j4 ^ ((i >> 2) & 2)) : (j4 ^ ((i >> 2) & 3))) * 4;
+}
+
+// LDS.  Prompt and state pass: k and q rows twice (the copy of the next chunk's
+// runs through a whole chunk), the waves' slices of v, which P takes over, and
+// the tables twice: two workgroups a CU in bf16.  Gradient runs: rows k, v, q, x
+// once, P, the tables twice.
+template <typename T, int DK, int DV, int MODE>
+constexpr int lds_bytes() {
+    const int sz = (int)sizeof(T), tables = 2 * (int)sizeof(Tables) + (MODE == kGrad ? (int)sizeof(Scratch) : (int)sizeof(float[2][C]));
+    if (MODE == kGrad) return C * (2 * DK + 2 * DV) * sz + C * C * sz + tables;
+    return 2 * C * DK * sz * (MODE == kState ? 1 : 2) + 4 * Slice<T, DV / 4>::SIZE * sz + tables;
 }
 
 // Eight values as a sum of NS operands of type T.  One: rounded to nearest.
@@ -414,13 +492,14 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
     constexpr int NU = kBf ? 3 : 1;         // parts of an update operand
     constexpr int NS = kBf && MODE == kGrad ? 3 : 1;   // parts of the state as an operand
     extern __shared__ __attribute__((aligned(16))) char smem[];
-    constexpr int KB = kbufs<MODE>();
-    T* const skb = reinterpret_cast<T*>(smem);          // [KB][C][DK]
-    T* const sv = skb + KB * C * DK;                    // [C][DV]
-    T* const sq = sv + C * DV;                          // [C][DK]
-    T* const sx = sq + (MODE == kState ? 0 : C * DK);   // [C][DV]
-    T* const sp = sx + (MODE == kGrad ? C * DV : 0);    // [C][C]
-    Tables* const tb = reinterpret_cast<Tables*>(sp + (MODE == kState ? 0 : C * C));
+    constexpr bool kPair = MODE != kGrad;               // two buffers of k and q
+    T* const skb = reinterpret_cast<T*>(smem);          // [2 or 1][C][DK]
+    T* const sqb = skb + (kPair ? 2 : 1) * C * DK;      // [2 or 1][C][DK]
+    T* const sv = sqb + (MODE == kState ? 0 : kPair ? 2 : 1) * C * DK;   // slices, or [C][DV]
+    T* const sx = sv + (kPair ? 4 * Slice<T, DV / 4>::SIZE : C * DV);   // [C][DV]
+    T* const sp = sx + (kPair ? 0 : C * DV);            // [C][C]
+    Tables* const tbb = reinterpret_cast<Tables*>(sp + (kPair ? 0 : C * C));
+    Scratch* const scr = reinterpret_cast<Scratch*>(tbb + 2);
 
     const int tid = threadIdx.x, lane0 = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     int lane = lane0, lr = lane & 15, lg = lane >> 4;
@@ -461,41 +540,49 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
     }
 
     double sum_total = 0.0;
-    // The log-decay of local row m goes to tb->g (wave 0), two chunks ahead.
+    constexpr int kTab = 3;    // the wave that makes the tables: one with two tiles of P
+    // The log-decay of local row m goes to LDS, two chunks ahead.
     auto fetch_g = [&](int m0) {
         int64_t tok = rows.token(m0 + lane) + (rev ? 1 : 0);   // backwards: the token after it
         tok = tok < 0 ? 0 : tok >= a.T_total ? a.T_total - 1 : tok;
-        copy4(uni(lds_addr(tb->g[(m0 / C) & 1])), a.g + (a.g_per_token ? tok * a.H + h : h));
+        copy4(uni(lds_addr(scr->g[(m0 / C) & 1])), a.g + (a.g_per_token ? tok * a.H + h : h));
     };
-    auto fetch_k = [&](int m0) {
-        copy_tile<T, DK>(skb + (KB == 2 ? ((m0 / C) & 1) * C * DK : 0), a.k, h, rows, m0, wave, lane);
+    Slice<T, DV / 4> rv;
+    auto fetch_kq = [&](int m0) {
+        const int at = kPair ? ((m0 / C) & 1) * C * DK : 0;
+        copy_tile<T, DK>(skb + at, a.k, h, rows, m0, wave, lane);
+        if constexpr (MODE == kOut) copy_tile<T, DK>(sqb + at, a.q, h, rows, m0, wave, lane);
     };
-    auto fetch_rest = [&](int m0) {
-        copy_tile<T, DV>(sv, a.v, h, rows, m0, wave, lane);
-        if constexpr (MODE != kState) copy_tile<T, DK>(sq, a.q, h, rows, m0, wave, lane);
-        if constexpr (MODE == kGrad) copy_tile<T, DV>(sx, a.x, h, rows, m0, wave, lane);
+    auto fetch_v = [&](int m0) {
+        if constexpr (kPair) {
+            rv.load(a.v, h, DV, wcol, rows, m0, lane);
+        } else {
+            copy_tile<T, DV>(sv, a.v, h, rows, m0, wave, lane);
+            copy_tile<T, DK>(sqb, a.q, h, rows, m0, wave, lane);
+            copy_tile<T, DV>(sx, a.x, h, rows, m0, wave, lane);
+        }
     };
     auto tables = [&](int m0) {
         const int m = m0 + lane;
         const bool valid = rows.has(m);
         // backwards nothing decays before the sequence's last token
-        const float g = valid && !(rev && first && rows.token(m) == bl.start + cnt - 1) ? tb->g[(m0 / C) & 1][lane] : 0.f;
+        const float g = valid && !(rev && first && rows.token(m) == bl.start + cnt - 1) ? scr->g[(m0 / C) & 1][lane] : 0.f;
         const double G = decay_scan(g);
-        write_tables(tb, G, lane, valid, rev);
+        write_tables(tbb + ((m0 / C) & 1), G, lane, valid, rev);
         if (MODE == kState) sum_total += lane_d(G, 63);
     };
     // Stores of a wave and chunk, the youngest of its memory operations where
     // the copies are waited for.
     constexpr int NST = MODE == kOut ? 4 * NT : 0;
     if (cnt > 0) {
-        if (wave == 0) {
+        if (wave == kTab) {
             fetch_g(0);
             if (C < rows.rows) fetch_g(C);
         }
-        fetch_k(0);
-        fetch_rest(0);
+        fetch_kq(0);
+        fetch_v(0);
         wait_vmcnt<0>();
-        if (wave == 0) tables(0);
+        if (wave == kTab) tables(0);
     }
     for (int m0 = 0; m0 < rows.rows; m0 += C) {
         // LDS addresses are formed anew in each chunk (a few dozen operations):
@@ -507,23 +594,27 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
         // A: this chunk's copies and tables are there; the chunk before is read
         if (m0 > 0) wait_vmcnt<NST>();
         barrier_keep_loads();
-        const T* const sk = skb + (KB == 2 ? ((m0 / C) & 1) * C * DK : 0);
+        const T* const sk = skb + (kPair ? ((m0 / C) & 1) * C * DK : 0);
+        const T* const sq = sqb + (kPair ? ((m0 / C) & 1) * C * DK : 0);
+        const Tables* const tb = tbb + ((m0 / C) & 1);
         const bool more = m0 + C < rows.rows;
-        if (wave == 0 && m0 + 2 * C < rows.rows) fetch_g(m0 + 2 * C);
-        if (KB == 2 && more) fetch_k(m0 + C);
-
-        // v's columns of this wave and the factors of the update, before v is
-        // overwritten
+        // v's columns of this wave, before v is overwritten
         Frag8<T> fv[2][NT];
-        f32x4_t eo[2][2];
+        T* const slice = sv + wave * Slice<T, DV / 4>::SIZE;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
+            if constexpr (kPair) {
+                rv.cols(slice, s, lane, fv[s]);
+            } else {
 #pragma unroll
-            for (int n = 0; n < NT; ++n) fv[s][n] = Tile<T, DV>::cols(sv, wcol + 16 * n, s, lane);
-            eo[s][0] = *reinterpret_cast<const f32x4_t*>(&tb->out[32 * s + 4 * lg]) * a.u_scale;
-            eo[s][1] = *reinterpret_cast<const f32x4_t*>(&tb->out[32 * s + 16 + 4 * lg]) * a.u_scale;
+                for (int n = 0; n < NT; ++n) fv[s][n] = Tile<T, DV>::cols(sv, wcol + 16 * n, s, lane);
+            }
         }
-        const float total = tb->total;
+        if (wave == kTab && m0 + 2 * C < rows.rows) fetch_g(m0 + 2 * C);
+        if (kPair && more) {
+            fetch_kq(m0 + C);
+            fetch_v(m0 + C);
+        }
 
         // outputs, transposed tiles: a lane holds 4 consecutive columns of row
         // 16 t + l % 16
@@ -532,6 +623,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
             // P, transposed tiles (rows j, columns i): a lane holds 4 consecutive
             // j of one i.  Waves take 3, 3, 2 and 2 of the 10 tiles on or below
             // the diagonal; two tiles above it are read as zeros.
+            auto put_p = [&](int ti, int tj, const f32x4_t& p) {
+                if constexpr (kPair) store4<T>(slice + p_slot(ti, tj).slot * 256 + p_off<T>(lr, lg), p);
+                else store4<T>(sp + Tile<T, C>::off(16 * ti + lr, 16 * tj + 4 * lg), p);
+            };
             auto ptile = [&](int ti, int tj) {
                 f32x4_t c = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -553,7 +648,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
                 f32x4_t p;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) p[r] = ti != tj || j + r <= i ? c[r] * w[r] * a.p_scale : 0.f;
-                store4<T>(sp + Tile<T, C>::off(i, j), p);
+                put_p(ti, tj, p);
                 if constexpr (MODE == kGrad) {
                     if (a.pairs) {
                         // weight of each pair i > j in the decay's gradient
@@ -567,18 +662,16 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
                             const float e = j + r < i ? p[r] * d[r] : 0.f;
                             sum += e;
                             const float col = row16_sum(e);
-                            if (lr == 0) atomicAdd(&tb->row[wave][j + r], -col);
+                            if (lr == 0) atomicAdd(&scr->row[wave][j + r], -col);
                         }
                         sum += __shfl_xor(sum, 16);
                         sum += __shfl_xor(sum, 32);
-                        if (lg == 0) atomicAdd(&tb->row[wave][i], sum);
+                        if (lg == 0) atomicAdd(&scr->row[wave][i], sum);
                     }
                 }
             };
-            auto pzero = [&](int ti, int tj) {
-                store4<T>(sp + Tile<T, C>::off(16 * ti + lr, 16 * tj + 4 * lg), f32x4_t{0.f, 0.f, 0.f, 0.f});
-            };
-            if constexpr (MODE == kGrad) tb->row[wave][lane] = 0.f;
+            auto pzero = [&](int ti, int tj) { put_p(ti, tj, f32x4_t{0.f, 0.f, 0.f, 0.f}); };
+            if constexpr (MODE == kGrad) scr->row[wave][lane] = 0.f;
             if (wave == 0) {
                 ptile(0, 0);
                 ptile(1, 0);
@@ -640,44 +733,66 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
                 if constexpr (MODE == kGrad) {
                     dot += __shfl_xor(dot, 16);
                     dot += __shfl_xor(dot, 32);
-                    if (lg == 0) atomicAdd(&tb->row[wave][i], dot);
+                    if (lg == 0) atomicAdd(&scr->row[wave][i], dot);
                 }
             }
-            // B: P is whole; v, q, x and the tables are read
+            // the next chunk's tables: its decays came with this chunk's copies
+            if (kPair && wave == kTab && more) tables(m0 + C);
+            // B: P is whole; v, q and x are read
             barrier_keep_loads();
             if constexpr (MODE == kGrad) {
                 if (tid < C && rows.has(m0 + tid)) {
                     a.sums[(int64_t)h * a.T_total + rows.token(m0 + tid)] =
-                        (tb->row[0][tid] + tb->row[1][tid]) + (tb->row[2][tid] + tb->row[3][tid]);
+                        (scr->row[0][tid] + scr->row[1][tid]) + (scr->row[2][tid] + scr->row[3][tid]);
                 }
             }
         }
-        if constexpr (MODE == kState) barrier_keep_loads();
-        if (more) {
-            fetch_rest(m0 + C);
-            if (wave == 0) tables(m0 + C);
-        }
+        if (MODE == kState && wave == kTab && more) tables(m0 + C);
+        if (!kPair && more) fetch_v(m0 + C);
+        const float total = tb->total;
 #pragma unroll
         for (int i = 0; i < KT; ++i)
 #pragma unroll
             for (int n = 0; n < NT; ++n) S[i][n] *= total;
+        auto get_p = [&](int t, int s) {
+            if constexpr (!kPair) return Tile<T, C>::rows(sp, 16 * t, s, lane);
+            Frag8<T> f;
+            const PSlot p0 = p_slot(t, 2 * s), p1 = p_slot(t, 2 * s + 1);
+            constexpr int SL = Slice<T, DV / 4>::SIZE;
+            const T* x = sv + p0.owner * SL + p0.slot * 256 + p_off<T>(lr, lg);
+            const T* y = sv + p1.owner * SL + p1.slot * 256 + p_off<T>(lr, lg);
+            if constexpr (kBf) {
+                f.v = __builtin_shufflevector(*reinterpret_cast<const bf16x4_t*>(x), *reinterpret_cast<const bf16x4_t*>(y),
+                                              0, 1, 2, 3, 4, 5, 6, 7);
+            } else {
+                const f32x4_t u = load4(x), w = load4(y);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    f.v[r] = u[r];
+                    f.v[4 + r] = w[r];
+                }
+            }
+            return f;
+        };
 #pragma unroll
         for (int s = 0; s < C / 32; ++s) {
             Frag8<T> fu[NT][NU];
+            const f32x4_t e0 = *reinterpret_cast<const f32x4_t*>(&tb->out[32 * s + 4 * lg]) * a.u_scale;
+            const f32x4_t e1 = *reinterpret_cast<const f32x4_t*>(&tb->out[32 * s + 16 + 4 * lg]) * a.u_scale;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 float x[8];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    x[r] = fv[s][n].get(r) * eo[s][0][r];
-                    x[4 + r] = fv[s][n].get(4 + r) * eo[s][1][r];
+                    x[r] = fv[s][n].get(r) * e0[r];
+                    x[4 + r] = fv[s][n].get(4 + r) * e1[r];
                 }
                 split(x, fu[n]);
             }
             if constexpr (MODE != kState) {
 #pragma unroll
                 for (int t = 2 * s; t < 4; ++t) {
-                    const Frag8<T> fp = Tile<T, C>::rows(sp, 16 * t, s, lane);
+                    const Frag8<T> fp = get_p(t, s);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) acc[t][n] = mma(fv[s][n], fp, acc[t][n]);
                 }
@@ -716,9 +831,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
                 }
             }
         }
-        if (KB == 1 && more) {
+        if (!kPair && more) {
+            if (wave == kTab) tables(m0 + C);
             barrier_keep_loads();   // k is read
-            fetch_k(m0 + C);
+            fetch_kq(m0 + C);
         }
     }
 
@@ -726,7 +842,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
     float f = 1.f;
     if (MODE == kState) {
         dst = a.states + ((int64_t)b * a.H + h) * DK * DV;
-        if (tid == 0) a.decays[(int64_t)b * a.H + h] = exp2_fast((float)sum_total);
+        if (tid == 64 * kTab) a.decays[(int64_t)b * a.H + h] = exp2_fast((float)sum_total);
     } else if (last && a.final) {
         dst = a.final + ((int64_t)bl.n * a.H + h) * DK * DV;
         // backwards: the first token's own decay is still to come
