@@ -105,6 +105,24 @@ struct Tile {
         }
         return f;
     }
+    // rows row0 + l % 16, contraction 32 s + 8 g + (0..7): for products of two
+    // operands that are both read by rows
+    static __device__ __forceinline__ Frag8<T> rows8(const T* t, int row0, int s, int lane) {
+        const int row = row0 + (lane & 15), k = 32 * s + 8 * (lane >> 4);
+        Frag8<T> f;
+        if constexpr (sizeof(T) == 2) {
+            f.v = *reinterpret_cast<const bf16x8_t*>(t + off(row, k));
+        } else {
+            const f32x4_t a = *reinterpret_cast<const f32x4_t*>(t + off(row, k));
+            const f32x4_t b = *reinterpret_cast<const f32x4_t*>(t + off(row, k + 4));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f.v[i] = a[i];
+                f.v[4 + i] = b[i];
+            }
+        }
+        return f;
+    }
     // columns col0 + l % 16, contraction over rows 32 s + {0, 16} + 4 g + (0..3)
     static __device__ __forceinline__ Frag8<T> cols(const T* t, int col0, int s, int lane) {
         Frag8<T> f;
@@ -130,6 +148,9 @@ struct Tile {
 
 // The same value in every lane, as a scalar.
 __device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ float unif(float x) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, x)));
+}
 __device__ __forceinline__ int64_t uni64(int64_t x) {
     return ((int64_t)uni((int)(x >> 32)) << 32) | (uint32_t)uni((int)x);
 }
@@ -315,12 +336,13 @@ __device__ __forceinline__ unsigned lds_addr(const void* p) {
     return (unsigned)(uintptr_t)(__attribute__((address_space(3))) const char*)p;
 }
 __device__ __forceinline__ void copy16(unsigned lds, const void* base, unsigned off) {
+    // (nothing the compiler does here keeps a value in m0)
     asm volatile("s_nop 4\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                 :: "s"(lds), "v"(off), "s"(base) : "memory", "m0");
+                 :: "s"(uni(lds)), "v"(off), "s"(uni64(reinterpret_cast<int64_t>(base))) : "memory");
 }
 __device__ __forceinline__ void copy4(unsigned lds, const void* addr) {
     asm volatile("s_nop 4\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
-                 :: "s"(lds), "v"(addr) : "memory", "m0");
+                 :: "s"(uni(lds)), "v"(addr) : "memory");
 }
 
 // The copy of a chunk's rows into a tile by the workgroup's four waves.  A
@@ -331,7 +353,7 @@ __device__ __forceinline__ void copy_tile(T* t, const LinRows& x, int h, const R
     constexpr int PIECES = Tile<T, D>::PIECES, RPW = 64 / PIECES, N = C / (4 * RPW);
     const int top = rows.tokens(m0) - 1;
     const unsigned step = (unsigned)x.stride * (unsigned)sizeof(T);
-    const T* base = (const T*)x.p + (rows.start + rows.low(m0)) * x.stride + (int64_t)(h / x.share) * D;
+    const T* base = (const T*)x.p + (rows.start + rows.low(m0)) * x.stride + (int64_t)h * D;
     const int64_t ub = uni64(reinterpret_cast<int64_t>(base));
     const unsigned lds = uni(lds_addr(t) + wave * 1024);
     const int row0 = wave * RPW + lane / PIECES;
@@ -369,7 +391,7 @@ struct Slice {
     }
     __device__ __forceinline__ void load(const LinRows& x, int h, int D, int col0, const Rows& rows, int m0, int lane) {
         const unsigned step = (unsigned)x.stride * (unsigned)sizeof(T);
-        const T* base = (const T*)x.p + (rows.start + rows.low(m0)) * x.stride + (int64_t)(h / x.share) * D + col0;
+        const T* base = (const T*)x.p + (rows.start + rows.low(m0)) * x.stride + (int64_t)h * D + col0;
         const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
             reinterpret_cast<void*>(uni64(reinterpret_cast<int64_t>(base))), 0,
             uni((unsigned)(rows.tokens(m0) - 1) * step + SW * (unsigned)sizeof(T)), 0x00027000);
@@ -503,7 +525,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
 
     const int tid = threadIdx.x, lane0 = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     int lane = lane0, lr = lane & 15, lg = lane >> 4;
-    const int b = blockIdx.x / a.H, h = blockIdx.x % a.H;
+    // divisions run on the vector unit; their results are the same in every lane
+    const int b = uni(blockIdx.x / a.H), h = blockIdx.x - b * a.H;
+    const int hq = MODE == kState ? 0 : uni(h / a.q.share), hk = uni(h / a.k.share), hv = uni(h / a.v.share);
+    const int hx = MODE == kGrad ? uni(h / a.x.share) : 0;
     const Block bl = find_block(a, b);
     if (bl.n < 0) return;
     const bool rev = a.reverse;
@@ -539,6 +564,9 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
             }
     }
 
+    // The state is c S: a chunk's decay multiplies c, and S (with the update
+    // divided by c) only once c gets small, 64 multiplications a chunk less.
+    float c = 1.f;
     double sum_total = 0.0;
     constexpr int kTab = 3;    // the wave that makes the tables: one with two tiles of P
     // The log-decay of local row m goes to LDS, two chunks ahead.
@@ -550,16 +578,16 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
     Slice<T, DV / 4> rv;
     auto fetch_kq = [&](int m0) {
         const int at = kPair ? ((m0 / C) & 1) * C * DK : 0;
-        copy_tile<T, DK>(skb + at, a.k, h, rows, m0, wave, lane);
-        if constexpr (MODE == kOut) copy_tile<T, DK>(sqb + at, a.q, h, rows, m0, wave, lane);
+        copy_tile<T, DK>(skb + at, a.k, hk, rows, m0, wave, lane);
+        if constexpr (MODE == kOut) copy_tile<T, DK>(sqb + at, a.q, hq, rows, m0, wave, lane);
     };
     auto fetch_v = [&](int m0) {
         if constexpr (kPair) {
-            rv.load(a.v, h, DV, wcol, rows, m0, lane);
+            rv.load(a.v, hv, DV, wcol, rows, m0, lane);
         } else {
-            copy_tile<T, DV>(sv, a.v, h, rows, m0, wave, lane);
-            copy_tile<T, DK>(sqb, a.q, h, rows, m0, wave, lane);
-            copy_tile<T, DV>(sx, a.x, h, rows, m0, wave, lane);
+            copy_tile<T, DV>(sv, a.v, hv, rows, m0, wave, lane);
+            copy_tile<T, DK>(sqb, a.q, hq, rows, m0, wave, lane);
+            copy_tile<T, DV>(sx, a.x, hx, rows, m0, wave, lane);
         }
     };
     auto tables = [&](int m0) {
@@ -628,10 +656,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
                 else store4<T>(sp + Tile<T, C>::off(16 * ti + lr, 16 * tj + 4 * lg), p);
             };
             auto ptile = [&](int ti, int tj) {
-                f32x4_t c = {0.f, 0.f, 0.f, 0.f};
+                f32x4_t x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int s = 0; s < DK / 32; ++s)
-                    c = mma(Tile<T, DK>::rows(sk, 16 * tj, s, lane), Tile<T, DK>::rows(sq, 16 * ti, s, lane), c);
+                    x = mma(Tile<T, DK>::rows8(sk, 16 * tj, s, lane), Tile<T, DK>::rows8(sq, 16 * ti, s, lane), x);
                 const int i = 16 * ti + lr, j = 16 * tj + 4 * lg;
                 f32x4_t w;
                 if (ti == tj) {
@@ -647,7 +675,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
                 }
                 f32x4_t p;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) p[r] = ti != tj || j + r <= i ? c[r] * w[r] * a.p_scale : 0.f;
+                for (int r = 0; r < 4; ++r) p[r] = ti != tj || j + r <= i ? x[r] * w[r] * a.p_scale : 0.f;
                 put_p(ti, tj, p);
                 if constexpr (MODE == kGrad) {
                     if (a.pairs) {
@@ -655,7 +683,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
                         f32x4_t d = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                         for (int s = 0; s < DV / 32; ++s)
-                            d = mma(Tile<T, DV>::rows(sv, 16 * tj, s, lane), Tile<T, DV>::rows(sx, 16 * ti, s, lane), d);
+                            d = mma(Tile<T, DV>::rows8(sv, 16 * tj, s, lane), Tile<T, DV>::rows8(sx, 16 * ti, s, lane), d);
                         float sum = 0.f;
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
@@ -719,7 +747,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 const int i = 16 * t + lr;
-                const float e = tb->in[i] * a.s_scale;
+                const float e = tb->in[i] * (a.s_scale * c);
                 float dot = 0.f;
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
@@ -749,11 +777,15 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
         }
         if (MODE == kState && wave == kTab && more) tables(m0 + C);
         if (!kPair && more) fetch_v(m0 + C);
-        const float total = tb->total;
+        c = unif(c * tb->total);
+        if (c < 1.f / 4096.f) {
 #pragma unroll
-        for (int i = 0; i < KT; ++i)
+            for (int i = 0; i < KT; ++i)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) S[i][n] *= total;
+                for (int n = 0; n < NT; ++n) S[i][n] *= c;
+            c = 1.f;
+        }
+        const float u = a.u_scale / c;
         auto get_p = [&](int t, int s) {
             if constexpr (!kPair) return Tile<T, C>::rows(sp, 16 * t, s, lane);
             Frag8<T> f;
@@ -777,8 +809,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
 #pragma unroll
         for (int s = 0; s < C / 32; ++s) {
             Frag8<T> fu[NT][NU];
-            const f32x4_t e0 = *reinterpret_cast<const f32x4_t*>(&tb->out[32 * s + 4 * lg]) * a.u_scale;
-            const f32x4_t e1 = *reinterpret_cast<const f32x4_t*>(&tb->out[32 * s + 16 + 4 * lg]) * a.u_scale;
+            const f32x4_t e0 = *reinterpret_cast<const f32x4_t*>(&tb->out[32 * s + 4 * lg]) * u;
+            const f32x4_t e1 = *reinterpret_cast<const f32x4_t*>(&tb->out[32 * s + 16 + 4 * lg]) * u;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 float x[8];
@@ -858,7 +890,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    dst[(int64_t)(16 * i + 4 * lg + r) * DV + wcol + 16 * n + lr] = S[i][n][r] * f;
+                    dst[(int64_t)(16 * i + 4 * lg + r) * DV + wcol + 16 * n + lr] = S[i][n][r] * (f * c);
     }
 }
 
