@@ -184,6 +184,10 @@ struct LinArgs {
     void* stream;
 };
 
+struct LinPair {
+    LinArgs a[2];
+};
+
 struct LinCarry {
     float* states;
     const float* decays;

@@ -42,15 +42,17 @@ int64_t block_len(int H, int64_t T, int64_t least, int64_t most) {
     return L < all ? L : all;
 }
 
-// Forward: blocks of at least 256 tokens.  The gradient keeps every block's
-// entering states and re-anchors its decay sums there: 256 to 1024 tokens.
-int64_t fwd_block(int H, int64_t T) { return block_len(H, T, 256, INT64_MAX); }
-int64_t bwd_block(int H, int64_t T) { return block_len(H, T, 256, 1024); }
+// One chunk at least: for few tokens the chain of chunks is what takes the time
+// (1531 ragged tokens of 8 heads, gradient: 105 us with blocks of 256 tokens or
+// more, 72 with 128, 67 with 64).  The gradient re-anchors its decay sums at
+// block ends: at most 1024 tokens.
+int64_t fwd_block(int H, int64_t T) { return block_len(H, T, 64, INT64_MAX); }
+int64_t bwd_block(int H, int64_t T) { return block_len(H, T, 64, 1024); }
 
 bool sizes_ok(kda_dtype dt, int H, int Hk, int dk, int dv, int num_seqs, int64_t T) {
     return dtype_ok(dt) && H > 0 && Hk > 0 && H % Hk == 0 && num_seqs > 0 && T >= 0 && T <= INT32_MAX - 64 &&
            (int64_t)num_seqs * H <= 65535 && head_ok(dk) && head_ok(dv) &&
-           (T / 256 + num_seqs) * H < (int64_t)1 << 31;
+           (T / 64 + num_seqs) * H < (int64_t)1 << 31;
 }
 
 // Parts of a workspace, each 256-byte aligned.
@@ -93,7 +95,7 @@ BwdLayout bwd_layout(int H, int Hk, int dk, int dv, int num_seqs, int64_t T) {
     l.sums_a = p.take(th);
     l.sums_b = p.take(th);
     l.dg = p.take(th);
-    l.share = p.take(Hk < H ? th * dk : 0);
+    l.share = p.take(Hk < H ? 2 * th * dk : 0);
     l.total = p.at;
     return l;
 }
@@ -335,10 +337,12 @@ kda_status kda_rope(kda_dtype dt, int64_t T, int Hq, int Hk, int d, int rot, kda
 
 namespace {
 
-// Rows walked side by side by the norm's gradient: a multiple of H, about
-// `want`, at most all rows.
-int64_t norm_slots(int64_t T, int H, int D) {
-    const int64_t want = D <= 256 ? 16384 : 2048;
+// Rows walked side by side by the norm's gradient: a multiple of H, at most all
+// rows, and about what fills the CUs (a row takes 16 to 1024 threads): each
+// adds a partial row of the weight's gradient.
+int64_t norm_slots(kda_dtype dt, int64_t T, int H, int D) {
+    const int vec = dt == KDA_BF16 ? 8 : 4, n = (D + vec - 1) / vec;
+    const int64_t want = n <= 16 ? 16384 : n <= 1024 / vec ? 4096 : n <= 4096 / vec ? 1024 : 512;
     int64_t p = (want + H - 1) / H;
     if (p > T) p = T;
     return (p < 1 ? 1 : p) * (int64_t)H;
@@ -385,7 +389,7 @@ kda_status kda_norm_fwd(kda_dtype dt, kda_norm_kind kind, int64_t T, int H, int 
 
 size_t kda_norm_bwd_workspace_size(kda_dtype dt, int64_t T, int H, int D) {
     if (!norm_sizes_ok(dt, T, H, D) || D > 16384) return 0;
-    return 2 * round_up((size_t)norm_slots(T, H, D) * D * 4, 256);
+    return 2 * round_up((size_t)norm_slots(dt, T, H, D) * D * 4, 256);
 }
 
 kda_status kda_norm_bwd(kda_dtype dt, kda_norm_kind kind, int64_t T, int H, int D, const void* x, const float* weight,
@@ -403,7 +407,7 @@ kda_status kda_norm_bwd(kda_dtype dt, kda_norm_kind kind, int64_t T, int H, int 
         !aligned(weight, 4) || !aligned(bias, 4) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(dweight, 4) ||
         !aligned(dbias, 4) || !aligned(workspace, 256))
         return KDA_ERR_INVALID_ARGUMENT;
-    const size_t half = round_up((size_t)norm_slots(T, H, D) * D * 4, 256);
+    const size_t half = round_up((size_t)norm_slots(dt, T, H, D) * D * 4, 256);
     if (workspace_bytes < 2 * half) return KDA_ERR_WORKSPACE_TOO_SMALL;
     kda::NormArgs a{};
     a.dtype = (int)dt;
@@ -424,7 +428,7 @@ kda_status kda_norm_bwd(kda_dtype dt, kda_norm_kind kind, int64_t T, int H, int 
     a.dbias = dbias;
     a.dwp = part<float>(workspace, 0);
     a.dbp = dbias ? part<float>(workspace, half) : nullptr;
-    a.slots = norm_slots(T, H, D);
+    a.slots = norm_slots(dt, T, H, D);
     a.stream = stream;
     return from_hip(kda::launch_norm(a));
 }

@@ -507,7 +507,8 @@ __device__ __forceinline__ f32x4_t load4(const float* p) { return *reinterpret_c
 // update's exp(G_63 - G_j) v_j enters as a sum of three bf16 values, so that
 // the state keeps its 24 bits.
 template <typename T, int DK, int DV, int MODE>
-__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(LinArgs a) {
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(LinPair pair) {
+    const LinArgs& a = pair.a[blockIdx.y];
     constexpr bool kBf = sizeof(T) == 2;
     constexpr int NT = DV / 64;             // 16-column tiles of a wave
     constexpr int KT = DK / 16;             // 16-row tiles of the state
@@ -1005,7 +1006,10 @@ __global__ __launch_bounds__(256) void linattn_dg_sum_kernel(int64_t T, int H, c
 
 // Sum over the value heads that share a key head: fp32 [T, H, D] to [T, H / r, D].
 template <typename T>
-__global__ __launch_bounds__(256) void linattn_share_kernel(int64_t n, int r, int D, const float* src, T* dst) {
+__global__ __launch_bounds__(256) void linattn_share_kernel(int64_t n, int r, int D, const float* src, T* dst0,
+                                                            T* dst1) {
+    T* dst = blockIdx.y ? dst1 : dst0;
+    src += blockIdx.y * n * r;
     const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
     if (i >= n) return;
     const int64_t row = i / D;
@@ -1017,31 +1021,32 @@ __global__ __launch_bounds__(256) void linattn_share_kernel(int64_t n, int r, in
 }
 
 template <typename T, int DK, int DV, int MODE>
-hipError_t launch_t(const LinArgs& a) {
+hipError_t launch_t(const LinArgs* a, int n) {
     constexpr int lds = lds_bytes<T, DK, DV, MODE>();
     static_assert(lds <= 160 * 1024, "LDS");
     const void* kern = reinterpret_cast<const void*>(&linattn_kernel<T, DK, DV, MODE>);
     hipError_t e = ensure_lds_limit(kern, lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((linattn_kernel<T, DK, DV, MODE>), dim3((unsigned)(a.nblocks * a.H)), dim3(256), lds,
-                       (hipStream_t)a.stream, a);
+    hipLaunchKernelGGL((linattn_kernel<T, DK, DV, MODE>), dim3((unsigned)(a->nblocks * a->H), n), dim3(256), lds,
+                       (hipStream_t)a->stream, LinPair{{a[0], a[n - 1]}});
     return hipGetLastError();
 }
 
 template <typename T, int MODE>
-hipError_t launch_m(const LinArgs& a, int dk, int dv) {
-    if (dk == 64) return dv == 64 ? launch_t<T, 64, 64, MODE>(a) : launch_t<T, 64, 128, MODE>(a);
-    return dv == 64 ? launch_t<T, 128, 64, MODE>(a) : launch_t<T, 128, 128, MODE>(a);
+hipError_t launch_m(const LinArgs* a, int n, int dk, int dv) {
+    if (dk == 64) return dv == 64 ? launch_t<T, 64, 64, MODE>(a, n) : launch_t<T, 64, 128, MODE>(a, n);
+    return dv == 64 ? launch_t<T, 128, 64, MODE>(a, n) : launch_t<T, 128, 128, MODE>(a, n);
 }
 
 template <typename T>
-hipError_t launch_k(const LinArgs& a, int dk, int dv, int mode) {
-    if (mode == kState) return launch_m<T, kState>(a, dk, dv);
-    return mode == kOut ? launch_m<T, kOut>(a, dk, dv) : launch_m<T, kGrad>(a, dk, dv);
+hipError_t launch_k(const LinArgs* a, int n, int dk, int dv, int mode) {
+    if (mode == kState) return launch_m<T, kState>(a, n, dk, dv);
+    return mode == kOut ? launch_m<T, kOut>(a, n, dk, dv) : launch_m<T, kGrad>(a, n, dk, dv);
 }
 
-hipError_t launch_core(const LinArgs& a, int dtype, int dk, int dv, int mode) {
-    return dtype == 0 ? launch_k<__bf16>(a, dk, dv, mode) : launch_k<float>(a, dk, dv, mode);
+// One or two runs of the same kernel, side by side in one launch.
+hipError_t launch_core(const LinArgs* a, int n, int dtype, int dk, int dv, int mode) {
+    return dtype == 0 ? launch_k<__bf16>(a, n, dk, dv, mode) : launch_k<float>(a, n, dk, dv, mode);
 }
 
 }  // namespace
@@ -1058,7 +1063,7 @@ hipError_t launch_linattn_fwd(const LinCall& c) {
         LinArgs s = a;
         s.states = c.states;
         s.decays = c.decays;
-        hipError_t e = launch_core(s, c.dtype, c.dk, c.dv, kState);
+        hipError_t e = launch_core(&s, 1, c.dtype, c.dk, c.dv, kState);
         if (e != hipSuccess) return e;
         const LinCarry f{c.states, c.decays, c.initial_state, nullptr, 0};
         hipLaunchKernelGGL(linattn_carry_kernel, dim3((unsigned)(c.dk * c.dv / 1024), (unsigned)(a.num_seqs * a.H), 1),
@@ -1071,7 +1076,7 @@ hipError_t launch_linattn_fwd(const LinCall& c) {
     }
     a.final = c.final_state;
     a.out = c.y;
-    return launch_core(a, c.dtype, c.dk, c.dv, kOut);
+    return launch_core(&a, 1, c.dtype, c.dk, c.dv, kOut);
 }
 
 hipError_t launch_linattn_bwd(const LinCall& c) {
@@ -1079,83 +1084,77 @@ hipError_t launch_linattn_bwd(const LinCall& c) {
     a.p_scale = c.scale;
     hipError_t e;
     // the blocks' own states, of the recurrence and of its gradient
-    LinArgs s = a;
-    s.k = c.k;
-    s.v = c.v;
-    s.u_scale = 1.f;
-    s.states = c.states;
-    s.decays = c.decays;
-    s.last_state = c.d_final_state != nullptr;
-    if ((e = launch_core(s, c.dtype, c.dk, c.dv, kState)) != hipSuccess) return e;
-    s.k = c.q;
-    s.v = c.dy;
-    s.u_scale = c.scale;
-    s.states = c.rstates;
-    s.decays = c.rdecays;
-    s.last_state = false;
-    s.reverse = true;
-    if ((e = launch_core(s, c.dtype, c.dk, c.dv, kState)) != hipSuccess) return e;
+    LinArgs s[2] = {a, a};
+    s[0].k = c.k;
+    s[0].v = c.v;
+    s[0].u_scale = 1.f;
+    s[0].states = c.states;
+    s[0].decays = c.decays;
+    s[0].last_state = c.d_final_state != nullptr;
+    s[1].k = c.q;
+    s[1].v = c.dy;
+    s[1].u_scale = c.scale;
+    s[1].states = c.rstates;
+    s[1].decays = c.rdecays;
+    s[1].reverse = true;
+    if ((e = launch_core(s, 2, c.dtype, c.dk, c.dv, kState)) != hipSuccess) return e;
     const LinCarry f{c.states, c.decays, c.initial_state, c.d_final_state ? c.s_end : nullptr, 0};
     const LinCarry r{c.rstates, c.rdecays, c.d_final_state, nullptr, 1};
     hipLaunchKernelGGL(linattn_carry_kernel, dim3((unsigned)(c.dk * c.dv / 1024), (unsigned)(a.num_seqs * a.H), 2),
                        dim3(256), 0, (hipStream_t)a.stream, a, f, r);
     if ((e = hipGetLastError()) != hipSuccess) return e;
 
+    // dq with the pairs' and the entering state's part of dg, and dk
     const bool shared = c.k.share > 1;
-    // dq, and the pairs' and entering state's part of dg
-    LinArgs x = a;
-    x.q = c.dy;
-    x.k = c.v;
-    x.v = c.k;
-    x.x = c.q;
-    x.s_scale = c.scale;
-    x.u_scale = 1.f;
-    x.states = c.states;
-    x.transposed = true;
-    x.pairs = true;
-    x.sums = c.sums_a;
-    x.out = shared ? c.share_buf : c.dq;
-    x.out_f32 = shared;
-    if ((e = launch_core(x, c.dtype, c.dv, c.dk, kGrad)) != hipSuccess) return e;
-    auto share = [&](void* dst) -> hipError_t {
-        const int64_t n = a.T_total * (a.H / c.k.share) * c.dk;
-        if (n == 0) return hipSuccess;
-        const dim3 grid((unsigned)((n / 4 + 255) / 256));
+    LinArgs x[2] = {a, a};
+    x[0].q = c.dy;
+    x[0].k = c.v;
+    x[0].v = c.k;
+    x[0].x = c.q;
+    x[0].s_scale = c.scale;
+    x[0].u_scale = 1.f;
+    x[0].states = c.states;
+    x[0].transposed = true;
+    x[0].pairs = true;
+    x[0].sums = c.sums_a;
+    x[0].out = shared ? c.share_buf : c.dq;
+    x[0].out_f32 = shared;
+    x[1] = x[0];
+    x[1].q = c.v;
+    x[1].k = c.dy;
+    x[1].v = c.q;
+    x[1].x = c.k;
+    x[1].s_scale = 1.f;
+    x[1].u_scale = c.scale;
+    x[1].states = c.rstates;
+    x[1].pairs = false;
+    x[1].reverse = true;
+    x[1].sums = c.sums_b;
+    x[1].out = shared ? static_cast<float*>(c.share_buf) + a.T_total * a.H * c.dk : c.dk_out;
+    if ((e = launch_core(x, 2, c.dtype, c.dv, c.dk, kGrad)) != hipSuccess) return e;
+    const int64_t n = a.T_total * (a.H / c.k.share) * c.dk;
+    if (shared && n > 0) {
+        const dim3 grid((unsigned)((n / 4 + 255) / 256), 2);
         if (c.dtype == 0)
             hipLaunchKernelGGL(linattn_share_kernel<__bf16>, grid, dim3(256), 0, (hipStream_t)a.stream, n, c.k.share,
-                               c.dk, (const float*)c.share_buf, (__bf16*)dst);
+                               c.dk, (const float*)c.share_buf, (__bf16*)c.dq, (__bf16*)c.dk_out);
         else
             hipLaunchKernelGGL(linattn_share_kernel<float>, grid, dim3(256), 0, (hipStream_t)a.stream, n, c.k.share,
-                               c.dk, (const float*)c.share_buf, (float*)dst);
-        return hipGetLastError();
-    };
-    if (shared && (e = share(c.dq)) != hipSuccess) return e;
-    // dk
-    x.q = c.v;
-    x.k = c.dy;
-    x.v = c.q;
-    x.x = c.k;
-    x.s_scale = 1.f;
-    x.u_scale = c.scale;
-    x.states = c.rstates;
-    x.pairs = false;
-    x.reverse = true;
-    x.sums = c.sums_b;
-    x.out = shared ? c.share_buf : c.dk_out;
-    if ((e = launch_core(x, c.dtype, c.dv, c.dk, kGrad)) != hipSuccess) return e;
-    if (shared && (e = share(c.dk_out)) != hipSuccess) return e;
+                               c.dk, (const float*)c.share_buf, (float*)c.dq, (float*)c.dk_out);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
     // dv and the gradient of the initial state
-    x = a;
-    x.q = c.k;
-    x.k = c.q;
-    x.v = c.dy;
-    x.s_scale = 1.f;
-    x.u_scale = c.scale;
-    x.states = c.rstates;
-    x.reverse = true;
-    x.final = c.d_initial_state;
-    x.out = c.dv_out;
-    if ((e = launch_core(x, c.dtype, c.dk, c.dv, kOut)) != hipSuccess) return e;
+    LinArgs d = a;
+    d.q = c.k;
+    d.k = c.q;
+    d.v = c.dy;
+    d.s_scale = 1.f;
+    d.u_scale = c.scale;
+    d.states = c.rstates;
+    d.reverse = true;
+    d.final = c.d_initial_state;
+    d.out = c.dv_out;
+    if ((e = launch_core(&d, 1, c.dtype, c.dk, c.dv, kOut)) != hipSuccess) return e;
     // dg
     if (c.dg) {
         float* per_token = a.g_per_token ? c.dg : c.dg_tokens;
@@ -1187,7 +1186,11 @@ __global__ __launch_bounds__(256) void linattn_decode_kernel(LinDecodeArgs a) {
     __shared__ float s_o[RG][COLS + 4];
     const int tid = threadIdx.x, cg = tid % CG, rg = tid / CG;
     const int slices = a.dv / COLS;
-    const int nh = blockIdx.x / slices, col0 = (blockIdx.x % slices) * COLS;
+    // whole states: each XCD takes them in runs of two (workgroups i, i + 8,
+    // ... share one), as the KDA decode step does
+    int id = blockIdx.x;
+    if (slices == 1 && gridDim.x % 16 == 0) id = id / 16 * 16 + id % 8 * 2 + id / 8 % 2;
+    const int nh = id / slices, col0 = (id % slices) * COLS;
     const int n = nh / a.H, h = nh % a.H;
     float* st = a.state + (int64_t)nh * DK * a.dv + col0 + 4 * cg;
     f32x4_t S[RPT];

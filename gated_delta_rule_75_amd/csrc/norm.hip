@@ -28,6 +28,7 @@ struct Cols {
     int lane, D;
     __device__ __forceinline__ int at(int j) const { return (j * LANES + lane) * VEC; }
     __device__ __forceinline__ bool in(int j) const { return at(j) < D; }
+    __device__ __forceinline__ int left(int j) const { return D - at(j); }   // elements of the run, >= VEC: all
 };
 
 template <typename T, int VEC, int LANES, int NV>
@@ -46,7 +47,7 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_fwd_kernel(
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         if (c.in(j)) {
-            load_vec<T, VEC>(x + base + c.at(j), v[j]);
+            load_run<T, VEC>(x + base + c.at(j), c.left(j), v[j]);
         } else {
 #pragma unroll
             for (int i = 0; i < VEC; ++i) v[j][i] = 0.f;
@@ -61,7 +62,7 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_fwd_kernel(
     for (int j = 0; j < NV; ++j)
         if (c.in(j)) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) q += (v[j][i] - m) * (v[j][i] - m);
+            for (int i = 0; i < VEC; ++i) q += i < c.left(j) ? (v[j][i] - m) * (v[j][i] - m) : 0.f;
         }
     q = lanes_sum<LANES>(q, part[1]);
     const float r = 1.f / sqrtf(q / (float)D + eps);
@@ -69,22 +70,22 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_fwd_kernel(
     for (int j = 0; j < NV; ++j) {
         if (!c.in(j)) continue;
         float wv[VEC], o[VEC];
-        load_vec<float, VEC>(w + wb + c.at(j), wv);
+        load_run<float, VEC>(w + wb + c.at(j), c.left(j), wv);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) o[i] = (v[j][i] - m) * r * wv[i];
         if (b) {
             float bv[VEC];
-            load_vec<float, VEC>(b + wb + c.at(j), bv);
+            load_run<float, VEC>(b + wb + c.at(j), c.left(j), bv);
 #pragma unroll
             for (int i = 0; i < VEC; ++i) o[i] += bv[i];
         }
         if (z) {
             float zv[VEC];
-            load_vec<T, VEC>(z + base + c.at(j), zv);
+            load_run<T, VEC>(z + base + c.at(j), c.left(j), zv);
 #pragma unroll
             for (int i = 0; i < VEC; ++i) o[i] *= sigmoid(zv[i]);
         }
-        store_vec<T, VEC>(y + base + c.at(j), o);
+        store_run<T, VEC>(y + base + c.at(j), c.left(j), o);
     }
     if (c.lane == 0) {
         if (mean) mean[row] = m;
@@ -99,7 +100,7 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_bwd_kernel(
     const float* __restrict__ rstd, const T* __restrict__ dy, T* __restrict__ dx, T* __restrict__ dz,
     float* __restrict__ dwp, float* __restrict__ dbp) {
     constexpr int RPB = LANES < 256 ? 256 / LANES : 1;
-    __shared__ float part[2][2][LANES > 64 ? LANES / 64 : 1];
+    __shared__ float part[2][LANES > 64 ? LANES / 32 : 1];
     const int64_t slot = (int64_t)blockIdx.x * RPB + threadIdx.x / LANES;
     if (slot >= S) return;   // whole lane groups (a whole workgroup where LANES > 64)
     const Cols<VEC, LANES, NV> c{(int)(threadIdx.x % LANES), D};
@@ -110,37 +111,53 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_bwd_kernel(
 #pragma unroll
         for (int i = 0; i < VEC; ++i) wv[j][i] = bv[j][i] = aw[j][i] = ab[j][i] = 0.f;
         if (c.in(j)) {
-            load_vec<float, VEC>(w + wb + c.at(j), wv[j]);
-            if (b) load_vec<float, VEC>(b + wb + c.at(j), bv[j]);
+            load_run<float, VEC>(w + wb + c.at(j), c.left(j), wv[j]);
+            if (b) load_run<float, VEC>(b + wb + c.at(j), c.left(j), bv[j]);
         }
     }
+    // a row's values are loaded while the row before is summed (not where 16
+    // elements a thread of 1024 leave no registers for it)
+    constexpr bool kAhead = LANES < 1024 || NV * VEC < 16;
+    typename VecOf<T, VEC>::type xn[NV], dn[NV], zn[NV];
+    float mn = 0.f, rn = 0.f;
+    auto fetch = [&](int64_t row) {
+        const int64_t base = row * D;
+        mn = mean ? mean[row] : 0.f;
+        rn = rstd[row];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if (!c.in(j)) continue;
+            xn[j] = load_raw<T, VEC>(x + base + c.at(j), c.left(j));
+            dn[j] = load_raw<T, VEC>(dy + base + c.at(j), c.left(j));
+            if (z) zn[j] = load_raw<T, VEC>(z + base + c.at(j), c.left(j));
+        }
+    };
+    if (kAhead && slot < rows) fetch(slot);
     int par = 0;
     for (int64_t row = slot; row < rows; row += S, par ^= 1) {
+        if (!kAhead) fetch(row);
         const int64_t base = row * D;
-        const float m = mean ? mean[row] : 0.f, r = rstd[row];
+        const float m = mn, r = rn;
         float h[NV][VEC], d[NV][VEC];
         float se = 0.f, seh = 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            if (!c.in(j)) {
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) h[j][i] = d[j][i] = 0.f;
-                continue;
+            for (int i = 0; i < VEC; ++i) {
+                const bool in = c.at(j) + i < D;
+                h[j][i] = in ? (to_f32((T)xn[j][i]) - m) * r : 0.f;
+                d[j][i] = in ? to_f32((T)dn[j][i]) : 0.f;
             }
-            load_vec<T, VEC>(x + base + c.at(j), h[j]);
-            load_vec<T, VEC>(dy + base + c.at(j), d[j]);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) h[j][i] = (h[j][i] - m) * r;
+            if (!c.in(j)) continue;
             if (z) {
-                float zv[VEC], o[VEC];
-                load_vec<T, VEC>(z + base + c.at(j), zv);
+                float o[VEC];
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
-                    const float s = sigmoid(zv[i]), ds = d[j][i] * s;
-                    o[i] = ds * (h[j][i] * wv[j][i] + bv[j][i]) * sigmoid(-zv[i]);   // 1 - s without cancellation
+                    const float g = to_f32((T)zn[j][i]), s = sigmoid(g), ds = d[j][i] * s;
+                    o[i] = ds * (h[j][i] * wv[j][i] + bv[j][i]) * sigmoid(-g);   // 1 - s without cancellation
                     d[j][i] = ds;
                 }
-                store_vec<T, VEC>(dz + base + c.at(j), o);
+                store_run<T, VEC>(dz + base + c.at(j), c.left(j), o);
             }
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
@@ -151,48 +168,52 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_bwd_kernel(
                 seh += d[j][i] * h[j][i];
             }
         }
+        if (kAhead && row + S < rows) fetch(row + S);
         // two buffers in turn: a row's sums are read before the barrier of the next row's
-        seh = lanes_sum<LANES>(seh, part[par][0]) / (float)D;
-        se = mean ? lanes_sum<LANES>(se, part[par][1]) / (float)D : 0.f;
+        lanes_sum2<LANES>(se, seh, part[par]);
+        seh /= (float)D;
+        se = mean ? se / (float)D : 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             if (!c.in(j)) continue;
             float o[VEC];
 #pragma unroll
             for (int i = 0; i < VEC; ++i) o[i] = r * (d[j][i] - h[j][i] * seh - se);
-            store_vec<T, VEC>(dx + base + c.at(j), o);
+            store_run<T, VEC>(dx + base + c.at(j), c.left(j), o);
         }
     }
     const int64_t pb = slot * D;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         if (!c.in(j)) continue;
-        store_vec<float, VEC>(dwp + pb + c.at(j), aw[j]);
-        if (dbp) store_vec<float, VEC>(dbp + pb + c.at(j), ab[j]);
+        store_run<float, VEC>(dwp + pb + c.at(j), c.left(j), aw[j]);
+        if (dbp) store_run<float, VEC>(dbp + pb + c.at(j), c.left(j), ab[j]);
     }
 }
 
-// dw[c] = sum over P partial rows of HD columns, in a fixed order: 16 threads
-// take every 16th partial of a column, then their sums are added.
-__global__ __launch_bounds__(256) void norm_reduce_kernel(int64_t P, int64_t HD, const float* __restrict__ dwp,
-                                                          const float* __restrict__ dbp, float* __restrict__ dw,
-                                                          float* __restrict__ db) {
-    __shared__ float s[16][17];
+// dw[c] = sum over P partial rows of HD columns, in a fixed order: 32 threads
+// take every 32nd partial of a column, then their sums are added.
+__global__ __launch_bounds__(1024) void norm_reduce_kernel(int64_t P, int64_t HD, const float* __restrict__ dwp,
+                                                           const float* __restrict__ dbp, float* __restrict__ dw,
+                                                           float* __restrict__ db) {
+    __shared__ float s[32][33];
     const float* src = blockIdx.y ? dbp : dwp;
     float* dst = blockIdx.y ? db : dw;
-    const int cx = threadIdx.x & 15, py = threadIdx.x >> 4;
-    const int64_t col = (int64_t)blockIdx.x * 16 + cx;
+    const int cx = threadIdx.x & 31, py = threadIdx.x >> 5;
+    const int64_t col = (int64_t)blockIdx.x * 32 + cx;
     float a = 0.f;
-    if (col < HD)
-        for (int64_t p = py; p < P; p += 16) a += src[p * HD + col];
+    if (col < HD) {
+#pragma unroll 4
+        for (int64_t p = py; p < P; p += 32) a += src[p * HD + col];
+    }
     s[py][cx] = a;
     __syncthreads();
-    if (py == 0 && col < HD) {
-        a = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) a += s[i][cx];
-        dst[col] = a;
-    }
+    // thread (py, cx) adds column py's 32 sums with its half wave
+    a = s[cx][py];
+    a = row16_sum(a);
+    a += __shfl_xor(a, 16);
+    const int64_t c2 = (int64_t)blockIdx.x * 32 + py;
+    if (cx == 0 && c2 < HD) dst[c2] = a;
 }
 
 template <typename T, int VEC, int LANES, int NV>
@@ -212,41 +233,25 @@ hipError_t launch_t(const NormArgs& a) {
 }
 
 // The narrowest lane group that holds a row with at most 16 elements a thread.
-template <typename T, int VEC>
-hipError_t launch_v(const NormArgs& a) {
+template <typename T>
+hipError_t launch_d(const NormArgs& a) {
+    constexpr int VEC = kVec16<T>;
     const int n = (a.D + VEC - 1) / VEC;   // runs of a row
     if (n <= 16) return launch_t<T, VEC, 16, 1>(a);
     if (n <= 64) return launch_t<T, VEC, 64, 1>(a);
     if (n <= 128) return launch_t<T, VEC, 64, 2>(a);
-    if constexpr (VEC <= 4) {
+    if constexpr (VEC == 4) {
         if (n <= 256) return launch_t<T, VEC, 64, 4>(a);
-    } else {
-        if (n <= 256) return launch_t<T, VEC, 256, 1>(a);
-    }
-    if (n <= 512) return launch_t<T, VEC, 256, 2>(a);
-    if constexpr (VEC == 1) {
-        if (n <= 1024) return launch_t<T, VEC, 256, 4>(a);
-        if (n <= 2048) return launch_t<T, VEC, 256, 8>(a);
-        if (n <= 4096) return launch_t<T, VEC, 256, 16>(a);
-        if (n <= 8192) return launch_t<T, VEC, 1024, 8>(a);
-        return launch_t<T, VEC, 1024, 16>(a);
-    } else if constexpr (VEC == 4) {
+        if (n <= 512) return launch_t<T, VEC, 256, 2>(a);
         if (n <= 1024) return launch_t<T, VEC, 256, 4>(a);
         if (n <= 2048) return launch_t<T, VEC, 1024, 2>(a);
         return launch_t<T, VEC, 1024, 4>(a);
     } else {
+        if (n <= 256) return launch_t<T, VEC, 256, 1>(a);
+        if (n <= 512) return launch_t<T, VEC, 256, 2>(a);
         if (n <= 1024) return launch_t<T, VEC, 1024, 1>(a);
         return launch_t<T, VEC, 1024, 2>(a);
     }
-}
-
-bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
-template <typename T>
-hipError_t launch_d(const NormArgs& a) {
-    const bool vec = a.D % kVec16<T> == 0 && al16(a.x) && al16(a.weight) && al16(a.bias) && al16(a.z) && al16(a.y) &&
-                     al16(a.dy) && al16(a.dx) && al16(a.dz);
-    return vec ? launch_v<T, kVec16<T>>(a) : launch_v<T, 1>(a);
 }
 
 }  // namespace
@@ -258,7 +263,7 @@ hipError_t launch_norm(const NormArgs& a) {
     }
     if (a.dweight) {
         const int64_t HD = (int64_t)a.H * a.D;
-        hipLaunchKernelGGL(norm_reduce_kernel, dim3((unsigned)((HD + 15) / 16), a.dbias ? 2 : 1), dim3(256), 0,
+        hipLaunchKernelGGL(norm_reduce_kernel, dim3((unsigned)((HD + 31) / 32), a.dbias ? 2 : 1), dim3(1024), 0,
                            (hipStream_t)a.stream, a.T > 0 ? a.slots / a.H : 0, HD, a.dwp, a.dbp, a.dweight, a.dbias);
         return hipGetLastError();
     }

@@ -10,7 +10,6 @@ that device's current stream.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import Optional, Tuple
 
@@ -27,13 +26,14 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
-def _device(first, *others):
+def _device(*ts):
     """The device that every given tensor lives on."""
-    dev = first.device
+    dev = ts[0].device
     if dev.type != "cuda":
         raise ValueError("libkda tensors must live on the GPU")
-    for t in others:
-        if t is not None and t.device != dev:
+    i = dev.index
+    for t in ts:
+        if t is not None and t.get_device() != i:
             raise ValueError("libkda tensors must share one device")
     return dev
 
@@ -44,15 +44,26 @@ def _contiguous(**ts):
             raise ValueError(f"{name} must be contiguous")
 
 
-def _on(dev):
-    """The call's device as the current one (a HIP launch needs its stream's)."""
-    if torch.cuda.current_device() == dev.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+def _call(dev, fn, name: str, *args) -> None:
+    """The C call on the device's current stream, with that device current (a HIP
+    launch needs its stream's)."""
+    i = dev.index
+    stream = _raw_stream(i)
+    if _current_device() == i:
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(i):
+            st = fn(*args, stream)
+    if st != 0:
+        raise KDAError(name, st)
 
 
-def _stream(dev) -> int:
-    return torch.cuda.current_stream(dev).cuda_stream
+def _raw_stream(i: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(i)
+
+
+def _current_device() -> int:
+    return torch._C._cuda_getDevice()
 
 
 def _rows(name: str, t: torch.Tensor) -> int:
@@ -141,11 +152,9 @@ def linattn_fwd(q, k, v, g, cu_seqlens: Optional[torch.Tensor] = None, initial_s
         final_state = torch.empty(N, H, dk, dv, dtype=torch.float32, device=dev)
     workspace = _workspace("kda_linattn_fwd", L.kda_linattn_fwd_workspace_size(dt, H, Hk, dk, dv, N, T), workspace,
                            dev)
-    with _on(dev):
-        st = L.kda_linattn_fwd(dt, H, Hk, dk, dv, scale, N, T, _p(cu_seqlens), _p(q), qs, _p(k), ks, _p(v), vs,
-                               _p(g), per_token, _p(initial_state), _p(final_state), _p(y), _p(workspace),
-                               workspace.numel(), _stream(dev))
-    _check("kda_linattn_fwd", st)
+    _call(dev, L.kda_linattn_fwd, "kda_linattn_fwd", dt, H, Hk, dk, dv, scale, N, T, _p(cu_seqlens), _p(q), qs,
+          _p(k), ks, _p(v), vs, _p(g), per_token, _p(initial_state), _p(final_state), _p(y), _p(workspace),
+          workspace.numel())
     return y, final_state
 
 
@@ -173,11 +182,9 @@ def linattn_bwd(q, k, v, g, dy, cu_seqlens: Optional[torch.Tensor] = None, initi
     ds0 = torch.empty(N, H, dk, dv, dtype=torch.float32, device=dev)
     workspace = _workspace("kda_linattn_bwd", L.kda_linattn_bwd_workspace_size(dt, H, Hk, dk, dv, N, T), workspace,
                            dev)
-    with _on(dev):
-        st = L.kda_linattn_bwd(dt, H, Hk, dk, dv, scale, N, T, _p(cu_seqlens), _p(q), qs, _p(k), ks, _p(v), vs,
-                               _p(g), per_token, _p(initial_state), _p(dy), _p(d_final_state), _p(dq), _p(dk_out),
-                               _p(dv_out), _p(dg), _p(ds0), _p(workspace), workspace.numel(), _stream(dev))
-    _check("kda_linattn_bwd", st)
+    _call(dev, L.kda_linattn_bwd, "kda_linattn_bwd", dt, H, Hk, dk, dv, scale, N, T, _p(cu_seqlens), _p(q), qs,
+          _p(k), ks, _p(v), vs, _p(g), per_token, _p(initial_state), _p(dy), _p(d_final_state), _p(dq),
+          _p(dk_out), _p(dv_out), _p(dg), _p(ds0), _p(workspace), workspace.numel())
     return dq, dk_out, dv_out, dg, ds0
 
 
@@ -194,10 +201,8 @@ def linattn_decode_step(q, k, v, g, state, scale: float = 1.0, y: Optional[torch
     dev = _device(q, k, v, g, state, y)
     if y is None:
         y = torch.empty(N, H, dv, dtype=q.dtype, device=dev)
-    with _on(dev):
-        st = lib().kda_linattn_decode_step(dt, N, H, Hk, dk, dv, scale, _p(q), qs, _p(k), ks, _p(v), vs, _p(g),
-                                           per_token, _p(state), _p(y), _stream(dev))
-    _check("kda_linattn_decode_step", st)
+    _call(dev, lib().kda_linattn_decode_step, "kda_linattn_decode_step", dt, N, H, Hk, dk, dv, scale, _p(q), qs,
+          _p(k), ks, _p(v), vs, _p(g), per_token, _p(state), _p(y))
     return y
 
 
@@ -250,11 +255,9 @@ def rope(q, k, positions, inv_freq, layout: str = "half", inverse: bool = False,
     if k is not None and k_out is None:
         k_out = torch.empty(T, Hk, d, dtype=q.dtype, device=dev)
     ks, kos = (_rows("k", k), _rows("k_out", k_out)) if k is not None else (0, 0)
-    with _on(dev):
-        st = lib().kda_rope(dt, T, Hq, Hk, d, 2 * inv_freq.shape[0], _LAYOUT[layout], int(inverse), mscale,
-                            _p(positions), _p(inv_freq), _p(q), _rows("q", q), _p(k), ks, _p(q_out),
-                            _rows("q_out", q_out), _p(k_out), kos, _stream(dev))
-    _check("kda_rope", st)
+    _call(dev, lib().kda_rope, "kda_rope", dt, T, Hq, Hk, d, 2 * inv_freq.shape[0], _LAYOUT[layout], int(inverse),
+          mscale, _p(positions), _p(inv_freq), _p(q), _rows("q", q), _p(k), ks, _p(q_out), _rows("q_out", q_out),
+          _p(k_out), kos)
     return q_out, k_out
 
 
@@ -288,10 +291,8 @@ def norm_fwd(x, weight, bias=None, z=None, eps: float = 1e-5, kind: str = "layer
         y = torch.empty(T, H, D, dtype=x.dtype, device=dev)
     mean = torch.empty(T, H, dtype=torch.float32, device=dev) if stats and kind == "layer" else None
     rstd = torch.empty(T, H, dtype=torch.float32, device=dev) if stats else None
-    with _on(dev):
-        st = lib().kda_norm_fwd(dt, _KIND[kind], T, H, D, eps, _p(x), _p(weight), _p(bias), _p(z), _p(y), _p(mean),
-                                _p(rstd), _stream(dev))
-    _check("kda_norm_fwd", st)
+    _call(dev, lib().kda_norm_fwd, "kda_norm_fwd", dt, _KIND[kind], T, H, D, eps, _p(x), _p(weight), _p(bias),
+          _p(z), _p(y), _p(mean), _p(rstd))
     return y, mean, rstd
 
 
@@ -319,8 +320,6 @@ def norm_bwd(dy, x, weight, mean, rstd, bias=None, z=None, kind: str = "layer",
     dw = torch.empty_like(weight)
     db = None if bias is None else torch.empty_like(bias)
     workspace = _workspace("kda_norm_bwd", L.kda_norm_bwd_workspace_size(dt, T, H, D), workspace, dev)
-    with _on(dev):
-        st = L.kda_norm_bwd(dt, _KIND[kind], T, H, D, _p(x), _p(weight), _p(bias), _p(z), _p(mean), _p(rstd), _p(dy),
-                            _p(dx), _p(dw), _p(db), _p(dz), _p(workspace), workspace.numel(), _stream(dev))
-    _check("kda_norm_bwd", st)
+    _call(dev, L.kda_norm_bwd, "kda_norm_bwd", dt, _KIND[kind], T, H, D, _p(x), _p(weight), _p(bias), _p(z),
+          _p(mean), _p(rstd), _p(dy), _p(dx), _p(dw), _p(db), _p(dz), _p(workspace), workspace.numel())
     return dx, dw, db, dz

@@ -368,7 +368,7 @@ kda_status kda_decode_replay(kda_dtype dt, int N, int Td, int H, int dk, int dv,
  *   y                [T_total, H, dv] in dtype dt; must not overlap inputs.
  *   workspace        at least kda_linattn_fwd_workspace_size bytes for the same
  *                    sizes, 256-byte aligned (0 bytes and NULL do where
- *                    T_total <= 256).  Sequences are cut into blocks of tokens
+ *                    T_total <= 64).  Sequences are cut into blocks of tokens
  *                    that run side by side; it holds the blocks' states.
  */
 size_t kda_linattn_fwd_workspace_size(kda_dtype dt, int H, int Hk, int dk, int dv, int num_seqs, int64_t T_total);

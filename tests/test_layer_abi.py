@@ -61,9 +61,9 @@ def test_linattn_decode_refuses(L):
 
 def test_linattn_workspaces(L):
     size = kda.linattn_fwd_workspace_size
-    assert size(BF16, 4, 4, 128, 128, 1, 256) == 256            # one block a sequence: nothing kept
-    # 8192 tokens of 4 heads: blocks of 256 tokens, a state and a decay for each and head
-    blocks = 8192 // 256 + 1
+    assert size(BF16, 4, 4, 128, 128, 1, 64) == 256             # one block a sequence: nothing kept
+    # 8192 tokens of 4 heads: blocks of 64 tokens, a state and a decay for each and head
+    blocks = 8192 // 64 + 1
     assert size(BF16, 4, 4, 128, 128, 1, 8192) == blocks * 4 * 128 * 128 * 4 + (blocks * 4 * 4 + 255) // 256 * 256
     assert size(BF16, 4, 3, 128, 128, 1, 8192) == 0
     assert size(7, 4, 4, 128, 128, 1, 8192) == 0
