@@ -314,11 +314,11 @@ enum : int { kOut = 0, kState = 1, kGrad = 2 };
 // Tokens of a block in the order they are handled: chunk boundaries lie at the
 // same tokens in both directions, so backwards the first rows may be empty.
 struct Rows {
-    int64_t start;
     int cnt, rows;   // tokens; rows, a multiple of 64
     bool rev;
     __device__ __forceinline__ bool has(int m) const { return rev ? m >= rows - cnt : m < cnt; }
-    __device__ __forceinline__ int64_t token(int m) const { return rev ? start + (rows - 1 - m) : start + m; }
+    // token of row m, counted from the block's first
+    __device__ __forceinline__ int token(int m) const { return rev ? rows - 1 - m : m; }
     // lowest token of the chunk of rows m0 .. m0 + 63, and its tokens
     __device__ __forceinline__ int low(int m0) const { return rev ? rows - C - m0 : m0; }
     __device__ __forceinline__ int tokens(int m0) const { return cnt - low(m0) < C ? cnt - low(m0) : C; }
@@ -326,6 +326,27 @@ struct Rows {
 
 typedef unsigned u32x4_t __attribute__((ext_vector_type(4)));
 typedef unsigned u32x2_t __attribute__((ext_vector_type(2)));
+
+// An operand's rows of one head from the block's first token on: address and
+// bytes from token to token, pinned to scalar registers (left to itself the
+// compiler reads them from the kernel's arguments again in every chunk, and each
+// such read waits for all LDS reads in flight).
+struct Src {
+    int64_t at;
+    unsigned step;
+    template <typename T>
+    __device__ __forceinline__ void set(const T* p, int64_t offset, int64_t stride) {
+        at = uni64(reinterpret_cast<int64_t>(p + offset));
+        step = uni((unsigned)stride * (unsigned)sizeof(T));
+        asm volatile("" : "+s"(at), "+s"(step));
+    }
+    __device__ __forceinline__ int64_t token(int t) const { return uni64(at + (int64_t)(uint64_t)((uint64_t)(unsigned)t * step)); }
+};
+__device__ __forceinline__ float pin(float x) {
+    int y = uni(__builtin_bit_cast(int, x));
+    asm volatile("" : "+s"(y));
+    return __builtin_bit_cast(float, y);
+}
 
 // 16 (or 4) bytes a lane from global memory straight to LDS address lds + 16
 // (4) lane.  As assembly: the compiler makes every later LDS read of the wave
@@ -349,12 +370,11 @@ __device__ __forceinline__ void copy4(unsigned lds, const void* addr) {
 // wave's copy is 1 KiB of LDS in order, so the swizzle is on the source side.
 // Rows without a token take the last token's: the tables give them no weight.
 template <typename T, int D>
-__device__ __forceinline__ void copy_tile(T* t, const LinRows& x, int h, const Rows& rows, int m0, int wave, int lane) {
+__device__ __forceinline__ void copy_tile(T* t, const Src& x, const Rows& rows, int m0, int wave, int lane) {
     constexpr int PIECES = Tile<T, D>::PIECES, RPW = 64 / PIECES, N = C / (4 * RPW);
     const int top = rows.tokens(m0) - 1;
-    const unsigned step = (unsigned)x.stride * (unsigned)sizeof(T);
-    const T* base = (const T*)x.p + (rows.start + rows.low(m0)) * x.stride + (int64_t)h * D;
-    const int64_t ub = uni64(reinterpret_cast<int64_t>(base));
+    const unsigned step = x.step;
+    const int64_t ub = x.token(rows.low(m0));
     const unsigned lds = uni(lds_addr(t) + wave * 1024);
     const int row0 = wave * RPW + lane / PIECES;
     if (top == C - 1) {
@@ -389,11 +409,10 @@ struct Slice {
         const int x = PIECES >= 4 ? ((row >> 2) & 1) * (PIECES / 2) : 0;
         return row * SW + (((col / EP) ^ x) * EP) + col % EP;
     }
-    __device__ __forceinline__ void load(const LinRows& x, int h, int D, int col0, const Rows& rows, int m0, int lane) {
-        const unsigned step = (unsigned)x.stride * (unsigned)sizeof(T);
-        const T* base = (const T*)x.p + (rows.start + rows.low(m0)) * x.stride + (int64_t)h * D + col0;
+    __device__ __forceinline__ void load(const Src& x, int col0, const Rows& rows, int m0, int lane) {
+        const unsigned step = x.step;
         const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
-            reinterpret_cast<void*>(uni64(reinterpret_cast<int64_t>(base))), 0,
+            reinterpret_cast<void*>(x.token(rows.low(m0)) + col0 * (int)sizeof(T)), 0,
             uni((unsigned)(rows.tokens(m0) - 1) * step + SW * (unsigned)sizeof(T)), 0x00027000);
         const int row = lane / PIECES;
         const unsigned at = (unsigned)(rows.rev ? RPI - 1 - row : row) * step + (lane % PIECES) * 16u;
@@ -537,7 +556,21 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
     const bool last = rev ? bl.j == 0 : bl.j == bl.nb - 1;
     if (MODE == kState && last && !a.last_state) return;
     const int cnt = bl.cnt;
-    const Rows rows{bl.start, cnt, (cnt + C - 1) / C * C, rev};
+    const Rows rows{cnt, (cnt + C - 1) / C * C, rev};
+    Src xk, xv, xq, xx, xo, xg;
+    xk.set((const T*)a.k.p, bl.start * a.k.stride + (int64_t)hk * DK, a.k.stride);
+    xv.set((const T*)a.v.p, bl.start * a.v.stride + (int64_t)hv * DV, a.v.stride);
+    if constexpr (MODE != kState) xq.set((const T*)a.q.p, bl.start * a.q.stride + (int64_t)hq * DK, a.q.stride);
+    if constexpr (MODE == kGrad) xx.set((const T*)a.x.p, bl.start * a.x.stride + (int64_t)hx * DV, a.x.stride);
+    const bool wide = MODE == kGrad && a.out_f32;
+    if (wide) xo.set((const float*)a.out, (bl.start * a.H + h) * DV, (int64_t)a.H * DV);
+    else xo.set((const T*)a.out, (bl.start * a.H + h) * DV, (int64_t)a.H * DV);
+    xg.set(a.g, a.g_per_token ? bl.start * a.H + h : h, a.g_per_token ? a.H : 0);
+    // tokens from the block's first to the end of everything, for the decays
+    const int64_t left = a.T_total - 1 - bl.start;
+    const int glast = uni(left < INT32_MAX ? (int)left : INT32_MAX);
+    const float p_scale = pin(a.p_scale), s_scale = pin(a.s_scale), u_scale = pin(a.u_scale);
+    const bool pairs = MODE == kGrad && uni(a.pairs) != 0;
     const int wcol = wave * (DV / 4);
 
     f32x4_t S[KT][NT];
@@ -572,43 +605,65 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
     constexpr int kTab = 3;    // the wave that makes the tables: one with two tiles of P
     // The log-decay of local row m goes to LDS, two chunks ahead.
     auto fetch_g = [&](int m0) {
-        int64_t tok = rows.token(m0 + lane) + (rev ? 1 : 0);   // backwards: the token after it
-        tok = tok < 0 ? 0 : tok >= a.T_total ? a.T_total - 1 : tok;
-        copy4(uni(lds_addr(scr->g[(m0 / C) & 1])), a.g + (a.g_per_token ? tok * a.H + h : h));
+        int tok = rows.token(m0 + lane) + (rev ? 1 : 0);   // backwards: the token after it
+        tok = tok < 0 ? 0 : tok > glast ? glast : tok;
+        copy4(uni(lds_addr(scr->g[(m0 / C) & 1])), reinterpret_cast<const void*>(xg.at + (int64_t)((uint64_t)(unsigned)tok * xg.step)));
     };
     Slice<T, DV / 4> rv;
-    auto fetch_kq = [&](int m0) {
-        const int at = kPair ? ((m0 / C) & 1) * C * DK : 0;
-        copy_tile<T, DK>(skb + at, a.k, hk, rows, m0, wave, lane);
-        if constexpr (MODE == kOut) copy_tile<T, DK>(sqb + at, a.q, hq, rows, m0, wave, lane);
+    auto fetch_k = [&](int m0) {
+        copy_tile<T, DK>(skb + (kPair ? ((m0 / C) & 1) * C * DK : 0), xk, rows, m0, wave, lane);
+    };
+    auto fetch_q = [&](int m0) {
+        if constexpr (MODE == kOut) copy_tile<T, DK>(sqb + ((m0 / C) & 1) * C * DK, xq, rows, m0, wave, lane);
     };
     auto fetch_v = [&](int m0) {
         if constexpr (kPair) {
-            rv.load(a.v, hv, DV, wcol, rows, m0, lane);
+            rv.load(xv, wcol, rows, m0, lane);
         } else {
-            copy_tile<T, DV>(sv, a.v, hv, rows, m0, wave, lane);
-            copy_tile<T, DK>(sqb, a.q, hq, rows, m0, wave, lane);
-            copy_tile<T, DV>(sx, a.x, hx, rows, m0, wave, lane);
+            copy_tile<T, DV>(sv, xv, rows, m0, wave, lane);
+            copy_tile<T, DK>(sqb, xq, rows, m0, wave, lane);
+            copy_tile<T, DV>(sx, xx, rows, m0, wave, lane);
         }
     };
     auto tables = [&](int m0) {
         const int m = m0 + lane;
         const bool valid = rows.has(m);
         // backwards nothing decays before the sequence's last token
-        const float g = valid && !(rev && first && rows.token(m) == bl.start + cnt - 1) ? scr->g[(m0 / C) & 1][lane] : 0.f;
+        const float g = valid && !(rev && first && rows.token(m) == cnt - 1) ? scr->g[(m0 / C) & 1][lane] : 0.f;
         const double G = decay_scan(g);
         write_tables(tbb + ((m0 / C) & 1), G, lane, valid, rev);
         if (MODE == kState) sum_total += lane_d(G, 63);
     };
-    // Stores of a wave and chunk, the youngest of its memory operations where
-    // the copies are waited for.
-    constexpr int NST = MODE == kOut ? 4 * NT : 0;
+    // Outputs in whole rows: through the chunk's own q rows once they are read,
+    // stored by all waves in the next chunk (a wave's own 8-byte pieces, 32 bytes
+    // of a row side by side, made the pass 25 % slower).  Where the q rows are
+    // too short for it, pieces; those stores are then the youngest of a wave's
+    // memory operations where the copies are waited for.
+    constexpr bool kRows = MODE == kOut && DK >= DV;
+    constexpr int NST = MODE == kOut && !kRows ? 4 * NT : 0;
+    auto store_rows = [&](int m0) {
+        typedef Tile<T, DV> O;
+        constexpr int RPW = 64 / O::PIECES, N = C / (4 * RPW);
+        const T* o = sqb + ((m0 / C) & 1) * C * DK;
+        const unsigned step = xo.step;
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
+            reinterpret_cast<void*>(xo.token(rows.low(m0))), 0,
+            uni((unsigned)(rows.tokens(m0) - 1) * step + DV * (unsigned)sizeof(T)), 0x00027000);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int row = (i * 4 + wave) * RPW + lane / O::PIECES, piece = lane % O::PIECES;
+            __builtin_amdgcn_raw_buffer_store_b128(
+                *reinterpret_cast<const u32x4_t*>(o + O::off(row, piece * O::EP)), rsrc,
+                (unsigned)(rev ? C - 1 - row : row) * step + piece * 16u, 0, 0);
+        }
+    };
     if (cnt > 0) {
         if (wave == kTab) {
             fetch_g(0);
             if (C < rows.rows) fetch_g(C);
         }
-        fetch_kq(0);
+        fetch_k(0);
+        fetch_q(0);
         fetch_v(0);
         wait_vmcnt<0>();
         if (wave == kTab) tables(0);
@@ -641,9 +696,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
         }
         if (wave == kTab && m0 + 2 * C < rows.rows) fetch_g(m0 + 2 * C);
         if (kPair && more) {
-            fetch_kq(m0 + C);
+            fetch_k(m0 + C);
             fetch_v(m0 + C);
         }
+        if (kRows && m0 > 0) store_rows(m0 - C);
+        if (MODE == kOut && !kRows && more) fetch_q(m0 + C);
 
         // outputs, transposed tiles: a lane holds 4 consecutive columns of row
         // 16 t + l % 16
@@ -676,10 +733,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
                 }
                 f32x4_t p;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) p[r] = ti != tj || j + r <= i ? x[r] * w[r] * a.p_scale : 0.f;
+                for (int r = 0; r < 4; ++r) p[r] = ti != tj || j + r <= i ? x[r] * w[r] * p_scale : 0.f;
                 put_p(ti, tj, p);
                 if constexpr (MODE == kGrad) {
-                    if (a.pairs) {
+                    if (pairs) {
                         // weight of each pair i > j in the decay's gradient
                         f32x4_t d = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -748,7 +805,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 const int i = 16 * t + lr;
-                const float e = tb->in[i] * (a.s_scale * c);
+                const float e = tb->in[i] * (s_scale * c);
                 float dot = 0.f;
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
@@ -771,13 +828,14 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
             barrier_keep_loads();
             if constexpr (MODE == kGrad) {
                 if (tid < C && rows.has(m0 + tid)) {
-                    a.sums[(int64_t)h * a.T_total + rows.token(m0 + tid)] =
+                    a.sums[(int64_t)h * a.T_total + bl.start + rows.token(m0 + tid)] =
                         (scr->row[0][tid] + scr->row[1][tid]) + (scr->row[2][tid] + scr->row[3][tid]);
                 }
             }
         }
         if (MODE == kState && wave == kTab && more) tables(m0 + C);
         if (!kPair && more) fetch_v(m0 + C);
+        if (kRows && more) fetch_q(m0 + C);
         c = unif(c * tb->total);
         if (c < 1.f / 4096.f) {
 #pragma unroll
@@ -786,7 +844,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
                 for (int n = 0; n < NT; ++n) S[i][n] *= c;
             c = 1.f;
         }
-        const float u = a.u_scale / c;
+        const float u = u_scale / c;
         auto get_p = [&](int t, int s) {
             if constexpr (!kPair) return Tile<T, C>::rows(sp, 16 * t, s, lane);
             Frag8<T> f;
@@ -839,15 +897,20 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
                     for (int p = NU - 1; p >= 0; --p) S[i][n] = mma(fk, fu[n][p], S[i][n]);
             }
         }
-        if constexpr (MODE != kState) {
+        if constexpr (kRows) {
+            T* const o = sqb + ((m0 / C) & 1) * C * DK;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    store4<T>(o + Tile<T, DV>::off(16 * t + lr, wcol + 16 * n + 4 * lg), acc[t][n]);
+        } else if constexpr (MODE != kState) {
             // buffer stores: the same number in every chunk, rows without a
             // token lie behind the bound and are dropped
-            const bool wide = MODE == kGrad && a.out_f32;
             const int es = wide ? 4 : (int)sizeof(T);
-            const unsigned step = (unsigned)(a.H * DV) * es;
-            char* base = static_cast<char*>(a.out) + ((rows.start + rows.low(m0)) * a.H + h) * DV * es;
+            const unsigned step = xo.step;
             const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
-                reinterpret_cast<void*>(uni64(reinterpret_cast<int64_t>(base))), 0,
+                reinterpret_cast<void*>(xo.token(rows.low(m0))), 0,
                 uni((unsigned)(rows.tokens(m0) - 1) * step + DV * es), 0x00027000);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
@@ -867,8 +930,12 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
         if (!kPair && more) {
             if (wave == kTab) tables(m0 + C);
             barrier_keep_loads();   // k is read
-            fetch_kq(m0 + C);
+            fetch_k(m0 + C);
         }
+    }
+    if (kRows && cnt > 0) {
+        barrier_keep_loads();
+        store_rows(rows.rows - C);
     }
 
     float* dst = nullptr;
