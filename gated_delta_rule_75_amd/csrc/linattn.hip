@@ -974,17 +974,24 @@ __global__ __launch_bounds__(256) void linattn_carry_kernel(LinArgs a, LinCarry 
     const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, size = (int64_t)gridDim.x * 1024;
     f32x4_t s = {0.f, 0.f, 0.f, 0.f};
     if (c.initial) s = *reinterpret_cast<const f32x4_t*>(c.initial + ((int64_t)n * a.H + h) * size + e);
+    // a block's own state and decay are read while the one before is passed on
+    auto index = [&](int i) { return (int64_t)(b0 + (c.reverse ? nb - 1 - i : i)) * a.H + h; };
+    auto own = [&](int i) { return i + 1 < nb || (c.after && i < nb); };   // built by the state pass
+    f32x4_t u = {0.f, 0.f, 0.f, 0.f};
+    float d = 0.f;
+    if (own(0)) {
+        u = *reinterpret_cast<const f32x4_t*>(c.states + index(0) * size + e);
+        d = c.decays[index(0)];
+    }
     for (int i = 0; i < nb; ++i) {
-        const int64_t at = (int64_t)(b0 + (c.reverse ? nb - 1 - i : i)) * a.H + h;
-        float* p = c.states + at * size + e;
-        if (i + 1 < nb || c.after) {
-            const f32x4_t u = *reinterpret_cast<const f32x4_t*>(p);
-            const float d = c.decays[at];
-            *reinterpret_cast<f32x4_t*>(p) = s;
-            s = s * d + u;
-        } else {
-            *reinterpret_cast<f32x4_t*>(p) = s;
+        const f32x4_t ui = u;
+        const float di = d;
+        if (own(i + 1)) {
+            u = *reinterpret_cast<const f32x4_t*>(c.states + index(i + 1) * size + e);
+            d = c.decays[index(i + 1)];
         }
+        *reinterpret_cast<f32x4_t*>(c.states + index(i) * size + e) = s;
+        if (own(i)) s = s * di + ui;
     }
     if (c.after) *reinterpret_cast<f32x4_t*>(c.after + ((int64_t)n * a.H + h) * size + e) = s;
 }
@@ -992,10 +999,10 @@ __global__ __launch_bounds__(256) void linattn_carry_kernel(LinArgs a, LinCarry 
 // The decay's gradient of a (block, head): dg_t = sum_{s >= t} (A_s - B_s) + E,
 // A and B the two kGrad runs' sums of the block's tokens, E what crosses the
 // block's end: the product of the state there with its gradient.
-__global__ __launch_bounds__(256) void linattn_dg_kernel(LinArgs a, int size, const float* S, const float* R,
+__global__ __launch_bounds__(1024) void linattn_dg_kernel(LinArgs a, int size, const float* S, const float* R,
                                                          const float* s_end, const float* r_end, const float* A,
                                                          const float* B, float* dg) {
-    __shared__ double part[4];
+    __shared__ double part[16];
     __shared__ double carry;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int b = blockIdx.x / a.H, h = blockIdx.x % a.H;
@@ -1013,7 +1020,8 @@ __global__ __launch_bounds__(256) void linattn_dg_kernel(LinArgs a, int size, co
     }
     if (x) {
         float f = 0.f;
-        for (int i = tid * 4; i < size; i += 1024) {
+#pragma unroll 4
+        for (int i = tid * 4; i < size; i += 4096) {
             const f32x4_t u = *reinterpret_cast<const f32x4_t*>(x + i), v = *reinterpret_cast<const f32x4_t*>(y + i);
             f += (u[0] * v[0] + u[1] * v[1]) + (u[2] * v[2] + u[3] * v[3]);
         }
@@ -1024,7 +1032,8 @@ __global__ __launch_bounds__(256) void linattn_dg_kernel(LinArgs a, int size, co
     if (lane == 0) part[wave] = e;
     __syncthreads();
     if (tid == 0) {
-        double s = (part[0] + part[1]) + (part[2] + part[3]);
+        double s = 0.0;
+        for (int w = 0; w < 16; ++w) s += part[w];
         if (!last) {
             const float g = a.g[a.g_per_token ? (bl.start + bl.cnt) * a.H + h : h];
             s *= exp((double)(g < kFloor ? kFloor : g));
@@ -1032,8 +1041,8 @@ __global__ __launch_bounds__(256) void linattn_dg_kernel(LinArgs a, int size, co
         carry = s;
     }
     __syncthreads();
-    // from the block's end, 256 tokens at a time
-    for (int m0 = 0; m0 < bl.cnt; m0 += 256) {
+    // from the block's end, 1024 tokens at a time (a block has no more)
+    for (int m0 = 0; m0 < bl.cnt; m0 += 1024) {
         const int m = m0 + tid;
         const int64_t tok = bl.start + bl.cnt - 1 - m;
         double d = 0.0;
@@ -1049,7 +1058,7 @@ __global__ __launch_bounds__(256) void linattn_dg_kernel(LinArgs a, int size, co
         for (int w = 0; w < wave; ++w) before += part[w];
         const double v = before + d;
         __syncthreads();
-        if (tid == 255) carry = v;
+        if (tid == 1023) carry = v;
         if (m < bl.cnt) dg[tok * a.H + h] = (float)v;
         __syncthreads();
     }
@@ -1225,7 +1234,7 @@ hipError_t launch_linattn_bwd(const LinCall& c) {
     // dg
     if (c.dg) {
         float* per_token = a.g_per_token ? c.dg : c.dg_tokens;
-        hipLaunchKernelGGL(linattn_dg_kernel, dim3((unsigned)(a.nblocks * a.H)), dim3(256), 0, (hipStream_t)a.stream, a,
+        hipLaunchKernelGGL(linattn_dg_kernel, dim3((unsigned)(a.nblocks * a.H)), dim3(1024), 0, (hipStream_t)a.stream, a,
                            c.dk * c.dv, c.states, c.rstates, c.s_end, c.d_final_state, c.sums_a, c.sums_b, per_token);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         if (!a.g_per_token) {

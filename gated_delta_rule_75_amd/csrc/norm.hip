@@ -23,15 +23,16 @@ namespace kda {
 namespace {
 
 // A thread's NV runs of VEC columns of a row of D: columns (j LANES + lane) VEC.
-template <int VEC, int LANES, int NV>
+// TAIL: the last run may be cut.
+template <int VEC, int LANES, int NV, bool TAIL>
 struct Cols {
     int lane, D;
     __device__ __forceinline__ int at(int j) const { return (j * LANES + lane) * VEC; }
     __device__ __forceinline__ bool in(int j) const { return at(j) < D; }
-    __device__ __forceinline__ int left(int j) const { return D - at(j); }   // elements of the run, >= VEC: all
+    __device__ __forceinline__ int left(int j) const { return TAIL ? D - at(j) : VEC; }   // elements of the run, >= VEC: all
 };
 
-template <typename T, int VEC, int LANES, int NV>
+template <typename T, int VEC, int LANES, int NV, bool TAIL>
 __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_fwd_kernel(
     int64_t rows, int H, int D, float eps, int rms, const T* __restrict__ x, const float* __restrict__ w,
     const float* __restrict__ b, const T* __restrict__ z, T* __restrict__ y, float* __restrict__ mean,
@@ -40,7 +41,7 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_fwd_kernel(
     __shared__ float part[2][LANES > 64 ? LANES / 64 : 1];
     const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / LANES;
     if (LANES <= 64 && row >= rows) return;              // no barrier below for these
-    const Cols<VEC, LANES, NV> c{(int)(threadIdx.x % LANES), D};
+    const Cols<VEC, LANES, NV, TAIL> c{(int)(threadIdx.x % LANES), D};
     const int64_t base = row * D, wb = (int64_t)(row % H) * D;
     float v[NV][VEC];
     float s = 0.f;
@@ -93,7 +94,7 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_fwd_kernel(
     }
 }
 
-template <typename T, int VEC, int LANES, int NV>
+template <typename T, int VEC, int LANES, int NV, bool TAIL>
 __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_bwd_kernel(
     int64_t rows, int64_t S, int H, int D, const T* __restrict__ x, const float* __restrict__ w,
     const float* __restrict__ b, const T* __restrict__ z, const float* __restrict__ mean,
@@ -103,7 +104,7 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_bwd_kernel(
     __shared__ float part[2][LANES > 64 ? LANES / 32 : 1];
     const int64_t slot = (int64_t)blockIdx.x * RPB + threadIdx.x / LANES;
     if (slot >= S) return;   // whole lane groups (a whole workgroup where LANES > 64)
-    const Cols<VEC, LANES, NV> c{(int)(threadIdx.x % LANES), D};
+    const Cols<VEC, LANES, NV, TAIL> c{(int)(threadIdx.x % LANES), D};
     const int64_t wb = (int64_t)(slot % H) * D;
     float wv[NV][VEC], bv[NV][VEC], aw[NV][VEC], ab[NV][VEC];
 #pragma unroll
@@ -144,7 +145,7 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_bwd_kernel(
         for (int j = 0; j < NV; ++j) {
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                const bool in = c.at(j) + i < D;
+                const bool in = TAIL ? c.at(j) + i < D : c.in(j);
                 h[j][i] = in ? (to_f32((T)xn[j][i]) - m) * r : 0.f;
                 d[j][i] = in ? to_f32((T)dn[j][i]) : 0.f;
             }
@@ -216,16 +217,16 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(int64_t P, int64_t HD
     if (cx == 0 && c2 < HD) dst[c2] = a;
 }
 
-template <typename T, int VEC, int LANES, int NV>
+template <typename T, int VEC, int LANES, int NV, bool TAIL>
 hipError_t launch_t(const NormArgs& a) {
     constexpr int RPB = LANES < 256 ? 256 / LANES : 1, NT = LANES < 256 ? 256 : LANES;
     const int64_t rows = a.T * a.H;
     if (!a.dy) {
-        hipLaunchKernelGGL((norm_fwd_kernel<T, VEC, LANES, NV>), dim3((unsigned)((rows + RPB - 1) / RPB)), dim3(NT), 0,
+        hipLaunchKernelGGL((norm_fwd_kernel<T, VEC, LANES, NV, TAIL>), dim3((unsigned)((rows + RPB - 1) / RPB)), dim3(NT), 0,
                            (hipStream_t)a.stream, rows, a.H, a.D, a.eps, a.rms, (const T*)a.x, a.weight, a.bias,
                            (const T*)a.z, (T*)a.y, a.mean, a.rstd);
     } else {
-        hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, LANES, NV>), dim3((unsigned)((a.slots + RPB - 1) / RPB)), dim3(NT),
+        hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, LANES, NV, TAIL>), dim3((unsigned)((a.slots + RPB - 1) / RPB)), dim3(NT),
                            0, (hipStream_t)a.stream, rows, a.slots, a.H, a.D, (const T*)a.x, a.weight, a.bias,
                            (const T*)a.z, a.mean, a.rstd, (const T*)a.dy, (T*)a.dx, (T*)a.dz, a.dwp, a.dbp);
     }
@@ -233,25 +234,30 @@ hipError_t launch_t(const NormArgs& a) {
 }
 
 // The narrowest lane group that holds a row with at most 16 elements a thread.
-template <typename T>
-hipError_t launch_d(const NormArgs& a) {
+template <typename T, bool TAIL>
+hipError_t launch_r(const NormArgs& a) {
     constexpr int VEC = kVec16<T>;
     const int n = (a.D + VEC - 1) / VEC;   // runs of a row
-    if (n <= 16) return launch_t<T, VEC, 16, 1>(a);
-    if (n <= 64) return launch_t<T, VEC, 64, 1>(a);
-    if (n <= 128) return launch_t<T, VEC, 64, 2>(a);
+    if (n <= 16) return launch_t<T, VEC, 16, 1, TAIL>(a);
+    if (n <= 64) return launch_t<T, VEC, 64, 1, TAIL>(a);
+    if (n <= 128) return launch_t<T, VEC, 64, 2, TAIL>(a);
     if constexpr (VEC == 4) {
-        if (n <= 256) return launch_t<T, VEC, 64, 4>(a);
-        if (n <= 512) return launch_t<T, VEC, 256, 2>(a);
-        if (n <= 1024) return launch_t<T, VEC, 256, 4>(a);
-        if (n <= 2048) return launch_t<T, VEC, 1024, 2>(a);
-        return launch_t<T, VEC, 1024, 4>(a);
+        if (n <= 256) return launch_t<T, VEC, 64, 4, TAIL>(a);
+        if (n <= 512) return launch_t<T, VEC, 256, 2, TAIL>(a);
+        if (n <= 1024) return launch_t<T, VEC, 256, 4, TAIL>(a);
+        if (n <= 2048) return launch_t<T, VEC, 1024, 2, TAIL>(a);
+        return launch_t<T, VEC, 1024, 4, TAIL>(a);
     } else {
-        if (n <= 256) return launch_t<T, VEC, 256, 1>(a);
-        if (n <= 512) return launch_t<T, VEC, 256, 2>(a);
-        if (n <= 1024) return launch_t<T, VEC, 1024, 1>(a);
-        return launch_t<T, VEC, 1024, 2>(a);
+        if (n <= 256) return launch_t<T, VEC, 256, 1, TAIL>(a);
+        if (n <= 512) return launch_t<T, VEC, 256, 2, TAIL>(a);
+        if (n <= 1024) return launch_t<T, VEC, 1024, 1, TAIL>(a);
+        return launch_t<T, VEC, 1024, 2, TAIL>(a);
     }
+}
+
+template <typename T>
+hipError_t launch_d(const NormArgs& a) {
+    return a.D % kVec16<T> ? launch_r<T, true>(a) : launch_r<T, false>(a);
 }
 
 }  // namespace
