@@ -33,57 +33,77 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, int tpb) {
         sn[i] = a.mscale * (a.inverse ? -s : s);
     }
     __syncthreads();
-    // a head's units: `pairs` runs of VEC pairs, then runs of VEC channels that
-    // are copied (none where the output is the input)
+    // a head's units, two runs of VEC channels each: the two runs of VEC pairs,
+    // or two neighbouring runs that are copied (none where the output is the
+    // input); a thread has two units in flight
     const int pairs = HALF ? n / VEC : a.rot / (2 * VEC);
     const int rest = (a.d - a.rot) / VEC;
     const int heads = a.Hq + a.Hk;
-    const int per = pairs + rest;
+    const int per = pairs + (rest + 1) / 2;
     const int total = nt * heads * per;
-    for (int i = threadIdx.x; i < total; i += 256) {
+    struct Unit {
+        const T* src;
+        T* dst;
+        int c0, c1, cs;       // channels of the runs (c1 < 0: one run); cosines, or -1: a copy
+        float x[VEC], w[VEC];
+    };
+    auto fetch = [&](Unit& m, int i) {
         const int u = i % per, th = i / per, hd = th % heads, t = th / heads;
         const bool isq = hd < a.Hq;
         const int hh = isq ? hd : hd - a.Hq;
-        const T* src = (const T*)(isq ? a.q : a.k) + (t0 + t) * (isq ? a.q_stride : a.k_stride) + (int64_t)hh * a.d;
-        T* dst = (T*)(isq ? a.q_out : a.k_out) + (t0 + t) * (isq ? a.qo_stride : a.ko_stride) + (int64_t)hh * a.d;
-        if (u >= pairs) {
-            if (src == dst) continue;
-            const int c = a.rot + (u - pairs) * VEC;
-            float x[VEC];
-            load_vec<T, VEC>(src + c, x);
-            store_vec<T, VEC>(dst + c, x);
-            continue;
-        }
-        const float* co = cs + t * n + u * VEC;
-        const float* si = sn + t * n + u * VEC;
-        float x[VEC], w[VEC], p[VEC], r[VEC];
-        if constexpr (HALF) {
-            load_vec<T, VEC>(src + u * VEC, x);
-            load_vec<T, VEC>(src + n + u * VEC, w);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                p[j] = x[j] * co[j] - w[j] * si[j];
-                r[j] = w[j] * co[j] + x[j] * si[j];
-            }
-            store_vec<T, VEC>(dst + u * VEC, p);
-            store_vec<T, VEC>(dst + n + u * VEC, r);
+        m.src = (const T*)(isq ? a.q : a.k) + (t0 + t) * (isq ? a.q_stride : a.k_stride) + (int64_t)hh * a.d;
+        m.dst = (T*)(isq ? a.q_out : a.k_out) + (t0 + t) * (isq ? a.qo_stride : a.ko_stride) + (int64_t)hh * a.d;
+        if (u < pairs) {
+            m.cs = t * n + u * VEC;
+            m.c0 = HALF ? u * VEC : 2 * u * VEC;
+            m.c1 = HALF ? n + u * VEC : 2 * u * VEC + VEC;
         } else {
-            // channels 2 VEC u .. 2 VEC u + 2 VEC - 1 as two runs
-            load_vec<T, VEC>(src + 2 * u * VEC, x);
-            load_vec<T, VEC>(src + 2 * u * VEC + VEC, w);
+            m.cs = -1;
+            m.c0 = a.rot + 2 * (u - pairs) * VEC;
+            m.c1 = 2 * (u - pairs) + 1 < rest ? m.c0 + VEC : -1;
+            if (m.src == m.dst) return;
+        }
+        load_vec<T, VEC>(m.src + m.c0, m.x);
+        if (m.c1 >= 0) load_vec<T, VEC>(m.src + m.c1, m.w);
+    };
+    auto put = [&](Unit& m) {
+        if (m.cs < 0) {
+            if (m.src == m.dst) return;
+            store_vec<T, VEC>(m.dst + m.c0, m.x);
+            if (m.c1 >= 0) store_vec<T, VEC>(m.dst + m.c1, m.w);
+            return;
+        }
+        const float* co = cs + m.cs;
+        const float* si = sn + m.cs;
+        float p[VEC], r[VEC];
+        if constexpr (HALF) {
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
-                const float e = 2 * j < VEC ? x[(2 * j) % VEC] : w[(2 * j) % VEC];
-                const float f = 2 * j + 1 < VEC ? x[(2 * j + 1) % VEC] : w[(2 * j + 1) % VEC];
+                p[j] = m.x[j] * co[j] - m.w[j] * si[j];
+                r[j] = m.w[j] * co[j] + m.x[j] * si[j];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const float e = 2 * j < VEC ? m.x[(2 * j) % VEC] : m.w[(2 * j) % VEC];
+                const float f = 2 * j + 1 < VEC ? m.x[(2 * j + 1) % VEC] : m.w[(2 * j + 1) % VEC];
                 const float pe = e * co[j] - f * si[j], pf = f * co[j] + e * si[j];
                 if (2 * j < VEC) p[(2 * j) % VEC] = pe;
                 else r[(2 * j) % VEC] = pe;
                 if (2 * j + 1 < VEC) p[(2 * j + 1) % VEC] = pf;
                 else r[(2 * j + 1) % VEC] = pf;
             }
-            store_vec<T, VEC>(dst + 2 * u * VEC, p);
-            store_vec<T, VEC>(dst + 2 * u * VEC + VEC, r);
         }
+        store_vec<T, VEC>(m.dst + m.c0, p);
+        store_vec<T, VEC>(m.dst + m.c1, r);
+    };
+    for (int i = threadIdx.x; i < total; i += 512) {
+        Unit m, o;
+        fetch(m, i);
+        const bool two = i + 256 < total;
+        if (two) fetch(o, i + 256);
+        put(m);
+        if (two) put(o);
     }
 }
 
@@ -97,7 +117,7 @@ hipError_t launch_t(const RopeArgs& a) {
                      a.qo_stride % V == 0 && a.ko_stride % V == 0 && al16(a.q) && al16(a.k) && al16(a.q_out) &&
                      al16(a.k_out);
     const int w = vec ? V : 1;
-    const int per = (n + (a.d - a.rot)) / w * (a.Hq + a.Hk);
+    const int per = (n + (a.d - a.rot) / 2) / w * (a.Hq + a.Hk);
     // tokens of a workgroup: about 8 units a thread, while the launch still has
     // workgroups for every CU and the table fits 16 KiB
     int tpb = 1;
