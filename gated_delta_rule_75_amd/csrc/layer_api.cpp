@@ -15,7 +15,16 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 bool dtype_ok(kda_dtype dt) { return dt == KDA_BF16 || dt == KDA_F32; }
 size_t elt(kda_dtype dt) { return dt == KDA_BF16 ? 2 : 4; }
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-kda_status from_hip(hipError_t e) { return e == hipSuccess ? KDA_OK : KDA_ERR_HIP; }
+
+// Nothing is thrown across the ABI (the launchers keep a locked set).
+template <typename F>
+kda_status launched(F f) {
+    try {
+        return f() == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+    } catch (...) {
+        return KDA_ERR_HIP;
+    }
+}
 
 bool head_ok(int d) { return d == 64 || d == 128; }
 
@@ -156,7 +165,7 @@ kda_status kda_linattn_fwd(kda_dtype dt, int H, int Hk, int dk, int dv, float sc
         c.states = part<float>(workspace, l.states);
         c.decays = part<float>(workspace, l.decays);
     }
-    return from_hip(kda::launch_linattn_fwd(c));
+    return launched([&] { return kda::launch_linattn_fwd(c); });
 }
 
 size_t kda_linattn_bwd_workspace_size(kda_dtype dt, int H, int Hk, int dk, int dv, int num_seqs, int64_t T_total) {
@@ -217,7 +226,7 @@ kda_status kda_linattn_bwd(kda_dtype dt, int H, int Hk, int dk, int dv, float sc
     c.sums_b = part<float>(workspace, l.sums_b);
     c.dg_tokens = part<float>(workspace, l.dg);
     c.share_buf = part<void>(workspace, l.share);
-    return from_hip(kda::launch_linattn_bwd(c));
+    return launched([&] { return kda::launch_linattn_bwd(c); });
 }
 
 kda_status kda_linattn_decode_step(kda_dtype dt, int N, int H, int Hk, int dk, int dv, float scale, const void* q,
@@ -246,7 +255,7 @@ kda_status kda_linattn_decode_step(kda_dtype dt, int N, int H, int Hk, int dk, i
     a.state = state;
     a.y = y;
     a.stream = stream;
-    return from_hip(kda::launch_linattn_decode(a));
+    return launched([&] { return kda::launch_linattn_decode(a); });
 }
 
 kda_status kda_rope_frequencies(int rot, double base, kda_rope_scaling scaling, double factor, double trained_len,
@@ -331,7 +340,7 @@ kda_status kda_rope(kda_dtype dt, int64_t T, int Hq, int Hk, int d, int rot, kda
     a.qo_stride = q_out_stride;
     a.ko_stride = k_out_stride;
     a.stream = stream;
-    return from_hip(kda::launch_rope(a));
+    return launched([&] { return kda::launch_rope(a); });
 }
 
 }  // extern "C"
@@ -385,7 +394,7 @@ kda_status kda_norm_fwd(kda_dtype dt, kda_norm_kind kind, int64_t T, int H, int 
     a.mean = mean;
     a.rstd = rstd;
     a.stream = stream;
-    return from_hip(kda::launch_norm(a));
+    return launched([&] { return kda::launch_norm(a); });
 }
 
 size_t kda_norm_bwd_workspace_size(kda_dtype dt, int64_t T, int H, int D) {
@@ -431,7 +440,7 @@ kda_status kda_norm_bwd(kda_dtype dt, kda_norm_kind kind, int64_t T, int H, int 
     a.dbp = dbias ? part<float>(workspace, half) : nullptr;
     a.slots = norm_slots(dt, T, H, D);
     a.stream = stream;
-    return from_hip(kda::launch_norm(a));
+    return launched([&] { return kda::launch_norm(a); });
 }
 
 }  // extern "C"

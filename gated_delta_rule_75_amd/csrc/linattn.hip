@@ -970,7 +970,8 @@ __global__ __launch_bounds__(256) void linattn_carry_kernel(LinArgs a, LinCarry 
     const LinCarry c = blockIdx.z ? c1 : c0;
     const int n = blockIdx.y / a.H, h = blockIdx.y % a.H;
     const int b0 = first_block(a, n);
-    const int nb = blocks_of(seq_at(a, n + 1) - seq_at(a, n), a.L);
+    int nb = blocks_of(seq_at(a, n + 1) - seq_at(a, n), a.L);
+    if (nb > a.nblocks - b0) nb = a.nblocks - b0;   // offsets out of order: stay inside the arrays
     const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, size = (int64_t)gridDim.x * 1024;
     f32x4_t s = {0.f, 0.f, 0.f, 0.f};
     if (c.initial) s = *reinterpret_cast<const f32x4_t*>(c.initial + ((int64_t)n * a.H + h) * size + e);
@@ -1008,7 +1009,7 @@ __global__ __launch_bounds__(1024) void linattn_dg_kernel(LinArgs a, int size, c
     const int b = blockIdx.x / a.H, h = blockIdx.x % a.H;
     const Block bl = find_block(a, b);
     if (bl.n < 0) return;
-    const bool last = bl.j == bl.nb - 1;
+    const bool last = bl.j == bl.nb - 1 || b + 1 >= a.nblocks;
     double e = 0.0;
     const float *x = nullptr, *y = nullptr;
     if (!last) {
@@ -1019,13 +1020,14 @@ __global__ __launch_bounds__(1024) void linattn_dg_kernel(LinArgs a, int size, c
         y = r_end + ((int64_t)bl.n * a.H + h) * size;
     }
     if (x) {
-        float f = 0.f;
+        // in fp64: under strong decays the tokens next to the block's end take
+        // nearly all of it away again
 #pragma unroll 4
         for (int i = tid * 4; i < size; i += 4096) {
             const f32x4_t u = *reinterpret_cast<const f32x4_t*>(x + i), v = *reinterpret_cast<const f32x4_t*>(y + i);
-            f += (u[0] * v[0] + u[1] * v[1]) + (u[2] * v[2] + u[3] * v[3]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) e += (double)u[r] * (double)v[r];
         }
-        e = f;
 #pragma unroll
         for (int d = 32; d > 0; d >>= 1) e += shfl_d(e, lane ^ d);
     }
@@ -1066,11 +1068,12 @@ __global__ __launch_bounds__(1024) void linattn_dg_kernel(LinArgs a, int size, c
 
 // dg of a decay that all tokens of a head share: the sum over tokens, one
 // workgroup a head, in a fixed order.
-__global__ __launch_bounds__(256) void linattn_dg_sum_kernel(int64_t T, int H, const float* dg, float* out) {
+__global__ __launch_bounds__(256) void linattn_dg_sum_kernel(LinArgs a, const float* dg, float* out) {
     __shared__ double part[256];
     const int h = blockIdx.x, tid = threadIdx.x;
+    const int64_t end = seq_at(a, a.num_seqs);
     double s = 0.0;
-    for (int64_t t = tid; t < T; t += 256) s += (double)dg[t * H + h];
+    for (int64_t t = seq_at(a, 0) + tid; t < end; t += 256) s += (double)dg[t * a.H + h];
     part[tid] = s;
     __syncthreads();
     for (int d = 128; d > 0; d >>= 1) {
@@ -1082,12 +1085,13 @@ __global__ __launch_bounds__(256) void linattn_dg_sum_kernel(int64_t T, int H, c
 
 // Sum over the value heads that share a key head: fp32 [T, H, D] to [T, H / r, D].
 template <typename T>
-__global__ __launch_bounds__(256) void linattn_share_kernel(int64_t n, int r, int D, const float* src, T* dst0,
-                                                            T* dst1) {
+__global__ __launch_bounds__(256) void linattn_share_kernel(LinArgs a, int64_t n, int r, int D, const float* src,
+                                                            T* dst0, T* dst1) {
     T* dst = blockIdx.y ? dst1 : dst0;
     src += blockIdx.y * n * r;
     const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-    if (i >= n) return;
+    const int64_t tok = i / ((int64_t)(a.H / r) * D);
+    if (i >= n || tok < seq_at(a, 0) || tok >= seq_at(a, a.num_seqs)) return;   // rows of no sequence stay
     const int64_t row = i / D;
     const float* p = src + row * r * D + i % D;
     f32x4_t s = *reinterpret_cast<const f32x4_t*>(p);
@@ -1212,10 +1216,10 @@ hipError_t launch_linattn_bwd(const LinCall& c) {
     if (shared && n > 0) {
         const dim3 grid((unsigned)((n / 4 + 255) / 256), 2);
         if (c.dtype == 0)
-            hipLaunchKernelGGL(linattn_share_kernel<__bf16>, grid, dim3(256), 0, (hipStream_t)a.stream, n, c.k.share,
+            hipLaunchKernelGGL(linattn_share_kernel<__bf16>, grid, dim3(256), 0, (hipStream_t)a.stream, a, n, c.k.share,
                                c.dk, (const float*)c.share_buf, (__bf16*)c.dq, (__bf16*)c.dk_out);
         else
-            hipLaunchKernelGGL(linattn_share_kernel<float>, grid, dim3(256), 0, (hipStream_t)a.stream, n, c.k.share,
+            hipLaunchKernelGGL(linattn_share_kernel<float>, grid, dim3(256), 0, (hipStream_t)a.stream, a, n, c.k.share,
                                c.dk, (const float*)c.share_buf, (float*)c.dq, (float*)c.dk_out);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
@@ -1239,7 +1243,7 @@ hipError_t launch_linattn_bwd(const LinCall& c) {
         if ((e = hipGetLastError()) != hipSuccess) return e;
         if (!a.g_per_token) {
             hipLaunchKernelGGL(linattn_dg_sum_kernel, dim3((unsigned)a.H), dim3(256), 0, (hipStream_t)a.stream,
-                               a.T_total, a.H, per_token, c.dg);
+                               a, per_token, c.dg);
             if ((e = hipGetLastError()) != hipSuccess) return e;
         }
     }

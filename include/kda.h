@@ -355,7 +355,9 @@ kda_status kda_decode_replay(kda_dtype dt, int N, int Td, int H, int dk, int dv,
  *                    h with equal h / (H / Hk) share a key head's q and k.
  *   dk, dv           64 or 128 each.
  *   num_seqs, T_total, cu_seqlens   as kda_chunk_fwd (num_seqs * H <= 65535).
- *                    Sequences may be empty: their state passes through.
+ *                    Sequences may be empty: their state passes through.  The
+ *                    offsets may begin after 0 or end before T_total; rows of no
+ *                    sequence are neither read nor written.
  *   q, k             [T_total, Hk, dk] in dtype dt, v [T_total, H, dv].
  *                    16-byte aligned, strides multiples of 16 bytes (at most
  *                    2^23 elements), finite.
@@ -369,7 +371,8 @@ kda_status kda_decode_replay(kda_dtype dt, int N, int Td, int H, int dk, int dv,
  *   workspace        at least kda_linattn_fwd_workspace_size bytes for the same
  *                    sizes, 256-byte aligned (0 bytes and NULL do where
  *                    T_total <= 64).  Sequences are cut into blocks of tokens
- *                    that run side by side; it holds the blocks' states.
+ *                    that run side by side; it holds the blocks' states.  Calls
+ *                    that may overlap in time need a workspace each.
  */
 size_t kda_linattn_fwd_workspace_size(kda_dtype dt, int H, int Hk, int dk, int dv, int num_seqs, int64_t T_total);
 kda_status kda_linattn_fwd(kda_dtype dt, int H, int Hk, int dk, int dv, float scale, int num_seqs, int64_t T_total,

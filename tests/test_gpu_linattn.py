@@ -217,6 +217,96 @@ def test_rows_outside_the_sequences_are_left(kda):
     assert bool((y[130] == 5).all()) and bool((s[2] == 5).all())
 
 
+@pytest.mark.parametrize("decay", ["token", "head"])
+def test_offsets_inside_the_rows(kda, decay):
+    """Offsets that begin after row 0 and end before the last row: the rows
+    around hold NaN, which nothing takes in, and gradients' rows stay."""
+    x = make("bf16", [5, 200, 90, 7], 4, 2, 64, 64, seed=21, decay=decay)
+    inner = dict(x, cu=[5, 205, 295], s0=x["s0"][1:3], ds=x["ds"][1:3])
+    part = {n: x[n][5:295] for n in ("q", "k", "v", "dy")}
+    part.update(inner, cu=[0, 200, 290], **part)
+    if decay == "token":
+        part["g"] = x["g"][5:295]
+        inner["g"] = x["g"].clone()
+        inner["g"][:5] = inner["g"][295:] = float("nan")
+    for n in ("q", "k", "v", "dy"):
+        inner[n] = x[n].clone()
+        inner[n][:5] = inner[n][295:] = float("nan")
+    y, s = fwd(kda, inner)
+    yr, sr = fwd(kda, part)
+    assert torch.equal(y[5:295], yr) and torch.equal(s, sr)
+    got, want = bwd(kda, inner), bwd(kda, part)
+    for n, a, b in zip(("dq", "dk", "dv", "dg", "ds0"), got, want):
+        a = a[5:295] if a.shape[0] == 302 else a
+        # the same tokens in the same blocks: the same bits, but for the order
+        # in which dg of a head is summed
+        if n == "dg" and decay == "head":
+            ref.check("dg of a head", a, b.double().cpu(), 1e-6)
+        else:
+            assert torch.equal(a, b), n
+
+
+def test_two_calls_at_once(kda):
+    """Two streams with a workspace each."""
+    xs = [make("bf16", [900, 300], 4, 4, 128, 128, seed=s) for s in (61, 62)]
+    want = [fwd(kda, x) + bwd(kda, x) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    for _ in range(3):
+        got = []
+        for x, st in zip(xs, streams):
+            with torch.cuda.stream(st):
+                got.append(fwd(kda, x) + bwd(kda, x))
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            for a, b in zip(g, w):
+                assert torch.equal(a, b)
+
+
+def test_decays_next_to_each_other(kda):
+    """Hard to tell apart in fp32 sums: a near-clearing decay and, behind it,
+    tiny ones whose products still have to be exact."""
+    x = make("f32", [256], 2, 2, 64, 64, seed=23)
+    x["g"][:] = -1e-4
+    x["g"][10::64] = -150.0
+    x["g"][33::64] = -200.0
+    y, s = fwd(kda, x)
+    yr, sr, _ = ref.linattn(x["q"], x["k"], x["v"], x["g"], x["cu"], x["s0"], x["scale"])
+    ref.check("y", y, yr, ref.TOL["f32"])
+    ref.check("state", s, sr, ref.TOL_STATE)
+    want = ref.linattn_grad(x["q"], x["k"], x["v"], x["g"], x["cu"], x["dy"], x["s0"], x["ds"], x["scale"])
+    for n, a, b in zip(("dq", "dk", "dv", "dg", "ds0"), bwd(kda, x), want):
+        ref.check(n, a, b, ref.TOL_DG if n == "dg" else ref.TOL["f32"])
+
+
+def test_many_sequences(kda):
+    """More sequences than a wave has lanes, empty ones among them."""
+    lens = [(7 * i) % 5 for i in range(200)]
+    x = make("bf16", lens, 2, 2, 64, 64, seed=24)
+    y, s = fwd(kda, x)
+    yr, sr, _ = ref.linattn(x["q"], x["k"], x["v"], x["g"], x["cu"], x["s0"], x["scale"])
+    ref.check("y", y, yr, ref.TOL["bf16"])
+    ref.check("state", s, sr, ref.TOL_STATE)
+    want = ref.linattn_grad(x["q"], x["k"], x["v"], x["g"], x["cu"], x["dy"], x["s0"], x["ds"], x["scale"])
+    for n, a, b in zip(("dq", "dk", "dv", "dg", "ds0"), bwd(kda, x), want):
+        ref.check(n, a, b, ref.TOL_DG if n == "dg" else ref.TOL_STATE if n == "ds0" else ref.TOL["bf16"])
+
+
+def test_weak_and_strong_decay_of_whole_sequences(kda):
+    """g = 0 keeps everything, g = -5 forgets within a tile: the state's scale
+    is renewed never and in every chunk."""
+    for g in (0.0, -5.0):
+        x = make("bf16", [400], 2, 2, 128, 128, seed=25)
+        x["g"][:] = g
+        y, s = fwd(kda, x)
+        yr, sr, _ = ref.linattn(x["q"], x["k"], x["v"], x["g"], x["cu"], x["s0"], x["scale"])
+        ref.check(f"g {g} y", y, yr, ref.TOL["bf16"])
+        ref.check(f"g {g} state", s, sr, ref.TOL_STATE)
+        want = ref.linattn_grad(x["q"], x["k"], x["v"], x["g"], x["cu"], x["dy"], x["s0"], x["ds"], x["scale"])
+        for n, a, b in zip(("dq", "dk", "dv", "dg", "ds0"), bwd(kda, x), want):
+            ref.check(f"g {g} {n}", a, b, ref.TOL_DG if n == "dg" else ref.TOL_STATE if n == "ds0" else ref.TOL["bf16"])
+
+
 def test_other_stream(kda):
     x = make("bf16", [700], 2, 2, 128, 128, seed=6)
     want = fwd(kda, x) + bwd(kda, x)
