@@ -246,7 +246,7 @@ struct __attribute__((aligned(16))) Tables {
     float frac[C];      // log2 sum G = whole + frac
     int whole[C];
     float tile[C];      // exp2(G_i - G at the start of i's 16-token tile)
-    float upto[3][C];   // exp2(G at the start of tile t + 1 - G_j), j before it
+    float upto[96];     // exp2(G at the start of tile t - G_j), j before it: at 8 t (t - 1) + j
     float in[C];        // exp2(G_i)
     float out[C];       // exp2(G_63 - G_j)
     float total;
@@ -301,9 +301,9 @@ __device__ __forceinline__ void write_tables(Tables* t, double G, int lane, bool
     const double r1 = lane_d(G, 15), r2 = lane_d(G, 31), r3 = lane_d(G, 47), end = lane_d(G, 63);
     const double mine = lane < 16 ? 0.0 : lane < 32 ? r1 : lane < 48 ? r2 : r3;
     t->tile[lane] = valid ? exp2_fast((float)(G - mine)) : 0.f;
-    t->upto[0][lane] = valid ? exp2_fast((float)(r1 - G)) : 0.f;   // read for j < 16 (t + 1) only
-    t->upto[1][lane] = valid ? exp2_fast((float)(r2 - G)) : 0.f;
-    t->upto[2][lane] = valid ? exp2_fast((float)(r3 - G)) : 0.f;
+    if (lane < 16) t->upto[lane] = valid ? exp2_fast((float)(r1 - G)) : 0.f;
+    if (lane < 32) t->upto[16 + lane] = valid ? exp2_fast((float)(r2 - G)) : 0.f;
+    if (lane < 48) t->upto[48 + lane] = valid ? exp2_fast((float)(r3 - G)) : 0.f;
     t->in[lane] = exp2_fast((float)G);
     t->out[lane] = valid ? exp2_fast((float)(end - G)) : 0.f;
     if (lane == 0) t->total = exp2_fast((float)end);
@@ -445,13 +445,39 @@ struct Slice {
     }
 };
 
-// P, 16 x 16 tiles of their own: rows of 16 elements, 4 at a time.  Tile
-// (ti, tj) is the slot-th of wave `owner`.
-struct PSlot { int owner, slot; };
-__device__ __forceinline__ constexpr PSlot p_slot(int ti, int tj) {
-    return ti == 0 ? (tj == 0 ? PSlot{0, 0} : PSlot{2, 2}) : ti == 1 ? PSlot{0, 1 + tj}
-         : ti == 2 ? (tj < 3 ? PSlot{1, tj} : PSlot{3, 2}) : tj < 2 ? PSlot{2, tj} : PSlot{3, tj - 2};
+// P as 16 x 16 tiles of their own (rows of 16 elements, 4 at a time), of bf16 in
+// two parts: value and remainder, since with few tokens its rounding would not
+// average out of a row.  Only tiles on and below the diagonal; the two above it
+// that are read, (0, 1) and (2, 3), are one tile of zeros.
+template <typename T> constexpr int kParts = sizeof(T) == 2 ? 2 : 1;
+constexpr int tri(int ti, int tj) { return ti * (ti + 1) / 2 + tj; }
+
+// Where a tile lies, in elements.  Gradient runs: an array of their own.
+template <typename T> constexpr int p_tiles() { return 10 * kParts<T> + 1; }
+template <typename T>
+__device__ __forceinline__ constexpr int p_at_own(int ti, int tj, int part) {
+    return 256 * (tj > ti ? 10 * kParts<T> : 10 * part + tri(ti, tj));
 }
+// Else the tiles of a wave lie in its slice of v (SIZE elements), where each
+// wave may write once it has read its own v, and what does not fit behind the
+// slices.  Waves hold (0,0) (1,0) (1,1); (2,*); (3,0) (3,1) and the zeros; (3,2) (3,3).
+template <int SIZE>
+__device__ __forceinline__ constexpr int p_at(int ti, int tj, int part) {
+    const int w = ti < 2 ? 0 : ti == 2 ? 1 : tj < 2 ? 2 : 3;
+    if (tj > ti) return 2 * SIZE + 512;
+    if (part == 0) return w * SIZE + 256 * (ti < 2 ? tri(ti, tj) : ti == 2 ? tj : tj & 1);
+    const int t = tri(ti, tj);   // remainders of (0,0) .. (3,3)
+    if (SIZE >= 1024) {
+        if (t == 0) return 0 * SIZE + 768;
+        if (t == 3) return 1 * SIZE + 768;
+        if (t == 6) return 2 * SIZE + 768;
+        if (t >= 8) return 3 * SIZE + 512 + 256 * (t - 8);
+        return 4 * SIZE + 256 * (t == 1 ? 0 : t == 2 ? 1 : t == 4 ? 2 : t == 5 ? 3 : 4);
+    }
+    if (t == 8) return 3 * SIZE + 512;
+    return 4 * SIZE + 256 * (t < 8 ? t : 8);
+}
+template <typename T, int SIZE> constexpr int p_extra() { return sizeof(T) == 4 ? 0 : SIZE >= 1024 ? 5 * 256 : 9 * 256; }
 template <typename T>
 __device__ __forceinline__ int p_off(int i, int j4) {   // row, run of 4 columns
     return i * 16 + (sizeof(T) == 2 ? (j4 ^ ((i >> 2) & 2)) : (j4 ^ ((i >> 2) & 3))) * 4;
@@ -464,8 +490,9 @@ __device__ __forceinline__ int p_off(int i, int j4) {   // row, run of 4 columns
 template <typename T, int DK, int DV, int MODE>
 constexpr int lds_bytes() {
     const int sz = (int)sizeof(T), tables = 2 * (int)sizeof(Tables) + (MODE == kGrad ? (int)sizeof(Scratch) : (int)sizeof(float[2][C]));
-    if (MODE == kGrad) return C * (2 * DK + 2 * DV) * sz + C * C * sz + tables;
-    return 2 * C * DK * sz * (MODE == kState ? 1 : 2) + 4 * Slice<T, DV / 4>::SIZE * sz + tables;
+    if (MODE == kGrad) return (C * (2 * DK + 2 * DV) + 256 * p_tiles<T>()) * sz + tables;
+    constexpr int SL = Slice<T, DV / 4>::SIZE;
+    return (2 * C * DK * (MODE == kState ? 1 : 2) + 4 * SL + (MODE == kState ? 0 : p_extra<T, SL>())) * sz + tables;
 }
 
 // Eight values as a sum of NS operands of type T.  One: rounded to nearest.
@@ -521,9 +548,9 @@ __device__ __forceinline__ f32x4_t load4(const float* p) { return *reinterpret_c
 // the decay's gradient the products of extra rows x_i with the part of o_i that
 // comes from the entering state, plus (a.pairs) those of pairs inside a chunk.
 //
-// Roundings of bf16 inputs: P and the entering state are rounded once to bf16
-// as operands (the state three ways in kGrad, whose sums are fp32 outputs); the
-// update's exp(G_63 - G_j) v_j enters as a sum of three bf16 values, so that
+// Roundings of bf16 inputs: as operands P enters as two bf16 values and the state
+// that enters the chunk as one, rounded to nearest (an output is a sum over all
+// its DK rows; as three in kGrad, whose sums are fp32 outputs); the update's exp(G_63 - G_j) v_j enters as a sum of three bf16 values, so that
 // the state keeps its 24 bits.
 template <typename T, int DK, int DV, int MODE>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(LinPair pair) {
@@ -538,9 +565,12 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
     T* const skb = reinterpret_cast<T*>(smem);          // [2 or 1][C][DK]
     T* const sqb = skb + (kPair ? 2 : 1) * C * DK;      // [2 or 1][C][DK]
     T* const sv = sqb + (MODE == kState ? 0 : kPair ? 2 : 1) * C * DK;   // slices, or [C][DV]
-    T* const sx = sv + (kPair ? 4 * Slice<T, DV / 4>::SIZE : C * DV);   // [C][DV]
-    T* const sp = sx + (kPair ? 0 : C * DV);            // [C][C]
-    Tables* const tbb = reinterpret_cast<Tables*>(sp + (kPair ? 0 : C * C));
+    constexpr int SL = Slice<T, DV / 4>::SIZE;
+    constexpr int NP = kParts<T>;
+    T* const sx = sv + (kPair ? 4 * SL : C * DV);       // [C][DV]
+    T* const sp = sx + (kPair ? 0 : C * DV);            // P's tiles, or those behind the slices
+    Tables* const tbb = reinterpret_cast<Tables*>(
+        sp + (!kPair ? 256 * p_tiles<T>() : MODE == kState ? 0 : p_extra<T, SL>()));
     Scratch* const scr = reinterpret_cast<Scratch*>(tbb + 2);
 
     const int tid = threadIdx.x, lane0 = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -684,7 +714,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
         const bool more = m0 + C < rows.rows;
         // v's columns of this wave, before v is overwritten
         Frag8<T> fv[2][NT];
-        T* const slice = sv + wave * Slice<T, DV / 4>::SIZE;
+        T* const slice = sv + wave * SL;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             if constexpr (kPair) {
@@ -708,10 +738,20 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
         if constexpr (MODE != kState) {
             // P, transposed tiles (rows j, columns i): a lane holds 4 consecutive
             // j of one i.  Waves take 3, 3, 2 and 2 of the 10 tiles on or below
-            // the diagonal; two tiles above it are read as zeros.
+            // the diagonal.
             auto put_p = [&](int ti, int tj, const f32x4_t& p) {
-                if constexpr (kPair) store4<T>(slice + p_slot(ti, tj).slot * 256 + p_off<T>(lr, lg), p);
-                else store4<T>(sp + Tile<T, C>::off(16 * ti + lr, 16 * tj + 4 * lg), p);
+                f32x4_t rest = p;
+#pragma unroll
+                for (int k = 0; k < NP; ++k) {
+                    T* const at = (kPair ? sv + p_at<SL>(ti, tj, k) : sp + p_at_own<T>(ti, tj, k)) + p_off<T>(lr, lg);
+                    store4<T>(at, rest);
+                    if constexpr (kBf) {
+                        if (k + 1 < NP) {
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) rest[r] -= (float)(__bf16)rest[r];
+                        }
+                    }
+                }
             };
             auto ptile = [&](int ti, int tj) {
                 f32x4_t x = {0.f, 0.f, 0.f, 0.f};
@@ -729,7 +769,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
                         w[r] = __builtin_amdgcn_ldexpf(e, wi - tb->whole[j + r]);
                     }
                 } else {
-                    w = *reinterpret_cast<const f32x4_t*>(&tb->upto[ti - 1][j]) * tb->tile[i];
+                    w = *reinterpret_cast<const f32x4_t*>(&tb->upto[8 * ti * (ti - 1) + j]) * tb->tile[i];
                 }
                 f32x4_t p;
 #pragma unroll
@@ -756,7 +796,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
                     }
                 }
             };
-            auto pzero = [&](int ti, int tj) { put_p(ti, tj, f32x4_t{0.f, 0.f, 0.f, 0.f}); };
+            auto pzero = [&] {
+                store4<T>((kPair ? sv + p_at<SL>(0, 1, 0) : sp + p_at_own<T>(0, 1, 0)) + p_off<T>(lr, lg),
+                          f32x4_t{0.f, 0.f, 0.f, 0.f});
+            };
             if constexpr (MODE == kGrad) scr->row[wave][lane] = 0.f;
             if (wave == 0) {
                 ptile(0, 0);
@@ -769,11 +812,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
             } else if (wave == 2) {
                 ptile(3, 0);
                 ptile(3, 1);
-                pzero(0, 1);
+                pzero();
             } else {
                 ptile(3, 2);
                 ptile(3, 3);
-                pzero(2, 3);
             }
             // the entering state's part, this wave's columns
 #pragma unroll
@@ -845,13 +887,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
             c = 1.f;
         }
         const float u = u_scale / c;
-        auto get_p = [&](int t, int s) {
-            if constexpr (!kPair) return Tile<T, C>::rows(sp, 16 * t, s, lane);
+        auto get_p = [&](int t, int s, int k) {
             Frag8<T> f;
-            const PSlot p0 = p_slot(t, 2 * s), p1 = p_slot(t, 2 * s + 1);
-            constexpr int SL = Slice<T, DV / 4>::SIZE;
-            const T* x = sv + p0.owner * SL + p0.slot * 256 + p_off<T>(lr, lg);
-            const T* y = sv + p1.owner * SL + p1.slot * 256 + p_off<T>(lr, lg);
+            const T* x = (kPair ? sv + p_at<SL>(t, 2 * s, k) : sp + p_at_own<T>(t, 2 * s, k)) + p_off<T>(lr, lg);
+            const T* y = (kPair ? sv + p_at<SL>(t, 2 * s + 1, k) : sp + p_at_own<T>(t, 2 * s + 1, k)) + p_off<T>(lr, lg);
             if constexpr (kBf) {
                 f.v = __builtin_shufflevector(*reinterpret_cast<const bf16x4_t*>(x), *reinterpret_cast<const bf16x4_t*>(y),
                                               0, 1, 2, 3, 4, 5, 6, 7);
@@ -883,9 +922,12 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
             if constexpr (MODE != kState) {
 #pragma unroll
                 for (int t = 2 * s; t < 4; ++t) {
-                    const Frag8<T> fp = get_p(t, s);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) acc[t][n] = mma(fv[s][n], fp, acc[t][n]);
+                    for (int k = NP - 1; k >= 0; --k) {
+                        const Frag8<T> fp = get_p(t, s, k);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) acc[t][n] = mma(fv[s][n], fp, acc[t][n]);
+                    }
                 }
             }
 #pragma unroll
