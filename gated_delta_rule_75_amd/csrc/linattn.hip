@@ -844,6 +844,30 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
                         for (int p = NS - 1; p >= 0; --p) acc[t][n] = mma(fs[n][p], fq, acc[t][n]);
                 }
             }
+            if (kBf && MODE == kOut && rows.rows == C) {
+                // a block of one chunk waits for memory, not for products, and
+                // may have few rows: the state's remainder too
+#pragma unroll
+                for (int s = 0; s < DK / 32; ++s) {
+                    Frag8<T> fs[NT][1];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        float x[8];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            x[r] = S[2 * s][n][r] - (float)(__bf16)S[2 * s][n][r];
+                            x[4 + r] = S[2 * s + 1][n][r] - (float)(__bf16)S[2 * s + 1][n][r];
+                        }
+                        split(x, fs[n]);
+                    }
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const Frag8<T> fq = Tile<T, DK>::rows(sq, 16 * t, s, lane);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) acc[t][n] = mma(fs[n][0], fq, acc[t][n]);
+                    }
+                }
+            }
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 const int i = 16 * t + lr;

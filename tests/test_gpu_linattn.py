@@ -120,6 +120,46 @@ def test_single_token(kda, N, shape, dtype):
         ref.check(f"token {dtype} {N} {shape} {decay} state", state, sr, ref.TOL_STATE)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 128), (128, 64), (64, 64)])
+def test_blocks_of_many_chunks(kda, dk, dv, dtype):
+    """With many heads a block holds several chunks (the operands of the next
+    one arrive while one is worked on); a few heads against the recurrence."""
+    H, heads = 256, [0, 77, 255]
+    for lens, decay in (([500, 130], "token"), ([449, 64, 1], "reset"), ([833], "head")):
+        x = make(dtype, lens, H, H, dk, dv, seed=90, decay=decay)
+        y, s = fwd(kda, x)
+        got = bwd(kda, x)
+        sub = dict(x, **{n: x[n][:, heads] for n in ("q", "k", "v", "dy", "s0", "ds")})
+        sub["g"] = x["g"][heads] if decay == "head" else x["g"][:, heads]
+        yr, sr, _ = ref.linattn(sub["q"], sub["k"], sub["v"], sub["g"], x["cu"], sub["s0"], x["scale"])
+        name = f"chunks {dtype} {dk}x{dv} {lens} {decay}"
+        ref.check(name + " y", y[:, heads], yr, ref.TOL[dtype])
+        ref.check(name + " state", s[:, heads], sr, ref.TOL_STATE)
+        g = sub["g"].expand(sum(lens), len(heads))
+        want = ref.linattn_grad(sub["q"], sub["k"], sub["v"], g, x["cu"], sub["dy"], sub["s0"], sub["ds"], x["scale"])
+        for n, a, b in zip(("dq", "dk", "dv", "dg", "ds0"), got, want):
+            if n == "dg" and decay == "head":
+                # a sum over tokens, of both signs: each is within TOL_DG of its
+                # size, so the sum is within TOL_DG of the sum of their sizes
+                # (50 times the sum here)
+                err, size = (a[heads].double().cpu() - b.sum(0)).abs(), b.abs().sum(0)
+                print(f"[layer] {name} dg of a head: {(err / size).max():.2e} of its terms", flush=True)
+                assert bool((err <= ref.TOL_DG * size).all())
+                continue
+            ref.check(f"{name} {n}", a[:, heads], b,
+                      ref.TOL_DG if n == "dg" else ref.TOL_STATE if n == "ds0" else ref.TOL[dtype])
+
+
+def test_many_chunks_same_bits_and_streams(kda):
+    x = make("bf16", [500, 130], 256, 128, 128, 128, seed=91)
+    want = fwd(kda, x) + bwd(kda, x)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for a, b in zip(fwd(kda, x) + bwd(kda, x), want):
+            assert torch.equal(a, b)
+
+
 def test_tokens_one_by_one_equal_the_prompt(kda):
     x = make("f32", [70, 70], 4, 2, 64, 128, seed=8)
     y, s = fwd(kda, x)
