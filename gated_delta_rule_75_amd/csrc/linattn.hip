@@ -695,9 +695,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
         fetch_k(0);
         fetch_q(0);
         fetch_v(0);
-        wait_vmcnt<0>();
-        if (wave == kTab) tables(0);
     }
+    // on every path: else the compiler still has the state's first loads to wait
+    // for inside the loop, and that wait takes the next chunk's copies with it
+    wait_vmcnt<0>();
+    if (cnt > 0 && wave == kTab) tables(0);
     for (int m0 = 0; m0 < rows.rows; m0 += C) {
         // LDS addresses are formed anew in each chunk (a few dozen operations):
         // kept across the loop they cost registers that spill
