@@ -369,29 +369,27 @@ __device__ __forceinline__ void copy4(unsigned lds, const void* addr) {
 // The copy of a chunk's rows into a tile by the workgroup's four waves.  A
 // wave's copy is 1 KiB of LDS in order, so the swizzle is on the source side.
 // Rows without a token take the last token's: the tables give them no weight.
+template <typename T, int D> constexpr int kCopies = C * D * (int)sizeof(T) / 4096;   // of a wave
+template <typename T, int D>
+__device__ __forceinline__ void copy_part(T* t, const Src& x, const Rows& rows, int m0, int wave, int lane, int i) {
+    constexpr int PIECES = Tile<T, D>::PIECES, RPW = 64 / PIECES, N = kCopies<T, D>;
+    const int top = rows.tokens(m0) - 1;
+    const int row0 = wave * RPW + lane / PIECES, row = 4 * RPW * i + row0;
+    const unsigned lds = uni(lds_addr(t) + wave * 1024) + i * 4096;
+    const unsigned piece = (unsigned)((lane % PIECES) ^ Tile<T, D>::swz(row)) * 16u;
+    const int64_t base = x.token(rows.low(m0));
+    if (top == C - 1) {
+        const int64_t at = base + (int64_t)((rows.rev ? N - 1 - i : i) * 4 * RPW) * x.step;
+        copy16(lds, reinterpret_cast<const void*>(at), (unsigned)(rows.rev ? 4 * RPW - 1 - row0 : row0) * x.step + piece);
+    } else {
+        const int tok = rows.rev ? C - 1 - row : row;
+        copy16(lds, reinterpret_cast<const void*>(base), (unsigned)(tok < top ? tok : top) * x.step + piece);
+    }
+}
 template <typename T, int D>
 __device__ __forceinline__ void copy_tile(T* t, const Src& x, const Rows& rows, int m0, int wave, int lane) {
-    constexpr int PIECES = Tile<T, D>::PIECES, RPW = 64 / PIECES, N = C / (4 * RPW);
-    const int top = rows.tokens(m0) - 1;
-    const unsigned step = x.step;
-    const int64_t ub = x.token(rows.low(m0));
-    const unsigned lds = uni(lds_addr(t) + wave * 1024);
-    const int row0 = wave * RPW + lane / PIECES;
-    if (top == C - 1) {
-        const unsigned off = (unsigned)(rows.rev ? 4 * RPW - 1 - row0 : row0) * step;
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            copy16(lds + i * 4096, reinterpret_cast<const void*>(ub + (int64_t)((rows.rev ? N - 1 - i : i) * 4 * RPW) * step),
-                   off + (unsigned)((lane % PIECES) ^ Tile<T, D>::swz(4 * RPW * i + row0)) * 16u);
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int row = i * 4 * RPW + row0;
-            const int tok = rows.rev ? C - 1 - row : row;
-            copy16(lds + i * 4096, reinterpret_cast<const void*>(ub),
-                   (unsigned)(tok < top ? tok : top) * step + (unsigned)((lane % PIECES) ^ Tile<T, D>::swz(row)) * 16u);
-        }
-    }
+    for (int i = 0; i < kCopies<T, D>; ++i) copy_part<T, D>(t, x, rows, m0, wave, lane, i);
 }
 
 // A wave's columns of the v rows (SW of them): to registers a chunk ahead, then
@@ -550,8 +548,9 @@ __device__ __forceinline__ f32x4_t load4(const float* p) { return *reinterpret_c
 //
 // Roundings of bf16 inputs: as operands P enters as two bf16 values and the state
 // that enters the chunk as one, rounded to nearest (an output is a sum over all
-// its DK rows; as three in kGrad, whose sums are fp32 outputs); the update's exp(G_63 - G_j) v_j enters as a sum of three bf16 values, so that
-// the state keeps its 24 bits.
+// its DK rows; as three in kGrad, whose sums are fp32 outputs); the update's
+// exp(G_63 - G_j) v_j enters as a sum of three bf16 values, so that the state
+// keeps its 24 bits.
 template <typename T, int DK, int DV, int MODE>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(LinPair pair) {
     const LinArgs& a = pair.a[blockIdx.y];
@@ -640,6 +639,16 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
         copy4(uni(lds_addr(scr->g[(m0 / C) & 1])), reinterpret_cast<const void*>(xg.at + (int64_t)((uint64_t)(unsigned)tok * xg.step)));
     };
     Slice<T, DV / 4> rv;
+    // A wave stalls on a copy while the memory pipe is full (about 100 cycles
+    // each when they come at once), so the copies of the next chunk are spread
+    // over the work on this one.
+    constexpr int NC = kCopies<T, DK>;
+    auto part_k = [&](int m0, int i) {
+        copy_part<T, DK>(skb + ((m0 / C) & 1) * C * DK, xk, rows, m0, wave, lane, i);
+    };
+    auto part_q = [&](int m0, int i) {
+        copy_part<T, DK>(sqb + ((m0 / C) & 1) * C * DK, xq, rows, m0, wave, lane, i);
+    };
     auto fetch_k = [&](int m0) {
         copy_tile<T, DK>(skb + (kPair ? ((m0 / C) & 1) * C * DK : 0), xk, rows, m0, wave, lane);
     };
@@ -728,15 +737,16 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
         }
         if (wave == kTab && m0 + 2 * C < rows.rows) fetch_g(m0 + 2 * C);
         if (kPair && more) {
-            fetch_k(m0 + C);
+            if (MODE == kState) fetch_k(m0 + C);
             fetch_v(m0 + C);
         }
-        if (kRows && m0 > 0) store_rows(m0 - C);
         if (MODE == kOut && !kRows && more) fetch_q(m0 + C);
 
         // outputs, transposed tiles: a lane holds 4 consecutive columns of row
         // 16 t + l % 16
         f32x4_t acc[4][NT];
+        Frag8<T> fk[KT];      // k's columns, tokens 0 to 31, then 32 to 63
+        const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
         if constexpr (MODE != kState) {
             // P, transposed tiles (rows j, columns i): a lane holds 4 consecutive
             // j of one i.  Waves take 3, 3, 2 and 2 of the 10 tiles on or below
@@ -755,11 +765,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
                     }
                 }
             };
-            auto ptile = [&](int ti, int tj) {
-                f32x4_t x = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int s = 0; s < DK / 32; ++s)
-                    x = mma(Tile<T, DK>::rows8(sk, 16 * tj, s, lane), Tile<T, DK>::rows8(sq, 16 * ti, s, lane), x);
+            auto ptile = [&](int ti, int tj, const f32x4_t& x) {
                 const int i = 16 * ti + lr, j = 16 * tj + 4 * lg;
                 f32x4_t w;
                 if (ti == tj) {
@@ -803,29 +809,79 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
                           f32x4_t{0.f, 0.f, 0.f, 0.f});
             };
             if constexpr (MODE == kGrad) scr->row[wave][lane] = 0.f;
+            // all operands of a wave's tiles are read before the first product
+            constexpr int SN = DK / 32;
+            auto read = [&](Frag8<T> (&f)[SN], const T* rows0, int tile) {
+#pragma unroll
+                for (int s = 0; s < SN; ++s) f[s] = Tile<T, DK>::rows8(rows0, 16 * tile, s, lane);
+            };
             if (wave == 0) {
-                ptile(0, 0);
-                ptile(1, 0);
-                ptile(1, 1);
+                Frag8<T> k0[SN], k1[SN], q0[SN], q1[SN];
+                read(k0, sk, 0);
+                read(q0, sq, 0);
+                read(q1, sq, 1);
+                read(k1, sk, 1);
+                __builtin_amdgcn_sched_barrier(0);
+                f32x4_t x = zero, y = zero, z = zero;
+#pragma unroll
+                for (int s = 0; s < SN; ++s) {
+                    x = mma(k0[s], q0[s], x);
+                    y = mma(k0[s], q1[s], y);
+                    z = mma(k1[s], q1[s], z);
+                }
+                ptile(0, 0, x);
+                ptile(1, 0, y);
+                ptile(1, 1, z);
             } else if (wave == 1) {
-                ptile(2, 0);
-                ptile(2, 1);
-                ptile(2, 2);
-            } else if (wave == 2) {
-                ptile(3, 0);
-                ptile(3, 1);
-                pzero();
+                Frag8<T> k0[SN], k1[SN], k2[SN], q2[SN];
+                read(q2, sq, 2);
+                read(k0, sk, 0);
+                read(k1, sk, 1);
+                read(k2, sk, 2);
+                __builtin_amdgcn_sched_barrier(0);
+                f32x4_t x = zero, y = zero, z = zero;
+#pragma unroll
+                for (int s = 0; s < SN; ++s) {
+                    x = mma(k0[s], q2[s], x);
+                    y = mma(k1[s], q2[s], y);
+                    z = mma(k2[s], q2[s], z);
+                }
+                ptile(2, 0, x);
+                ptile(2, 1, y);
+                ptile(2, 2, z);
             } else {
-                ptile(3, 2);
-                ptile(3, 3);
+                const int tj = wave == 2 ? 0 : 2;
+                Frag8<T> k0[SN], k1[SN], q3[SN];
+                read(q3, sq, 3);
+                read(k0, sk, tj);
+                read(k1, sk, tj + 1);
+                __builtin_amdgcn_sched_barrier(0);
+                f32x4_t x = zero, y = zero;
+#pragma unroll
+                for (int s = 0; s < SN; ++s) {
+                    x = mma(k0[s], q3[s], x);
+                    y = mma(k1[s], q3[s], y);
+                }
+                if (wave == 2) {
+                    ptile(3, 0, x);
+                    ptile(3, 1, y);
+                    pzero();
+                } else {
+                    ptile(3, 2, x);
+                    ptile(3, 3, y);
+                }
             }
+            if (kRows && m0 > 0) store_rows(m0 - C);
             // the entering state's part, this wave's columns
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
                 for (int n = 0; n < NT; ++n) acc[t][n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            Frag8<T> fq[4];
 #pragma unroll
-            for (int s = 0; s < DK / 32; ++s) {
+            for (int t = 0; t < 4; ++t) fq[t] = Tile<T, DK>::rows(sq, 16 * t, 0, lane);
+#pragma unroll
+            for (int s = 0; s < SN; ++s) {
                 Frag8<T> fs[NT][NS];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
@@ -839,11 +895,16 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
                 }
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
-                    const Frag8<T> fq = Tile<T, DK>::rows(sq, 16 * t, s, lane);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                    for (int p = NS - 1; p >= 0; --p)
 #pragma unroll
-                        for (int p = NS - 1; p >= 0; --p) acc[t][n] = mma(fs[n][p], fq, acc[t][n]);
+                        for (int n = 0; n < NT; ++n) acc[t][n] = mma(fs[n][p], fq[t], acc[t][n]);
+                    if (s + 1 < SN) fq[t] = Tile<T, DK>::rows(sq, 16 * t, s + 1, lane);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                if (MODE == kOut && more) {
+#pragma unroll
+                    for (int i = s * NC / SN; i < (s + 1) * NC / SN; ++i) part_k(m0 + C, i);
                 }
             }
             if (kBf && MODE == kOut && rows.rows == C) {
@@ -890,6 +951,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
                     if (lg == 0) atomicAdd(&scr->row[wave][i], dot);
                 }
             }
+#pragma unroll
+            for (int i = 0; i < KT; ++i) fk[i] = Tile<T, DK>::cols(sk, 16 * i, 0, lane);
             // the next chunk's tables: its decays came with this chunk's copies
             if (kPair && wave == kTab && more) tables(m0 + C);
             // B: P is whole; v, q and x are read
@@ -901,9 +964,13 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
                 }
             }
         }
-        if (MODE == kState && wave == kTab && more) tables(m0 + C);
+        if constexpr (MODE == kState) {
+#pragma unroll
+            for (int i = 0; i < KT; ++i) fk[i] = Tile<T, DK>::cols(sk, 16 * i, 0, lane);
+            if (wave == kTab && more) tables(m0 + C);
+        }
         if (!kPair && more) fetch_v(m0 + C);
-        if (kRows && more) fetch_q(m0 + C);
+        if (kRows && more) part_q(m0 + C, 0);
         c = unif(c * tb->total);
         if (c < 1.f / 4096.f) {
 #pragma unroll
@@ -945,6 +1012,13 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
                 }
                 split(x, fu[n]);
             }
+            auto rest_q = [&](int from, int to) {   // the first half's three places for the other copies
+                if (kRows && more && s == 0) {
+#pragma unroll
+                    for (int i = from; i < to; ++i) part_q(m0 + C, i);
+                }
+            };
+            rest_q(1, 1 + (NC - 1 + 2) / 3);
             if constexpr (MODE != kState) {
 #pragma unroll
                 for (int t = 2 * s; t < 4; ++t) {
@@ -956,13 +1030,19 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
                     }
                 }
             }
+            rest_q(1 + (NC - 1 + 2) / 3, 1 + (2 * (NC - 1) + 2) / 3);
+            // one part for all of the state's tiles, then the next: a product on
+            // the accumulator of the one before it would wait for that
 #pragma unroll
-            for (int i = 0; i < KT; ++i) {
-                const Frag8<T> fk = Tile<T, DK>::cols(sk, 16 * i, s, lane);
+            for (int p = NU - 1; p >= 0; --p) {
+                if (p == 0) rest_q(1 + (2 * (NC - 1) + 2) / 3, NC);
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int i = 0; i < KT; ++i) {
 #pragma unroll
-                    for (int p = NU - 1; p >= 0; --p) S[i][n] = mma(fk, fu[n][p], S[i][n]);
+                    for (int n = 0; n < NT; ++n) S[i][n] = mma(fk[i], fu[n][p], S[i][n]);
+                    if (s == 0 && p == 0) fk[i] = Tile<T, DK>::cols(sk, 16 * i, 1, lane);
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
         if constexpr (kRows) {
