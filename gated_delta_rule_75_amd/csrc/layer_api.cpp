@@ -235,7 +235,7 @@ kda_status kda_linattn_decode_step(kda_dtype dt, int N, int H, int Hk, int dk, i
                                    void* stream) {
     if (!dtype_ok(dt) || N < 0 || H <= 0 || Hk <= 0 || H % Hk != 0) return KDA_ERR_INVALID_ARGUMENT;
     if (!head_ok(dk) || !head_ok(dv)) return KDA_ERR_UNSUPPORTED;
-    if ((int64_t)N * H > (int64_t)1 << 30) return KDA_ERR_INVALID_ARGUMENT;
+    if ((int64_t)N * H >= (int64_t)1 << 24) return KDA_ERR_INVALID_ARGUMENT;
     if (N > 0 && (!q || !k || !v || !g || !state || !y)) return KDA_ERR_INVALID_ARGUMENT;
     if (!rows_ok(dt, q, q_stride, Hk, dk) || !rows_ok(dt, k, k_stride, Hk, dk) || !rows_ok(dt, v, v_stride, H, dv) ||
         !aligned(y, 16) || !aligned(g, 4) || !aligned(state, 16))
@@ -359,7 +359,7 @@ int64_t norm_slots(kda_dtype dt, int64_t T, int H, int D) {
 }
 
 bool norm_sizes_ok(kda_dtype dt, int64_t T, int H, int D) {
-    return dtype_ok(dt) && T >= 0 && H > 0 && D > 0 && T <= ((int64_t)1 << 31) / H - 1 && (int64_t)H * D <= 1 << 28;
+    return dtype_ok(dt) && T >= 0 && H > 0 && D > 0 && T <= ((int64_t)1 << 31) / H - 1 && (int64_t)H * D <= 1 << 26;
 }
 
 bool kind_ok(kda_norm_kind kind) { return kind == KDA_NORM_LAYER || kind == KDA_NORM_RMS; }

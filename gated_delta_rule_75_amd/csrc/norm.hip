@@ -39,8 +39,8 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_fwd_kernel(
     float* __restrict__ rstd) {
     constexpr int RPB = LANES < 256 ? 256 / LANES : 1;   // rows of a workgroup
     __shared__ float part[2][LANES > 64 ? LANES / 64 : 1];
-    const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / LANES;
-    if (LANES <= 64 && row >= rows) return;              // no barrier below for these
+    const int64_t row = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * RPB + threadIdx.x / LANES;
+    if (row >= rows) return;                             // LANES > 64: a whole workgroup
     const Cols<VEC, LANES, NV, TAIL> c{(int)(threadIdx.x % LANES), D};
     const int64_t base = row * D, wb = (int64_t)(row % H) * D;
     float v[NV][VEC];
@@ -222,7 +222,7 @@ hipError_t launch_t(const NormArgs& a) {
     constexpr int RPB = LANES < 256 ? 256 / LANES : 1, NT = LANES < 256 ? 256 : LANES;
     const int64_t rows = a.T * a.H;
     if (!a.dy) {
-        hipLaunchKernelGGL((norm_fwd_kernel<T, VEC, LANES, NV, TAIL>), dim3((unsigned)((rows + RPB - 1) / RPB)), dim3(NT), 0,
+        hipLaunchKernelGGL((norm_fwd_kernel<T, VEC, LANES, NV, TAIL>), folded_grid((rows + RPB - 1) / RPB), dim3(NT), 0,
                            (hipStream_t)a.stream, rows, a.H, a.D, a.eps, a.rms, (const T*)a.x, a.weight, a.bias,
                            (const T*)a.z, (T*)a.y, a.mean, a.rstd);
     } else {

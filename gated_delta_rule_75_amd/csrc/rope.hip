@@ -22,7 +22,8 @@ template <typename T, int VEC, bool HALF>
 __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, int tpb) {
     extern __shared__ float cs[];   // cos [tpb][n], then sin [tpb][n]
     const int n = a.rot / 2;
-    const int64_t t0 = (int64_t)blockIdx.x * tpb;
+    const int64_t t0 = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * tpb;
+    if (t0 >= a.T) return;
     const int nt = (int)(a.T - t0 < tpb ? a.T - t0 : tpb);
     float* sn = cs + tpb * n;
     for (int i = threadIdx.x; i < nt * n; i += 256) {
@@ -122,7 +123,7 @@ hipError_t launch_t(const RopeArgs& a) {
     // workgroups for every CU and the table fits 16 KiB
     int tpb = 1;
     while (tpb < 16 && tpb * 2 * per <= 2048 && tpb * 2 * n <= 2048 && a.T / (tpb * 2) >= 2048) tpb *= 2;
-    const dim3 grid((unsigned)((a.T + tpb - 1) / tpb));
+    const dim3 grid = folded_grid((a.T + tpb - 1) / tpb);
     const size_t lds = (size_t)tpb * n * 2 * sizeof(float);
     if (vec) {
         if (a.half) hipLaunchKernelGGL((rope_kernel<T, V, true>), grid, dim3(256), lds, (hipStream_t)a.stream, a, tpb);

@@ -68,6 +68,13 @@ __device__ __forceinline__ void store_run(T* p, int n, const float (&x)[N]) {
     }
 }
 
+// n workgroups as a grid: an axis of a launch holds less than 2^32 threads, so
+// many small rows take a second axis, whose last line may reach past n.
+inline dim3 folded_grid(int64_t n) {
+    constexpr int64_t line = 1 << 20;
+    return n <= line ? dim3((unsigned)n) : dim3((unsigned)line, (unsigned)((n + line - 1) / line));
+}
+
 // Sum over LANES consecutive threads of a workgroup, the same bits in each of
 // them.  Up to a wave: DPP adds over 16 lanes, then two permutes.  More: the
 // waves' sums through LDS (`part`, one float a wave; the caller's barriers keep

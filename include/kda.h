@@ -392,6 +392,8 @@ kda_status kda_linattn_fwd(kda_dtype dt, int H, int Hk, int dk, int dv, float sc
  *                    that share a key head (in fp32, rounded once).
  *   dv_out           [T_total, H, dv] in dtype dt.
  *   dg               fp32, [T_total, H] or [H] (summed over all tokens) as g.
+ *                    A sum of terms of both signs, accurate to a few 1e-6 of
+ *                    the sum of their sizes; for [H] also those of the tokens.
  *                    Where g is below -200 the gradient is taken at -200.
  *   d_initial_state  fp32 [num_seqs, H, dk, dv] or NULL.
  *   workspace        at least kda_linattn_bwd_workspace_size bytes, 256-byte
@@ -407,8 +409,8 @@ kda_status kda_linattn_bwd(kda_dtype dt, int H, int Hk, int dk, int dv, float sc
                            size_t workspace_bytes, void* stream);
 
 /*
- * kda_linattn_decode_step -- one token for each of N requests against resident
- * states: q, k [N, Hk, dk], v [N, H, dv] (strides as above), g [N, H] or [H],
+ * kda_linattn_decode_step -- one token for each of N requests (N * H < 2^24)
+ * against resident states: q, k [N, Hk, dk], v [N, H, dv] (strides as above), g [N, H] or [H],
  * state fp32 [N, H, dk, dv] updated in place, y [N, H, dv] in dtype dt.
  */
 kda_status kda_linattn_decode_step(kda_dtype dt, int N, int H, int Hk, int dk, int dv, float scale, const void* q,
@@ -479,7 +481,8 @@ typedef enum {
  *   weight, bias     fp32 [H, D]; bias may be NULL.
  *   mean, rstd       fp32 [T, H], each NULL or written (mean only for
  *                    KDA_NORM_LAYER): what the gradient needs.
- *   D                1 to 16384 (else KDA_ERR_UNSUPPORTED).
+ *   D                1 to 16384 (else KDA_ERR_UNSUPPORTED); T * H < 2^31 and
+ *                    H * D <= 2^26.
  */
 kda_status kda_norm_fwd(kda_dtype dt, kda_norm_kind kind, int64_t T, int H, int D, float eps, const void* x,
                         const float* weight, const float* bias, const void* z, void* y, float* mean, float* rstd,

@@ -124,6 +124,34 @@ def test_norm_unaligned_rows(kda):
     ref.check("unaligned", y, yr, EXACT["bf16"])
 
 
+# more workgroups than one axis of a launch holds (2^32 threads)
+def test_norm_of_very_many_rows(kda):
+    T, D = 2 ** 28 + 5, 2
+    x = torch.randn(T, 1, D, device="cuda", dtype=torch.bfloat16, generator=torch.Generator("cuda").manual_seed(1))
+    w = torch.tensor([[0.5, -2.0]], device="cuda")
+    y, _, _ = kda.norm_fwd(x, w, eps=1e-3, kind="rms", stats=False)
+    for at in (0, T // 2, T - 4096):
+        r = x[at:at + 4096].double()
+        want = r / (r.square().mean(-1, keepdim=True) + 1e-3).sqrt() * w.double()
+        ref.check(f"row {at}", y[at:at + 4096], want.cpu(), EXACT["bf16"])
+    assert torch.equal(torch.signbit(y[..., 0]), torch.signbit(x[..., 0])), "a row was left out"
+    assert torch.equal(torch.signbit(y[..., 1]), ~torch.signbit(x[..., 1])), "a row was left out"
+
+
+def test_rope_of_very_many_tokens(kda):
+    T = 2 ** 28 + 5
+    q = torch.randn(T, 1, 2, device="cuda", dtype=torch.bfloat16, generator=torch.Generator("cuda").manual_seed(2))
+    pos = (torch.arange(T, device="cuda", dtype=torch.int32) % 4) * 2   # turns by 0, 1/4, 1/2, 3/4 of a circle
+    freq = torch.tensor([torch.pi / 4], dtype=torch.float64, device="cuda")
+    out, _ = kda.rope(q, None, pos, freq)
+    for n in range(4):
+        a, b = q[n::4, 0, 0], q[n::4, 0, 1]
+        want = ((a, b), (-b, a), (-a, -b), (b, -a))[n]
+        # sine and cosine of a quarter turn: exact up to their rounding in fp32
+        assert torch.allclose(out[n::4, 0, 0].float(), want[0].float(), rtol=2.0 ** -8, atol=1e-5)
+        assert torch.allclose(out[n::4, 0, 1].float(), want[1].float(), rtol=2.0 ** -8, atol=1e-5)
+
+
 def test_norm_constant_and_large_rows(kda):
     """A constant row has variance 0 exactly; a large mean costs no digits."""
     x = torch.full((2, 1, 1024), 3.0).cuda()
