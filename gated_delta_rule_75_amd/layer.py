@@ -44,6 +44,16 @@ def _contiguous(**ts):
             raise ValueError(f"{name} must be contiguous")
 
 
+def _buf(name: str, t, shape, dtype) -> None:
+    """A contiguous tensor of this shape and dtype, or None."""
+    if t is None:
+        return
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape:
+        _need(name, t, shape, dtype)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
 def _call(dev, fn, name: str, *args) -> None:
     """The C call on the device's current stream, with that device current (a HIP
     launch needs its stream's)."""
@@ -69,6 +79,8 @@ def _current_device() -> int:
 def _rows(name: str, t: torch.Tensor) -> int:
     """The token stride of [T, heads, d] rows whose heads are contiguous."""
     T, heads, d = t.shape
+    if t.is_contiguous():
+        return heads * d
     st = t.stride()
     if T == 0:
         return heads * d
@@ -194,10 +206,10 @@ def linattn_decode_step(q, k, v, g, state, scale: float = 1.0, y: Optional[torch
     dt, N, H, Hk, dk, dv, per_token = _qkv(q, k, v, g)
     if state is None:
         raise ValueError("state is required")
-    _need("state", state, (N, H, dk, dv), torch.float32)
-    _need("y", y, (N, H, dv), q.dtype)
+    _buf("state", state, (N, H, dk, dv), torch.float32)
+    _buf("y", y, (N, H, dv), q.dtype)
+    _buf("g", g, g.shape, torch.float32)
     qs, ks, vs = _rows("q", q), _rows("k", k), _rows("v", v)
-    _contiguous(g=g, state=state, y=y)
     dev = _device(q, k, v, g, state, y)
     if y is None:
         y = torch.empty(N, H, dv, dtype=q.dtype, device=dev)
@@ -242,13 +254,12 @@ def rope(q, k, positions, inv_freq, layout: str = "half", inverse: bool = False,
         raise ValueError("k_out given without k")
     if layout not in _LAYOUT:
         raise ValueError("layout must be 'half' or 'interleaved'")
-    _need("positions", positions, (T,), torch.int32)
+    _buf("positions", positions, (T,), torch.int32)
     if inv_freq.dim() != 1:
         raise ValueError("inv_freq must be 1-D")
-    _need("inv_freq", inv_freq, inv_freq.shape, torch.float64)
+    _buf("inv_freq", inv_freq, inv_freq.shape, torch.float64)
     _need("q_out", q_out, q.shape, q.dtype)
     _need("k_out", k_out, None if k is None else k.shape, q.dtype)
-    _contiguous(positions=positions, inv_freq=inv_freq)
     dev = _device(q, k, positions, inv_freq, q_out, k_out)
     if q_out is None:
         q_out = torch.empty(T, Hq, d, dtype=q.dtype, device=dev)
@@ -270,10 +281,10 @@ def _norm_args(x, weight, bias, z, kind):
     T, H, D = x.shape
     if weight is None:
         raise ValueError("weight is required")
-    _need("weight", weight, (H, D), torch.float32)
-    _need("bias", bias, (H, D), torch.float32)
-    _need("z", z, (T, H, D), x.dtype)
-    _contiguous(x=x, weight=weight, bias=bias, z=z)
+    _buf("weight", weight, (H, D), torch.float32)
+    _buf("bias", bias, (H, D), torch.float32)
+    _buf("z", z, x.shape, x.dtype)
+    _buf("x", x, x.shape, x.dtype)
     return dt, T, H, D
 
 
@@ -284,13 +295,15 @@ def norm_fwd(x, weight, bias=None, z=None, eps: float = 1e-5, kind: str = "layer
     the mean square.  Returns (y, mean, rstd): fp32 [T, H], what norm_bwd needs
     (mean None for "rms", both None without stats)."""
     dt, T, H, D = _norm_args(x, weight, bias, z, kind)
-    _need("y", y, (T, H, D), x.dtype)
-    _contiguous(y=y)
+    _buf("y", y, x.shape, x.dtype)
     dev = _device(x, weight, bias, z, y)
     if y is None:
-        y = torch.empty(T, H, D, dtype=x.dtype, device=dev)
-    mean = torch.empty(T, H, dtype=torch.float32, device=dev) if stats and kind == "layer" else None
-    rstd = torch.empty(T, H, dtype=torch.float32, device=dev) if stats else None
+        y = torch.empty_like(x)
+    mean = rstd = None
+    if stats:
+        rstd = torch.empty(T, H, dtype=torch.float32, device=dev)
+        if kind == "layer":
+            mean = torch.empty_like(rstd)
     _call(dev, lib().kda_norm_fwd, "kda_norm_fwd", dt, _KIND[kind], T, H, D, eps, _p(x), _p(weight), _p(bias),
           _p(z), _p(y), _p(mean), _p(rstd))
     return y, mean, rstd
@@ -306,13 +319,13 @@ def norm_bwd(dy, x, weight, mean, rstd, bias=None, z=None, kind: str = "layer",
     """The gradient of norm_fwd with the mean and rstd it returned.  Returns
     (dx, dweight, dbias, dz); dbias and dz are None where bias and z are."""
     dt, T, H, D = _norm_args(x, weight, bias, z, kind)
-    _need("dy", dy, (T, H, D), x.dtype)
+    _buf("dy", dy, x.shape, x.dtype)
     if rstd is None or (mean is None) != (kind == "rms"):
         raise ValueError("rstd is required, and mean exactly for kind 'layer'")
-    _need("mean", mean, (T, H), torch.float32)
-    _need("rstd", rstd, (T, H), torch.float32)
+    _buf("mean", mean, (T, H), torch.float32)
+    _buf("rstd", rstd, (T, H), torch.float32)
     _need_workspace(workspace)
-    _contiguous(dy=dy, mean=mean, rstd=rstd, workspace=workspace)
+    _contiguous(workspace=workspace)
     dev = _device(x, dy, weight, mean, rstd, bias, z, workspace)
     L = lib()
     dx = torch.empty_like(x)
