@@ -59,10 +59,13 @@ int64_t block_len(int H, int64_t T, int groups, int64_t least, int64_t most) {
 int64_t fwd_block(int H, int64_t T) { return block_len(H, T, 512, 64, INT64_MAX); }
 int64_t bwd_block(int H, int64_t T) { return block_len(H, T, 256, 64, 1024); }
 
+// A launch's axis holds less than 2^32 threads, and a (block, head) has up to
+// 1024 of them.  Blocks shorter than 1024 tokens are 512 a head set at most.
+constexpr int64_t kMaxBlocks = (int64_t(1) << 22) - 1024;
+
 bool sizes_ok(kda_dtype dt, int H, int Hk, int dk, int dv, int num_seqs, int64_t T) {
     return dtype_ok(dt) && H > 0 && Hk > 0 && H % Hk == 0 && num_seqs > 0 && T >= 0 && T <= INT32_MAX - 64 &&
-           (int64_t)num_seqs * H <= 65535 && head_ok(dk) && head_ok(dv) &&
-           (T / 64 + num_seqs) * H < (int64_t)1 << 31;
+           head_ok(dk) && head_ok(dv) && (T / 1024 + num_seqs) * (int64_t)H < kMaxBlocks;
 }
 
 // Parts of a workspace, each 256-byte aligned.

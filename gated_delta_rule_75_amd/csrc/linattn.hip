@@ -29,6 +29,25 @@
 // in that order, and the token-contracted operands by transposing LDS reads.
 // Rows are kept in LDS in 16-byte pieces, piece index xor row, against bank
 // conflicts.
+//
+// Sequences are cut into blocks that run side by side: a first pass leaves each
+// block's own state from zero (kState), a small kernel chains them, a second
+// pass makes the outputs (kOut, kGrad) from the states that enter.
+//
+// What bounds it (d = 128, bf16): the products.  With the update's operand in
+// three parts and P in two, a chunk of a head takes 18 MFLOP in the two passes;
+// 8192 tokens x 96 heads are 221 GFLOP, 171 us at the 1.29 PFLOP/s that a large
+// bf16 product reaches here, where their 815 MB need 131 us at a copy's
+// 6.2 TB/s.  The call takes 327 us: about 120 the state pass, 10 the chain, 200
+// the output pass.  Without its products the output pass takes 134 us (183 with
+// the stores), without its loads 182.  By counters its SIMDs are busy 46 % with
+// vector and 28 % with matrix instructions (operands are split and decayed on
+// the way), 27 % of the waves' time is waiting, with two workgroups a CU (240 to
+// 256 registers a thread).
+// Measured and not kept: eight waves a workgroup (276 against 258 us, the pass
+// alone), half a head's columns a workgroup (457 the call), nontemporal output
+// stores (80 more), placement of a head's blocks on one XCD (no change).
+// The gradient, 4 x 2048 tokens x 32 heads: 229 GFLOP and 497 MB, 391 us.
 #include <type_traits>
 
 #include "launch.h"
@@ -1116,11 +1135,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(Li
 // after (one state a sequence and head) gets the state behind the last block.
 __global__ __launch_bounds__(256) void linattn_carry_kernel(LinArgs a, LinCarry c0, LinCarry c1) {
     const LinCarry c = blockIdx.z ? c1 : c0;
-    const int n = blockIdx.y / a.H, h = blockIdx.y % a.H;
+    const int n = blockIdx.x / a.H, h = blockIdx.x % a.H;
     const int b0 = first_block(a, n);
     int nb = blocks_of(seq_at(a, n + 1) - seq_at(a, n), a.L);
     if (nb > a.nblocks - b0) nb = a.nblocks - b0;   // offsets out of order: stay inside the arrays
-    const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, size = (int64_t)gridDim.x * 1024;
+    const int64_t e = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4, size = (int64_t)gridDim.y * 1024;
     f32x4_t s = {0.f, 0.f, 0.f, 0.f};
     if (c.initial) s = *reinterpret_cast<const f32x4_t*>(c.initial + ((int64_t)n * a.H + h) * size + e);
     // a block's own state and decay are read while the one before is passed on
@@ -1294,7 +1313,7 @@ hipError_t launch_linattn_fwd(const LinCall& c) {
         hipError_t e = launch_core(&s, 1, c.dtype, c.dk, c.dv, kState);
         if (e != hipSuccess) return e;
         const LinCarry f{c.states, c.decays, c.initial_state, nullptr, 0};
-        hipLaunchKernelGGL(linattn_carry_kernel, dim3((unsigned)(c.dk * c.dv / 1024), (unsigned)(a.num_seqs * a.H), 1),
+        hipLaunchKernelGGL(linattn_carry_kernel, dim3((unsigned)(a.num_seqs * a.H), (unsigned)(c.dk * c.dv / 1024), 1),
                            dim3(256), 0, (hipStream_t)a.stream, a, f, f);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
@@ -1328,7 +1347,7 @@ hipError_t launch_linattn_bwd(const LinCall& c) {
     if ((e = launch_core(s, 2, c.dtype, c.dk, c.dv, kState)) != hipSuccess) return e;
     const LinCarry f{c.states, c.decays, c.initial_state, c.d_final_state ? c.s_end : nullptr, 0};
     const LinCarry r{c.rstates, c.rdecays, c.d_final_state, nullptr, 1};
-    hipLaunchKernelGGL(linattn_carry_kernel, dim3((unsigned)(c.dk * c.dv / 1024), (unsigned)(a.num_seqs * a.H), 2),
+    hipLaunchKernelGGL(linattn_carry_kernel, dim3((unsigned)(a.num_seqs * a.H), (unsigned)(c.dk * c.dv / 1024), 2),
                        dim3(256), 0, (hipStream_t)a.stream, a, f, r);
     if ((e = hipGetLastError()) != hipSuccess) return e;
 

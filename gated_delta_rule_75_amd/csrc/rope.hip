@@ -8,7 +8,9 @@
 // angle is off by 0.06): the product is taken in fp64 in turns (radians / 2 pi),
 // its fraction is exact, and only that goes to fp32.  A workgroup's tokens share
 // their cosines and sines among all heads through LDS, one sincospi for each
-// (token, pair).  The rest is a copy at memory speed in 16-byte pieces.
+// (token, pair).  The rest is a copy at memory speed in 16-byte pieces: 8192 x
+// 192 heads of 128 in bf16 (806 MB) take 150 us, 5.4 TB/s, where a large copy
+// reaches 6.2.
 #include "launch.h"
 #include "vec.h"
 

@@ -354,7 +354,8 @@ kda_status kda_decode_replay(kda_dtype dt, int N, int Td, int H, int dk, int dv,
  *   H, Hk            value heads and key heads; Hk divides H, and value heads
  *                    h with equal h / (H / Hk) share a key head's q and k.
  *   dk, dv           64 or 128 each.
- *   num_seqs, T_total, cu_seqlens   as kda_chunk_fwd (num_seqs * H <= 65535).
+ *   num_seqs, T_total, cu_seqlens   as kda_chunk_fwd; (T_total / 1024 +
+ *                    num_seqs) * H at most about 4 million.
  *                    Sequences may be empty: their state passes through.  The
  *                    offsets may begin after 0 or end before T_total; rows of no
  *                    sequence are neither read nor written.
@@ -396,6 +397,7 @@ kda_status kda_linattn_fwd(kda_dtype dt, int H, int Hk, int dk, int dv, float sc
  *                    the sum of their sizes; for [H] also those of the tokens.
  *                    Where g is below -200 the gradient is taken at -200.
  *   d_initial_state  fp32 [num_seqs, H, dk, dv] or NULL.
+ *                    No output may overlap an input or another output.
  *   workspace        at least kda_linattn_bwd_workspace_size bytes, 256-byte
  *                    aligned.
  *   all other arguments: as kda_linattn_fwd.

@@ -120,6 +120,26 @@ def test_single_token(kda, N, shape, dtype):
         ref.check(f"token {dtype} {N} {shape} {decay} state", state, sr, ref.TOL_STATE)
 
 
+def test_very_many_sequences(kda):
+    """More (sequence, head) pairs than 65535, the last sequence in three blocks."""
+    H, N, long = 64, 1030, 400
+    x = make("bf16", [1] * (N - 1) + [long], H, H, 64, 64, seed=31, state=False)
+    y, s = fwd(kda, x)
+    got = bwd(kda, x)
+    for n, at, m in ((0, 0, 1), (N - 2, N - 2, 1), (N - 1, N - 1, long)):
+        sub = {k: x[k][at:at + m] for k in ("q", "k", "v", "g", "dy")}
+        yr, sr, _ = ref.linattn(sub["q"], sub["k"], sub["v"], sub["g"], [0, m], None, x["scale"])
+        ref.check(f"sequence {n} y", y[at:at + m], yr, ref.TOL["bf16"])
+        ref.check(f"sequence {n} state", s[n:n + 1], sr, ref.TOL_STATE)
+        want = ref.linattn_grad(sub["q"], sub["k"], sub["v"], sub["g"], [0, m], sub["dy"], None, None, x["scale"])
+        for name, a, b in zip(("dq", "dk", "dv", "dg"), got, want):
+            if name == "dg" and m == 1:
+                assert not a[at:at + m].any()      # nothing decays before a first token without a state
+                continue
+            ref.check(f"sequence {n} {name}", a[at:at + m], b, ref.TOL_DG if name == "dg" else ref.TOL["bf16"])
+        ref.check(f"sequence {n} ds0", got[4][n:n + 1], want[4], ref.TOL_STATE)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("dk,dv", [(128, 128), (64, 128), (128, 64), (64, 64)])
 def test_blocks_of_many_chunks(kda, dk, dv, dtype):

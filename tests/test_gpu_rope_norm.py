@@ -166,6 +166,19 @@ def test_norm_constant_and_large_rows(kda):
     ref.check("large mean", y, yr, 1e-3)
 
 
+@pytest.mark.parametrize("D", [128, 257, 5000])
+def test_norm_over_its_input_or_gate(kda, D):
+    gen = torch.Generator().manual_seed(D)
+    x, z = (randn(gen, 33, 2, D, dtype=torch.bfloat16).cuda() for _ in range(2))
+    w, b = (randn(gen, 2, D).cuda() for _ in range(2))
+    want, mean, rstd = kda.norm_fwd(x, w, b, z)
+    for k in range(2):
+        t = [x.clone(), z.clone()]
+        y, m, r = kda.norm_fwd(t[0], w, b, t[1], y=t[k])
+        assert y is t[k] and torch.equal(y, want) and torch.equal(m, mean) and torch.equal(r, rstd)
+        assert torch.equal(t[1 - k], (x, z)[1 - k])
+
+
 def test_norm_no_tokens(kda):
     x = torch.zeros(0, 2, 64, device="cuda")
     w = torch.ones(2, 64, device="cuda")

@@ -34,7 +34,7 @@ def test_linattn_refuses(L, call):
     for bad in (dict(dt=3), dict(H=0), dict(Hk=0), dict(Hk=3), dict(N=0), dict(T=-1), dict(N=2), dict(q=None),
                 dict(k=None), dict(v=None), dict(g=None), dict(q=A + 8), dict(v=A + 2), dict(qs=255), dict(qs=260),
                 dict(ks=128), dict(vs=0), dict(s0=A + 8), dict(ws=None), dict(ws=A + 128), dict(T=1 << 31),
-                dict(N=70000, cu=A), dict(cu=A + 2), dict(g=A + 2)):
+                dict(N=1 << 21, cu=A), dict(cu=A + 2), dict(g=A + 2)):
         assert call(L, **bad) == INVALID, bad
     for bad in (dict(dk=96), dict(dv=256), dict(dk=0)):
         assert call(L, **bad) == UNSUPPORTED, bad
