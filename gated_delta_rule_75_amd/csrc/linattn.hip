@@ -34,20 +34,20 @@
 // block's own state from zero (kState), a small kernel chains them, a second
 // pass makes the outputs (kOut, kGrad) from the states that enter.
 //
-// What bounds it (d = 128, bf16): the products.  With the update's operand in
-// three parts and P in two, a chunk of a head takes 18 MFLOP in the two passes;
-// 8192 tokens x 96 heads are 221 GFLOP, 171 us at the 1.29 PFLOP/s that a large
-// bf16 product reaches here, where their 815 MB need 131 us at a copy's
-// 6.2 TB/s.  The call takes 327 us: about 120 the state pass, 10 the chain, 200
-// the output pass.  Without its products the output pass takes 134 us (183 with
-// the stores), without its loads 182.  By counters its SIMDs are busy 46 % with
-// vector and 28 % with matrix instructions (operands are split and decayed on
-// the way), 27 % of the waves' time is waiting, with two workgroups a CU (240 to
-// 256 registers a thread).
+// What bounds it (d = 128, bf16): instructions.  With the update's operand in
+// three parts and P in two, 8192 tokens x 96 heads are 193 GFLOP in the two
+// passes, 150 us at the 1.29 PFLOP/s that a large bf16 product reaches here;
+// their 815 MB need 131 us at a copy's 6.2 TB/s.  The call takes 327 us: about
+// 110 the state pass, 10 the chain, 205 the output pass.  Without its products
+// the output pass takes 134 us (183 with the stores), without its loads 182.  By
+// counters its SIMDs are busy 46 % with vector and 27 % with matrix instructions
+// (operands are split and decayed on the way), and 27 % of the waves' time is
+// waiting, with two workgroups a CU (240 to 256 registers a thread).
 // Measured and not kept: eight waves a workgroup (276 against 258 us, the pass
 // alone), half a head's columns a workgroup (457 the call), nontemporal output
 // stores (80 more), placement of a head's blocks on one XCD (no change).
-// The gradient, 4 x 2048 tokens x 32 heads: 229 GFLOP and 497 MB, 391 us.
+// The gradient, 4 x 2048 tokens x 32 heads (206 GFLOP; 497 MB, of which its
+// passes read most more than once, 1.4 GB in all): 375 to 390 us.
 #include <type_traits>
 
 #include "launch.h"
