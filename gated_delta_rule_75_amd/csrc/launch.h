@@ -188,6 +188,16 @@ struct LinPair {
     LinArgs a[2];
 };
 
+// Beside the gradient's last run: the decay's gradient from the blocks' states
+// and the sums of the runs before, and dq and dk of shared key heads.
+struct LinTail {
+    const float *states, *rstates, *s_end, *r_end, *sums_a, *sums_b;
+    float* dg;             // per token; NULL: no tokens, nothing beside the run
+    const float* parts;    // fp32 [2][T][H][dk]
+    void *dq, *dk;
+    int share;             // value heads of a key head
+};
+
 struct LinCarry {
     float* states;
     const float* decays;

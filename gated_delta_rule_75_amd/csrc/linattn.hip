@@ -571,8 +571,7 @@ __device__ __forceinline__ f32x4_t load4(const float* p) { return *reinterpret_c
 // exp(G_63 - G_j) v_j enters as a sum of three bf16 values, so that the state
 // keeps its 24 bits.
 template <typename T, int DK, int DV, int MODE>
-__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(LinPair pair) {
-    const LinArgs& a = pair.a[blockIdx.y];
+__device__ __forceinline__ void linattn_body(const LinArgs& a) {
     constexpr bool kBf = sizeof(T) == 2;
     constexpr int NT = DV / 64;             // 16-column tiles of a wave
     constexpr int KT = DK / 16;             // 16-row tiles of the state
@@ -1164,34 +1163,38 @@ __global__ __launch_bounds__(256) void linattn_carry_kernel(LinArgs a, LinCarry 
     if (c.after) *reinterpret_cast<f32x4_t*>(c.after + ((int64_t)n * a.H + h) * size + e) = s;
 }
 
+template <typename T, int DK, int DV, int MODE>
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_kernel(LinPair pair) {
+    linattn_body<T, DK, DV, MODE>(pair.a[blockIdx.y]);
+}
+
 // The decay's gradient of a (block, head): dg_t = sum_{s >= t} (A_s - B_s) + E,
 // A and B the two kGrad runs' sums of the block's tokens, E what crosses the
 // block's end: the product of the state there with its gradient.
-__global__ __launch_bounds__(1024) void linattn_dg_kernel(LinArgs a, int size, const float* S, const float* R,
-                                                         const float* s_end, const float* r_end, const float* A,
-                                                         const float* B, float* dg) {
-    __shared__ double part[16];
-    __shared__ double carry;
+__device__ __forceinline__ void decay_gradient(const LinArgs& a, const LinTail& x, int size) {
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    double* const part = reinterpret_cast<double*>(smem);   // [4], of the waves
+    double& carry = part[4];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int b = blockIdx.x / a.H, h = blockIdx.x % a.H;
     const Block bl = find_block(a, b);
     if (bl.n < 0) return;
     const bool last = bl.j == bl.nb - 1 || b + 1 >= a.nblocks;
-    double e = 0.0;
-    const float *x = nullptr, *y = nullptr;
+    const float *S = nullptr, *R = nullptr;
     if (!last) {
-        x = S + ((int64_t)(b + 1) * a.H + h) * size;
-        y = R + ((int64_t)b * a.H + h) * size;
-    } else if (r_end) {
-        x = s_end + ((int64_t)bl.n * a.H + h) * size;
-        y = r_end + ((int64_t)bl.n * a.H + h) * size;
+        S = x.states + ((int64_t)(b + 1) * a.H + h) * size;
+        R = x.rstates + ((int64_t)b * a.H + h) * size;
+    } else if (x.r_end) {
+        S = x.s_end + ((int64_t)bl.n * a.H + h) * size;
+        R = x.r_end + ((int64_t)bl.n * a.H + h) * size;
     }
-    if (x) {
+    double e = 0.0;
+    if (S) {
         // in fp64: under strong decays the tokens next to the block's end take
         // nearly all of it away again
-#pragma unroll 4
-        for (int i = tid * 4; i < size; i += 4096) {
-            const f32x4_t u = *reinterpret_cast<const f32x4_t*>(x + i), v = *reinterpret_cast<const f32x4_t*>(y + i);
+#pragma unroll 8
+        for (int i = tid * 4; i < size; i += 1024) {
+            const f32x4_t u = *reinterpret_cast<const f32x4_t*>(S + i), v = *reinterpret_cast<const f32x4_t*>(R + i);
 #pragma unroll
             for (int r = 0; r < 4; ++r) e += (double)u[r] * (double)v[r];
         }
@@ -1201,8 +1204,7 @@ __global__ __launch_bounds__(1024) void linattn_dg_kernel(LinArgs a, int size, c
     if (lane == 0) part[wave] = e;
     __syncthreads();
     if (tid == 0) {
-        double s = 0.0;
-        for (int w = 0; w < 16; ++w) s += part[w];
+        double s = (part[0] + part[1]) + (part[2] + part[3]);
         if (!last) {
             const float g = a.g[a.g_per_token ? (bl.start + bl.cnt) * a.H + h : h];
             s *= exp((double)(g < kFloor ? kFloor : g));
@@ -1210,12 +1212,11 @@ __global__ __launch_bounds__(1024) void linattn_dg_kernel(LinArgs a, int size, c
         carry = s;
     }
     __syncthreads();
-    // from the block's end, 1024 tokens at a time (a block has no more)
-    for (int m0 = 0; m0 < bl.cnt; m0 += 1024) {
+    // from the block's end, 256 tokens at a time
+    for (int m0 = 0; m0 < bl.cnt; m0 += 256) {
         const int m = m0 + tid;
-        const int64_t tok = bl.start + bl.cnt - 1 - m;
-        double d = 0.0;
-        if (m < bl.cnt) d = (double)A[(int64_t)h * a.T_total + tok] - (double)B[(int64_t)h * a.T_total + tok];
+        const int64_t tok = bl.start + bl.cnt - 1 - m, at = (int64_t)h * a.T_total + tok;
+        double d = m < bl.cnt ? (double)x.sums_a[at] - (double)x.sums_b[at] : 0.0;
 #pragma unroll
         for (int k = 1; k < kWave; k <<= 1) {
             const double o = shfl_d(d, lane - k < 0 ? 0 : lane - k);
@@ -1227,10 +1228,52 @@ __global__ __launch_bounds__(1024) void linattn_dg_kernel(LinArgs a, int size, c
         for (int w = 0; w < wave; ++w) before += part[w];
         const double v = before + d;
         __syncthreads();
-        if (tid == 1023) carry = v;
-        if (m < bl.cnt) dg[tok * a.H + h] = (float)v;
+        if (tid == 255) carry = v;
+        if (m < bl.cnt) x.dg[tok * a.H + h] = (float)v;
         __syncthreads();
     }
+}
+
+// Sums over the value heads that share a key head, fp32 [T, H, D] to
+// [T, H / r, D], of dq's and dk's parts: runs of 4 elements, four a thread in
+// flight.
+template <typename T, int D>
+__device__ __forceinline__ void share_sums(const LinArgs& a, const LinTail& x) {
+    const int r = x.share;
+    const int64_t n4 = a.T_total * (a.H / r) * (D / 4), all = 2 * n4, step = (int64_t)gridDim.x * 256;
+    const int64_t t0 = seq_at(a, 0), t1 = seq_at(a, a.num_seqs);
+    const int per = a.H / r * (D / 4);   // runs of a token
+    for (int64_t u0 = (int64_t)blockIdx.x * 256 + threadIdx.x; u0 < all; u0 += 4 * step) {
+        const float* p[4];
+        f32x4_t s[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const int64_t u = u0 + m * step < all ? u0 + m * step : u0;
+            p[m] = x.parts + (u / (D / 4)) * r * D + u % (D / 4) * 4;
+            s[m] = *reinterpret_cast<const f32x4_t*>(p[m]);
+        }
+        for (int j = 1; j < r; ++j)
+#pragma unroll
+            for (int m = 0; m < 4; ++m) s[m] += *reinterpret_cast<const f32x4_t*>(p[m] + (int64_t)j * D);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const int64_t u = u0 + m * step, i = u < n4 ? u : u - n4;
+            const int64_t tok = i / per;
+            if (u >= all || tok < t0 || tok >= t1) continue;   // rows of no sequence stay
+            const float o[4] = {s[m][0], s[m][1], s[m][2], s[m][3]};
+            store_vec<T, 4>((T*)(u < n4 ? x.dq : x.dk) + i * 4, o);
+        }
+    }
+}
+
+// The gradient's last run, for dv, and beside it what waits for the runs before
+// only: a launch each for these cost the ragged fp32 gradient of 1531 tokens
+// 59 us in all, and dv's workgroups leave CUs half empty.
+template <typename T, int DK, int DV>
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_last_kernel(LinArgs a, LinTail x) {
+    if (blockIdx.y == 0) linattn_body<T, DK, DV, kOut>(a);
+    else if (blockIdx.y == 1) decay_gradient(a, x, DK * DV);
+    else share_sums<T, DK>(a, x);
 }
 
 // dg of a decay that all tokens of a head share: the sum over tokens, one
@@ -1250,23 +1293,6 @@ __global__ __launch_bounds__(256) void linattn_dg_sum_kernel(LinArgs a, const fl
     if (tid == 0) out[h] = (float)part[0];
 }
 
-// Sum over the value heads that share a key head: fp32 [T, H, D] to [T, H / r, D].
-template <typename T>
-__global__ __launch_bounds__(256) void linattn_share_kernel(LinArgs a, int64_t n, int r, int D, const float* src,
-                                                            T* dst0, T* dst1) {
-    T* dst = blockIdx.y ? dst1 : dst0;
-    src += blockIdx.y * n * r;
-    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-    const int64_t tok = i / ((int64_t)(a.H / r) * D);
-    if (i >= n || tok < seq_at(a, 0) || tok >= seq_at(a, a.num_seqs)) return;   // rows of no sequence stay
-    const int64_t row = i / D;
-    const float* p = src + row * r * D + i % D;
-    f32x4_t s = *reinterpret_cast<const f32x4_t*>(p);
-    for (int j = 1; j < r; ++j) s += *reinterpret_cast<const f32x4_t*>(p + (int64_t)j * D);
-    const float o[4] = {s[0], s[1], s[2], s[3]};
-    store_vec<T, 4>(dst + i, o);
-}
-
 template <typename T, int DK, int DV, int MODE>
 hipError_t launch_t(const LinArgs* a, int n) {
     constexpr int lds = lds_bytes<T, DK, DV, MODE>();
@@ -1277,6 +1303,23 @@ hipError_t launch_t(const LinArgs* a, int n) {
     hipLaunchKernelGGL((linattn_kernel<T, DK, DV, MODE>), dim3((unsigned)(a->nblocks * a->H), n), dim3(256), lds,
                        (hipStream_t)a->stream, LinPair{{a[0], a[n - 1]}});
     return hipGetLastError();
+}
+
+template <typename T, int DK, int DV>
+hipError_t launch_last_t(const LinArgs& a, const LinTail& x) {
+    constexpr int lds = lds_bytes<T, DK, DV, kOut>();
+    const void* kern = reinterpret_cast<const void*>(&linattn_last_kernel<T, DK, DV>);
+    hipError_t e = ensure_lds_limit(kern, lds);
+    if (e != hipSuccess) return e;
+    const unsigned parts = !x.dg ? 1 : x.share > 1 ? 3 : 2;
+    hipLaunchKernelGGL((linattn_last_kernel<T, DK, DV>), dim3((unsigned)(a.nblocks * a.H), parts), dim3(256), lds,
+                       (hipStream_t)a.stream, a, x);
+    return hipGetLastError();
+}
+template <typename T>
+hipError_t launch_last(const LinArgs& a, const LinTail& x, int dk, int dv) {
+    if (dk == 64) return dv == 64 ? launch_last_t<T, 64, 64>(a, x) : launch_last_t<T, 64, 128>(a, x);
+    return dv == 64 ? launch_last_t<T, 128, 64>(a, x) : launch_last_t<T, 128, 128>(a, x);
 }
 
 template <typename T, int MODE>
@@ -1379,17 +1422,6 @@ hipError_t launch_linattn_bwd(const LinCall& c) {
     x[1].sums = c.sums_b;
     x[1].out = shared ? static_cast<float*>(c.share_buf) + a.T_total * a.H * c.dk : c.dk_out;
     if ((e = launch_core(x, 2, c.dtype, c.dv, c.dk, kGrad)) != hipSuccess) return e;
-    const int64_t n = a.T_total * (a.H / c.k.share) * c.dk;
-    if (shared && n > 0) {
-        const dim3 grid((unsigned)((n / 4 + 255) / 256), 2);
-        if (c.dtype == 0)
-            hipLaunchKernelGGL(linattn_share_kernel<__bf16>, grid, dim3(256), 0, (hipStream_t)a.stream, a, n, c.k.share,
-                               c.dk, (const float*)c.share_buf, (__bf16*)c.dq, (__bf16*)c.dk_out);
-        else
-            hipLaunchKernelGGL(linattn_share_kernel<float>, grid, dim3(256), 0, (hipStream_t)a.stream, a, n, c.k.share,
-                               c.dk, (const float*)c.share_buf, (float*)c.dq, (float*)c.dk_out);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
     // dv and the gradient of the initial state
     LinArgs d = a;
     d.q = c.k;
@@ -1401,18 +1433,25 @@ hipError_t launch_linattn_bwd(const LinCall& c) {
     d.reverse = true;
     d.final = c.d_initial_state;
     d.out = c.dv_out;
-    if ((e = launch_core(&d, 1, c.dtype, c.dk, c.dv, kOut)) != hipSuccess) return e;
-    // dg
-    if (c.dg) {
-        float* per_token = a.g_per_token ? c.dg : c.dg_tokens;
-        hipLaunchKernelGGL(linattn_dg_kernel, dim3((unsigned)(a.nblocks * a.H)), dim3(1024), 0, (hipStream_t)a.stream, a,
-                           c.dk * c.dv, c.states, c.rstates, c.s_end, c.d_final_state, c.sums_a, c.sums_b, per_token);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-        if (!a.g_per_token) {
-            hipLaunchKernelGGL(linattn_dg_sum_kernel, dim3((unsigned)a.H), dim3(256), 0, (hipStream_t)a.stream,
-                               a, per_token, c.dg);
-            if ((e = hipGetLastError()) != hipSuccess) return e;
-        }
+    // beside it dg, and dq and dk of shared heads
+    LinTail t{};
+    t.states = c.states;
+    t.rstates = c.rstates;
+    t.s_end = c.s_end;
+    t.r_end = c.d_final_state;
+    t.sums_a = c.sums_a;
+    t.sums_b = c.sums_b;
+    t.dg = c.dg && !a.g_per_token ? c.dg_tokens : c.dg;
+    t.share = c.k.share;
+    t.parts = (const float*)c.share_buf;
+    t.dq = c.dq;
+    t.dk = c.dk_out;
+    e = c.dtype == 0 ? launch_last<__bf16>(d, t, c.dk, c.dv) : launch_last<float>(d, t, c.dk, c.dv);
+    if (e != hipSuccess) return e;
+    if (c.dg && !a.g_per_token) {
+        hipLaunchKernelGGL(linattn_dg_sum_kernel, dim3((unsigned)a.H), dim3(256), 0, (hipStream_t)a.stream, a,
+                           c.dg_tokens, c.dg);
+        return hipGetLastError();
     }
     return hipSuccess;
 }
