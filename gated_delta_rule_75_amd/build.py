@@ -32,8 +32,8 @@ COMMON = [
 
 
 # MFMA results in ordinary VGPRs: the scan, preparation and linear-attention
-# kernels scale and
-# convert accumulators with VALU instructions, which cannot read AGPRs
+# kernels scale and convert accumulators with VALU instructions, which cannot
+# read AGPRs
 PER_SOURCE = {
     "chunk_state.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "chunk_prep.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
