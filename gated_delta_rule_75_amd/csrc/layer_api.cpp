@@ -59,8 +59,9 @@ int64_t block_len(int H, int64_t T, int groups, int64_t least, int64_t most) {
 int64_t fwd_block(int H, int64_t T) { return block_len(H, T, 512, 64, INT64_MAX); }
 int64_t bwd_block(int H, int64_t T) { return block_len(H, T, 256, 64, 1024); }
 
-// A launch's axis holds less than 2^32 threads, and a (block, head) has up to
-// 1024 of them.  Blocks shorter than 1024 tokens are 512 a head set at most.
+// (block, head) pairs of a call: an axis of a launch holds less than 2^32
+// threads, 256 a pair; well inside that, as blocks shorter than 1024 tokens add
+// at most 512 pairs or one block a head.
 constexpr int64_t kMaxBlocks = (int64_t(1) << 22) - 1024;
 
 bool sizes_ok(kda_dtype dt, int H, int Hk, int dk, int dv, int num_seqs, int64_t T) {

@@ -37,17 +37,18 @@
 // What bounds it (d = 128, bf16): instructions.  With the update's operand in
 // three parts and P in two, 8192 tokens x 96 heads are 193 GFLOP in the two
 // passes, 150 us at the 1.29 PFLOP/s that a large bf16 product reaches here;
-// their 815 MB need 131 us at a copy's 6.2 TB/s.  The call takes 327 us: about
-// 110 the state pass, 10 the chain, 205 the output pass.  Without its products
-// the output pass takes 134 us (183 with the stores), without its loads 182.  By
-// counters its SIMDs are busy 46 % with vector and 27 % with matrix instructions
-// (operands are split and decayed on the way), and 27 % of the waves' time is
-// waiting, with two workgroups a CU (240 to 256 registers a thread).
+// their 815 MB need 131 us at a copy's 6.2 TB/s.  The call takes 311 to 330 us:
+// about 110 the state pass, 10 the chain, 200 the output pass.  Without its
+// products the output pass takes 134 us (183 with the stores), without its loads
+// 182.  By counters its SIMDs are busy 46 % with vector and 27 % with matrix
+// instructions (operands are split and decayed on the way), and 27 % of the
+// waves' time is waiting, with two workgroups a CU (240 to 256 registers a
+// thread).
 // Measured and not kept: eight waves a workgroup (276 against 258 us, the pass
 // alone), half a head's columns a workgroup (457 the call), nontemporal output
 // stores (80 more), placement of a head's blocks on one XCD (no change).
 // The gradient, 4 x 2048 tokens x 32 heads (206 GFLOP; 497 MB, of which its
-// passes read most more than once, 1.4 GB in all): 375 to 390 us.
+// passes read most more than once, 1.4 GB in all): 363 to 375 us.
 #include <type_traits>
 
 #include "launch.h"
