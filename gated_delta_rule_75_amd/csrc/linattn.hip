@@ -1281,8 +1281,9 @@ __device__ __forceinline__ void share_sums(const LinArgs& a, const LinTail& x) {
 }
 
 // The gradient's last run, for dv, and beside it what waits for the runs before
-// only: a launch each for these cost the ragged fp32 gradient of 1531 tokens
-// 59 us in all, and dv's workgroups leave CUs half empty.
+// only (dv's workgroups leave CUs half empty).  1531 ragged tokens of 8 heads in
+// fp32: the gradient 49 us, 59 with a launch each for these; 8192 tokens x 32
+// heads on 8 key heads 390 and 420.
 template <typename T, int DK, int DV>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void linattn_last_kernel(LinArgs a, LinTail x) {
     if (blockIdx.y == 0) linattn_body<T, DK, DV, kOut>(a);
