@@ -166,6 +166,7 @@ struct LinArgs {
     const int32_t* cu_seqlens;
     int64_t L;                  // tokens of a block, a multiple of 64
     int nblocks;                // a bound on the blocks of all sequences
+    int32_t* first;             // [num_seqs + 1] or NULL: the sequences' first blocks
     const float* g;
     bool g_per_token;           // [T, H], else [H]
     LinRows q, k, v, x;

@@ -79,7 +79,13 @@ struct Parts {
     }
 };
 
-struct FwdLayout { size_t states, decays, total; int64_t L, nblocks; };
+// Above this many sequences, cut ones get a table of their first blocks: a
+// workgroup finds its block by counting otherwise, 64 sequences at a step, which
+// with N sequences is N^2 / 64 steps in all.
+constexpr int kPlanSeqs = 256;
+size_t plan_bytes(int num_seqs) { return num_seqs > kPlanSeqs ? ((size_t)num_seqs + 1) * 4 : 0; }
+
+struct FwdLayout { size_t states, decays, plan, total; int64_t L, nblocks; };
 FwdLayout fwd_layout(int H, int dk, int dv, int num_seqs, int64_t T) {
     FwdLayout l{};
     l.L = fwd_block(H, T);
@@ -89,12 +95,13 @@ FwdLayout fwd_layout(int H, int dk, int dv, int num_seqs, int64_t T) {
     if (cut) {
         l.states = p.take((size_t)l.nblocks * H * dk * dv * 4);
         l.decays = p.take((size_t)l.nblocks * H * 4);
+        l.plan = p.take(plan_bytes(num_seqs));
     }
     l.total = p.at;
     return l;
 }
 
-struct BwdLayout { size_t states, decays, rstates, rdecays, s_end, sums_a, sums_b, dg, share, total; int64_t L, nblocks; };
+struct BwdLayout { size_t states, decays, rstates, rdecays, s_end, sums_a, sums_b, dg, share, plan, total; int64_t L, nblocks; };
 BwdLayout bwd_layout(int H, int Hk, int dk, int dv, int num_seqs, int64_t T) {
     BwdLayout l{};
     l.L = bwd_block(H, T);
@@ -110,6 +117,7 @@ BwdLayout bwd_layout(int H, int Hk, int dk, int dv, int num_seqs, int64_t T) {
     l.sums_b = p.take(th);
     l.dg = p.take(th);
     l.share = p.take(Hk < H ? 2 * th * dk : 0);
+    l.plan = p.take(l.L < T ? plan_bytes(num_seqs) : 0);
     l.total = p.at;
     return l;
 }
@@ -168,6 +176,7 @@ kda_status kda_linattn_fwd(kda_dtype dt, int H, int Hk, int dk, int dv, float sc
     if (l.total) {
         c.states = part<float>(workspace, l.states);
         c.decays = part<float>(workspace, l.decays);
+        if (num_seqs > kPlanSeqs) c.args.first = part<int32_t>(workspace, l.plan);
     }
     return launched([&] { return kda::launch_linattn_fwd(c); });
 }
@@ -230,6 +239,7 @@ kda_status kda_linattn_bwd(kda_dtype dt, int H, int Hk, int dk, int dv, float sc
     c.sums_b = part<float>(workspace, l.sums_b);
     c.dg_tokens = part<float>(workspace, l.dg);
     c.share_buf = part<void>(workspace, l.share);
+    if (num_seqs > kPlanSeqs && l.L < T_total) c.args.first = part<int32_t>(workspace, l.plan);
     return launched([&] { return kda::launch_linattn_bwd(c); });
 }
 

@@ -191,8 +191,10 @@ __device__ __forceinline__ int64_t seq_at(const LinArgs& a, int n) {
     return x < 0 ? 0 : x > a.T_total ? a.T_total : x;
 }
 
-__device__ __forceinline__ int blocks_of(int64_t len, int64_t L) {
-    return len <= L ? 1 : (int)((len + L - 1) / L);
+// At most the bound on all blocks: offsets out of order stay inside the arrays.
+__device__ __forceinline__ int blocks_of(const LinArgs& a, int64_t len) {
+    const int64_t nb = len <= a.L ? 1 : (len + a.L - 1) / a.L;
+    return nb < a.nblocks ? (int)nb : a.nblocks;
 }
 
 __device__ __forceinline__ int wave_incl_sum(int x, int lane) {
@@ -204,61 +206,126 @@ __device__ __forceinline__ int wave_incl_sum(int x, int lane) {
     return x;
 }
 
-// Every wave finds the block itself, 64 sequences at a time.
+__device__ __forceinline__ int64_t shfl_i64(int64_t x, int src) {
+    return ((int64_t)__shfl((int)(x >> 32), src) << 32) | (uint32_t)__shfl((int)x, src);
+}
+
+// Every wave finds the block itself.  Uncut sequences are their blocks.  Else by
+// the sequences' first blocks, a 64th of what is left at a step; for up to
+// kPlanSeqs sequences, which have no such table, by counting, 64 at a time.
 __device__ __forceinline__ Block find_block(const LinArgs& a, int b) {
     const int lane = threadIdx.x & 63;
     Block r;
     r.n = -1;
-    int before = 0;
-    for (int n0 = 0; n0 < a.num_seqs; n0 += kWave) {
-        const int n = n0 + lane;
-        int64_t s = 0, e = 0;
-        int nb = 0;
-        if (n < a.num_seqs) {
-            s = seq_at(a, n);
-            e = seq_at(a, n + 1);
-            if (e < s) e = s;
-            nb = blocks_of(e - s, a.L);
+    r.j = 0;
+    r.nb = 1;
+    int64_t s = 0, e = 0;
+    if (a.L >= a.T_total) {
+        if (b < a.num_seqs) r.n = b;
+    } else if (a.first) {
+        if (b < a.first[a.num_seqs]) {
+            int lo = 0, span = a.num_seqs;   // it is one of [lo, lo + span)
+            while (span > 1) {
+                const int step = (span + kWave - 1) / kWave, at = lane * step;
+                const int k = __popcll(__ballot(at < span && a.first[lo + (at < span ? at : 0)] <= b)) - 1;
+                lo += k * step;
+                span = span - k * step < step ? span - k * step : step;
+            }
+            r.n = lo;
+            r.j = b - a.first[lo];
+            r.nb = a.first[lo + 1] - a.first[lo];
         }
-        const int incl = wave_incl_sum(nb, lane);
-        const int total = __shfl(incl, kWave - 1);
-        if (b < before + total) {
-            const uint64_t m = __ballot(before + incl > b);
-            const int src = __ffsll((unsigned long long)m) - 1;
-            r.n = n0 + src;
-            r.nb = __shfl(nb, src);
-            r.j = b - before - (__shfl(incl, src) - r.nb);
-            const int64_t sb = ((int64_t)__shfl((int)(s >> 32), src) << 32) | (uint32_t)__shfl((int)s, src);
-            const int64_t eb = ((int64_t)__shfl((int)(e >> 32), src) << 32) | (uint32_t)__shfl((int)e, src);
-            r.begin = sb;
-            r.start = sb + (int64_t)r.j * a.L;
-            const int64_t left = eb - r.start;
-            r.cnt = (int)(left < a.L ? left : a.L);
-            break;
+    } else {
+        int before = 0;
+        for (int n0 = 0; n0 < a.num_seqs; n0 += kWave) {
+            const int n = n0 + lane;
+            int nb = 0;
+            if (n < a.num_seqs) {
+                s = seq_at(a, n);
+                e = seq_at(a, n + 1);
+                nb = blocks_of(a, e - s);
+            }
+            const int incl = wave_incl_sum(nb, lane);
+            const int total = __shfl(incl, kWave - 1);
+            if (b < before + total) {
+                const uint64_t m = __ballot(before + incl > b);
+                const int src = __ffsll((unsigned long long)m) - 1;
+                r.n = n0 + src;
+                r.nb = __shfl(nb, src);
+                r.j = b - before - (__shfl(incl, src) - r.nb);
+                s = shfl_i64(s, src);
+                e = shfl_i64(e, src);
+                break;
+            }
+            before += total;
         }
-        before += total;
     }
     r.n = uni(r.n);
     if (r.n < 0) return r;
     r.j = uni(r.j);
     r.nb = uni(r.nb);
-    r.cnt = uni(r.cnt);
-    r.begin = uni64(r.begin);
-    r.start = uni64(r.start);
+    if (a.L >= a.T_total || a.first) {
+        s = seq_at(a, r.n);
+        e = seq_at(a, r.n + 1);
+    }
+    r.begin = uni64(s);
+    r.start = r.begin + (int64_t)r.j * a.L;
+    const int64_t left = uni64(e) - r.start;
+    r.cnt = uni((int)(left < 0 ? 0 : left < a.L ? left : a.L));
     return r;
 }
 
 // Index of sequence n's first block.
 __device__ __forceinline__ int first_block(const LinArgs& a, int n) {
+    if (a.L >= a.T_total) return n;
+    if (a.first) return a.first[n];
     const int lane = threadIdx.x & 63;
     int sum = 0;
-    for (int m = lane; m < n; m += kWave) {
-        const int64_t len = seq_at(a, m + 1) - seq_at(a, m);
-        sum += blocks_of(len, a.L);
-    }
+    for (int m = lane; m < n; m += kWave) sum += blocks_of(a, seq_at(a, m + 1) - seq_at(a, m));
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
     return sum;
+}
+
+// The sequences' first blocks, and behind them their number, none above the
+// bound: one workgroup, 4096 sequences a step.
+__global__ __launch_bounds__(1024) void linattn_plan_kernel(LinArgs a) {
+    __shared__ int part[16];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    int before = 0;   // of the steps done
+    for (int64_t n0 = 0; n0 < a.num_seqs; n0 += 4096) {
+        int nb[4], sum = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t n = n0 + 4 * tid + i;
+            nb[i] = n < a.num_seqs ? blocks_of(a, seq_at(a, (int)n + 1) - seq_at(a, (int)n)) : 0;
+            sum += nb[i];
+        }
+        // more than the bound only where the offsets are out of order: held there
+        // (it is below 2^22, so no sum of these overflows)
+        sum = sum < a.nblocks ? sum : a.nblocks;
+        int incl = sum;
+#pragma unroll
+        for (int d = 1; d < kWave; d <<= 1) {
+            const int y = __shfl_up(incl, d);
+            if (lane >= d) incl += y;
+            incl = incl < a.nblocks ? incl : a.nblocks;
+        }
+        if (lane == kWave - 1) part[wave] = incl;
+        __syncthreads();
+        int at = before + (incl - sum);
+        for (int w = 0; w < wave; ++w) at += part[w];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t n = n0 + 4 * tid + i;
+            if (n < a.num_seqs) a.first[n] = at < a.nblocks ? at : a.nblocks;
+            at += nb[i];
+        }
+        for (int w = 0; w < 16; ++w) before += part[w];
+        before = before < a.nblocks ? before : a.nblocks;
+        __syncthreads();
+    }
+    if (tid == 0) a.first[a.num_seqs] = before;
 }
 
 // Decay tables of a chunk, one token a lane.
@@ -1119,7 +1186,7 @@ __global__ __launch_bounds__(256) void linattn_carry_kernel(LinArgs a, LinCarry 
     const LinCarry c = blockIdx.z ? c1 : c0;
     const int n = blockIdx.x / a.H, h = blockIdx.x % a.H;
     const int b0 = first_block(a, n);
-    int nb = blocks_of(seq_at(a, n + 1) - seq_at(a, n), a.L);
+    int nb = blocks_of(a, seq_at(a, n + 1) - seq_at(a, n));
     if (nb > a.nblocks - b0) nb = a.nblocks - b0;   // offsets out of order: stay inside the arrays
     const int64_t e = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4, size = (int64_t)gridDim.y * 1024;
     f32x4_t s = {0.f, 0.f, 0.f, 0.f};
@@ -1336,10 +1403,18 @@ hipError_t launch_core(const LinArgs* a, int n, int dtype, int dk, int dv, int m
     return dtype == 0 ? launch_k<__bf16>(a, n, dk, dv, mode) : launch_k<float>(a, n, dk, dv, mode);
 }
 
+hipError_t launch_plan(const LinArgs& a) {
+    if (!a.first) return hipSuccess;
+    hipLaunchKernelGGL(linattn_plan_kernel, dim3(1), dim3(1024), 0, (hipStream_t)a.stream, a);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_linattn_fwd(const LinCall& c) {
     LinArgs a = c.args;
+    const hipError_t planned = launch_plan(a);
+    if (planned != hipSuccess) return planned;
     a.q = c.q;
     a.k = c.k;
     a.v = c.v;
@@ -1369,7 +1444,8 @@ hipError_t launch_linattn_fwd(const LinCall& c) {
 hipError_t launch_linattn_bwd(const LinCall& c) {
     LinArgs a = c.args;
     a.p_scale = c.scale;
-    hipError_t e;
+    hipError_t e = launch_plan(a);
+    if (e != hipSuccess) return e;
     // the blocks' own states, of the recurrence and of its gradient
     LinArgs s[2] = {a, a};
     s[0].k = c.k;

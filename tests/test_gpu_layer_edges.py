@@ -61,3 +61,56 @@ def test_precision_does_not_depend_on_the_cut(kda, dk, dv):
             tail = (lens[n] - 1) % 64 + 1
             only_rounded(f"{name} y of the last {tail} rows", y[end - tail:end, heads], yr[end - tail:end])
         only_rounded(f"{name} y, heads alone", fwd(kda, sub)[0], yr)
+
+
+def ones_and_a_long(kda, N, long, seed):
+    """N - 2 sequences of one token around one of `long` tokens and an empty one,
+    one head: no state enters, so a token's output is scale (q.k) v."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    at = N // 3
+    lens = torch.ones(N, dtype=torch.int64)
+    lens[at], lens[at + 1] = long, 0
+    cu = torch.zeros(N + 1, dtype=torch.int32)
+    cu[1:] = lens.cumsum(0)
+    T = int(cu[-1])
+    x = {n: torch.randn(T, 1, 64, generator=gen, device="cuda") for n in ("q", "k", "v", "dy")}
+    x["g"] = -torch.rand(T, 1, generator=gen, device="cuda")
+    return x, cu.cuda(), int(cu[at])
+
+
+@pytest.mark.parametrize("N", [257, 4095, 4096, 4097, 70000])
+def test_sequences_by_the_thousand(kda, N):
+    """Cut into blocks, with the block of each workgroup found by the table of
+    first blocks: sizes around a step of the scan and of the search."""
+    x, cu, at = ones_and_a_long(kda, N, 500, seed=N)
+    y, _ = kda.linattn_fwd(x["q"], x["k"], x["v"], x["g"], cu_seqlens=cu, output_final_state=False, scale=0.125)
+    dq, dk, dv, dg, _ = kda.linattn_bwd(x["q"], x["k"], x["v"], x["g"], x["dy"], cu_seqlens=cu, scale=0.125)
+    q, k, v, dy = (x[n].double() for n in ("q", "k", "v", "dy"))
+    dot = lambda a, b: 0.125 * (a * b).sum(-1, keepdim=True)  # noqa: E731
+    mid = slice(at, at + 500)
+    sub = {n: x[n][mid].cpu() for n in x}
+    want = [dot(q, k) * v, dot(dy, v) * k, dot(dy, v) * q, dot(q, k) * dy, torch.zeros_like(x["g"]).double()]
+    args = (sub["q"], sub["k"], sub["v"], sub["g"], [0, 500])
+    inner = (ref.linattn(*args, None, 0.125)[0],) + ref.linattn_grad(*args, sub["dy"], None, None, 0.125)[:4]
+    for n, a, b, c in zip(("y", "dq", "dk", "dv", "dg"), (y, dq, dk, dv, dg), want, inner):
+        b[mid] = c.cuda()
+        ref.check(f"{N} sequences {n}", a, b.cpu(), ref.TOL_DG if n == "dg" else ref.TOL["f32"])
+
+
+def test_time_grows_with_the_sequences_not_their_square(kda):
+    """16 times the sequences of one token: 16 times the work.  A search through
+    all sequences in every workgroup would be 256 times as much."""
+    ms = []
+    for N in (1 << 14, 1 << 18):
+        x, cu, _ = ones_and_a_long(kda, N, 500, seed=1)
+        best = float("inf")
+        for _ in range(4):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            kda.linattn_fwd(x["q"], x["k"], x["v"], x["g"], cu_seqlens=cu, output_final_state=False)
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        ms.append(best)
+    print(f"[layer] 2^14 and 2^18 sequences: {ms[0]:.3f} and {ms[1]:.3f} ms", flush=True)
+    assert ms[1] <= 64 * ms[0]
