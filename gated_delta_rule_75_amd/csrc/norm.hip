@@ -37,11 +37,11 @@ struct Cols {
     __device__ __forceinline__ int left(int j) const { return TAIL ? D - at(j) : VEC; }   // elements of the run, >= VEC: all
 };
 
+// y may be x or z: a thread reads all of its elements before it writes them.
 template <typename T, int VEC, int LANES, int NV, bool TAIL>
 __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_fwd_kernel(
-    int64_t rows, int H, int D, float eps, int rms, const T* __restrict__ x, const float* __restrict__ w,
-    const float* __restrict__ b, const T* __restrict__ z, T* __restrict__ y, float* __restrict__ mean,
-    float* __restrict__ rstd) {
+    int64_t rows, int H, int D, float eps, int rms, const T* x, const float* __restrict__ w,
+    const float* __restrict__ b, const T* z, T* y, float* __restrict__ mean, float* __restrict__ rstd) {
     constexpr int RPB = LANES < 256 ? 256 / LANES : 1;   // rows of a workgroup
     __shared__ float part[2][LANES > 64 ? LANES / 64 : 1];
     const int64_t row = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * RPB + threadIdx.x / LANES;
@@ -49,11 +49,13 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_fwd_kernel(
     const Cols<VEC, LANES, NV, TAIL> c{(int)(threadIdx.x % LANES), D};
     const int64_t base = row * D, wb = (int64_t)(row % H) * D;
     float v[NV][VEC];
+    typename VecOf<T, VEC>::type zv[NV];
     float s = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         if (c.in(j)) {
             load_run<T, VEC>(x + base + c.at(j), c.left(j), v[j]);
+            if (z) zv[j] = load_raw<T, VEC>(z + base + c.at(j), c.left(j));
         } else {
 #pragma unroll
             for (int i = 0; i < VEC; ++i) v[j][i] = 0.f;
@@ -86,10 +88,8 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_fwd_kernel(
             for (int i = 0; i < VEC; ++i) o[i] += bv[i];
         }
         if (z) {
-            float zv[VEC];
-            load_run<T, VEC>(z + base + c.at(j), c.left(j), zv);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) o[i] *= sigmoid(zv[i]);
+            for (int i = 0; i < VEC; ++i) o[i] *= sigmoid(to_f32((T)zv[j][i]));
         }
         store_run<T, VEC>(y + base + c.at(j), c.left(j), o);
     }

@@ -114,3 +114,20 @@ def test_time_grows_with_the_sequences_not_their_square(kda):
         ms.append(best)
     print(f"[layer] 2^14 and 2^18 sequences: {ms[0]:.3f} and {ms[1]:.3f} ms", flush=True)
     assert ms[1] <= 64 * ms[0]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D", [64, 257, 1000, 2047, 4100, 8192, 16384])
+def test_norm_over_its_input_or_gate_at_every_width(kda, D, dtype):
+    """Lane groups of every size, one to four runs a thread; x and z in one buffer too."""
+    gen = torch.Generator(device="cuda").manual_seed(D)
+    x, z = (torch.randn(37, 3, D, generator=gen, device="cuda").to(dtype) for _ in range(2))
+    w, b = (torch.randn(3, D, generator=gen, device="cuda") for _ in range(2))
+    for gate in (z, x):
+        want, mean, rstd = kda.norm_fwd(x, w, b, gate)
+        for k in range(2):
+            t = [x.clone(), gate.clone()]
+            if gate is x:
+                t[1] = t[0]
+            y, m, r = kda.norm_fwd(t[0], w, b, t[1], y=t[k])
+            assert torch.equal(y, want) and torch.equal(m, mean) and torch.equal(r, rstd), (gate is x, k)
