@@ -27,6 +27,23 @@ namespace kda {
 
 namespace {
 
+// sigmoid(z), and sigmoid(-z), which is 1 - sigmoid(z) without cancellation.  fp32:
+// from the accurate exponential of -|z|, which does not overflow.  bf16: the fast
+// exponential (off by up to 5e-6 of the value at |z| = 80) is far below the
+// output's rounding.
+template <typename T>
+__device__ __forceinline__ float gate(float z) {
+    if constexpr (sizeof(T) == 2) return sigmoid(z);
+    const float t = expf(-fabsf(z)), r = __builtin_amdgcn_rcpf(1.f + t);
+    return z < 0.f ? t * r : r;
+}
+template <typename T>
+__device__ __forceinline__ void gate(float z, float& s, float& c) {
+    const float t = sizeof(T) == 2 ? __expf(-fabsf(z)) : expf(-fabsf(z)), r = __builtin_amdgcn_rcpf(1.f + t);
+    s = z < 0.f ? t * r : r;
+    c = z < 0.f ? r : t * r;
+}
+
 // A thread's NV runs of VEC columns of a row of D: columns (j LANES + lane) VEC.
 // TAIL: the last run may be cut.
 template <int VEC, int LANES, int NV, bool TAIL>
@@ -89,7 +106,7 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_fwd_kernel(
         }
         if (z) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) o[i] *= sigmoid(to_f32((T)zv[j][i]));
+            for (int i = 0; i < VEC; ++i) o[i] *= gate<T>(to_f32((T)zv[j][i]));
         }
         store_run<T, VEC>(y + base + c.at(j), c.left(j), o);
     }
@@ -159,9 +176,10 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_bwd_kernel(
                 float o[VEC];
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
-                    const float g = to_f32((T)zn[j][i]), s = sigmoid(g), ds = d[j][i] * s;
-                    o[i] = ds * (h[j][i] * wv[j][i] + bv[j][i]) * sigmoid(-g);   // 1 - s without cancellation
-                    d[j][i] = ds;
+                    float s, rest;
+                    gate<T>(to_f32((T)zn[j][i]), s, rest);
+                    d[j][i] *= s;
+                    o[i] = d[j][i] * (h[j][i] * wv[j][i] + bv[j][i]) * rest;
                 }
                 store_run<T, VEC>(dz + base + c.at(j), c.left(j), o);
             }

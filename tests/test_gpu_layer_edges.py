@@ -131,3 +131,33 @@ def test_norm_over_its_input_or_gate_at_every_width(kda, D, dtype):
                 t[1] = t[0]
             y, m, r = kda.norm_fwd(t[0], w, b, t[1], y=t[k])
             assert torch.equal(y, want) and torch.equal(m, mean) and torch.equal(r, rstd), (gate is x, k)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [128, 1000])
+def test_gate_far_from_zero(kda, D, dtype):
+    """z from -100 to 100, each value of y and dz for itself: a product of a few
+    fp32 factors, each off by a few 2^-24 (rstd's sum of up to 1000 squares by
+    less than 8), so 32 2^-24 = 2^-19 in all, and for bf16 the output's rounding
+    of 2^-8 and the fast exponential's 100 2^-24.  Below the least normal value,
+    2^-126, steps of a subnormal output and factor take over."""
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+    tol = {"bf16": 2.0 ** -8 + 2.0 ** -16, "f32": 2.0 ** -19}[dtype]
+    gen = torch.Generator().manual_seed(D)
+    x, dy = (torch.randn(64, 1, D, generator=gen).to(dt) for _ in range(2))
+    z = (200 * torch.rand(64, 1, D, generator=gen) - 100).to(dt)
+    z[0, 0, :8] = torch.tensor([0.0, -0.0, 88.0, -88.0, float("inf"), -float("inf"), 1e-8, -1e-8])
+    w = 1 + 0.2 * torch.randn(1, D, generator=gen)
+    c = [t.cuda() for t in (x, w, z, dy)]
+    y, _, rstd = kda.norm_fwd(c[0], c[1], z=c[2], kind="rms")
+    dx, dw, _, dz = kda.norm_bwd(c[3], c[0], c[1], None, rstd, z=c[2], kind="rms")
+    s, r = torch.sigmoid(z.double()), torch.sigmoid(-z.double())
+    n, _, _ = ref.norm(x, w, None, None, 1e-5, "rms")
+    step = 2.0 ** -126 if dtype == "bf16" else 2.0 ** -147
+    for name, got, want, factor in (("y", y, n * s, n), ("dz", dz, dy.double() * n * s * r, dy.double() * n)):
+        far = (got.cpu().double() - want).abs() - step * (1 + factor.abs())
+        print(f"[layer] gate {dtype} {name}: {float((far / want.abs().clamp_min(2.0 ** -126)).max()):.2e}", flush=True)
+        assert bool((far <= tol * want.abs()).all()), name
+    xr, wr, _, _ = ref.norm_grad(x, w, None, z, 1e-5, "rms", dy)
+    ref.check(f"gate {dtype} dx", dx, xr, 2.0 ** -8 if dtype == "bf16" else 2e-6)
+    ref.check(f"gate {dtype} dw", dw, wr, 2e-6)
