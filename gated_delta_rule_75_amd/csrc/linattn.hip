@@ -443,14 +443,16 @@ __device__ __forceinline__ float pin(float x) {
 __device__ __forceinline__ unsigned lds_addr(const void* p) {
     return (unsigned)(uintptr_t)(__attribute__((address_space(3))) const char*)p;
 }
+// (m0 is no register that a statement can name as changed: it is put back.)
 __device__ __forceinline__ void copy16(unsigned lds, const void* base, unsigned off) {
-    // (nothing the compiler does here keeps a value in m0)
-    asm volatile("s_nop 4\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                 :: "s"(uni(lds)), "v"(off), "s"(uni64(reinterpret_cast<int64_t>(base))) : "memory");
+    unsigned old;
+    asm volatile("s_mov_b32 %0, m0\n\ts_nop 4\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3\n\ts_mov_b32 m0, %0"
+                 : "=&s"(old) : "s"(uni(lds)), "v"(off), "s"(uni64(reinterpret_cast<int64_t>(base))) : "memory");
 }
 __device__ __forceinline__ void copy4(unsigned lds, const void* addr) {
-    asm volatile("s_nop 4\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
-                 :: "s"(uni(lds)), "v"(addr) : "memory");
+    unsigned old;
+    asm volatile("s_mov_b32 %0, m0\n\ts_nop 4\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %2, off\n\ts_mov_b32 m0, %0"
+                 : "=&s"(old) : "s"(uni(lds)), "v"(addr) : "memory");
 }
 
 // The copy of a chunk's rows into a tile by the workgroup's four waves.  A
