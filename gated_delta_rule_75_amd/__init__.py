@@ -39,8 +39,8 @@ SYMBOLS = ("kda_version", "kda_status_string", "kda_chunk_fwd_workspace_size",
            "kda_kcp_workspace_size", "kda_kcp_workspace_min", "kda_kcp_scan",
            "kda_decode_step", "kda_decode_replay", "kda_chunk_fwd_fused", "kda_decode_step_fused",
            "kda_chunk_fwd_noalloc", "kda_noalloc_scratch_bytes",
-           "kda_linattn_fwd", "kda_linattn_fwd_workspace_size", "kda_linattn_bwd",
-           "kda_linattn_bwd_workspace_size", "kda_linattn_decode_step", "kda_rope",
+           "kda_linattn_fwd", "kda_linattn_fwd_padded", "kda_linattn_fwd_workspace_size", "kda_linattn_bwd",
+           "kda_linattn_bwd_padded", "kda_linattn_bwd_workspace_size", "kda_linattn_decode_step", "kda_rope",
            "kda_rope_frequencies", "kda_norm_fwd", "kda_norm_bwd", "kda_norm_bwd_workspace_size")
 
 
@@ -99,10 +99,12 @@ def lib() -> ctypes.CDLL:
     L.kda_decode_replay.argtypes = [i, i, i, i, i, i, f, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     L.kda_decode_replay.restype = i
     lin = [i, i, i, i, i, f, i, i64, vp, vp, i64, vp, i64, vp, i64, vp, i]
-    L.kda_linattn_fwd.argtypes = lin + [vp, vp, vp, vp, sz, vp]
-    L.kda_linattn_fwd.restype = i
-    L.kda_linattn_bwd.argtypes = lin + [vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
-    L.kda_linattn_bwd.restype = i
+    for fn in (L.kda_linattn_fwd, L.kda_linattn_fwd_padded):
+        fn.argtypes = lin + [vp, vp, vp, vp, sz, vp]
+        fn.restype = i
+    for fn in (L.kda_linattn_bwd, L.kda_linattn_bwd_padded):
+        fn.argtypes = lin + [vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        fn.restype = i
     for fn in (L.kda_linattn_fwd_workspace_size, L.kda_linattn_bwd_workspace_size):
         fn.argtypes = [i, i, i, i, i, i, i64]
         fn.restype = sz

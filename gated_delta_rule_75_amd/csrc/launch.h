@@ -181,6 +181,7 @@ struct LinArgs {
     float* final;
     void* out;                  // [T, H, D]
     bool out_f32;
+    bool clear;                 // outputs' rows of no sequence become zeros (else they stay)
     float* sums;                // [H, T]
     void* stream;
 };

@@ -126,21 +126,12 @@ template <typename P> P* part(void* ws, size_t at) { return reinterpret_cast<P*>
 
 kda::LinRows rows(const void* p, int64_t stride, int share) { return kda::LinRows{p, stride, share}; }
 
-}  // namespace
-
-extern "C" {
-
-size_t kda_linattn_fwd_workspace_size(kda_dtype dt, int H, int Hk, int dk, int dv, int num_seqs, int64_t T_total) {
-    if (!sizes_ok(dt, H, Hk, dk, dv, num_seqs, T_total)) return 0;
-    const size_t n = fwd_layout(H, dk, dv, num_seqs, T_total).total;
-    return n ? n : 256;
-}
-
-kda_status kda_linattn_fwd(kda_dtype dt, int H, int Hk, int dk, int dv, float scale, int num_seqs, int64_t T_total,
-                           const int32_t* cu_seqlens, const void* q, int64_t q_stride, const void* k,
-                           int64_t k_stride, const void* v, int64_t v_stride, const float* g, int g_per_token,
-                           const float* initial_state, float* final_state, void* y, void* workspace,
-                           size_t workspace_bytes, void* stream) {
+// clear: rows of no sequence of the outputs become zeros.
+kda_status linattn_fwd(bool clear, kda_dtype dt, int H, int Hk, int dk, int dv, float scale, int num_seqs,
+                       int64_t T_total, const int32_t* cu_seqlens, const void* q, int64_t q_stride, const void* k,
+                       int64_t k_stride, const void* v, int64_t v_stride, const float* g, int g_per_token,
+                       const float* initial_state, float* final_state, void* y, void* workspace,
+                       size_t workspace_bytes, void* stream) {
     if (!dtype_ok(dt)) return KDA_ERR_INVALID_ARGUMENT;
     if (!cu_seqlens && num_seqs != 1) return KDA_ERR_INVALID_ARGUMENT;
     if (H > 0 && Hk > 0 && (!head_ok(dk) || !head_ok(dv))) return KDA_ERR_UNSUPPORTED;
@@ -162,6 +153,7 @@ kda_status kda_linattn_fwd(kda_dtype dt, int H, int Hk, int dk, int dv, float sc
     c.args.nblocks = (int)l.nblocks;
     c.args.g = g;
     c.args.g_per_token = g_per_token != 0;
+    c.args.clear = clear;
     c.args.stream = stream;
     c.dtype = (int)dt;
     c.dk = dk;
@@ -181,17 +173,12 @@ kda_status kda_linattn_fwd(kda_dtype dt, int H, int Hk, int dk, int dv, float sc
     return launched([&] { return kda::launch_linattn_fwd(c); });
 }
 
-size_t kda_linattn_bwd_workspace_size(kda_dtype dt, int H, int Hk, int dk, int dv, int num_seqs, int64_t T_total) {
-    if (!sizes_ok(dt, H, Hk, dk, dv, num_seqs, T_total)) return 0;
-    return bwd_layout(H, Hk, dk, dv, num_seqs, T_total).total;
-}
-
-kda_status kda_linattn_bwd(kda_dtype dt, int H, int Hk, int dk, int dv, float scale, int num_seqs, int64_t T_total,
-                           const int32_t* cu_seqlens, const void* q, int64_t q_stride, const void* k,
-                           int64_t k_stride, const void* v, int64_t v_stride, const float* g, int g_per_token,
-                           const float* initial_state, const void* dy, const float* d_final_state, void* dq,
-                           void* dk_out, void* dv_out, float* dg, float* d_initial_state, void* workspace,
-                           size_t workspace_bytes, void* stream) {
+kda_status linattn_bwd(bool clear, kda_dtype dt, int H, int Hk, int dk, int dv, float scale, int num_seqs,
+                       int64_t T_total, const int32_t* cu_seqlens, const void* q, int64_t q_stride, const void* k,
+                       int64_t k_stride, const void* v, int64_t v_stride, const float* g, int g_per_token,
+                       const float* initial_state, const void* dy, const float* d_final_state, void* dq,
+                       void* dk_out, void* dv_out, float* dg, float* d_initial_state, void* workspace,
+                       size_t workspace_bytes, void* stream) {
     if (!dtype_ok(dt)) return KDA_ERR_INVALID_ARGUMENT;
     if (!cu_seqlens && num_seqs != 1) return KDA_ERR_INVALID_ARGUMENT;
     if (H > 0 && Hk > 0 && (!head_ok(dk) || !head_ok(dv))) return KDA_ERR_UNSUPPORTED;
@@ -214,6 +201,7 @@ kda_status kda_linattn_bwd(kda_dtype dt, int H, int Hk, int dk, int dv, float sc
     c.args.nblocks = (int)l.nblocks;
     c.args.g = g;
     c.args.g_per_token = g_per_token != 0;
+    c.args.clear = clear;
     c.args.stream = stream;
     c.dtype = (int)dt;
     c.dk = dk;
@@ -241,6 +229,63 @@ kda_status kda_linattn_bwd(kda_dtype dt, int H, int Hk, int dk, int dv, float sc
     c.share_buf = part<void>(workspace, l.share);
     if (num_seqs > kPlanSeqs && l.L < T_total) c.args.first = part<int32_t>(workspace, l.plan);
     return launched([&] { return kda::launch_linattn_bwd(c); });
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kda_linattn_fwd_workspace_size(kda_dtype dt, int H, int Hk, int dk, int dv, int num_seqs, int64_t T_total) {
+    if (!sizes_ok(dt, H, Hk, dk, dv, num_seqs, T_total)) return 0;
+    const size_t n = fwd_layout(H, dk, dv, num_seqs, T_total).total;
+    return n ? n : 256;
+}
+
+kda_status kda_linattn_fwd(kda_dtype dt, int H, int Hk, int dk, int dv, float scale, int num_seqs, int64_t T_total,
+                           const int32_t* cu_seqlens, const void* q, int64_t q_stride, const void* k,
+                           int64_t k_stride, const void* v, int64_t v_stride, const float* g, int g_per_token,
+                           const float* initial_state, float* final_state, void* y, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+    return linattn_fwd(false, dt, H, Hk, dk, dv, scale, num_seqs, T_total, cu_seqlens, q, q_stride, k,
+                       k_stride, v, v_stride, g, g_per_token, initial_state, final_state, y, workspace,
+                       workspace_bytes, stream);
+}
+
+kda_status kda_linattn_fwd_padded(kda_dtype dt, int H, int Hk, int dk, int dv, float scale, int num_seqs,
+                                  int64_t T_total, const int32_t* cu_seqlens, const void* q, int64_t q_stride,
+                                  const void* k, int64_t k_stride, const void* v, int64_t v_stride, const float* g, int g_per_token,
+                                  const float* initial_state, float* final_state, void* y, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+    return linattn_fwd(true, dt, H, Hk, dk, dv, scale, num_seqs, T_total, cu_seqlens, q, q_stride, k,
+                       k_stride, v, v_stride, g, g_per_token, initial_state, final_state, y, workspace,
+                       workspace_bytes, stream);
+}
+
+size_t kda_linattn_bwd_workspace_size(kda_dtype dt, int H, int Hk, int dk, int dv, int num_seqs, int64_t T_total) {
+    if (!sizes_ok(dt, H, Hk, dk, dv, num_seqs, T_total)) return 0;
+    return bwd_layout(H, Hk, dk, dv, num_seqs, T_total).total;
+}
+
+kda_status kda_linattn_bwd(kda_dtype dt, int H, int Hk, int dk, int dv, float scale, int num_seqs, int64_t T_total,
+                           const int32_t* cu_seqlens, const void* q, int64_t q_stride, const void* k,
+                           int64_t k_stride, const void* v, int64_t v_stride, const float* g, int g_per_token,
+                           const float* initial_state, const void* dy, const float* d_final_state, void* dq,
+                           void* dk_out, void* dv_out, float* dg, float* d_initial_state, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+    return linattn_bwd(false, dt, H, Hk, dk, dv, scale, num_seqs, T_total, cu_seqlens, q, q_stride, k,
+                       k_stride, v, v_stride, g, g_per_token, initial_state, dy, d_final_state, dq, dk_out,
+                       dv_out, dg, d_initial_state, workspace, workspace_bytes, stream);
+}
+
+kda_status kda_linattn_bwd_padded(kda_dtype dt, int H, int Hk, int dk, int dv, float scale, int num_seqs,
+                                  int64_t T_total, const int32_t* cu_seqlens, const void* q, int64_t q_stride,
+                                  const void* k, int64_t k_stride, const void* v, int64_t v_stride, const float* g, int g_per_token,
+                                  const float* initial_state, const void* dy, const float* d_final_state, void* dq,
+                                  void* dk_out, void* dv_out, float* dg, float* d_initial_state, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+    return linattn_bwd(true, dt, H, Hk, dk, dv, scale, num_seqs, T_total, cu_seqlens, q, q_stride, k,
+                       k_stride, v, v_stride, g, g_per_token, initial_state, dy, d_final_state, dq, dk_out,
+                       dv_out, dg, d_initial_state, workspace, workspace_bytes, stream);
 }
 
 kda_status kda_linattn_decode_step(kda_dtype dt, int N, int H, int Hk, int dk, int dv, float scale, const void* q,

@@ -396,6 +396,19 @@ __device__ __forceinline__ void write_tables(Tables* t, double G, int lane, bool
     if (lane == 0) t->total = exp2_fast((float)end);
 }
 
+// Zeros into the rows of no sequence of out [T, H, D], of head h: the block b of
+// the launch's takes its share of them.
+template <typename T, int D>
+__device__ __forceinline__ void clear_rest(const LinArgs& a, T* out, int b, int h) {
+    constexpr int EP = 16 / (int)sizeof(T) < D ? 16 / (int)sizeof(T) : D, P = D / EP, RPW = 256 / P;
+    const int64_t t0 = seq_at(a, 0), end = seq_at(a, a.num_seqs), t1 = end < t0 ? t0 : end;
+    for (int64_t r = (int64_t)b * RPW + threadIdx.x / P; r < t0 + (a.T_total - t1); r += (int64_t)a.nblocks * RPW) {
+        const int64_t tok = r < t0 ? r : t1 + (r - t0);
+        const float zero[EP] = {};
+        store_vec<T, EP>(out + (tok * a.H + h) * D + threadIdx.x % P * EP, zero);
+    }
+}
+
 enum : int { kOut = 0, kState = 1, kGrad = 2 };
 
 // Tokens of a block in the order they are handled: chunk boundaries lie at the
@@ -673,6 +686,7 @@ __device__ __forceinline__ void linattn_body(const LinArgs& a) {
     const int b = uni(blockIdx.x / a.H), h = blockIdx.x - b * a.H;
     const int hq = MODE == kState ? 0 : uni(h / a.q.share), hk = uni(h / a.k.share), hv = uni(h / a.v.share);
     const int hx = MODE == kGrad ? uni(h / a.x.share) : 0;
+    if (MODE != kState && a.clear && !a.out_f32) clear_rest<T, DV>(a, (T*)a.out, b, h);
     const Block bl = find_block(a, b);
     if (bl.n < 0) return;
     const bool rev = a.reverse;
@@ -1242,6 +1256,7 @@ __device__ __forceinline__ void decay_gradient(const LinArgs& a, const LinTail& 
     double& carry = part[4];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int b = blockIdx.x / a.H, h = blockIdx.x % a.H;
+    if (a.clear) clear_rest<float, 1>(a, x.dg, b, h);
     const Block bl = find_block(a, b);
     if (bl.n < 0) return;
     const bool last = bl.j == bl.nb - 1 || b + 1 >= a.nblocks;
@@ -1324,7 +1339,9 @@ __device__ __forceinline__ void share_sums(const LinArgs& a, const LinTail& x) {
         for (int m = 0; m < 4; ++m) {
             const int64_t u = u0 + m * step, i = u < n4 ? u : u - n4;
             const int64_t tok = i / per;
-            if (u >= all || tok < t0 || tok >= t1) continue;   // rows of no sequence stay
+            const bool outside = tok < t0 || tok >= t1;
+            if (u >= all || (outside && !a.clear)) continue;
+            if (outside) s[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
             const float o[4] = {s[m][0], s[m][1], s[m][2], s[m][3]};
             store_vec<T, 4>((T*)(u < n4 ? x.dq : x.dk) + i * 4, o);
         }

@@ -145,8 +145,10 @@ def linattn_fwd(q, k, v, g, cu_seqlens: Optional[torch.Tensor] = None, initial_s
     S_t = exp(g_t) S_{t-1} + k_t v_t^T, y_t = scale S_t^T q_t.
 
     q, k [T, Hk, dk] and v [T, H, dv] (bf16 or fp32; H / Hk value heads share a
-    key head), g fp32 [T, H] or, one decay for all tokens, [H].  Returns (y,
-    final_state or None)."""
+    key head), g fp32 [T, H] or, one decay for all tokens, [H].  cu_seqlens may
+    begin after 0 or end before T: rows of no sequence are not read; they are
+    zeros in a y made here, and left as they are in one that is given.  Returns
+    (y, final_state or None)."""
     dt, T, H, Hk, dk, dv, per_token = _qkv(q, k, v, g)
     N = _seqs(cu_seqlens)
     _need("initial_state", initial_state, (N, H, dk, dv), torch.float32)
@@ -158,13 +160,15 @@ def linattn_fwd(q, k, v, g, cu_seqlens: Optional[torch.Tensor] = None, initial_s
                 workspace=workspace)
     dev = _device(q, k, v, g, cu_seqlens, initial_state, final_state, y, workspace)
     L = lib()
+    fn = L.kda_linattn_fwd
     if y is None:
         y = torch.empty(T, H, dv, dtype=q.dtype, device=dev)
+        fn = L.kda_linattn_fwd_padded
     if final_state is None and output_final_state:
         final_state = torch.empty(N, H, dk, dv, dtype=torch.float32, device=dev)
     workspace = _workspace("kda_linattn_fwd", L.kda_linattn_fwd_workspace_size(dt, H, Hk, dk, dv, N, T), workspace,
                            dev)
-    _call(dev, L.kda_linattn_fwd, "kda_linattn_fwd", dt, H, Hk, dk, dv, scale, N, T, _p(cu_seqlens), _p(q), qs,
+    _call(dev, fn, "kda_linattn_fwd", dt, H, Hk, dk, dv, scale, N, T, _p(cu_seqlens), _p(q), qs,
           _p(k), ks, _p(v), vs, _p(g), per_token, _p(initial_state), _p(final_state), _p(y), _p(workspace),
           workspace.numel())
     return y, final_state
@@ -175,7 +179,8 @@ def linattn_bwd(q, k, v, g, dy, cu_seqlens: Optional[torch.Tensor] = None, initi
     """The gradient of linattn_fwd for the gradients dy [T, H, dv] of y and
     (optional) d_final_state of the final state.  Returns (dq, dk, dv, dg,
     d_initial_state): dq, dk [T, Hk, dk] summed over the value heads that share
-    a key head, dg shaped like g (one decay for all tokens: summed over them)."""
+    a key head, dg shaped like g (one decay for all tokens: summed over them);
+    zeros in rows of no sequence."""
     dt, T, H, Hk, dk, dv, per_token = _qkv(q, k, v, g)
     N = _seqs(cu_seqlens)
     _need("dy", dy, (T, H, dv), q.dtype)
@@ -194,7 +199,7 @@ def linattn_bwd(q, k, v, g, dy, cu_seqlens: Optional[torch.Tensor] = None, initi
     ds0 = torch.empty(N, H, dk, dv, dtype=torch.float32, device=dev)
     workspace = _workspace("kda_linattn_bwd", L.kda_linattn_bwd_workspace_size(dt, H, Hk, dk, dv, N, T), workspace,
                            dev)
-    _call(dev, L.kda_linattn_bwd, "kda_linattn_bwd", dt, H, Hk, dk, dv, scale, N, T, _p(cu_seqlens), _p(q), qs,
+    _call(dev, L.kda_linattn_bwd_padded, "kda_linattn_bwd", dt, H, Hk, dk, dv, scale, N, T, _p(cu_seqlens), _p(q), qs,
           _p(k), ks, _p(v), vs, _p(g), per_token, _p(initial_state), _p(dy), _p(d_final_state), _p(dq),
           _p(dk_out), _p(dv_out), _p(dg), _p(ds0), _p(workspace), workspace.numel())
     return dq, dk_out, dv_out, dg, ds0

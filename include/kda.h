@@ -358,7 +358,8 @@ kda_status kda_decode_replay(kda_dtype dt, int N, int Td, int H, int dk, int dv,
  *                    num_seqs) * H at most about 4 million.
  *                    Sequences may be empty: their state passes through.  The
  *                    offsets may begin after 0 or end before T_total; rows of no
- *                    sequence are neither read nor written.
+ *                    sequence are neither read nor written (for zeros in the
+ *                    outputs there: kda_linattn_fwd_padded).
  *   q, k             [T_total, Hk, dk] in dtype dt, v [T_total, H, dv].
  *                    16-byte aligned, strides multiples of 16 bytes (at most
  *                    2^23 elements), finite.
@@ -381,6 +382,17 @@ kda_status kda_linattn_fwd(kda_dtype dt, int H, int Hk, int dk, int dv, float sc
                            int64_t k_stride, const void* v, int64_t v_stride, const float* g, int g_per_token,
                            const float* initial_state, float* final_state, void* y, void* workspace,
                            size_t workspace_bytes, void* stream);
+
+/*
+ * kda_linattn_fwd_padded -- kda_linattn_fwd for a padded batch in a fresh y:
+ * rows of no sequence, before cu_seqlens[0] and from cu_seqlens[num_seqs] on, are
+ * set to zeros, in the same launches.
+ */
+kda_status kda_linattn_fwd_padded(kda_dtype dt, int H, int Hk, int dk, int dv, float scale, int num_seqs,
+                                  int64_t T_total, const int32_t* cu_seqlens, const void* q, int64_t q_stride,
+                                  const void* k, int64_t k_stride, const void* v, int64_t v_stride, const float* g,
+                                  int g_per_token, const float* initial_state, float* final_state, void* y,
+                                  void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * kda_linattn_bwd -- the gradient of kda_linattn_fwd for given gradients of y
@@ -409,6 +421,17 @@ kda_status kda_linattn_bwd(kda_dtype dt, int H, int Hk, int dk, int dv, float sc
                            const float* initial_state, const void* dy, const float* d_final_state, void* dq,
                            void* dk_out, void* dv_out, float* dg, float* d_initial_state, void* workspace,
                            size_t workspace_bytes, void* stream);
+
+/*
+ * kda_linattn_bwd_padded -- kda_linattn_bwd; dq, dk_out, dv_out and dg [T_total,
+ * H] of rows of no sequence, whose gradient is 0, are set to zeros.
+ */
+kda_status kda_linattn_bwd_padded(kda_dtype dt, int H, int Hk, int dk, int dv, float scale, int num_seqs,
+                                  int64_t T_total, const int32_t* cu_seqlens, const void* q, int64_t q_stride,
+                                  const void* k, int64_t k_stride, const void* v, int64_t v_stride, const float* g,
+                                  int g_per_token, const float* initial_state, const void* dy,
+                                  const float* d_final_state, void* dq, void* dk_out, void* dv_out, float* dg,
+                                  float* d_initial_state, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * kda_linattn_decode_step -- one token for each of N requests (N * H < 2^24)

@@ -161,3 +161,82 @@ def test_gate_far_from_zero(kda, D, dtype):
     xr, wr, _, _ = ref.norm_grad(x, w, None, z, 1e-5, "rms", dy)
     ref.check(f"gate {dtype} dx", dx, xr, 2.0 ** -8 if dtype == "bf16" else 2e-6)
     ref.check(f"gate {dtype} dw", dw, wr, 2e-6)
+
+
+def dirty(nbytes):
+    """Leaves NaN in the memory that the next allocations get."""
+    for n in (nbytes, nbytes // 2, nbytes // 4, 1 << 20):
+        torch.full((n // 4,), float("nan"), device="cuda")
+
+
+PADDED = [([5, 200, 90, 7], (2, 2, 64, 64), "token"), ([0, 130, 61], (4, 2, 128, 64), "token"),
+          ([70, 333, 0], (3, 1, 64, 128), "head"), ([3000, 100, 1000], (4, 4, 128, 128), "token"),
+          ([64, 0, 9], (2, 1, 64, 64), "token"), ([1, 1, 1], (2, 2, 64, 64), "head")]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,shape,decay", PADDED, ids=str)
+def test_rows_of_no_sequence_are_zeros(kda, lens, shape, decay, dtype):
+    """Padding in front of and behind one or two sequences.  Outputs that the
+    call makes are zeros there, whatever was in their memory."""
+    before, after = lens[0], lens[-1]
+    x = make(dtype, lens, *shape, seed=160, decay=decay)
+    T = sum(lens)
+    x.update(cu=[before, before, T - after], s0=x["s0"][:2], ds=x["ds"][:2])
+    rest = torch.ones(T, dtype=torch.bool)
+    rest[before:T - after] = False
+    for n in ("q", "k", "v", "dy") + (("g",) if decay == "token" else ()):
+        x[n][rest] = float("nan")
+    dirty(T * shape[0] * 128 * 4)
+    y, s = fwd(kda, x)
+    dirty(T * shape[0] * 128 * 4)
+    got = bwd(kda, x)
+    inner = {n: x[n][~rest] for n in ("q", "k", "v", "dy")}
+    inner["g"] = x["g"][~rest] if decay == "token" else x["g"]
+    cu = [0, 0, T - after - before]
+    yr, sr, _ = ref.linattn(inner["q"], inner["k"], inner["v"], inner["g"], cu, x["s0"], x["scale"])
+    want = ref.linattn_grad(inner["q"], inner["k"], inner["v"], inner["g"], cu, inner["dy"], x["s0"], x["ds"], x["scale"])
+    ref.check("y", y[~rest], yr, ref.TOL[dtype])
+    ref.check("state", s, sr, ref.TOL_STATE)
+    assert not bool(y[rest].any()), "y"
+    for n, a, b in zip(("dq", "dk", "dv", "dg"), got, want):
+        if a.shape[0] == T:
+            assert not bool(a[rest].any()), n
+            a = a[~rest]
+        ref.check(n, a, b, ref.TOL_DG if n == "dg" else ref.TOL[dtype])
+    ref.check("ds0", got[4], want[4], ref.TOL_STATE)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,shape,decay", PADDED, ids=str)
+def test_rows_of_no_sequence_stay_in_the_callers_outputs(kda, lens, shape, decay, dtype):
+    """A y that is given, and the C calls without _padded: those rows keep what they held."""
+    H, Hk, dk, dv = shape
+    before, after, T = lens[0], lens[-1], sum(lens)
+    x = make(dtype, lens, *shape, seed=161, decay=decay)
+    x.update(cu=[before, before, T - after], s0=x["s0"][:2], ds=x["ds"][:2])
+    rest = torch.ones(T, dtype=torch.bool)
+    rest[before:T - after] = False
+    fives = lambda t: torch.full_like(t, 5.0)  # noqa: E731
+    want = fwd(kda, x)[0]
+    y = fives(want)
+    fwd(kda, x, y=y)
+    assert torch.equal(y[~rest], want[~rest]) and bool((y[rest] == 5).all())
+
+    want = bwd(kda, x)
+    out = [fives(t) for t in want]
+    c = {n: t.cuda() for n, t in x.items() if isinstance(t, torch.Tensor)}
+    cu = torch.tensor(x["cu"], dtype=torch.int32).cuda()
+    dt = kda.KDA_BF16 if dtype == "bf16" else kda.KDA_F32
+    ws = torch.empty(kda.linattn_bwd_workspace_size(dt, H, Hk, dk, dv, 2, T), dtype=torch.uint8, device="cuda")
+    p = lambda t: t.data_ptr()  # noqa: E731
+    st = kda.lib().kda_linattn_bwd(dt, H, Hk, dk, dv, x["scale"], 2, T, p(cu), p(c["q"]), Hk * dk, p(c["k"]), Hk * dk,
+                                   p(c["v"]), H * dv, p(c["g"]), int(decay == "token"), p(c["s0"]), p(c["dy"]),
+                                   p(c["ds"]), *(p(t) for t in out), p(ws), ws.numel(),
+                                   torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    for n, a, b in zip(("dq", "dk", "dv", "dg", "ds0"), out, want):
+        if a.shape[0] == T:
+            assert torch.equal(a[~rest], b[~rest]) and bool((a[rest] == 5).all()), n
+        else:
+            assert torch.equal(a, b), n
