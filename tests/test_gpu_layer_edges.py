@@ -240,3 +240,39 @@ def test_rows_of_no_sequence_stay_in_the_callers_outputs(kda, lens, shape, decay
             assert torch.equal(a[~rest], b[~rest]) and bool((a[rest] == 5).all()), n
         else:
             assert torch.equal(a, b), n
+
+
+# rows a slot of the norm's gradient, for each lane group: 16, 64 (one, two and
+# for fp32 four runs a thread), 256, and 1024 threads a row
+ROWS = [(40000, 1, 64), (30011, 1, 128), (29001, 1, 100), (7001, 1, 512), (7000, 1, 203), (9000, 1, 1024), (4097, 2, 1000),
+        (2003, 1, 2048), (2500, 1, 1999), (1801, 1, 4096), (1700, 1, 8192), (1301, 1, 7001), (1100, 1, 16384),
+        (1200, 1, 16001), (5000, 40, 128), (3100, 13, 64)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H,D", ROWS)
+def test_norm_gradient_of_many_rows(kda, T, H, D, dtype):
+    """Each slot walks several rows: the row ahead, the running sums of the
+    weight's gradient, the two buffers in turn.  The definition in 64 bits on the
+    GPU.  A sum over T tokens of terms of random sign in fp32: tens of roundings
+    a slot and up to 400 behind it, each 2^-24 at most of sums that are smaller
+    than the whole: 1e-5 of the gradient's size."""
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+    vec = 8 if dtype == "bf16" else 4
+    slots = kda.norm_bwd_workspace_size(kda.KDA_BF16 if dtype == "bf16" else kda.KDA_F32, T, H, D) // (8 * D)
+    assert T * H > slots, "one row a slot"
+    gen = torch.Generator(device="cuda").manual_seed(T + D)
+    rnd = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    for kind, gated, biased in (("layer", False, True), ("rms", True, False), ("layer", True, True)):
+        x, dy = (rnd(T, H, D) + 0.5).to(dt), rnd(T, H, D).to(dt)
+        z = rnd(T, H, D).to(dt) if gated else None
+        w, b = 1 + 0.3 * rnd(H, D), 0.3 * rnd(H, D) if biased else None
+        _, mean, rstd = kda.norm_fwd(x, w, b, z, kind=kind)
+        dx, dw, db, dz = kda.norm_bwd(dy, x, w, mean, rstd, b, z, kind=kind)
+        want = ref.norm_grad(x, w, b, z, 1e-5, kind, dy)
+        name = f"rows {dtype} {T}x{H}x{D} ({T * H / slots:.1f} a slot, {-(-D // vec)} runs) {kind}{' gated' if gated else ''}"
+        e = 2.0 ** -8 if dtype == "bf16" else 2e-6
+        for n, a, r, tol in zip(("dx", "dw", "db", "dz"), (dx, dw, db, dz), want, (e, 1e-5, 1e-5, e)):
+            assert (a is None) == (r is None)
+            if a is not None:
+                ref.check(f"{name} {n}", a, r.cpu(), tol)
