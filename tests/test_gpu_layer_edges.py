@@ -276,3 +276,69 @@ def test_norm_gradient_of_many_rows(kda, T, H, D, dtype):
             assert (a is None) == (r is None)
             if a is not None:
                 ref.check(f"{name} {n}", a, r.cpu(), tol)
+
+
+def linattn_grad_gpu(x):
+    """linattn_grad of layer_ref for one sequence after the other, on the GPU and
+    with the states before a token kept for 256 tokens at a time."""
+    c = {n: t.cuda().double() for n, t in x.items() if isinstance(t, torch.Tensor)}
+    T, H = c["v"].shape[:2]
+    q, k = (c[n].repeat_interleave(H // c[n].shape[1], 1) for n in ("q", "k"))
+    v, dy, a = c["v"], c["dy"] * x["scale"], torch.exp(c["g"]).expand(T, H)
+    dq, dk, dv = torch.zeros_like(q), torch.zeros_like(k), torch.zeros_like(v)
+    dg, R0, y = torch.zeros(T, H, dtype=torch.float64, device="cuda"), c["ds"].clone(), torch.zeros_like(v)
+    S_end = torch.empty_like(R0)
+    step = lambda S, t: a[t][:, None, None] * S + k[t][:, :, None] * v[t][:, None, :]  # noqa: E731
+    for n in range(len(x["cu"]) - 1):
+        lo, hi = x["cu"][n], x["cu"][n + 1]
+        S, kept = c["s0"][n], []
+        for t in range(lo, hi):
+            if (t - lo) % 256 == 0:
+                kept.append(S)
+            S = step(S, t)
+            y[t] = x["scale"] * (q[t][:, :, None] * S).sum(1)
+        S_end[n] = S
+        R = c["ds"][n].clone()
+        for i in range(len(kept) - 1, -1, -1):
+            part = range(lo + 256 * i, min(lo + 256 * (i + 1), hi))
+            before = [kept[i]]
+            for t in part:
+                before.append(step(before[-1], t))
+            for j in range(len(part) - 1, -1, -1):
+                t = part[j]
+                dq[t] = (before[j + 1] * dy[t][:, None, :]).sum(-1)
+                R = R + q[t][:, :, None] * dy[t][:, None, :]
+                dk[t] = (R * v[t][:, None, :]).sum(-1)
+                dv[t] = (R * k[t][:, :, None]).sum(-2)
+                dg[t] = a[t] * (R * before[j]).sum((-1, -2))
+                R = a[t][:, None, None] * R
+        R0[n] = R
+    fold = lambda g: g.view(T, x["q"].shape[1], -1, g.shape[-1]).sum(2)  # noqa: E731
+    return y, S_end, fold(dq), fold(dk), dv, dg, R0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,shape,decay", [([2500], (32, 32, 128, 128), "token"), ([1100, 1500], (16, 4, 64, 128), "reset"),
+                                              ([2049], (12, 12, 64, 64), "head"), ([1985], (24, 8, 128, 64), "token")],
+                         ids=str)
+def test_several_blocks_of_several_chunks(kda, lens, shape, decay, dtype):
+    """What a training step has: the states of both directions pass between
+    blocks of many chunks, and dg starts anew at their ends."""
+    x = make(dtype, lens, *shape, seed=170, decay=decay)
+    H, T = shape[0], sum(lens)
+    y, s, dq, dk, dv, dg, ds0 = linattn_grad_gpu(x)
+    name = f"blocks {dtype} {lens} {shape} {decay}"
+    got = fwd(kda, x)
+    ref.check(name + " y", got[0], y.cpu(), ref.TOL[dtype])
+    ref.check(name + " state", got[1], s.cpu(), ref.TOL_STATE)
+    got = bwd(kda, x)
+    for n, a, b in zip(("dq", "dk", "dv", "dg", "ds0"), got, (dq, dk, dv, dg, ds0)):
+        if n == "dg" and decay == "head":
+            # within TOL_DG of the sum of the terms' sizes, as each term is of its own
+            err, size = (a.double() - b.sum(0)).abs(), b.abs().sum(0)
+            print(f"[layer] {name} dg of a head: {(err / size).max():.2e} of its terms", flush=True)
+            assert bool((err <= ref.TOL_DG * size).all())
+            continue
+        ref.check(f"{name} {n}", a, b.cpu(), ref.TOL_DG if n == "dg" else ref.TOL_STATE if n == "ds0" else ref.TOL[dtype])
+    if dtype == "bf16":
+        only_rounded(name + " dv", got[2], dv.cpu())
