@@ -342,3 +342,39 @@ def test_several_blocks_of_several_chunks(kda, lens, shape, decay, dtype):
         ref.check(f"{name} {n}", a, b.cpu(), ref.TOL_DG if n == "dg" else ref.TOL_STATE if n == "ds0" else ref.TOL[dtype])
     if dtype == "bf16":
         only_rounded(name + " dv", got[2], dv.cpu())
+
+
+def test_calls_side_by_side_on_two_streams(kda):
+    """Everything is on the GPU beforehand, with a workspace for each stream, and
+    several calls are queued on each before anything is waited for."""
+    jobs = []
+    for seed, lens, shape in ((181, [4000, 1300], (8, 4, 128, 128)), (182, [2600, 0, 3100], (8, 8, 128, 128))):
+        x = make("bf16", lens, *shape, seed=seed)
+        c = {n: t.cuda() for n, t in x.items() if isinstance(t, torch.Tensor)}
+        cu, T, N = torch.tensor(x["cu"], dtype=torch.int32).cuda(), sum(lens), len(lens)
+        size = [f(kda.KDA_BF16, *shape, N, T) for f in (kda.linattn_fwd_workspace_size, kda.linattn_bwd_workspace_size)]
+        ws = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in size]
+        w = torch.randn(shape[0], shape[3], device="cuda")
+
+        def call(c=c, cu=cu, ws=ws, w=w, scale=x["scale"]):
+            y, s = kda.linattn_fwd(c["q"], c["k"], c["v"], c["g"], cu_seqlens=cu, initial_state=c["s0"], scale=scale,
+                                   workspace=ws[0])
+            n, mean, rstd = kda.norm_fwd(y, w, z=c["v"])
+            dx, dw, _, dz = kda.norm_bwd(c["dy"], y, w, mean, rstd, z=c["v"])
+            return (y, s, n, dx, dw, dz) + kda.linattn_bwd(c["q"], c["k"], c["v"], c["g"], dx, cu_seqlens=cu,
+                                                           initial_state=c["s0"], d_final_state=c["ds"], scale=scale,
+                                                           workspace=ws[1])
+        jobs.append(call)
+    want = [call() for call in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    got = [[], []]
+    for _ in range(6):
+        for i, call in enumerate(jobs):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(call())
+    torch.cuda.synchronize()
+    for i, calls in enumerate(got):
+        for r, out in enumerate(calls):
+            for m, (a, b) in enumerate(zip(out, want[i])):
+                assert torch.equal(a, b), (i, r, m)
