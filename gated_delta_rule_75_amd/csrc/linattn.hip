@@ -851,11 +851,11 @@ __device__ __forceinline__ void linattn_body(const LinArgs& a) {
         }
         if (MODE == kOut && !kRows && more) fetch_q(m0 + C);
 
+        const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
         // outputs, transposed tiles: a lane holds 4 consecutive columns of row
         // 16 t + l % 16
         f32x4_t acc[4][NT];
         Frag8<T> fk[KT];      // k's columns, tokens 0 to 31, then 32 to 63
-        const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
         if constexpr (MODE != kState) {
             // P, transposed tiles (rows j, columns i): a lane holds 4 consecutive
             // j of one i.  Waves take 3, 3, 2 and 2 of the 10 tiles on or below
@@ -1015,10 +1015,21 @@ __device__ __forceinline__ void linattn_body(const LinArgs& a) {
                     for (int i = s * NC / SN; i < (s + 1) * NC / SN; ++i) part_k(m0 + C, i);
                 }
             }
+            float in[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) in[t] = tb->in[16 * t + lr];
+            if (__any(in[3] == 0.f)) {
+                // a decay of 0 in the chunk (its last row has it too): behind it a
+                // state that is not finite ends
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) acc[t][n] = in[t] == 0.f ? zero : acc[t][n];
+            }
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 const int i = 16 * t + lr;
-                const float e = tb->in[i] * (s_scale * c);
+                const float e = in[t] * (s_scale * c);
                 float dot = 0.f;
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
@@ -1057,10 +1068,11 @@ __device__ __forceinline__ void linattn_body(const LinArgs& a) {
         if (kRows && more) part_q(m0 + C, 0);
         c = unif(c * tb->total);
         if (c < 1.f / 4096.f) {
+            const bool off = c == 0.f;
 #pragma unroll
             for (int i = 0; i < KT; ++i)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) S[i][n] *= c;
+                for (int n = 0; n < NT; ++n) S[i][n] = off ? zero : S[i][n] * c;
             c = 1.f;
         }
         const float u = u_scale / c;
@@ -1236,7 +1248,7 @@ __global__ __launch_bounds__(256) void linattn_carry_kernel(LinArgs a, LinCarry 
         for (int m = 0; m < A; ++m) {
             if (i0 + m >= nb) break;
             *reinterpret_cast<f32x4_t*>(c.states + index(i0 + m) * size + e) = s;
-            if (own(i0 + m)) s = s * d[m] + u[m];
+            if (own(i0 + m)) s = d[m] == 0.f ? u[m] : s * d[m] + u[m];
         }
     }
     if (c.after) *reinterpret_cast<f32x4_t*>(c.after + ((int64_t)n * a.H + h) * size + e) = s;
@@ -1586,6 +1598,10 @@ __global__ __launch_bounds__(256) void linattn_decode_kernel(LinDecodeArgs a) {
     load_vec<T, 4>(v, vv);
     const f32x4_t v4 = {vv[0], vv[1], vv[2], vv[3]};
     const float decay = expf(a.g[a.g_per_token ? nh : h]);
+    if (decay == 0.f) {   // anew, whatever the state holds
+#pragma unroll
+        for (int r = 0; r < RPT; ++r) S[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
     __syncthreads();
     f32x4_t o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll

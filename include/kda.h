@@ -366,7 +366,8 @@ kda_status kda_decode_replay(kda_dtype dt, int N, int Td, int H, int dk, int dv,
  *   g                fp32 natural log of the decay, <= 0: [T_total, H]
  *                    (g_per_token != 0) or one for each head [H].  Below -200
  *                    it counts as -200: the factor is 0 in fp32, so -INFINITY
- *                    starts the head's state anew at that token.
+ *                    starts the head's state anew at that token, also where it
+ *                    held infinities or NaN.
  *   initial_state, final_state   fp32 [num_seqs, H, dk, dv] or NULL, as
  *                    kda_chunk_fwd; they may be the same buffer.
  *   y                [T_total, H, dv] in dtype dt; must not overlap inputs.

@@ -378,3 +378,63 @@ def test_calls_side_by_side_on_two_streams(kda):
         for r, out in enumerate(calls):
             for m, (a, b) in enumerate(zip(out, want[i])):
                 assert torch.equal(a, b), (i, r, m)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,shape", [([40, 1, 0], (4, 2, 128, 128)), ([500, 64, 200], (4, 4, 64, 64)),
+                                        ([300, 700, 0], (256, 128, 64, 128)), ([1, 1, 1], (3, 1, 128, 64))], ids=str)
+def test_a_decay_of_zero_ends_any_state(kda, lens, shape, dtype):
+    """States that hold NaN and infinities, cleared by the first token's decay or
+    by a later one's: nothing behind it sees them.  An empty sequence keeps its own."""
+    H, heads = shape[0], [0, 1, shape[0] - 1]
+    x = make(dtype, lens, *shape, seed=190)
+    at = [0 if n % 2 == 0 else length // 2 for n, length in enumerate(lens)]
+    for n, length in enumerate(lens):
+        if length:
+            x["g"][x["cu"][n] + at[n]] = -float("inf")
+    good = dict(x, s0=torch.zeros_like(x["s0"]))
+    x["s0"][:, :, ::3] = float("nan")
+    x["s0"][:, :, 1::3] = float("inf")
+    y, s = fwd(kda, x)
+    grads = bwd(kda, x)
+    shared = shape[1] != H     # for the recurrence each value head has its own copy of the key head
+    good.update({n: good[n].repeat_interleave(H // shape[1], 1) for n in ("q", "k")})
+    sub = heads_of(good, heads, "token")
+    yr, sr, _ = ref.linattn(sub["q"], sub["k"], sub["v"], sub["g"], x["cu"], sub["s0"], x["scale"])
+    want = ref.linattn_grad(sub["q"], sub["k"], sub["v"], sub["g"], x["cu"], sub["dy"], sub["s0"], sub["ds"], x["scale"])
+    for n, length in enumerate(lens):
+        lo, hi = x["cu"][n] + at[n], x["cu"][n + 1]
+        if length == 0:
+            assert torch.equal(torch.nan_to_num(s[n]).cpu(), torch.nan_to_num(x["s0"][n]))
+            continue
+        ref.check(f"zero {dtype} {n} y", y[lo:hi, heads], yr[lo:hi], ref.TOL[dtype])
+        ref.check(f"zero {dtype} {n} state", s[n, heads], sr[n], ref.TOL_STATE)
+        if at[n] == 0:     # no gradient but that of the state itself passes the first token
+            for m, i in (("dq", 0), ("dk", 1), ("dv", 2), ("dg", 3)):
+                if shared and i < 2:
+                    assert bool(torch.isfinite(grads[i][lo:hi]).all()), m
+                elif i == 3 and length == 1:
+                    # 0 as the difference of <S, R> and the token's own products:
+                    # within fp32's error of their terms
+                    S = sub["k"][lo].double()[:, :, None] * sub["v"][lo].double()[:, None]
+                    R = sub["ds"][n].double() + x["scale"] * sub["q"][lo].double()[:, :, None] * sub["dy"][lo].double()[:, None]
+                    assert bool((grads[i][lo, heads].double().cpu().abs() <= ref.TOL_DG * (S * R).abs().sum((1, 2))).all())
+                else:
+                    ref.check(f"zero {dtype} {n} {m}", grads[i][lo:hi, heads], want[i][lo:hi],
+                              ref.TOL_DG if m == "dg" else ref.TOL[dtype])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,shape", [(1, (3, 1, 128, 64)), (70, (8, 8, 64, 64)), (70, (8, 4, 128, 128))], ids=str)
+def test_a_token_starts_any_state_anew(kda, N, shape, dtype):
+    x = make(dtype, [1] * N, *shape, seed=191)
+    anew = torch.arange(N * shape[0]).view(N, -1) % 3 == 0
+    x["g"][anew] = -float("inf")
+    good = x["s0"].clone()
+    good[anew] = 0
+    x["s0"][anew] = float("nan")
+    c = {n: t.cuda() for n, t in x.items() if isinstance(t, torch.Tensor)}
+    y = kda.linattn_decode_step(c["q"], c["k"], c["v"], c["g"], c["s0"], scale=x["scale"])
+    yr, sr, _ = ref.linattn(x["q"], x["k"], x["v"], x["g"], x["cu"], good, x["scale"])
+    ref.check(f"anew {dtype} y", y, yr, ref.TOL[dtype])
+    ref.check(f"anew {dtype} state", c["s0"], sr, ref.TOL_STATE)
