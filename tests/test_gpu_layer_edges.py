@@ -438,3 +438,48 @@ def test_a_token_starts_any_state_anew(kda, N, shape, dtype):
     yr, sr, _ = ref.linattn(x["q"], x["k"], x["v"], x["g"], x["cu"], good, x["scale"])
     ref.check(f"anew {dtype} y", y, yr, ref.TOL[dtype])
     ref.check(f"anew {dtype} state", c["s0"], sr, ref.TOL_STATE)
+
+
+@pytest.mark.parametrize("N", [40, 300])
+def test_a_graph_follows_its_offsets(kda, N):
+    """Recorded once; between the replays the offsets change, padding in front and
+    behind included, so blocks, their table and the zeros are found anew."""
+    T, H, Hk, dk, dv = 4000, 4, 2, 64, 128
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda").bfloat16()  # noqa: E731
+    q, k, v, dy = r(T, Hk, dk), r(T, Hk, dk), r(T, H, dv), r(T, H, dv)
+    g = -torch.rand(T, H, generator=gen, device="cuda")
+    cu = torch.zeros(N + 1, dtype=torch.int32, device="cuda")
+    offsets = []
+    for seed in range(3):
+        c = torch.randint(0, T + 1, (N + 1,), generator=torch.Generator().manual_seed(seed)).sort().values
+        if seed == 1:
+            c[-1], c[0] = T, 0
+        if seed == 2:
+            c[:N // 2] = 17        # many empty ones, one long
+            c[N // 2:] = 3100
+        offsets.append(c.int())
+
+    def once():
+        return kda.linattn_fwd(q, k, v, g, cu_seqlens=cu) + kda.linattn_bwd(q, k, v, g, dy, cu_seqlens=cu)
+
+    want = []
+    for c in offsets:
+        cu.copy_(c)
+        want.append([t.clone() for t in once()])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = once()
+    for n in (0, 1, 2, 1, 0):
+        cu.copy_(offsets[n])
+        for t in out:
+            t.fill_(float("nan"))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        lo, hi = int(offsets[n][0]), int(offsets[n][-1])
+        for i, (a, b) in enumerate(zip(out, want[n])):
+            assert torch.equal(a, b), (n, i)
+            if a.shape[0] == T:
+                assert not bool(a[:lo].any()) and not bool(a[hi:].any()), (n, i)
