@@ -39,9 +39,12 @@ bool rows_ok(kda_dtype dt, const void* p, int64_t stride, int heads, int d) {
 // Tokens of a block.  Sequences longer than a block are cut, and their blocks
 // run side by side from states that a first pass over k and v builds (about half
 // the call's reads again): worth it where uncut sequences leave CUs without
-// work.  512 workgroups (two a CU) run at once, and the ones behind them would
-// take a second round: so the blocks of one long sequence are as many as that
-// holds (`groups` workgroups), and no shorter than `least`.
+// work.  In bf16 512 workgroups (two a CU) run at once, and the ones behind them
+// would take a second round: so the blocks of one long sequence are as many as
+// that holds (`groups` workgroups), and no shorter than `least`.  The rule is of
+// tokens and heads alone.  In fp32 with d = 128 a CU holds one workgroup, so the
+// blocks take two rounds; and in a batch of sequences that are all shorter than a
+// block, each still gets an entering state in the workspace.
 int64_t block_len(int H, int64_t T, int groups, int64_t least, int64_t most) {
     const int64_t n = H < groups ? groups / H : 1;
     int64_t L = ((T + n - 1) / n + 63) / 64 * 64;

@@ -35,20 +35,21 @@
 // pass makes the outputs (kOut, kGrad) from the states that enter.
 //
 // What bounds it (d = 128, bf16): instructions.  With the update's operand in
-// three parts and P in two, 8192 tokens x 96 heads are 193 GFLOP in the two
-// passes, 150 us at the 1.29 PFLOP/s that a large bf16 product reaches here;
-// their 815 MB need 131 us at a copy's 6.2 TB/s.  The call takes 311 to 330 us:
-// about 110 the state pass, 10 the chain, 200 the output pass.  Without its
-// products the output pass takes 134 us (183 with the stores), without its loads
-// 182.  By counters its SIMDs are busy 46 % with vector and 27 % with matrix
-// instructions (operands are split and decayed on the way), and 27 % of the
-// waves' time is waiting, with two workgroups a CU (240 to 256 registers a
-// thread).
+// three parts, P and the entering state in two, 8192 tokens x 96 heads are 219
+// GFLOP in the two passes, 170 us at the 1.29 PFLOP/s that a large bf16 product
+// reaches here; their 815 MB need 131 us at a copy's 6.2 TB/s.  The call takes 326
+// to 341 us: about 107 the state pass, 11 the chain, 215 the output pass.  (With
+// the entering state in one part, 309 to 322.  Of that output pass its loads and
+// stores alone took 183, its products alone 182.)  By counters its SIMDs are busy
+// 49 % with vector and 30 % with matrix instructions (operands are split and
+// decayed on the way), and 25 % of the waves' time is waiting, with two workgroups
+// a CU (190 to 250 registers a thread).  Under load without pauses the clock
+// falls, and a call takes 397 us at the median.
 // Measured and not kept: eight waves a workgroup (276 against 258 us, the pass
 // alone), half a head's columns a workgroup (457 the call), nontemporal output
 // stores (80 more), placement of a head's blocks on one XCD (no change).
-// The gradient, 4 x 2048 tokens x 32 heads (206 GFLOP; 497 MB, of which its
-// passes read most more than once, 1.4 GB in all): 363 to 375 us.
+// The gradient, 4 x 2048 tokens x 32 heads (215 GFLOP; 497 MB, of which its
+// passes read most more than once, 1.4 GB in all): 367 to 377 us.
 #include <type_traits>
 
 #include "launch.h"

@@ -16,7 +16,7 @@
 // columns, never change), keep dw and db in registers, and write one partial
 // row each; a second kernel adds the partials in a fixed order.
 //
-// Measured: 8192 x 96 heads of 128 with the gate (bf16, 607 MB) 104 us, 5.8 TB/s
+// Measured: 8192 x 96 heads of 128 with the gate (bf16, 607 MB) 105 us, 5.8 TB/s
 // (a large copy reaches 6.2); its gradient for 4096 x 32 heads (168 MB) 38 us a
 // call, 29 and 4 in the two kernels; for 4099 rows of 2047 (fp32, layer, 101 MB)
 // 30, 21 and 6 in the kernels.

@@ -7,6 +7,10 @@ Rows q, k, v of linear attention and of rotary positions may be slices of one
 projection's output: [T, heads, d] views whose heads are contiguous within a
 token (any stride from token to token).  A call runs on its tensors' device, on
 that device's current stream.
+
+Nothing here is recorded for autograd, also where an input requires a gradient:
+a training step calls the gradients itself (linattn_bwd, norm_bwd, rope with
+inverse), as from the two halves of a torch.autograd.Function.
 """
 from __future__ import annotations
 
@@ -145,10 +149,11 @@ def linattn_fwd(q, k, v, g, cu_seqlens: Optional[torch.Tensor] = None, initial_s
     S_t = exp(g_t) S_{t-1} + k_t v_t^T, y_t = scale S_t^T q_t.
 
     q, k [T, Hk, dk] and v [T, H, dv] (bf16 or fp32; H / Hk value heads share a
-    key head), g fp32 [T, H] or, one decay for all tokens, [H].  cu_seqlens may
-    begin after 0 or end before T: rows of no sequence are not read; they are
-    zeros in a y made here, and left as they are in one that is given.  Returns
-    (y, final_state or None)."""
+    key head), all finite; g fp32 [T, H] or, one decay for all tokens, [H], never
+    above 0 (-inf starts the state anew, whatever it held).  cu_seqlens may begin
+    after 0 or end before T: rows of no sequence are not read; they are zeros in a
+    y made here, and left as they are in one that is given.  Returns (y,
+    final_state or None)."""
     dt, T, H, Hk, dk, dv, per_token = _qkv(q, k, v, g)
     N = _seqs(cu_seqlens)
     _need("initial_state", initial_state, (N, H, dk, dv), torch.float32)
@@ -207,7 +212,7 @@ def linattn_bwd(q, k, v, g, dy, cu_seqlens: Optional[torch.Tensor] = None, initi
 
 def linattn_decode_step(q, k, v, g, state, scale: float = 1.0, y: Optional[torch.Tensor] = None) -> torch.Tensor:
     """One token for each of N requests: q, k [N, Hk, dk], v [N, H, dv], g [N, H]
-    or [H], state fp32 [N, H, dk, dv] updated in place.  Returns y [N, H, dv]."""
+    or [H] as in linattn_fwd, state fp32 [N, H, dk, dv] updated in place.  Returns y [N, H, dv]."""
     dt, N, H, Hk, dk, dv, per_token = _qkv(q, k, v, g)
     if state is None:
         raise ValueError("state is required")

@@ -369,7 +369,8 @@ kda_status kda_decode_replay(kda_dtype dt, int N, int Td, int H, int dk, int dv,
  *                    starts the head's state anew at that token, also where it
  *                    held infinities or NaN.
  *   initial_state, final_state   fp32 [num_seqs, H, dk, dv] or NULL, as
- *                    kda_chunk_fwd; they may be the same buffer.
+ *                    kda_chunk_fwd; they may be the same buffer.  Infinities or
+ *                    NaN in a state spread up to the next decay of 0.
  *   y                [T_total, H, dv] in dtype dt; must not overlap inputs.
  *   workspace        at least kda_linattn_fwd_workspace_size bytes for the same
  *                    sizes, 256-byte aligned (0 bytes and NULL do where
