@@ -483,3 +483,34 @@ def test_a_graph_follows_its_offsets(kda, N):
             assert torch.equal(a, b), (n, i)
             if a.shape[0] == T:
                 assert not bool(a[:lo].any()) and not bool(a[hi:].any()), (n, i)
+
+
+@pytest.mark.parametrize("shape", [(32, 32, 128, 128), (32, 8, 64, 128)], ids=str)
+def test_offsets_that_pass_32_bits(kda, shape):
+    """v, dy, y and the gradients hold more than 2^31 elements.  The long sequence
+    starts anew 300 tokens before its end, so that its last rows and the short
+    sequence behind it have values in 64 bits of their own."""
+    H, Hk, dk, dv = shape
+    long, short, tail = 600000, 90, 300
+    T = long + short
+    assert T * H * dv > 2 ** 31
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    x = dict(q=r(T, Hk, dk), k=r(T, Hk, dk), v=r(T, H, dv), dy=r(T, H, dv))
+    x["g"] = -torch.rand(T, H, generator=gen, device="cuda") * 0.1
+    x["g"][long - tail] = -float("inf")
+    cu = torch.tensor([0, long, T], dtype=torch.int32, device="cuda")
+    y, s = kda.linattn_fwd(x["q"], x["k"], x["v"], x["g"], cu_seqlens=cu, scale=dk ** -0.5)
+    got = kda.linattn_bwd(x["q"], x["k"], x["v"], x["g"], x["dy"], cu_seqlens=cu, scale=dk ** -0.5)
+    end = {n: t[long - tail:].cpu() for n, t in x.items()}
+    args = (end["q"], end["k"], end["v"], end["g"], [0, tail, tail + short])
+    yr, sr, _ = ref.linattn(*args, None, dk ** -0.5)
+    ref.check(f"far {shape} y", y[long - tail:], yr, ref.TOL["bf16"])
+    ref.check(f"far {shape} state", s, sr, ref.TOL_STATE)
+    want = ref.linattn_grad(*args, end["dy"], None, None, dk ** -0.5)
+    for n, a, b in zip(("dq", "dk", "dv", "dg"), got, want):
+        ref.check(f"far {shape} {n}", a[long - tail:], b, ref.TOL_DG if n == "dg" else ref.TOL["bf16"])
+    # the first rows, which hold no carry of an index that wrapped around
+    head = {n: t[:100].cpu() for n, t in x.items()}
+    yr, _, _ = ref.linattn(head["q"], head["k"], head["v"], head["g"], [0, 100], None, dk ** -0.5)
+    ref.check(f"far {shape} first rows", y[:100], yr, ref.TOL["bf16"])
