@@ -225,6 +225,8 @@ struct LinCall {
     float *rstates, *rdecays, *s_end, *sums_a, *sums_b, *dg_tokens;
     void* share_buf;
 };
+// The table of first blocks, where a.first is given.
+hipError_t launch_block_plan(const LinArgs& a);
 hipError_t launch_linattn_fwd(const LinCall& c);
 hipError_t launch_linattn_bwd(const LinCall& c);
 
