@@ -21,7 +21,8 @@ __all__ = [
     "chunk_fwd_fused", "chunk_fwd_noalloc", "kcp_scan", "kcp_workspace_size", "kcp_workspace_min", "decode_step",
     "decode_step_fused", "decode_replay",
     "linattn_fwd", "linattn_fwd_workspace_size", "linattn_bwd", "linattn_bwd_workspace_size",
-    "linattn_decode_step", "rope", "rope_frequencies", "norm_fwd", "norm_bwd", "norm_bwd_workspace_size",
+    "linattn_decode_step", "gdr_fwd", "gdr_fwd_workspace_size", "gdr_bwd", "gdr_bwd_workspace_size",
+    "gdr_decode_step", "rope", "rope_frequencies", "norm_fwd", "norm_bwd", "norm_bwd_workspace_size",
     "KDA_BF16", "KDA_F32",
 ]
 
@@ -40,7 +41,9 @@ SYMBOLS = ("kda_version", "kda_status_string", "kda_chunk_fwd_workspace_size",
            "kda_decode_step", "kda_decode_replay", "kda_chunk_fwd_fused", "kda_decode_step_fused",
            "kda_chunk_fwd_noalloc", "kda_noalloc_scratch_bytes",
            "kda_linattn_fwd", "kda_linattn_fwd_padded", "kda_linattn_fwd_workspace_size", "kda_linattn_bwd",
-           "kda_linattn_bwd_padded", "kda_linattn_bwd_workspace_size", "kda_linattn_decode_step", "kda_rope",
+           "kda_linattn_bwd_padded", "kda_linattn_bwd_workspace_size", "kda_linattn_decode_step",
+           "kda_gdr_fwd", "kda_gdr_fwd_padded", "kda_gdr_fwd_workspace_size", "kda_gdr_bwd", "kda_gdr_bwd_padded",
+           "kda_gdr_bwd_workspace_size", "kda_gdr_decode_step", "kda_rope",
            "kda_rope_frequencies", "kda_norm_fwd", "kda_norm_bwd", "kda_norm_bwd_workspace_size")
 
 
@@ -110,6 +113,18 @@ def lib() -> ctypes.CDLL:
         fn.restype = sz
     L.kda_linattn_decode_step.argtypes = [i, i, i, i, i, i, f, vp, i64, vp, i64, vp, i64, vp, i, vp, vp, vp]
     L.kda_linattn_decode_step.restype = i
+    gdr = [i, i, i, i, i, f, i, i64, vp, vp, i64, vp, i64, vp, i64, vp, vp]
+    for fn in (L.kda_gdr_fwd, L.kda_gdr_fwd_padded):
+        fn.argtypes = gdr + [vp, vp, vp, vp, sz, vp]
+        fn.restype = i
+    for fn in (L.kda_gdr_bwd, L.kda_gdr_bwd_padded):
+        fn.argtypes = gdr + [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        fn.restype = i
+    for fn in (L.kda_gdr_fwd_workspace_size, L.kda_gdr_bwd_workspace_size):
+        fn.argtypes = [i, i, i, i, i, i, i64]
+        fn.restype = sz
+    L.kda_gdr_decode_step.argtypes = [i, i, i, i, i, i, f, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp]
+    L.kda_gdr_decode_step.restype = i
     d = ctypes.c_double
     L.kda_rope_frequencies.argtypes = [i, d, i, d, d, d, d, vp, ctypes.POINTER(f)]
     L.kda_rope_frequencies.restype = i
@@ -463,6 +478,7 @@ def decode_replay(q, k, v, g, beta, state, accepted=None, z=None, scale: float =
     return y
 
 
-from .layer import (linattn_bwd, linattn_bwd_workspace_size, linattn_decode_step, linattn_fwd,  # noqa: E402
+from .layer import (gdr_bwd, gdr_bwd_workspace_size, gdr_decode_step, gdr_fwd, gdr_fwd_workspace_size,  # noqa: E402
+                    linattn_bwd, linattn_bwd_workspace_size, linattn_decode_step, linattn_fwd,
                     linattn_fwd_workspace_size, norm_bwd, norm_bwd_workspace_size, norm_fwd, rope,
                     rope_frequencies)

@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libkda.so")
 SOURCES = ["api.cpp", "decode.hip", "chunk_prep.hip", "chunk_state.hip", "kcp.hip",
-           "linattn.hip", "layer_api.cpp", "norm.hip", "rope.hip"]
+           "linattn.hip", "delta.hip", "layer_api.cpp", "norm.hip", "rope.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -31,13 +31,14 @@ COMMON = [
 ]
 
 
-# MFMA results in ordinary VGPRs: the scan, preparation and linear-attention
-# kernels scale and convert accumulators with VALU instructions, which cannot
+# MFMA results in ordinary VGPRs: the scan, preparation, linear-attention and
+# delta-rule kernels scale and convert accumulators with VALU instructions, which cannot
 # read AGPRs
 PER_SOURCE = {
     "chunk_state.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "chunk_prep.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "linattn.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    "delta.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
 }
 
 

@@ -1,0 +1,1171 @@
+// The gated delta rule with a decay for each head, by chunks of 64 tokens.
+//
+// Per sequence and value head, from token to token:
+//   u = exp(g) S,   e = v - u^T k,   S <- u + beta k e^T,   y = scale S^T q
+// For a chunk, with G the sum of g inside it, D_ij = exp(G_i - G_j) for j <= i
+// and S the state that enters:
+//   M = strictly lower part of (K K^T . D),   X = (I + M diag(beta))^-1
+//   E = X (V - exp(G) K S)                    errors of prediction
+//   y = P diag(beta) E + scale exp(G) Q S,    P = scale Q K^T . D
+//   S <- exp(G_63) S + K^T diag(exp(G_63 - G) beta) E
+// and for the gradient, with R that of the state behind the chunk:
+//   Z = (I + M^T diag(beta))^-1,  U = Z (P^T dY + exp(G_63 - G) K R),  dV = diag(beta) U
+//   R <- exp(G_63) R + scale Q^T diag(exp(G)) dY - K^T diag(exp(G)) dV
+//   W = scale dY E^T . D,   Y = -(strictly lower part of dV E^T . D)
+//   dQ = W diag(beta) K + scale exp(G) dY S^T
+//   dK = Y diag(beta) K - exp(G) dV S^T + diag(beta) (W^T Q + Y^T K + exp(G_63 - G) E R^T)
+//   dbeta_t = e_t.u_t,   dg_t = sum over tokens s >= t of (q.dq - v.dv)_s,
+// the last sum begun anew from the product of state and gradient where a block of
+// kBlock chunks ends.
+//
+// A first kernel makes what does not involve the state (X, Z, P and P^T as operands,
+// the tables of decays) for all chunks at once.  A second walks a sequence's chunks
+// with the state in its accumulators, a workgroup for 64 value columns of a head.
+// The gradient walks twice, forwards (keeping each chunk's state and E) and
+// backwards (its R and U); then a kernel makes dQ, dK, dV, dbeta and the tokens'
+// terms of dg for all chunks at once, and a small one sums those.
+//
+// bf16 inputs enter products as they are.  What is computed enters as a sum of
+// bf16 values: of three, 24 bits, on the way to fp32 outputs (states, E, U, X, Z,
+// the gates' gradients), of two, 16 bits, on the way to an output in bf16 alone, whose
+// own rounding is then the one that shows.
+#include "tiles.h"
+
+namespace kda {
+
+namespace {
+
+// Parts of a computed operand: for outputs in T, and for fp32 ones.
+template <typename T> constexpr int kTwo = sizeof(T) == 2 ? 2 : 1;
+template <typename T> constexpr int kThree = sizeof(T) == 2 ? 3 : 1;
+constexpr int kBlock = 8;   // chunks between two anchors of the decay's gradient
+
+// c += a b for operands in parts, the smallest products first (those beyond the
+// finer operand's own bits are left out).
+template <typename T, int NA, int NB>
+__device__ __forceinline__ f32x4_t mma_parts(const Frag8<T> (&a)[NA], const Frag8<T> (&b)[NB], f32x4_t c) {
+#pragma unroll
+    for (int s = NA + NB - 2; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            if (s - i >= 0 && s - i < NB && s < (NA > NB ? NA : NB)) c = mma(a[i], b[s - i], c);
+    return c;
+}
+
+// Operand tiles of a lower triangle (rows i, contraction j <= i) and of its
+// transpose, in the order in which lanes read them: 6 pieces of 16 rows x 32 that
+// are not all zeros, each lane's 8 values in runs of 16 bytes (bf16: a run a part;
+// fp32: two halves), a run of all lanes side by side.
+__device__ __forceinline__ constexpr int tri_piece(int t, int s) { return t < 2 ? t : 2 * (t - 1) + s; }
+__device__ __forceinline__ constexpr int tri_piece_t(int t, int s) { return t < 2 ? 2 * t + s : t + 2; }
+template <typename T, int N> constexpr int kRuns = sizeof(T) == 2 ? N : 2;
+template <typename T, int N> constexpr int kTri = 6 * 1024 * kRuns<T, N>;   // bytes
+static_assert(kTri<__bf16, 3> <= kTriBytes && kTri<float, 1> <= kTriBytes, "workspace");
+
+template <typename T, int N>
+__device__ __forceinline__ void put_operand(char* base, int piece, int lane, const float (&x)[8]) {
+    Frag8<T> f[N];
+    split(x, f);
+    u32x4_t* const at = reinterpret_cast<u32x4_t*>(base) + piece * 64 * kRuns<T, N> + lane;
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int p = 0; p < N; ++p) at[64 * p] = __builtin_bit_cast(u32x4_t, f[p].v);
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            f32x4_t u;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) u[r] = f[0].v[4 * h + r];
+            at[64 * h] = __builtin_bit_cast(u32x4_t, u);
+        }
+    }
+}
+// Half of one in two parts: contraction 4 g + (0..3) of the first (0) or second (1) 16.
+template <typename T>
+__device__ __forceinline__ void put_half(char* base, int piece, int half, int lane, const f32x4_t& x) {
+    char* const at = base + piece * 2048 + lane * 16;
+    if constexpr (sizeof(T) == 2) {
+        store4<T>(reinterpret_cast<T*>(at + 8 * half), x);
+        f32x4_t rest;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) rest[r] = x[r] - (float)(__bf16)x[r];
+        store4<T>(reinterpret_cast<T*>(at + 1024 + 8 * half), rest);
+    } else {
+        *reinterpret_cast<f32x4_t*>(at + 1024 * half) = x;
+    }
+}
+template <typename T, int N>
+__device__ __forceinline__ void get_operand(const char* base, int piece, int lane, Frag8<T> (&f)[N]) {
+    const u32x4_t* const at = reinterpret_cast<const u32x4_t*>(base) + piece * 64 * kRuns<T, N> + lane;
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int p = 0; p < N; ++p) f[p].v = __builtin_bit_cast(bf16x8_t, at[64 * p]);
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const f32x4_t u = __builtin_bit_cast(f32x4_t, at[64 * h]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) f[0].v[4 * h + r] = u[r];
+        }
+    }
+}
+
+// Eight consecutive elements as an operand of type T, from global memory.
+__device__ __forceinline__ Frag8<__bf16> frag_at(const __bf16* p) {
+    Frag8<__bf16> f;
+    f.v = *reinterpret_cast<const bf16x8_t*>(p);
+    return f;
+}
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+    const f32x4_t a = *reinterpret_cast<const f32x4_t*>(p), b = *reinterpret_cast<const f32x4_t*>(p + 4);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        x[r] = a[r];
+        x[4 + r] = b[r];
+    }
+}
+__device__ __forceinline__ Frag8<float> frag_at(const float* p) {
+    Frag8<float> f;
+    load8(p, f.v);
+    return f;
+}
+
+// The state's rows in a wave's accumulators: tile 2 s + h, row 4 g + r holds
+// channel 32 s + 8 g + 4 h + r, so that two tiles are an operand whose contraction
+// runs over 8 consecutive channels a lane.  cols8: the operand whose rows are a
+// tile's channels, contraction over tokens 32 s2 + {0, 16} + 4 g + (0..3).
+template <typename T, int D>
+__device__ __forceinline__ Frag8<T> cols8(const T* t, int s, int h, int s2, int lane) {
+    Frag8<T> f;
+    if constexpr (sizeof(T) == 2) {
+        const int row = 32 * s2 + 4 * (lane >> 4) + ((lane & 15) >> 2), col = 32 * s + 8 * (lane & 3) + 4 * h;
+        const bf16x4_t x = __builtin_bit_cast(bf16x4_t, lds_tr(t + Tile<T, D>::off(row, col)));
+        const bf16x4_t y = __builtin_bit_cast(bf16x4_t, lds_tr(t + Tile<T, D>::off(row + 16, col)));
+        f.v = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+    } else {
+        const int m = lane & 15, row = 32 * s2 + 4 * (lane >> 4), col = 32 * s + 8 * (m >> 2) + 4 * h + (m & 3);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f.v[i] = t[Tile<T, D>::off(row + i, col)];
+            f.v[4 + i] = t[Tile<T, D>::off(row + 16 + i, col)];
+        }
+    }
+    return f;
+}
+
+// 2^(difference of two sums), each as integer and fraction.
+struct Sums {
+    float frac[C];
+    int whole[C];
+    __device__ __forceinline__ void set(int lane, double G, bool valid) {
+        const double w = floor(G);
+        frac[lane] = (float)(G - w);
+        whole[lane] = valid ? (int)w : -(1 << 20);   // a row without a token reads nothing
+    }
+    __device__ __forceinline__ float ratio(int i, int j) const {
+        return __builtin_amdgcn_ldexpf(exp2_fast(frac[i] - frac[j]), whole[i] - whole[j]);
+    }
+};
+
+__device__ __forceinline__ f32x4_t mma16(const f32x4_t& a, const f32x4_t& b, f32x4_t c) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
+    return c;
+}
+
+constexpr int kLd = C + 4;   // pitch of a 64 x 64 matrix in LDS
+
+// The inverse of I + A, in place in LDS, A strictly lower: the four 16 x 16 blocks on
+// the diagonal by forward substitution, a column a lane, then block column by
+// block column X_ij = -X_ii sum_k A_ik X_kj with fp32 products.  (As a product of
+// powers, (I - A)(I + A^2)..., a chunk of equal keys would lose four digits.)  A
+// wave has a block and a block column; what lies above the diagonal blocks is
+// neither read nor written.
+__device__ __forceinline__ void invert(float* sx, int wave, int lane) {
+    const int lr = lane & 15, lg = lane >> 4;
+    const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+    {
+        float x[16];
+        const float* const m = sx + 16 * wave * (kLd + 1);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float d = i == lr ? 1.f : 0.f;
+#pragma unroll
+            for (int j4 = 0; j4 < i; j4 += 4) {
+                const f32x4_t v = *reinterpret_cast<const f32x4_t*>(m + i * kLd + j4);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (j4 + r < i) d -= v[r] * x[j4 + r];
+            }
+            x[i] = d;
+        }
+        if (lg == 0) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sx[(16 * wave + i) * kLd + 16 * wave + lr] = x[i];
+        }
+    }
+    __syncthreads();
+    f32x4_t col[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (i < wave) continue;
+        if (i == wave) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) col[i][r] = sx[(16 * i + 4 * lg + r) * kLd + 16 * i + lr];
+            continue;
+        }
+        f32x4_t s = zero;
+#pragma unroll
+        for (int k = 0; k < i; ++k)
+            if (k >= wave) s = mma16(*reinterpret_cast<const f32x4_t*>(sx + (16 * i + lr) * kLd + 16 * k + 4 * lg), col[k], s);
+        col[i] = -mma16(*reinterpret_cast<const f32x4_t*>(sx + (16 * i + lr) * kLd + 16 * i + 4 * lg), s, zero);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 1; i < 4; ++i)
+        if (i > wave) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sx[(16 * i + 4 * lg + r) * kLd + 16 * wave + lr] = col[i][r];
+        }
+    __syncthreads();
+}
+
+// Tables, scores and inverse of a (chunk, head).  GRAD: X, Z and P^T.
+template <typename T, int DK, bool GRAD>
+__global__ __launch_bounds__(256) void gdr_prep_kernel(GdrArgs a) {
+    __shared__ __attribute__((aligned(16))) float sx[C * kLd], sz[GRAD ? C * kLd : 4];
+    __shared__ Sums sums;
+    __shared__ __attribute__((aligned(16))) float s_beta[C];
+    const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6), lr = lane & 15, lg = lane >> 4;
+    const int H = a.at.H, b = uni(blockIdx.x / H), h = blockIdx.x - b * H;
+    if (a.at.clear) {
+        if constexpr (GRAD) {
+            LinArgs shared = a.at;
+            shared.H = H / a.k.share;
+            if (h < shared.H) {
+                clear_rest<T, DK>(shared, (T*)a.dq, b, h);
+                clear_rest<T, DK>(shared, (T*)a.dk, b, h);
+            }
+            if (a.dg) clear_rest<float, 1>(a.at, a.dg, b, h);
+            clear_rest<float, 1>(a.at, a.dbeta, b, h);
+        }
+        T* const out = (T*)(GRAD ? a.dv_out : a.y);
+        if (a.head_v == 64) clear_rest<T, 64>(a.at, out, b, h);
+        else clear_rest<T, 128>(a.at, out, b, h);
+    }
+    const Block bl = find_block(a.at, b);
+    if (bl.n < 0 || bl.cnt == 0) return;
+    const int64_t slot = (int64_t)b * H + h;
+    if (wave == 0) {
+        const bool valid = lane < bl.cnt;
+        const int64_t at = (bl.start + lane) * H + h;
+        const double G = decay_scan(valid && a.g ? a.g[at] : 0.f), end = lane_d(G, 63);
+        const float beta = valid ? a.beta[at] : 0.f;
+        sums.set(lane, G, valid);
+        s_beta[lane] = beta;
+        float* const tab = a.tab + slot * kGdrTab;
+        tab[lane] = valid ? exp2_fast((float)G) : 0.f;
+        tab[C + lane] = valid ? exp2_fast((float)(end - G)) : 0.f;
+        tab[2 * C + lane] = beta;
+        tab[3 * C + lane] = exp2_fast((float)end);
+    }
+    const T* const k = (const T*)a.k.p + bl.start * a.k.stride + (int64_t)(h / a.k.share) * DK;
+    const T* const q = (const T*)a.q.p + bl.start * a.q.stride + (int64_t)(h / a.q.share) * DK;
+    auto row = [&](int t) { return 16 * t + lr < bl.cnt ? 16 * t + lr : bl.cnt - 1; };   // rows without a token: the last one's
+    constexpr int SN = DK / 32;
+    auto read = [&](Frag8<T> (&f)[SN], const T* p, int64_t stride, int t) {
+#pragma unroll
+        for (int s = 0; s < SN; ++s) f[s] = frag_at(p + row(t) * stride + 32 * s + 8 * lg);
+    };
+    __syncthreads();
+    const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+    Frag8<T> own[SN];
+    // keys of the wave's rows against all before: M beta, rows i in lanes
+    read(own, k, a.k.stride, wave);
+#pragma unroll
+    for (int tj = 0; tj < 4; ++tj) {
+        if (tj > wave) continue;
+        Frag8<T> other[SN];
+        read(other, k, a.k.stride, tj);
+        f32x4_t m = zero;
+#pragma unroll
+        for (int s = 0; s < SN; ++s) m = mma(other[s], own[s], m);
+        const int i = 16 * wave + lr, j = 16 * tj + 4 * lg;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) m[r] = j + r < i ? m[r] * sums.ratio(i, j + r) : 0.f;
+        *reinterpret_cast<f32x4_t*>(sx + i * kLd + j) = m * *reinterpret_cast<const f32x4_t*>(s_beta + j);
+        if constexpr (GRAD) *reinterpret_cast<f32x4_t*>(sz + i * kLd + j) = m * s_beta[i];
+    }
+    // scores, as operands: rows i of the wave, or (transposed) its rows j
+    char* const p = a.p + slot * kTriBytes;
+    if constexpr (!GRAD) read(own, q, a.q.stride, wave);
+#pragma unroll
+    for (int s2 = 0; s2 < 2; ++s2) {
+        float x[8];
+        bool some = false;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int t = 2 * s2 + half;
+            const bool in = GRAD ? t >= wave : t <= wave;
+            some |= in;
+            f32x4_t d = zero;
+            if (in) {
+                Frag8<T> other[SN];
+                read(other, GRAD ? q : k, GRAD ? a.q.stride : a.k.stride, t);
+#pragma unroll
+                for (int s = 0; s < SN; ++s) d = mma(other[s], own[s], d);
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int c = 16 * t + 4 * lg + r, w = 16 * wave + lr, i = GRAD ? c : w, j = GRAD ? w : c;
+                x[4 * half + r] = in && j <= i ? d[r] * sums.ratio(i, j) * a.scale : 0.f;
+            }
+        }
+        if (some) put_operand<T, GRAD ? kThree<T> : kTwo<T>>(p, GRAD ? tri_piece_t(wave, s2) : tri_piece(wave, s2), lane, x);
+    }
+    __syncthreads();
+    invert(sx, wave, lane);
+    if constexpr (GRAD) invert(sz, wave, lane);
+    char* const xo = a.x + slot * kTriBytes;
+#pragma unroll
+    for (int s2 = 0; s2 < 2; ++s2) {
+        float x[8];
+        if (2 * s2 <= wave) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const f32x4_t v = *reinterpret_cast<const f32x4_t*>(sx + (16 * wave + lr) * kLd + 32 * s2 + 16 * half + 4 * lg);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) x[4 * half + r] = 2 * s2 + half <= wave ? v[r] : 0.f;
+            }
+            put_operand<T, kThree<T>>(xo, tri_piece(wave, s2), lane, x);
+        }
+        if constexpr (GRAD) {
+            if (2 * s2 + 1 >= wave) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int t = 2 * s2 + (e >> 2);
+                    x[e] = t >= wave ? sz[(16 * t + 4 * lg + (e & 3)) * kLd + 16 * wave + lr] : 0.f;
+                }
+                put_operand<T, kThree<T>>(a.z + slot * kTriBytes, tri_piece_t(wave, s2), lane, x);
+            }
+        }
+    }
+}
+
+enum : int { kGdrOut = 0, kGdrStates = 1, kGdrBack = 2 };
+
+// LDS of the walks: rows of k and q, 64 columns of v or dy, operand tiles of the
+// inverse and the scores, the tables; twice where two fit (the next chunk's are
+// then copied while this one is worked on).
+template <typename T, int DK, int MODE> constexpr int walk_bytes() {
+    return C * DK * (int)sizeof(T) * (MODE == kGdrStates ? 1 : 2) + C * 64 * (int)sizeof(T) +
+           kTri<T, kThree<T>> + (MODE == kGdrStates ? 0 : MODE == kGdrOut ? kTri<T, kTwo<T>> : kTri<T, kThree<T>>) + kGdrTab * 4;
+}
+template <typename T, int DK, int MODE> constexpr int walk_bufs() { return 2 * walk_bytes<T, DK, MODE>() <= 160 * 1024 ? 2 : 1; }
+
+template <int BYTES>
+__device__ __forceinline__ void copy_flat(char* lds, const char* src, int wave, int lane) {
+    static_assert(BYTES % 1024 == 0, "whole copies");
+#pragma unroll
+    for (int i = 0; i < (BYTES + 4095) / 4096; ++i)
+        if ((i + 1) * 4096 <= BYTES || wave * 1024 + i * 4096 < BYTES)
+            copy16(uni(lds_addr(lds) + wave * 1024 + i * 4096), src, (unsigned)(wave * 1024 + i * 4096 + lane * 16));
+}
+
+// A walk over a sequence's chunks: a workgroup has 64 value columns of a head, a
+// wave 16 of them, the state (or its gradient) in its accumulators.
+template <typename T, int DK, int MODE>
+__global__ __launch_bounds__(256, 1) void gdr_walk_kernel(GdrArgs a) {
+    constexpr int SN = DK / 32, KT = DK / 16, N3 = kThree<T>, NPP = MODE == kGdrOut ? kTwo<T> : N3, NB = walk_bufs<T, DK, MODE>(), SZ = (int)sizeof(T);
+    constexpr bool kBack = MODE == kGdrBack, kQ = MODE != kGdrStates;
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6), lr = lane & 15, lg = lane >> 4;
+    const int H = a.at.H, DV = a.head_v, slices = DV / 64, chains = a.at.num_seqs * H;
+    // the slices of a head read the same rows: 8 heads apart in the launch, so
+    // that they run on one XCD
+    const int group = uni(blockIdx.x / (8 * slices)), rem = blockIdx.x - group * 8 * slices;
+    const int width = chains - group * 8 < 8 ? chains - group * 8 : 8;
+    const int slice = uni(rem / width), chain = group * 8 + rem - slice * width;
+    const int n = uni(chain / H), h = chain - n * H;
+    const int64_t begin = uni64(seq_at(a.at, n)), end_at = uni64(seq_at(a.at, n + 1));
+    const int cnt = (int)(end_at > begin ? end_at - begin : 0);
+    const int fb = uni(first_block(a.at, n));
+    int nch = (cnt + C - 1) / C;
+    nch = nch < a.at.nblocks - fb ? nch : a.at.nblocks - fb;   // offsets out of order: stay inside the workspace
+    const Rows rows{cnt, nch * C, false};
+    const int col0 = slice * 64, wcol = 16 * wave;
+    const int64_t DKV = (int64_t)DK * DV;
+
+    Src xk, xq, xv, xo;
+    xk.set((const T*)a.k.p, begin * a.k.stride + (int64_t)(h / a.k.share) * DK, a.k.stride);
+    xq.set((const T*)a.q.p, begin * a.q.stride + (int64_t)(h / a.q.share) * DK, a.q.stride);
+    if constexpr (kBack) xv.set((const T*)a.dy, (begin * H + h) * DV + col0, (int64_t)H * DV);
+    else xv.set((const T*)a.v.p, begin * a.v.stride + (int64_t)h * DV + col0, a.v.stride);
+    if constexpr (MODE == kGdrOut) xo.set((const T*)a.y, (begin * H + h) * DV + col0, (int64_t)H * DV);
+    const float scale = pin(a.scale);
+
+    struct Buf {
+        T *k, *q, *v;
+        char *x, *p;
+        float* tab;
+    };
+    auto buf = [&](int c) {
+        char* at = smem + (NB == 2 ? (c & 1) * walk_bytes<T, DK, MODE>() : 0);
+        Buf f;
+        f.k = reinterpret_cast<T*>(at);
+        at += C * DK * SZ;
+        f.q = reinterpret_cast<T*>(at);
+        if (kQ) at += C * DK * SZ;
+        f.v = reinterpret_cast<T*>(at);
+        at += C * 64 * SZ;
+        f.x = at;
+        at += kTri<T, N3>;
+        f.p = at;
+        if (kQ) at += kTri<T, NPP>;
+        f.tab = reinterpret_cast<float*>(at);
+        return f;
+    };
+    auto fetch = [&](int c) {
+        const Buf f = buf(c);
+        const int m0 = c * C;
+        const int64_t slot = (int64_t)(fb + c) * H + h;
+        copy_tile<T, DK>(f.k, xk, rows, m0, wave, lane);
+        copy_tile<T, 64>(f.v, xv, rows, m0, wave, lane);
+        copy_flat<kTri<T, N3>>(f.x, (kBack ? a.z : a.x) + slot * kTriBytes, wave, lane);
+        if constexpr (kQ) {
+            copy_tile<T, DK>(f.q, xq, rows, m0, wave, lane);
+            copy_flat<kTri<T, NPP>>(f.p, a.p + slot * kTriBytes, wave, lane);
+        }
+        if (wave == 3) copy16(uni(lds_addr(f.tab)), a.tab + slot * kGdrTab, (unsigned)lane * 16);
+    };
+    // channel of the state's tile i, row r of this lane
+    auto channel = [&](int i, int r) { return 32 * (i >> 1) + 8 * lg + 4 * (i & 1) + r; };
+
+    f32x4_t S[KT];
+    {
+        const float* s0 = kBack ? a.d_final : a.initial;
+        if (s0) s0 += ((int64_t)n * H + h) * DKV + col0 + wcol + lr;
+#pragma unroll
+        for (int i = 0; i < KT; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) S[i][r] = s0 ? s0[(int64_t)channel(i, r) * DV] : 0.f;
+    }
+    // stores of a chunk, issued behind the copies of the next one
+    constexpr int NST = NB == 1 ? 0 : MODE == kGdrOut ? 4 : KT * 4 + 16;
+    if (nch > 0) fetch(kBack ? nch - 1 : 0);
+    wait_vmcnt<0>();
+    for (int step = 0; step < nch; ++step) {
+        const int c = kBack ? nch - 1 - step : step, m0 = c * C;
+        const bool more = step + 1 < nch;
+        const int next = kBack ? c - 1 : c + 1;
+        // the chunk's copies are there; the chunk before is read
+        if (step > 0) wait_vmcnt<NST>();
+        barrier_keep_loads();
+        if (NB == 2 && more) fetch(next);
+        const Buf f = buf(c);
+        const int64_t slot = (int64_t)(fb + c) * H + h;
+        const float end = unif(f.tab[3 * C]);
+        const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+        unsigned long long lost = 0;   // columns of a state that is not finite and that a decay of 0 ends here
+        if (MODE == kGdrOut && end == 0.f) {
+            float m = 0.f;
+#pragma unroll
+            for (int i = 0; i < KT; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) m += S[i][r] * 0.f;
+            m += __shfl_xor(m, 16);
+            m += __shfl_xor(m, 32);
+            lost = __ballot(!(m == 0.f));
+            if (!(m == 0.f)) {
+#pragma unroll
+                for (int i = 0; i < KT; ++i) S[i] = zero;
+            }
+        }
+        if constexpr (MODE != kGdrOut) {
+            // the state before the chunk, or the gradient behind it
+            float* const dst = (kBack ? a.rstates : a.states) + slot * DKV + col0 + wcol;
+            const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(dst, 0, (unsigned)(DKV * 4), 0x00027000);
+#pragma unroll
+            for (int i = 0; i < KT; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[i][r]), rsrc,
+                                                          (unsigned)((channel(i, r) * DV + lr) * 4), 0, 0);
+        }
+        // K S (or K R), a lane 4 tokens of a column
+        Frag8<T> fs[SN][N3];
+        f32x4_t ks[4] = {zero, zero, zero, zero};
+#pragma unroll
+        for (int s = 0; s < SN; ++s) {
+            float x[8];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                x[r] = S[2 * s][r];
+                x[4 + r] = S[2 * s + 1][r];
+            }
+            split(x, fs[s]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const Frag8<T> fk[1] = {Tile<T, DK>::rows8(f.k, 16 * t, s, lane)};
+                ks[t] = mma_parts(fk, fs[s], ks[t]);
+            }
+        }
+        f32x4_t in[4], out[4], beta[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            in[t] = *reinterpret_cast<const f32x4_t*>(f.tab + 16 * t + 4 * lg);
+            out[t] = *reinterpret_cast<const f32x4_t*>(f.tab + C + 16 * t + 4 * lg);
+            beta[t] = *reinterpret_cast<const f32x4_t*>(f.tab + 2 * C + 16 * t + 4 * lg);
+        }
+        // the wave's columns of v (or dy), a lane 4 tokens of each tile
+        const Frag8<T> fv[2] = {Tile<T, 64>::cols(f.v, wcol, 0, lane), Tile<T, 64>::cols(f.v, wcol, 1, lane)};
+        // two 16-token tiles as an operand in parts
+        auto operand = [&](const f32x4_t& lo, const f32x4_t& hi, auto& o) {
+            float x[8];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                x[r] = lo[r];
+                x[4 + r] = hi[r];
+            }
+            split(x, o);
+        };
+        f32x4_t e[4];      // V - exp(G) K S, then E; backwards P^T dY + exp(G_63 - G) K R, then U
+        Frag8<T> fe[2][N3];
+        if constexpr (!kBack) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) e[t][r] = fv[t >> 1].get(4 * (t & 1) + r) - in[t][r] * ks[t][r];
+        } else {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                e[t] = out[t] * ks[t];
+#pragma unroll
+                for (int s2 = 0; s2 < 2; ++s2) {
+                    if (2 * s2 + 1 < t) continue;
+                    Frag8<T> fp[NPP];
+                    get_operand<T, NPP>(f.p, tri_piece_t(t, s2), lane, fp);
+                    const Frag8<T> d[1] = {fv[s2]};
+                    e[t] = mma_parts(fp, d, e[t]);
+                }
+            }
+        }
+#pragma unroll
+        for (int s2 = 0; s2 < 2; ++s2) operand(e[2 * s2], e[2 * s2 + 1], fe[s2]);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            e[t] = zero;
+#pragma unroll
+            for (int s2 = 0; s2 < 2; ++s2) {
+                if (kBack ? 2 * s2 + 1 < t : 2 * s2 > t) continue;
+                Frag8<T> fx[N3];
+                get_operand<T, N3>(f.x, kBack ? tri_piece_t(t, s2) : tri_piece(t, s2), lane, fx);
+                e[t] = mma_parts(fx, fe[s2], e[t]);
+            }
+        }
+        if constexpr (MODE != kGdrOut) {
+            float* const dst = (kBack ? a.u : a.errors) + slot * C * DV + col0 + wcol;
+            const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(dst, 0, (unsigned)(C * DV * 4), 0x00027000);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(e[t][r]), rsrc,
+                                                          (unsigned)(((16 * t + 4 * lg + r) * DV + lr) * 4), 0, 0);
+        }
+        if constexpr (MODE == kGdrOut) {
+            // y, transposed tiles: a lane 4 columns of token 16 t + l % 16
+            f32x4_t y[4];
+            Frag8<T> fb[2][NPP];
+#pragma unroll
+            for (int s2 = 0; s2 < 2; ++s2) operand(beta[2 * s2] * e[2 * s2], beta[2 * s2 + 1] * e[2 * s2 + 1], fb[s2]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                y[t] = zero;
+#pragma unroll
+                for (int s = 0; s < SN; ++s) {
+                    // the state's leading 16 bits
+                    const Frag8<T> fq[1] = {Tile<T, DK>::rows8(f.q, 16 * t, s, lane)};
+                    Frag8<T> f2[NPP];
+#pragma unroll
+                    for (int p = 0; p < NPP; ++p) f2[p] = fs[s][p];
+                    y[t] = mma_parts(f2, fq, y[t]);
+                }
+                y[t] *= f.tab[16 * t + lr] * scale;
+#pragma unroll
+                for (int s2 = 0; s2 < 2; ++s2) {
+                    if (2 * s2 > t) continue;
+                    Frag8<T> fp[NPP];
+                    get_operand<T, NPP>(f.p, tri_piece(t, s2), lane, fp);
+                    y[t] = mma_parts(fb[s2], fp, y[t]);
+                }
+                if (lost) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if ((lost >> (4 * lg + r) & 1) && f.tab[16 * t + lr] != 0.f) y[t][r] = __builtin_nanf("");
+                }
+            }
+            // rows without a token lie behind the bound and are dropped
+            const unsigned step_o = xo.step;
+            const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(xo.token(m0)), 0,
+                                                                uni((unsigned)(rows.tokens(m0) - 1) * step_o + 64 * SZ), 0x00027000);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const unsigned at = (unsigned)(16 * t + lr) * step_o + (unsigned)((wcol + 4 * lg) * SZ);
+                if constexpr (SZ == 4) {
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, y[t]), rsrc, at, 0, 0);
+                } else {
+                    const u32x2_t o = {cvt2(y[t][0], y[t][1]), cvt2(y[t][2], y[t][3])};
+                    __builtin_amdgcn_raw_buffer_store_b64(o, rsrc, at, 0, 0);
+                }
+            }
+        }
+        // the state behind the chunk (or the gradient before it)
+#pragma unroll
+        for (int i = 0; i < KT; ++i) S[i] = end == 0.f ? zero : S[i] * end;
+#pragma unroll
+        for (int s2 = 0; s2 < 2; ++s2) {
+            Frag8<T> u[N3];
+            if constexpr (!kBack) {
+                operand(out[2 * s2] * beta[2 * s2] * e[2 * s2], out[2 * s2 + 1] * beta[2 * s2 + 1] * e[2 * s2 + 1], u);
+            } else {
+                f32x4_t d[2];
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) d[half][r] = fv[s2].get(4 * half + r) * (in[2 * s2 + half][r] * scale);
+                operand(d[0], d[1], u);
+#pragma unroll
+                for (int i = 0; i < KT; ++i) {
+                    const Frag8<T> fq[1] = {cols8<T, DK>(f.q, i >> 1, i & 1, s2, lane)};
+                    S[i] = mma_parts(fq, u, S[i]);
+                }
+                operand(-(in[2 * s2] * beta[2 * s2] * e[2 * s2]), -(in[2 * s2 + 1] * beta[2 * s2 + 1] * e[2 * s2 + 1]), u);
+            }
+#pragma unroll
+            for (int i = 0; i < KT; ++i) {
+                const Frag8<T> fk[1] = {cols8<T, DK>(f.k, i >> 1, i & 1, s2, lane)};
+                S[i] = mma_parts(fk, u, S[i]);
+            }
+        }
+        if (NB == 1 && more) {
+            barrier_keep_loads();
+            fetch(next);
+        }
+    }
+    float* dst = kBack ? a.d_initial : a.final;
+    if (dst) {
+        dst += ((int64_t)n * H + h) * DKV + col0 + wcol + lr;
+#pragma unroll
+        for (int i = 0; i < KT; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) dst[(int64_t)channel(i, r) * DV] = S[i][r];
+    }
+}
+
+// dQ, dK, dV in the inputs' type, dbeta and the tokens' terms of dg of a (chunk,
+// key head): the value heads that share the key head one after another, their
+// sums in registers.  A wave has DK / 4 channels of dQ and dK.
+template <typename T, int DK> constexpr int grad_bytes() { return 2 * C * DK * (int)sizeof(T) + 4 * kTri<T, kTwo<T>>; }
+
+template <typename T, int DK, int DV>
+__global__ __launch_bounds__(256, 1) void gdr_grad_kernel(GdrArgs a) {
+    constexpr int SV = DV / 32, SK = DK / 32, NT = DK / 64, N2 = kTwo<T>, N3 = kThree<T>, EP = 16 / (int)sizeof(T);
+    constexpr int TRI = kTri<T, N2>;
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    T* const sk = reinterpret_cast<T*>(smem);
+    T* const sq = sk + C * DK;
+    char* const w1 = reinterpret_cast<char*>(sq + C * DK);   // W beta and Y beta, rows i, then rows j
+    char* const y1 = w1 + TRI;
+    char* const w2 = y1 + TRI;
+    char* const y2 = w2 + TRI;
+    __shared__ Sums sums;
+    __shared__ __attribute__((aligned(16))) float tab[kGdrTab];
+    __shared__ float part_s[4][C], part_p[C], part_v[C];
+    const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6), lr = lane & 15, lg = lane >> 4;
+    const int H = a.at.H, r_heads = a.k.share, Hk = H / r_heads;
+    const int b = uni(blockIdx.x / Hk), hk = blockIdx.x - b * Hk;
+    const Block bl = find_block(a.at, b);
+    if (bl.n < 0 || bl.cnt == 0) return;
+    const int cnt = bl.cnt;
+    for (int i = tid; i < C * DK / EP; i += 256) {
+        const int row = i / (DK / EP), col = i % (DK / EP) * EP;
+        const int64_t tok = bl.start + (row < cnt ? row : cnt - 1);
+        *reinterpret_cast<u32x4_t*>(sk + Tile<T, DK>::off(row, col)) =
+            *reinterpret_cast<const u32x4_t*>((const T*)a.k.p + tok * a.k.stride + (int64_t)hk * DK + col);
+        *reinterpret_cast<u32x4_t*>(sq + Tile<T, DK>::off(row, col)) =
+            *reinterpret_cast<const u32x4_t*>((const T*)a.q.p + tok * a.q.stride + (int64_t)hk * DK + col);
+    }
+    const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+    f32x4_t dq[4][NT], dk[4][NT];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) dq[t][n] = dk[t][n] = zero;
+    const int ch0 = wave * (DK / 4);
+    for (int m = 0; m < r_heads; ++m) {
+        const int h = hk * r_heads + m;
+        const int64_t slot = (int64_t)b * H + h;
+        const float* const E = a.errors + slot * C * DV;
+        const float* const U = a.u + slot * C * DV;
+        const T* const dy = (const T*)a.dy + (bl.start * H + h) * DV;
+        __syncthreads();
+        tab[tid] = a.tab[slot * kGdrTab + tid];
+        if (wave == 0) {
+            const bool valid = lane < cnt;
+            sums.set(lane, decay_scan(valid && a.g ? a.g[(bl.start + lane) * H + h] : 0.f), valid);
+        }
+        __syncthreads();
+        auto dy_at = [&](int t, int s) {
+            const int row = 16 * t + lr < cnt ? 16 * t + lr : cnt - 1;
+            return frag_at(dy + (int64_t)row * H * DV + 32 * s + 8 * lg);
+        };
+        auto read_dy = [&](int t, Frag8<T> (&f)[SV][1]) {
+#pragma unroll
+            for (int s = 0; s < SV; ++s) f[s][0] = dy_at(t, s);
+        };
+        // rows of E, or of dV = beta U
+        auto part_at = [&](const float* p, int t, int s, bool scaled, auto& f) {
+            float x[8];
+            load8(p + (16 * t + lr) * DV + 32 * s + 8 * lg, x);
+            if (scaled) {
+                const float be = tab[2 * C + 16 * t + lr];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] *= be;
+            }
+            split(x, f);
+        };
+        // W and Y: rows i of the wave against all before, then its rows j against all behind
+        {
+            Frag8<T> fy[SV][1], fx[SV][N2];
+            read_dy(wave, fy);
+#pragma unroll
+            for (int s = 0; s < SV; ++s) part_at(U, wave, s, true, fx[s]);
+            const int i = 16 * wave + lr;
+            float pairs = 0.f;   // sum over j of W beta q_i.k_j, with the scores' 24 bits: an fp32 output's
+#pragma unroll
+            for (int tj = 0; tj < 4; ++tj) {
+                if (tj > (wave | 1)) continue;
+                f32x4_t w = zero, y = zero, qk = zero;
+                if (tj <= wave) {
+#pragma unroll
+                    for (int s = 0; s < SV; ++s) {
+                        Frag8<T> e3[N3], e2[N2];
+                        part_at(E, tj, s, false, e3);
+                        w = mma_parts(e3, fy[s], w);
+#pragma unroll
+                        for (int p = 0; p < N2; ++p) e2[p] = e3[p];
+                        y = mma_parts(e2, fx[s], y);
+                    }
+#pragma unroll
+                    for (int s = 0; s < SK; ++s)
+                        qk = mma(Tile<T, DK>::rows8(sk, 16 * tj, s, lane), Tile<T, DK>::rows8(sq, 16 * wave, s, lane), qk);
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int j = 16 * tj + 4 * lg + r;
+                    const float d = j <= i ? sums.ratio(i, j) * tab[2 * C + j] : 0.f;
+                    w[r] = j <= i ? w[r] * d * a.scale : 0.f;
+                    y[r] = j < i ? -y[r] * d : 0.f;
+                    pairs += w[r] * qk[r];
+                }
+                put_half<T>(w1, tri_piece(wave, tj >> 1), tj & 1, lane, w);
+                put_half<T>(y1, tri_piece(wave, tj >> 1), tj & 1, lane, y);
+            }
+            pairs += __shfl_xor(pairs, 16);
+            pairs += __shfl_xor(pairs, 32);
+            if (lg == 0) part_p[i] = pairs;
+            Frag8<T> fe[SV][N2];
+#pragma unroll
+            for (int s = 0; s < SV; ++s) part_at(E, wave, s, false, fe[s]);
+            const int j = 16 * wave + lr;
+#pragma unroll
+            for (int ti = 0; ti < 4; ++ti) {
+                if (ti < (wave & ~1)) continue;
+                f32x4_t w = zero, y = zero;
+                if (ti >= wave) {
+                    read_dy(ti, fy);
+#pragma unroll
+                    for (int s = 0; s < SV; ++s) {
+                        part_at(U, ti, s, true, fx[s]);
+                        w = mma_parts(fy[s], fe[s], w);
+                        y = mma_parts(fx[s], fe[s], y);
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int i = 16 * ti + 4 * lg + r;
+                    const float d = j <= i ? sums.ratio(i, j) * tab[2 * C + j] : 0.f;
+                    w[r] = j <= i ? w[r] * d * a.scale : 0.f;
+                    y[r] = j < i ? -y[r] * d : 0.f;
+                }
+                put_half<T>(w2, tri_piece_t(wave, ti >> 1), ti & 1, lane, w);
+                put_half<T>(y2, tri_piece_t(wave, ti >> 1), ti & 1, lane, y);
+            }
+        }
+        __syncthreads();
+        // the states' parts, the wave's channels
+        f32x4_t sq_[4][NT], sa[4][NT], sb[4][NT];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) sq_[t][n] = sa[t][n] = sb[t][n] = zero;
+#pragma unroll
+        for (int s = 0; s < SV; ++s) {
+            Frag8<T> s3[NT][N3], s2[NT][N2], r2[NT][N2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int64_t at = slot * DK * DV + (int64_t)(ch0 + 16 * n + lr) * DV + 32 * s + 8 * lg;
+                float x[8];
+                load8(a.states + at, x);
+                split(x, s3[n]);
+#pragma unroll
+                for (int p = 0; p < N2; ++p) s2[n][p] = s3[n][p];
+                load8(a.rstates + at, x);
+                split(x, r2[n]);
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const Frag8<T> fy[1] = {dy_at(t, s)};
+                Frag8<T> fx[N2], fe[N2];
+                part_at(U, t, s, true, fx);
+                part_at(E, t, s, false, fe);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    sq_[t][n] = mma_parts(fy, s3[n], sq_[t][n]);
+                    sa[t][n] = mma_parts(fx, s2[n], sa[t][n]);
+                    sb[t][n] = mma_parts(fe, r2[n], sb[t][n]);
+                }
+            }
+        }
+        float dot[4][4];   // q . (state's part of dq)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const f32x4_t in = *reinterpret_cast<const f32x4_t*>(tab + 16 * t + 4 * lg);
+            const f32x4_t out = *reinterpret_cast<const f32x4_t*>(tab + C + 16 * t + 4 * lg);
+            const f32x4_t beta = *reinterpret_cast<const f32x4_t*>(tab + 2 * C + 16 * t + 4 * lg);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) dot[t][r] = 0.f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                sq_[t][n] *= in * a.scale;
+                dq[t][n] += sq_[t][n];
+                dk[t][n] += out * beta * sb[t][n] - in * sa[t][n];
+            }
+        }
+        // inside the chunk
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const Frag8<T> fk[2] = {Tile<T, DK>::cols(sk, ch0 + 16 * n, 0, lane), Tile<T, DK>::cols(sk, ch0 + 16 * n, 1, lane)};
+            const Frag8<T> fq[2] = {Tile<T, DK>::cols(sq, ch0 + 16 * n, 0, lane), Tile<T, DK>::cols(sq, ch0 + 16 * n, 1, lane)};
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) dot[t][r] += fq[t >> 1].get(4 * (t & 1) + r) * sq_[t][n][r];
+#pragma unroll
+                for (int s2 = 0; s2 < 2; ++s2) {
+                    const Frag8<T> bk[1] = {fk[s2]}, bq[1] = {fq[s2]};
+                    Frag8<T> f[N2];
+                    if (2 * s2 <= t) {
+                        get_operand<T, N2>(w1, tri_piece(t, s2), lane, f);
+                        dq[t][n] = mma_parts(f, bk, dq[t][n]);
+                        get_operand<T, N2>(y1, tri_piece(t, s2), lane, f);
+                        dk[t][n] = mma_parts(f, bk, dk[t][n]);
+                    }
+                    if (2 * s2 + 1 >= t) {
+                        get_operand<T, N2>(w2, tri_piece_t(t, s2), lane, f);
+                        dk[t][n] = mma_parts(f, bq, dk[t][n]);
+                        get_operand<T, N2>(y2, tri_piece_t(t, s2), lane, f);
+                        dk[t][n] = mma_parts(f, bk, dk[t][n]);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float u = row16_sum(dot[t][r]);
+                if (lr == 0) part_s[wave][16 * t + 4 * lg + r] = u;
+            }
+        // dv = beta u, v.dv and e.u by tokens: 4 threads a token
+        {
+            const int row = tid >> 2, c0 = (tid & 3) * (DV / 4);
+            float s = 0.f, eu = 0.f;
+            if (row < cnt) {
+                const int64_t tok = bl.start + row;
+                const T* const v = (const T*)a.v.p + tok * a.v.stride + (int64_t)h * DV + c0;
+                T* const o = (T*)a.dv_out + (tok * H + h) * DV + c0;
+                const float be = tab[2 * C + row];
+#pragma unroll
+                for (int c = 0; c < DV / 4; c += 8) {
+                    float x[8], z[8];
+                    load8(U + row * DV + c0 + c, x);
+                    load8(E + row * DV + c0 + c, z);
+#pragma unroll
+                    for (int e = 0; e < 8; e += EP) {
+                        float u[EP], w[EP];
+                        load_vec<T, EP>(v + c + e, u);
+#pragma unroll
+                        for (int i = 0; i < EP; ++i) {
+                            eu += z[e + i] * x[e + i];
+                            w[i] = be * x[e + i];
+                            s += u[i] * w[i];
+                        }
+                        store_vec<T, EP>(o + c + e, w);
+                    }
+                }
+            }
+            s += dpp_mov<0xB1>(s);
+            s += dpp_mov<0x4E>(s);
+            eu += dpp_mov<0xB1>(eu);
+            eu += dpp_mov<0x4E>(eu);
+            if ((tid & 3) == 0) {
+                part_v[row] = s;
+                if (row < cnt) a.dbeta[(bl.start + row) * H + h] = eu;
+            }
+        }
+        __syncthreads();
+        if (tid < cnt && a.dg)
+            a.terms[slot * C + tid] = ((part_s[0][tid] + part_s[1][tid]) + (part_s[2][tid] + part_s[3][tid])) +
+                                      (part_p[tid] - part_v[tid]);
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = 16 * t + 4 * lg + r;
+            if (row >= cnt) continue;
+            const int64_t at = ((bl.start + row) * Hk + hk) * DK + ch0 + lr;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                gstore((T*)a.dq + at + 16 * n, dq[t][n][r]);
+                gstore((T*)a.dk + at + 16 * n, dk[t][n][r]);
+            }
+        }
+}
+
+// dg of a block of kBlock chunks of a (sequence, head): the sum of the terms from
+// each token to the block's end, and the product of the state there with its
+// gradient, which stands for all that is behind.  In fp64: where decays are
+// strong the tokens take nearly all of the product away again.
+__global__ __launch_bounds__(256) void gdr_decay_kernel(GdrArgs a, int size) {
+    __shared__ double part[5];
+    double& carry = part[4];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int H = a.at.H, b = uni(blockIdx.x / H), h = blockIdx.x - b * H;
+    const Block bl = find_block(a.at, b);   // the block's last chunk, or none
+    if (bl.n < 0 || bl.cnt == 0) return;
+    const bool last = bl.j == bl.nb - 1;
+    if (!last && bl.j % kBlock != kBlock - 1) return;
+    const int first = b - bl.j % kBlock;
+    const float *S = nullptr, *R = nullptr;
+    if (!last && b + 1 < a.at.nblocks) {
+        S = a.states + ((int64_t)(b + 1) * H + h) * size;
+        R = a.rstates + ((int64_t)b * H + h) * size;
+    } else if (a.d_final) {
+        S = a.final + ((int64_t)bl.n * H + h) * size;
+        R = a.d_final + ((int64_t)bl.n * H + h) * size;
+    }
+    double e = 0.0;
+    if (S) {
+#pragma unroll 8
+        for (int i = tid * 4; i < size; i += 1024) {
+            const f32x4_t u = *reinterpret_cast<const f32x4_t*>(S + i), v = *reinterpret_cast<const f32x4_t*>(R + i);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) e += (double)u[r] * (double)v[r];
+        }
+#pragma unroll
+        for (int d = 32; d > 0; d >>= 1) e += shfl_d(e, lane ^ d);
+    }
+    if (lane == 0) part[wave] = e;
+    __syncthreads();
+    if (tid == 0) carry = (part[0] + part[1]) + (part[2] + part[3]);
+    __syncthreads();
+    // from the block's end, 4 chunks at a time
+    for (int c = b; c >= first; c -= 4) {
+        const int mine = c - (3 - wave);            // the wave's chunk; the last one by wave 3
+        const bool in = mine >= first && (mine < b || lane < bl.cnt);
+        double d = in ? (double)a.terms[((int64_t)mine * H + h) * C + lane] : 0.0;
+#pragma unroll
+        for (int k = 1; k < kWave; k <<= 1) {
+            const double o = shfl_d(d, lane + k < kWave ? lane + k : lane);
+            if (lane + k < kWave) d += o;
+        }
+        if (lane == 0) part[wave] = d;
+        __syncthreads();
+        double v = carry + d;
+        for (int w = wave + 1; w < 4; ++w) v += part[w];
+        __syncthreads();
+        if (tid == 0) carry = v;
+        if (in) a.dg[(bl.start + (int64_t)(mine - b) * C + lane) * H + h] = (float)v;
+        __syncthreads();
+    }
+}
+
+template <typename T, int DK, bool GRAD>
+hipError_t prep_t(const GdrArgs& a) {
+    if (a.at.T_total == 0) return hipSuccess;
+    hipLaunchKernelGGL((gdr_prep_kernel<T, DK, GRAD>), dim3((unsigned)((int64_t)a.at.nblocks * a.at.H)), dim3(256), 0,
+                       (hipStream_t)a.at.stream, a);
+    return hipGetLastError();
+}
+
+template <typename T, int DK, int MODE>
+hipError_t walk_t(const GdrArgs& a) {
+    constexpr int lds = walk_bytes<T, DK, MODE>() * walk_bufs<T, DK, MODE>();
+    static_assert(lds <= 160 * 1024, "LDS");
+    const void* kern = reinterpret_cast<const void*>(&gdr_walk_kernel<T, DK, MODE>);
+    const hipError_t e = ensure_lds_limit(kern, lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((gdr_walk_kernel<T, DK, MODE>), dim3((unsigned)((int64_t)a.at.num_seqs * a.at.H * (a.head_v / 64))),
+                       dim3(256), lds, (hipStream_t)a.at.stream, a);
+    return hipGetLastError();
+}
+
+template <typename T, int DK, int DV>
+hipError_t grad_t(const GdrArgs& a) {
+    if (a.at.T_total == 0) return hipSuccess;
+    constexpr int lds = grad_bytes<T, DK>();
+    const void* kern = reinterpret_cast<const void*>(&gdr_grad_kernel<T, DK, DV>);
+    const hipError_t e = ensure_lds_limit(kern, lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((gdr_grad_kernel<T, DK, DV>), dim3((unsigned)((int64_t)a.at.nblocks * (a.at.H / a.k.share))),
+                       dim3(256), lds, (hipStream_t)a.at.stream, a);
+    return hipGetLastError();
+}
+
+template <typename T, int DK>
+hipError_t fwd_t(const GdrArgs& a) {
+    const hipError_t e = prep_t<T, DK, false>(a);
+    return e != hipSuccess ? e : walk_t<T, DK, kGdrOut>(a);
+}
+
+template <typename T, int DK>
+hipError_t bwd_t(const GdrArgs& a) {
+    hipError_t e = prep_t<T, DK, true>(a);
+    if (e != hipSuccess) return e;
+    if (a.at.T_total > 0 && (e = walk_t<T, DK, kGdrStates>(a)) != hipSuccess) return e;
+    if ((a.at.T_total > 0 || a.d_initial) && (e = walk_t<T, DK, kGdrBack>(a)) != hipSuccess) return e;
+    if ((e = a.head_v == 64 ? grad_t<T, DK, 64>(a) : grad_t<T, DK, 128>(a)) != hipSuccess) return e;
+    if (!a.dg || a.at.T_total == 0) return hipSuccess;
+    hipLaunchKernelGGL(gdr_decay_kernel, dim3((unsigned)((int64_t)a.at.nblocks * a.at.H)), dim3(256), 0,
+                       (hipStream_t)a.at.stream, a, a.head_k * a.head_v);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_gdr_fwd(const GdrArgs& a) {
+    const hipError_t e = launch_block_plan(a.at);
+    if (e != hipSuccess) return e;
+    if (a.dtype == 0) return a.head_k == 64 ? fwd_t<__bf16, 64>(a) : fwd_t<__bf16, 128>(a);
+    return a.head_k == 64 ? fwd_t<float, 64>(a) : fwd_t<float, 128>(a);
+}
+
+hipError_t launch_gdr_bwd(const GdrArgs& a) {
+    const hipError_t e = launch_block_plan(a.at);
+    if (e != hipSuccess) return e;
+    if (a.dtype == 0) return a.head_k == 64 ? bwd_t<__bf16, 64>(a) : bwd_t<__bf16, 128>(a);
+    return a.head_k == 64 ? bwd_t<float, 64>(a) : bwd_t<float, 128>(a);
+}
+
+// One token a request against the resident fp32 state [N, H, dk, dv], updated in
+// place.  Columns of a state are independent: a workgroup takes COLS of them, all
+// or narrow slices to spread few states over the CUs.  S^T k and S^T q are summed
+// in one pass over the state in registers (S' ^T q = exp(g) S^T q + beta (k.q) e), so
+// it crosses memory once each way, which bounds the step.
+namespace {
+
+template <typename T, int DK, int COLS>
+__global__ __launch_bounds__(256) void gdr_decode_kernel(GdrDecodeArgs a) {
+    constexpr int CG = COLS / 4, RG = 256 / CG, RPT = DK / RG;
+    static_assert(RG * CG == 256 && RPT * RG == DK, "decode tiling");
+    __shared__ float s_k[DK], s_q[DK], s_e[COLS], s_kq[RG];
+    __shared__ float s_p[RG][COLS + 4], s_o[RG][COLS + 4];
+    const int tid = threadIdx.x, cg = tid % CG, rg = tid / CG;
+    const int slices = a.dv / COLS;
+    // whole states: each XCD takes them in runs of two (workgroups i, i + 8,
+    // ... share one), as the KDA decode step does
+    int id = blockIdx.x;
+    if (slices == 1 && gridDim.x % 16 == 0) id = id / 16 * 16 + id % 8 * 2 + id / 8 % 2;
+    const int nh = id / slices, col0 = (id % slices) * COLS;
+    const int n = nh / a.H, h = nh % a.H;
+    float* st = a.state + (int64_t)nh * DK * a.dv + col0 + 4 * cg;
+    f32x4_t S[RPT];
+#pragma unroll
+    for (int r = 0; r < RPT; ++r) S[r] = __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(st + (int64_t)(r * RG + rg) * a.dv));
+    const T* q = (const T*)a.q.p + (int64_t)n * a.q.stride + (int64_t)(h / a.q.share) * DK;
+    const T* k = (const T*)a.k.p + (int64_t)n * a.k.stride + (int64_t)(h / a.k.share) * DK;
+    const T* v = (const T*)a.v.p + (int64_t)n * a.v.stride + (int64_t)h * a.dv + col0;
+    for (int c = tid; c < DK; c += 256) {
+        s_k[c] = gload(k + c);
+        s_q[c] = gload(q + c);
+    }
+    const float vt = tid < COLS ? gload(v + tid) : 0.f;
+    const float decay = a.g ? expf(a.g[nh]) : 1.f, beta = a.beta[nh];
+    if (decay == 0.f) {   // anew, whatever the state holds
+#pragma unroll
+        for (int r = 0; r < RPT; ++r) S[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+    __syncthreads();
+    f32x4_t p = {0.f, 0.f, 0.f, 0.f}, o = p;
+    float kq = 0.f;
+#pragma unroll
+    for (int r = 0; r < RPT; ++r) {
+        const int row = r * RG + rg;
+        S[r] *= decay;
+        p += s_k[row] * S[r];
+        o += s_q[row] * S[r];
+        kq += s_k[row] * s_q[row];
+    }
+    if (cg == 0) s_kq[rg] = kq;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        s_p[rg][4 * cg + i] = p[i];
+        s_o[rg][4 * cg + i] = o[i];
+    }
+    __syncthreads();
+    if (tid < COLS) {
+        float x = 0.f, y = 0.f, z = 0.f;
+#pragma unroll
+        for (int r = 0; r < RG; ++r) {
+            x += s_p[r][tid];
+            y += s_o[r][tid];
+            z += s_kq[r];
+        }
+        const float e = beta * (vt - x);
+        s_e[tid] = e;
+        gstore((T*)a.y + (int64_t)nh * a.dv + col0 + tid, a.scale * (y + z * e));
+    }
+    __syncthreads();
+    const f32x4_t e = {s_e[4 * cg], s_e[4 * cg + 1], s_e[4 * cg + 2], s_e[4 * cg + 3]};
+#pragma unroll
+    for (int r = 0; r < RPT; ++r) {
+        const int row = r * RG + rg;
+        __builtin_nontemporal_store(S[r] + s_k[row] * e, reinterpret_cast<f32x4_t*>(st + (int64_t)row * a.dv));
+    }
+}
+
+template <typename T, int DK, int COLS>
+hipError_t decode_t(const GdrDecodeArgs& a) {
+    hipLaunchKernelGGL((gdr_decode_kernel<T, DK, COLS>), dim3((unsigned)((int64_t)a.N * a.H * (a.dv / COLS))), dim3(256),
+                       0, (hipStream_t)a.stream, a);
+    return hipGetLastError();
+}
+
+template <typename T, int DK>
+hipError_t decode_c(const GdrDecodeArgs& a) {
+    if (a.N * (int64_t)a.H < 512) return decode_t<T, DK, 16>(a);
+    return a.dv == 64 ? decode_t<T, DK, 64>(a) : decode_t<T, DK, 128>(a);
+}
+
+}  // namespace
+
+hipError_t launch_gdr_decode(const GdrDecodeArgs& a) {
+    if (a.N == 0) return hipSuccess;
+    if (a.dtype == 0) return a.dk == 64 ? decode_c<__bf16, 64>(a) : decode_c<__bf16, 128>(a);
+    return a.dk == 64 ? decode_c<float, 64>(a) : decode_c<float, 128>(a);
+}
+
+}  // namespace kda

@@ -243,4 +243,43 @@ struct LinDecodeArgs {
 };
 hipError_t launch_linattn_decode(const LinDecodeArgs& a);
 
+// The gated delta rule.  Per (chunk of 64 tokens, head) the workspace holds
+// operand tiles of 64 x 64 lower triangles (kTriBytes each) and the tables.
+constexpr int kTriBytes = 18 * 1024;
+constexpr int kGdrTab = 256;     // floats: decays from the chunk's start, to its end, beta, (the whole chunk's)
+struct GdrArgs {
+    LinArgs at;                  // sizes, offsets, clear, stream
+    LinRows q, k, v;
+    const void* dy;
+    const float *g, *beta;       // [T, H]; g NULL: no decay
+    float scale;
+    char *x, *z, *p;             // inverses (z: backwards) and scores
+    float* tab;
+    const float* initial;
+    float* final;                // gradient: in the workspace, or NULL
+    void* y;
+    // gradient, by chunk and head: states before it, errors of prediction; the
+    // state's gradient behind it, dv / beta; the tokens' terms of dg
+    float *states, *errors, *rstates, *u, *terms;
+    const float* d_final;
+    float* d_initial;
+    void *dq, *dk, *dv_out;
+    float *dg, *dbeta;
+    int dtype, head_k, head_v;
+};
+hipError_t launch_gdr_fwd(const GdrArgs& a);
+hipError_t launch_gdr_bwd(const GdrArgs& a);
+
+struct GdrDecodeArgs {
+    int dtype;
+    int N, H, dk, dv;
+    float scale;
+    LinRows q, k, v;
+    const float *g, *beta;
+    float* state;
+    void* y;
+    void* stream;
+};
+hipError_t launch_gdr_decode(const GdrDecodeArgs& a);
+
 }  // namespace kda

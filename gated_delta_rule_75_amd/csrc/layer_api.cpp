@@ -409,6 +409,217 @@ kda_status kda_rope(kda_dtype dt, int64_t T, int Hq, int Hk, int d, int rot, kda
 
 namespace {
 
+// Chunks of 64 tokens: (chunk, head) pairs as workgroups of 256 threads, and two a
+// head of a sequence, on an axis of less than 2^32 threads.
+constexpr int64_t kMaxChunks = int64_t(1) << 23;
+
+bool gdr_sizes_ok(kda_dtype dt, int H, int Hk, int dk, int dv, int num_seqs, int64_t T) {
+    return dtype_ok(dt) && H > 0 && Hk > 0 && H % Hk == 0 && num_seqs > 0 && T >= 0 && T <= INT32_MAX - 64 &&
+           head_ok(dk) && head_ok(dv) && (T / 64 + num_seqs) * (int64_t)H < kMaxChunks;
+}
+
+struct GdrLayout { size_t x, p, z, tab, states, rstates, errors, u, terms, s_end, plan, total; int64_t chunks; };
+GdrLayout gdr_layout(bool grad, int H, int dk, int dv, int num_seqs, int64_t T) {
+    GdrLayout l{};
+    l.chunks = T > 64 ? T / 64 + num_seqs : num_seqs;
+    Parts p;
+    if (T > 0) {
+        const size_t n = (size_t)l.chunks * H;
+        l.x = p.take(n * kda::kTriBytes);
+        l.p = p.take(n * kda::kTriBytes);
+        l.tab = p.take(n * kda::kGdrTab * 4);
+        if (grad) {
+            l.z = p.take(n * kda::kTriBytes);
+            l.states = p.take(n * dk * dv * 4);
+            l.rstates = p.take(n * dk * dv * 4);
+            l.errors = p.take(n * 64 * dv * 4);
+            l.u = p.take(n * 64 * dv * 4);
+            l.terms = p.take(n * 64 * 4);
+            l.s_end = p.take((size_t)num_seqs * H * dk * dv * 4);
+        }
+        l.plan = p.take(T > 64 ? plan_bytes(num_seqs) : 0);
+    }
+    l.total = p.at ? p.at : 256;
+    return l;
+}
+
+// What both directions check and hand on.
+kda_status gdr_args(bool grad, kda_dtype dt, int H, int Hk, int dk, int dv, float scale, int num_seqs, int64_t T_total,
+                    const int32_t* cu_seqlens, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                    const void* v, int64_t v_stride, const float* g, const float* beta, const float* initial_state,
+                    void* workspace, size_t workspace_bytes, void* stream, kda::GdrArgs& a) {
+    if (!dtype_ok(dt)) return KDA_ERR_INVALID_ARGUMENT;
+    if (!cu_seqlens && num_seqs != 1) return KDA_ERR_INVALID_ARGUMENT;
+    if (H > 0 && Hk > 0 && (!head_ok(dk) || !head_ok(dv))) return KDA_ERR_UNSUPPORTED;
+    if (!gdr_sizes_ok(dt, H, Hk, dk, dv, num_seqs, T_total)) return KDA_ERR_INVALID_ARGUMENT;
+    if (T_total > 0 && (!q || !k || !v || !beta)) return KDA_ERR_INVALID_ARGUMENT;
+    if (!rows_ok(dt, q, q_stride, Hk, dk) || !rows_ok(dt, k, k_stride, Hk, dk) || !rows_ok(dt, v, v_stride, H, dv) ||
+        (int64_t)H * dv > kMaxStride || !aligned(g, 4) || !aligned(beta, 4) || !aligned(cu_seqlens, 4) ||
+        !aligned(initial_state, 16) || !aligned(workspace, 256) || !workspace)
+        return KDA_ERR_INVALID_ARGUMENT;
+    const GdrLayout l = gdr_layout(grad, H, dk, dv, num_seqs, T_total);
+    if (workspace_bytes < l.total) return KDA_ERR_WORKSPACE_TOO_SMALL;
+    a.at.H = H;
+    a.at.num_seqs = num_seqs;
+    a.at.T_total = T_total;
+    a.at.cu_seqlens = cu_seqlens;
+    a.at.L = 64;
+    a.at.nblocks = (int)l.chunks;
+    a.at.stream = stream;
+    if (num_seqs > kPlanSeqs && T_total > 64) a.at.first = part<int32_t>(workspace, l.plan);
+    a.q = rows(q, q_stride, H / Hk);
+    a.k = rows(k, k_stride, H / Hk);
+    a.v = rows(v, v_stride, 1);
+    a.g = g;
+    a.beta = beta;
+    a.scale = scale;
+    a.x = part<char>(workspace, l.x);
+    a.p = part<char>(workspace, l.p);
+    a.tab = part<float>(workspace, l.tab);
+    a.initial = initial_state;
+    if (grad) {
+        a.z = part<char>(workspace, l.z);
+        a.states = part<float>(workspace, l.states);
+        a.rstates = part<float>(workspace, l.rstates);
+        a.errors = part<float>(workspace, l.errors);
+        a.u = part<float>(workspace, l.u);
+        a.terms = part<float>(workspace, l.terms);
+        a.final = part<float>(workspace, l.s_end);
+    }
+    a.dtype = (int)dt;
+    a.head_k = dk;
+    a.head_v = dv;
+    return KDA_OK;
+}
+
+// clear: rows of no sequence of the outputs become zeros.
+kda_status gdr_fwd(bool clear, kda_dtype dt, int H, int Hk, int dk, int dv, float scale, int num_seqs, int64_t T_total,
+                   const int32_t* cu_seqlens, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                   const void* v, int64_t v_stride, const float* g, const float* beta, const float* initial_state,
+                   float* final_state, void* y, void* workspace, size_t workspace_bytes, void* stream) {
+    kda::GdrArgs a{};
+    if ((T_total > 0 && !y) || !aligned(y, 16) || !aligned(final_state, 16)) return KDA_ERR_INVALID_ARGUMENT;
+    const kda_status st = gdr_args(false, dt, H, Hk, dk, dv, scale, num_seqs, T_total, cu_seqlens, q, q_stride, k, k_stride,
+                                   v, v_stride, g, beta, initial_state, workspace, workspace_bytes, stream, a);
+    if (st != KDA_OK) return st;
+    a.at.clear = clear;
+    a.final = final_state;
+    a.y = y;
+    return launched([&] { return kda::launch_gdr_fwd(a); });
+}
+
+kda_status gdr_bwd(bool clear, kda_dtype dt, int H, int Hk, int dk, int dv, float scale, int num_seqs, int64_t T_total,
+                   const int32_t* cu_seqlens, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                   const void* v, int64_t v_stride, const float* g, const float* beta, const float* initial_state,
+                   const void* dy, const float* d_final_state, void* dq, void* dk_out, void* dv_out, float* dg,
+                   float* dbeta, float* d_initial_state, void* workspace, size_t workspace_bytes, void* stream) {
+    kda::GdrArgs a{};
+    if (T_total > 0 && (!dy || !dq || !dk_out || !dv_out || !dbeta || (g != nullptr) != (dg != nullptr)))
+        return KDA_ERR_INVALID_ARGUMENT;
+    if (!aligned(dy, 16) || !aligned(dq, 16) || !aligned(dk_out, 16) || !aligned(dv_out, 16) || !aligned(dg, 4) ||
+        !aligned(dbeta, 4) || !aligned(d_final_state, 16) || !aligned(d_initial_state, 16))
+        return KDA_ERR_INVALID_ARGUMENT;
+    const kda_status st = gdr_args(true, dt, H, Hk, dk, dv, scale, num_seqs, T_total, cu_seqlens, q, q_stride, k, k_stride,
+                                   v, v_stride, g, beta, initial_state, workspace, workspace_bytes, stream, a);
+    if (st != KDA_OK) return st;
+    a.at.clear = clear;
+    a.dy = dy;
+    if (!d_final_state) a.final = nullptr;
+    a.d_final = d_final_state;
+    a.d_initial = d_initial_state;
+    a.dq = dq;
+    a.dk = dk_out;
+    a.dv_out = dv_out;
+    a.dg = dg;
+    a.dbeta = dbeta;
+    return launched([&] { return kda::launch_gdr_bwd(a); });
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kda_gdr_fwd_workspace_size(kda_dtype dt, int H, int Hk, int dk, int dv, int num_seqs, int64_t T_total) {
+    return gdr_sizes_ok(dt, H, Hk, dk, dv, num_seqs, T_total) ? gdr_layout(false, H, dk, dv, num_seqs, T_total).total : 0;
+}
+
+size_t kda_gdr_bwd_workspace_size(kda_dtype dt, int H, int Hk, int dk, int dv, int num_seqs, int64_t T_total) {
+    return gdr_sizes_ok(dt, H, Hk, dk, dv, num_seqs, T_total) ? gdr_layout(true, H, dk, dv, num_seqs, T_total).total : 0;
+}
+
+kda_status kda_gdr_fwd(kda_dtype dt, int H, int Hk, int dk, int dv, float scale, int num_seqs, int64_t T_total,
+                       const int32_t* cu_seqlens, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                       const void* v, int64_t v_stride, const float* g, const float* beta,
+                       const float* initial_state, float* final_state, void* y, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+    return gdr_fwd(false, dt, H, Hk, dk, dv, scale, num_seqs, T_total, cu_seqlens, q, q_stride, k, k_stride, v, v_stride, g,
+                   beta, initial_state, final_state, y, workspace, workspace_bytes, stream);
+}
+
+kda_status kda_gdr_fwd_padded(kda_dtype dt, int H, int Hk, int dk, int dv, float scale, int num_seqs,
+                              int64_t T_total, const int32_t* cu_seqlens, const void* q, int64_t q_stride,
+                              const void* k, int64_t k_stride, const void* v, int64_t v_stride, const float* g,
+                              const float* beta, const float* initial_state, float* final_state, void* y,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+    return gdr_fwd(true, dt, H, Hk, dk, dv, scale, num_seqs, T_total, cu_seqlens, q, q_stride, k, k_stride, v, v_stride, g,
+                   beta, initial_state, final_state, y, workspace, workspace_bytes, stream);
+}
+
+kda_status kda_gdr_bwd(kda_dtype dt, int H, int Hk, int dk, int dv, float scale, int num_seqs, int64_t T_total,
+                       const int32_t* cu_seqlens, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                       const void* v, int64_t v_stride, const float* g, const float* beta,
+                       const float* initial_state, const void* dy, const float* d_final_state, void* dq, void* dk_out,
+                       void* dv_out, float* dg, float* dbeta, float* d_initial_state, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+    return gdr_bwd(false, dt, H, Hk, dk, dv, scale, num_seqs, T_total, cu_seqlens, q, q_stride, k, k_stride, v, v_stride, g,
+                   beta, initial_state, dy, d_final_state, dq, dk_out, dv_out, dg, dbeta, d_initial_state, workspace,
+                   workspace_bytes, stream);
+}
+
+kda_status kda_gdr_bwd_padded(kda_dtype dt, int H, int Hk, int dk, int dv, float scale, int num_seqs,
+                              int64_t T_total, const int32_t* cu_seqlens, const void* q, int64_t q_stride,
+                              const void* k, int64_t k_stride, const void* v, int64_t v_stride, const float* g,
+                              const float* beta, const float* initial_state, const void* dy,
+                              const float* d_final_state, void* dq, void* dk_out, void* dv_out, float* dg,
+                              float* dbeta, float* d_initial_state, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+    return gdr_bwd(true, dt, H, Hk, dk, dv, scale, num_seqs, T_total, cu_seqlens, q, q_stride, k, k_stride, v, v_stride, g,
+                   beta, initial_state, dy, d_final_state, dq, dk_out, dv_out, dg, dbeta, d_initial_state, workspace,
+                   workspace_bytes, stream);
+}
+
+kda_status kda_gdr_decode_step(kda_dtype dt, int N, int H, int Hk, int dk, int dv, float scale, const void* q,
+                               int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                               const float* g, const float* beta, float* state, void* y, void* stream) {
+    if (!dtype_ok(dt) || N < 0 || H <= 0 || Hk <= 0 || H % Hk != 0) return KDA_ERR_INVALID_ARGUMENT;
+    if (!head_ok(dk) || !head_ok(dv)) return KDA_ERR_UNSUPPORTED;
+    if ((int64_t)N * H >= (int64_t)1 << 24) return KDA_ERR_INVALID_ARGUMENT;
+    if (N > 0 && (!q || !k || !v || !beta || !state || !y)) return KDA_ERR_INVALID_ARGUMENT;
+    if (!rows_ok(dt, q, q_stride, Hk, dk) || !rows_ok(dt, k, k_stride, Hk, dk) || !rows_ok(dt, v, v_stride, H, dv) ||
+        !aligned(y, 16) || !aligned(g, 4) || !aligned(beta, 4) || !aligned(state, 16))
+        return KDA_ERR_INVALID_ARGUMENT;
+    kda::GdrDecodeArgs a{};
+    a.dtype = (int)dt;
+    a.N = N;
+    a.H = H;
+    a.dk = dk;
+    a.dv = dv;
+    a.scale = scale;
+    a.q = rows(q, q_stride, H / Hk);
+    a.k = rows(k, k_stride, H / Hk);
+    a.v = rows(v, v_stride, 1);
+    a.g = g;
+    a.beta = beta;
+    a.state = state;
+    a.y = y;
+    a.stream = stream;
+    return launched([&] { return kda::launch_gdr_decode(a); });
+}
+
+}  // extern "C"
+
+namespace {
+
 // Rows walked side by side by the norm's gradient: a multiple of H, at most all
 // rows, and about what fills the CUs with three workgroups each (two of 1024
 // threads); each adds a partial row of the weight's gradient.  Rounded down:

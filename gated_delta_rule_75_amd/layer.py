@@ -228,6 +228,110 @@ def linattn_decode_step(q, k, v, g, state, scale: float = 1.0, y: Optional[torch
     return y
 
 
+def _gdr(q, k, v, g, beta) -> Tuple[int, int, int, int, int, int]:
+    """(dtype, T, H, Hk, dk, dv) of q, k [T, Hk, dk], v [T, H, dv], g (or None) and
+    beta [T, H]."""
+    if beta is None:
+        raise ValueError("beta is required")
+    dt, T, H, Hk, dk, dv, _ = _qkv(q, k, v, beta if g is None else g)
+    _buf("g", g, (T, H), torch.float32)
+    _buf("beta", beta, (T, H), torch.float32)
+    return dt, T, H, Hk, dk, dv
+
+
+def gdr_fwd_workspace_size(dtype: int, H: int, Hk: int, dk: int, dv: int, num_seqs: int, T_total: int) -> int:
+    """Bytes of workspace that gdr_fwd needs for these sizes (0: not supported)."""
+    return int(lib().kda_gdr_fwd_workspace_size(dtype, H, Hk, dk, dv, num_seqs, T_total))
+
+
+def gdr_bwd_workspace_size(dtype: int, H: int, Hk: int, dk: int, dv: int, num_seqs: int, T_total: int) -> int:
+    """Bytes of workspace that gdr_bwd needs for these sizes (0: not supported)."""
+    return int(lib().kda_gdr_bwd_workspace_size(dtype, H, Hk, dk, dv, num_seqs, T_total))
+
+
+def gdr_fwd(q, k, v, g, beta, cu_seqlens: Optional[torch.Tensor] = None, initial_state=None,
+            output_final_state: bool = True, scale: float = 1.0, y: Optional[torch.Tensor] = None,
+            final_state: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """The gated delta rule with a decay for each head over packed sequences:
+    u = exp(g_t) S_{t-1}, S_t = u + beta_t k_t (v_t - u^T k_t)^T, y_t = scale S_t^T q_t.
+
+    q, k [T, Hk, dk] and v [T, H, dv] (bf16 or fp32; H / Hk value heads share a
+    key head), all finite; g fp32 [T, H], never above 0 (-inf starts the state
+    anew, whatever it held), or None: no decay; beta fp32 [T, H].  Stable for
+    beta |k|^2 <= 2.  cu_seqlens may begin after 0 or end before T: rows of no
+    sequence are not read; they are zeros in a y made here, and left as they are
+    in one that is given.  Returns (y, final_state or None)."""
+    dt, T, H, Hk, dk, dv = _gdr(q, k, v, g, beta)
+    N = _seqs(cu_seqlens)
+    _need("initial_state", initial_state, (N, H, dk, dv), torch.float32)
+    _need("final_state", final_state, (N, H, dk, dv), torch.float32)
+    _need("y", y, (T, H, dv), q.dtype)
+    _need_workspace(workspace)
+    qs, ks, vs = _rows("q", q), _rows("k", k), _rows("v", v)
+    _contiguous(cu_seqlens=cu_seqlens, initial_state=initial_state, final_state=final_state, y=y, workspace=workspace)
+    dev = _device(q, k, v, g, beta, cu_seqlens, initial_state, final_state, y, workspace)
+    L = lib()
+    fn = L.kda_gdr_fwd
+    if y is None:
+        y = torch.empty(T, H, dv, dtype=q.dtype, device=dev)
+        fn = L.kda_gdr_fwd_padded
+    if final_state is None and output_final_state:
+        final_state = torch.empty(N, H, dk, dv, dtype=torch.float32, device=dev)
+    workspace = _workspace("kda_gdr_fwd", L.kda_gdr_fwd_workspace_size(dt, H, Hk, dk, dv, N, T), workspace, dev)
+    _call(dev, fn, "kda_gdr_fwd", dt, H, Hk, dk, dv, scale, N, T, _p(cu_seqlens), _p(q), qs, _p(k), ks, _p(v), vs,
+          _p(g), _p(beta), _p(initial_state), _p(final_state), _p(y), _p(workspace), workspace.numel())
+    return y, final_state
+
+
+def gdr_bwd(q, k, v, g, beta, dy, cu_seqlens: Optional[torch.Tensor] = None, initial_state=None, d_final_state=None,
+            scale: float = 1.0, workspace: Optional[torch.Tensor] = None):
+    """The gradient of gdr_fwd for the gradients dy [T, H, dv] of y and (optional)
+    d_final_state of the final state.  Returns (dq, dk, dv, dg, dbeta,
+    d_initial_state): dq, dk [T, Hk, dk] summed over the value heads that share a
+    key head, dg and dbeta [T, H] (dg None where g is); zeros in rows of no
+    sequence."""
+    dt, T, H, Hk, dk, dv = _gdr(q, k, v, g, beta)
+    N = _seqs(cu_seqlens)
+    _need("dy", dy, (T, H, dv), q.dtype)
+    _need("initial_state", initial_state, (N, H, dk, dv), torch.float32)
+    _need("d_final_state", d_final_state, (N, H, dk, dv), torch.float32)
+    _need_workspace(workspace)
+    qs, ks, vs = _rows("q", q), _rows("k", k), _rows("v", v)
+    _contiguous(dy=dy, cu_seqlens=cu_seqlens, initial_state=initial_state, d_final_state=d_final_state,
+                workspace=workspace)
+    dev = _device(q, k, v, g, beta, dy, cu_seqlens, initial_state, d_final_state, workspace)
+    L = lib()
+    dq = torch.empty(T, Hk, dk, dtype=q.dtype, device=dev)
+    dk_out = torch.empty_like(dq)
+    dv_out = torch.empty(T, H, dv, dtype=q.dtype, device=dev)
+    dg = None if g is None else torch.empty_like(g)
+    dbeta = torch.empty_like(beta)
+    ds0 = torch.empty(N, H, dk, dv, dtype=torch.float32, device=dev)
+    workspace = _workspace("kda_gdr_bwd", L.kda_gdr_bwd_workspace_size(dt, H, Hk, dk, dv, N, T), workspace, dev)
+    _call(dev, L.kda_gdr_bwd_padded, "kda_gdr_bwd", dt, H, Hk, dk, dv, scale, N, T, _p(cu_seqlens), _p(q), qs, _p(k),
+          ks, _p(v), vs, _p(g), _p(beta), _p(initial_state), _p(dy), _p(d_final_state), _p(dq), _p(dk_out), _p(dv_out),
+          _p(dg), _p(dbeta), _p(ds0), _p(workspace), workspace.numel())
+    return dq, dk_out, dv_out, dg, dbeta, ds0
+
+
+def gdr_decode_step(q, k, v, g, beta, state, scale: float = 1.0, y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One token for each of N requests: q, k [N, Hk, dk], v [N, H, dv], g (or None)
+    and beta [N, H] as in gdr_fwd, state fp32 [N, H, dk, dv] updated in place.
+    Returns y [N, H, dv]."""
+    dt, N, H, Hk, dk, dv = _gdr(q, k, v, g, beta)
+    if state is None:
+        raise ValueError("state is required")
+    _buf("state", state, (N, H, dk, dv), torch.float32)
+    _buf("y", y, (N, H, dv), q.dtype)
+    qs, ks, vs = _rows("q", q), _rows("k", k), _rows("v", v)
+    dev = _device(q, k, v, g, beta, state, y)
+    if y is None:
+        y = torch.empty(N, H, dv, dtype=q.dtype, device=dev)
+    _call(dev, lib().kda_gdr_decode_step, "kda_gdr_decode_step", dt, N, H, Hk, dk, dv, scale, _p(q), qs, _p(k), ks,
+          _p(v), vs, _p(g), _p(beta), _p(state), _p(y))
+    return y
+
+
 def rope_frequencies(rot: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
                      trained_len: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0):
     """The rot / 2 angles a position as a float64 CPU tensor, and the factor on

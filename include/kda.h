@@ -445,6 +445,99 @@ kda_status kda_linattn_decode_step(kda_dtype dt, int N, int H, int Hk, int dk, i
                                    int64_t v_stride, const float* g, int g_per_token, float* state, void* y,
                                    void* stream);
 
+/*
+ * kda_gdr_fwd -- the gated delta rule with one decay for each head: per sequence
+ * and value head h
+ *     u = exp(g_t) S_{t-1},   e_t = v_t - u^T k_t,
+ *     S_t = u + beta_t k_t e_t^T,   y_t = scale * S_t^T q_t
+ * over packed sequences, by chunks of 64 tokens.  Unlike kda_chunk_fwd the decay
+ * is a head's and has no lower bound, key heads may be shared, dk and dv may
+ * differ, and there is a gradient.
+ *
+ *   H, Hk, dk, dv, num_seqs, T_total, cu_seqlens, q, k, v, their strides
+ *                    as kda_linattn_fwd, except that (T_total / 64 + num_seqs) * H
+ *                    must stay below 2^23.  The rule is stable for
+ *                    beta |k|^2 <= 2 (unit keys: beta in [0, 2]); beyond that the
+ *                    states may grow without bound.
+ *   g                fp32 [T_total, H], natural log of the decay, <= 0, or NULL: no
+ *                    decay.  Below -200 it counts as -200 (a factor of 0):
+ *                    -INFINITY starts the head's state anew at that token, also
+ *                    where it held infinities or NaN.
+ *   beta             fp32 [T_total, H].
+ *   initial_state, final_state   fp32 [num_seqs, H, dk, dv] or NULL, as
+ *                    kda_chunk_fwd; they may be the same buffer.
+ *   y                [T_total, H, dv] in dtype dt; must not overlap inputs.
+ *   workspace        at least kda_gdr_fwd_workspace_size bytes for the same sizes,
+ *                    256-byte aligned.  Calls that may overlap in time need a
+ *                    workspace each.
+ */
+size_t kda_gdr_fwd_workspace_size(kda_dtype dt, int H, int Hk, int dk, int dv, int num_seqs, int64_t T_total);
+kda_status kda_gdr_fwd(kda_dtype dt, int H, int Hk, int dk, int dv, float scale, int num_seqs, int64_t T_total,
+                       const int32_t* cu_seqlens, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                       const void* v, int64_t v_stride, const float* g, const float* beta,
+                       const float* initial_state, float* final_state, void* y, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
+ * kda_gdr_fwd_padded -- kda_gdr_fwd; rows of no sequence, before cu_seqlens[0] and
+ * from cu_seqlens[num_seqs] on, are set to zeros (kda_gdr_fwd leaves them).
+ */
+kda_status kda_gdr_fwd_padded(kda_dtype dt, int H, int Hk, int dk, int dv, float scale, int num_seqs,
+                              int64_t T_total, const int32_t* cu_seqlens, const void* q, int64_t q_stride,
+                              const void* k, int64_t k_stride, const void* v, int64_t v_stride, const float* g,
+                              const float* beta, const float* initial_state, float* final_state, void* y,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * kda_gdr_bwd -- the gradient of kda_gdr_fwd for given gradients of y and of the
+ * final state, recomputing the states (nothing is kept from the forward call).
+ *
+ *   dy               [T_total, H, dv] in dtype dt, contiguous.
+ *   initial_state    as given to the forward call; finite.
+ *   d_final_state    fp32 [num_seqs, H, dk, dv], or NULL (zeros).
+ *   dq, dk_out       [T_total, Hk, dk] in dtype dt, summed over the value heads
+ *                    that share a key head (in fp32, rounded once).
+ *   dv_out           [T_total, H, dv] in dtype dt.
+ *   dg, dbeta        fp32 [T_total, H]; dg given exactly where g is.  Sums of
+ *                    terms of both signs, accurate to a few 1e-6 of the sum of
+ *                    their sizes.  Where g is below -200 its gradient is taken at
+ *                    -200.
+ *   d_initial_state  fp32 [num_seqs, H, dk, dv] or NULL.
+ *                    No output may overlap an input or another output.
+ *   workspace        at least kda_gdr_bwd_workspace_size bytes, 256-byte aligned:
+ *                    it holds two states for every 64 tokens of a head.
+ *   all other arguments: as kda_gdr_fwd.
+ */
+size_t kda_gdr_bwd_workspace_size(kda_dtype dt, int H, int Hk, int dk, int dv, int num_seqs, int64_t T_total);
+kda_status kda_gdr_bwd(kda_dtype dt, int H, int Hk, int dk, int dv, float scale, int num_seqs, int64_t T_total,
+                       const int32_t* cu_seqlens, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                       const void* v, int64_t v_stride, const float* g, const float* beta,
+                       const float* initial_state, const void* dy, const float* d_final_state, void* dq, void* dk_out,
+                       void* dv_out, float* dg, float* dbeta, float* d_initial_state, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
+ * kda_gdr_bwd_padded -- kda_gdr_bwd; dq, dk_out, dv_out, dg and dbeta of rows of no
+ * sequence, whose gradient is 0, are set to zeros.
+ */
+kda_status kda_gdr_bwd_padded(kda_dtype dt, int H, int Hk, int dk, int dv, float scale, int num_seqs,
+                              int64_t T_total, const int32_t* cu_seqlens, const void* q, int64_t q_stride,
+                              const void* k, int64_t k_stride, const void* v, int64_t v_stride, const float* g,
+                              const float* beta, const float* initial_state, const void* dy,
+                              const float* d_final_state, void* dq, void* dk_out, void* dv_out, float* dg,
+                              float* dbeta, float* d_initial_state, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/*
+ * kda_gdr_decode_step -- one token for each of N requests (N * H < 2^24) against
+ * resident states: q, k [N, Hk, dk], v [N, H, dv] (strides as above), g [N, H] or
+ * NULL, beta [N, H], state fp32 [N, H, dk, dv] updated in place, y [N, H, dv] in
+ * dtype dt.
+ */
+kda_status kda_gdr_decode_step(kda_dtype dt, int N, int H, int Hk, int dk, int dv, float scale, const void* q,
+                               int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                               const float* g, const float* beta, float* state, void* y, void* stream);
+
 typedef enum {
     KDA_ROPE_HALF = 0,         /* pairs (i, i + rot / 2) */
     KDA_ROPE_INTERLEAVED = 1   /* pairs (2 i, 2 i + 1) */
