@@ -22,7 +22,8 @@ __all__ = [
     "decode_step_fused", "decode_replay",
     "linattn_fwd", "linattn_fwd_workspace_size", "linattn_bwd", "linattn_bwd_workspace_size",
     "linattn_decode_step", "gdr_fwd", "gdr_fwd_workspace_size", "gdr_bwd", "gdr_bwd_workspace_size",
-    "gdr_decode_step", "rope", "rope_frequencies", "norm_fwd", "norm_bwd", "norm_bwd_workspace_size",
+    "gdr_decode_step", "rope", "rope_axes", "rope_frequencies", "rope_pair_axes", "norm_fwd", "norm_bwd",
+    "norm_bwd_workspace_size", "norm_fwd_kept", "norm_bwd_kept",
     "KDA_BF16", "KDA_F32",
 ]
 
@@ -44,7 +45,8 @@ SYMBOLS = ("kda_version", "kda_status_string", "kda_chunk_fwd_workspace_size",
            "kda_linattn_bwd_padded", "kda_linattn_bwd_workspace_size", "kda_linattn_decode_step",
            "kda_gdr_fwd", "kda_gdr_fwd_padded", "kda_gdr_fwd_workspace_size", "kda_gdr_bwd", "kda_gdr_bwd_padded",
            "kda_gdr_bwd_workspace_size", "kda_gdr_decode_step", "kda_rope",
-           "kda_rope_frequencies", "kda_norm_fwd", "kda_norm_bwd", "kda_norm_bwd_workspace_size")
+           "kda_rope_axes", "kda_rope_frequencies", "kda_rope_pair_axes", "kda_norm_fwd", "kda_norm_bwd",
+           "kda_norm_bwd_workspace_size", "kda_norm_fwd_kept", "kda_norm_bwd_kept")
 
 
 class KDAError(RuntimeError):
@@ -130,6 +132,14 @@ def lib() -> ctypes.CDLL:
     L.kda_rope_frequencies.restype = i
     L.kda_rope.argtypes = [i, i64, i, i, i, i, i, i, f, vp, vp, vp, i64, vp, i64, vp, i64, vp, i64, vp]
     L.kda_rope.restype = i
+    L.kda_rope_axes.argtypes = [i, i64, i, i, i, i, i, i, f, i, vp, vp, vp, vp, i64, vp, i64, vp, i64, vp, i64, vp]
+    L.kda_rope_axes.restype = i
+    L.kda_rope_pair_axes.argtypes = [i, vp, i, vp]
+    L.kda_rope_pair_axes.restype = i
+    L.kda_norm_fwd_kept.argtypes = [i, i, i64, i, i, f, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.kda_norm_fwd_kept.restype = i
+    L.kda_norm_bwd_kept.argtypes = [i, i, i64, i, i, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.kda_norm_bwd_kept.restype = i
     L.kda_norm_fwd.argtypes = [i, i, i64, i, i, f, vp, vp, vp, vp, vp, vp, vp, vp]
     L.kda_norm_fwd.restype = i
     L.kda_norm_bwd.argtypes = [i, i, i64, i, i, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
@@ -480,5 +490,5 @@ def decode_replay(q, k, v, g, beta, state, accepted=None, z=None, scale: float =
 
 from .layer import (gdr_bwd, gdr_bwd_workspace_size, gdr_decode_step, gdr_fwd, gdr_fwd_workspace_size,  # noqa: E402
                     linattn_bwd, linattn_bwd_workspace_size, linattn_decode_step, linattn_fwd,
-                    linattn_fwd_workspace_size, norm_bwd, norm_bwd_workspace_size, norm_fwd, rope,
-                    rope_frequencies)
+                    linattn_fwd_workspace_size, norm_bwd, norm_bwd_kept, norm_bwd_workspace_size, norm_fwd,
+                    norm_fwd_kept, rope, rope_axes, rope_frequencies, rope_pair_axes)

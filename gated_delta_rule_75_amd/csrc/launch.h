@@ -122,7 +122,9 @@ struct RopeArgs {
     bool half;                 // pairs (i, i + rot/2), else (2i, 2i + 1)
     bool inverse;
     float mscale;
-    const int32_t* positions;  // [T]
+    const int32_t* positions;  // [T], or [axes, T]
+    const uint8_t* pair_axis;  // [rot / 2] or NULL: one axis
+    int axes;
     const double* inv_freq;    // [rot / 2]
     const void *q, *k;         // rows of heads at a token stride (elements)
     int64_t q_stride, k_stride;
@@ -132,6 +134,7 @@ struct RopeArgs {
 };
 hipError_t launch_rope(const RopeArgs& a);
 
+constexpr int kKeepBlock = 128;
 // The gated norm (dy NULL) or its gradient over rows [T, H, D].
 struct NormArgs {
     int dtype;
@@ -147,6 +150,9 @@ struct NormArgs {
     void *dx, *dz;
     float *dweight, *dbias;
     float *dwp, *dbp;       // partial rows [slots, D]
+    // x and z in 8 bits, written beside y or read in their place by the gradient;
+    // a byte for each kKeepBlock elements of a row
+    uint8_t *x8, *xe, *z8, *ze;
     int64_t slots;          // rows walked side by side, a multiple of H
     void* stream;
 };

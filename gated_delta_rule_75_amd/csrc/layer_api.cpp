@@ -129,6 +129,50 @@ template <typename P> P* part(void* ws, size_t at) { return reinterpret_cast<P*>
 
 kda::LinRows rows(const void* p, int64_t stride, int share) { return kda::LinRows{p, stride, share}; }
 
+kda_status rope_call(kda_dtype dt, int64_t T, int Hq, int Hk, int d, int rot, kda_rope_layout layout, int inverse,
+                     float mscale, int axes, const int32_t* positions, const uint8_t* pair_axis, const double* inv_freq, const void* q, int64_t q_stride,
+                     const void* k, int64_t k_stride, void* q_out, int64_t q_out_stride, void* k_out,
+                     int64_t k_out_stride, void* stream) {
+    if (!dtype_ok(dt) || T < 0 || T > INT32_MAX || Hq <= 0 || Hk < 0 || d <= 0) return KDA_ERR_INVALID_ARGUMENT;
+    if (layout != KDA_ROPE_HALF && layout != KDA_ROPE_INTERLEAVED) return KDA_ERR_INVALID_ARGUMENT;
+    if (rot <= 0 || rot % 2 != 0 || rot > d) return KDA_ERR_INVALID_ARGUMENT;
+    if (d > 1024 || (int64_t)(Hq + (int64_t)Hk) * d > 1 << 24) return KDA_ERR_UNSUPPORTED;
+    if (T > 0 && (!positions || !inv_freq || !q || !q_out || (Hk > 0 && (!k || !k_out)))) return KDA_ERR_INVALID_ARGUMENT;
+    if (q_stride < (int64_t)Hq * d || q_out_stride < (int64_t)Hq * d || k_stride < (int64_t)Hk * d ||
+        k_out_stride < (int64_t)Hk * d)
+        return KDA_ERR_INVALID_ARGUMENT;
+    if ((q == q_out && q_stride != q_out_stride) || (Hk > 0 && k == k_out && k_stride != k_out_stride))
+        return KDA_ERR_INVALID_ARGUMENT;
+    const size_t e = elt(dt);
+    if (!aligned(q, e) || !aligned(k, e) || !aligned(q_out, e) || !aligned(k_out, e) || !aligned(positions, 4) ||
+        !aligned(inv_freq, 8))
+        return KDA_ERR_INVALID_ARGUMENT;
+    kda::RopeArgs a{};
+    a.dtype = (int)dt;
+    a.T = T;
+    a.Hq = Hq;
+    a.Hk = Hk;
+    a.d = d;
+    a.rot = rot;
+    a.half = layout == KDA_ROPE_HALF;
+    a.inverse = inverse != 0;
+    a.mscale = mscale;
+    a.positions = positions;
+    a.pair_axis = pair_axis;
+    a.axes = axes;
+    a.inv_freq = inv_freq;
+    a.q = q;
+    a.k = k;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.q_out = q_out;
+    a.k_out = k_out;
+    a.qo_stride = q_out_stride;
+    a.ko_stride = k_out_stride;
+    a.stream = stream;
+    return launched([&] { return kda::launch_rope(a); });
+}
+
 // clear: rows of no sequence of the outputs become zeros.
 kda_status linattn_fwd(bool clear, kda_dtype dt, int H, int Hk, int dk, int dv, float scale, int num_seqs,
                        int64_t T_total, const int32_t* cu_seqlens, const void* q, int64_t q_stride, const void* k,
@@ -363,46 +407,42 @@ kda_status kda_rope_frequencies(int rot, double base, kda_rope_scaling scaling, 
     return KDA_ERR_INVALID_ARGUMENT;
 }
 
+kda_status kda_rope_pair_axes(int axes, const int32_t* sections, kda_rope_order order, uint8_t* pair_axis) {
+    if (axes <= 0 || axes > 255 || !sections || !pair_axis) return KDA_ERR_INVALID_ARGUMENT;
+    if (order != KDA_ROPE_RUNS && order != KDA_ROPE_TURNS) return KDA_ERR_INVALID_ARGUMENT;
+    int64_t pairs = 0;
+    for (int x = 0; x < axes; ++x) {
+        if (sections[x] < 0) return KDA_ERR_INVALID_ARGUMENT;
+        pairs += sections[x];
+    }
+    if (pairs == 0 || pairs > 512) return KDA_ERR_INVALID_ARGUMENT;   // a head has 1024 channels at most
+    // turn n takes a pair of every axis that has more than n; runs: an axis's all at once
+    if (order == KDA_ROPE_RUNS) {
+        for (int x = 0; x < axes; ++x)
+            for (int n = 0; n < sections[x]; ++n) *pair_axis++ = (uint8_t)x;
+    } else {
+        for (int n = 0; n < 512; ++n)
+            for (int x = 0; x < axes; ++x)
+                if (sections[x] > n) *pair_axis++ = (uint8_t)x;
+    }
+    return KDA_OK;
+}
+
 kda_status kda_rope(kda_dtype dt, int64_t T, int Hq, int Hk, int d, int rot, kda_rope_layout layout, int inverse,
                     float mscale, const int32_t* positions, const double* inv_freq, const void* q, int64_t q_stride,
                     const void* k, int64_t k_stride, void* q_out, int64_t q_out_stride, void* k_out,
                     int64_t k_out_stride, void* stream) {
-    if (!dtype_ok(dt) || T < 0 || T > INT32_MAX || Hq <= 0 || Hk < 0 || d <= 0) return KDA_ERR_INVALID_ARGUMENT;
-    if (layout != KDA_ROPE_HALF && layout != KDA_ROPE_INTERLEAVED) return KDA_ERR_INVALID_ARGUMENT;
-    if (rot <= 0 || rot % 2 != 0 || rot > d) return KDA_ERR_INVALID_ARGUMENT;
-    if (d > 1024 || (int64_t)(Hq + (int64_t)Hk) * d > 1 << 24) return KDA_ERR_UNSUPPORTED;
-    if (T > 0 && (!positions || !inv_freq || !q || !q_out || (Hk > 0 && (!k || !k_out)))) return KDA_ERR_INVALID_ARGUMENT;
-    if (q_stride < (int64_t)Hq * d || q_out_stride < (int64_t)Hq * d || k_stride < (int64_t)Hk * d ||
-        k_out_stride < (int64_t)Hk * d)
-        return KDA_ERR_INVALID_ARGUMENT;
-    if ((q == q_out && q_stride != q_out_stride) || (Hk > 0 && k == k_out && k_stride != k_out_stride))
-        return KDA_ERR_INVALID_ARGUMENT;
-    const size_t e = elt(dt);
-    if (!aligned(q, e) || !aligned(k, e) || !aligned(q_out, e) || !aligned(k_out, e) || !aligned(positions, 4) ||
-        !aligned(inv_freq, 8))
-        return KDA_ERR_INVALID_ARGUMENT;
-    kda::RopeArgs a{};
-    a.dtype = (int)dt;
-    a.T = T;
-    a.Hq = Hq;
-    a.Hk = Hk;
-    a.d = d;
-    a.rot = rot;
-    a.half = layout == KDA_ROPE_HALF;
-    a.inverse = inverse != 0;
-    a.mscale = mscale;
-    a.positions = positions;
-    a.inv_freq = inv_freq;
-    a.q = q;
-    a.k = k;
-    a.q_stride = q_stride;
-    a.k_stride = k_stride;
-    a.q_out = q_out;
-    a.k_out = k_out;
-    a.qo_stride = q_out_stride;
-    a.ko_stride = k_out_stride;
-    a.stream = stream;
-    return launched([&] { return kda::launch_rope(a); });
+    return rope_call(dt, T, Hq, Hk, d, rot, layout, inverse, mscale, 1, positions, nullptr, inv_freq, q, q_stride, k,
+                     k_stride, q_out, q_out_stride, k_out, k_out_stride, stream);
+}
+
+kda_status kda_rope_axes(kda_dtype dt, int64_t T, int Hq, int Hk, int d, int rot, kda_rope_layout layout, int inverse,
+                         float mscale, int axes, const int32_t* positions, const uint8_t* pair_axis,
+                         const double* inv_freq, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                         void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* stream) {
+    if (axes <= 0 || axes > 255 || (T > 0 && !pair_axis)) return KDA_ERR_INVALID_ARGUMENT;
+    return rope_call(dt, T, Hq, Hk, d, rot, layout, inverse, mscale, axes, positions, pair_axis, inv_freq, q, q_stride, k,
+                     k_stride, q_out, q_out_stride, k_out, k_out_stride, stream);
 }
 
 }  // extern "C"
@@ -640,13 +680,14 @@ bool norm_sizes_ok(kda_dtype dt, int64_t T, int H, int D) {
 
 bool kind_ok(kda_norm_kind kind) { return kind == KDA_NORM_LAYER || kind == KDA_NORM_RMS; }
 
-}  // namespace
+// x and z in 8 bits: values and, for each 128 of a row, the power of two.
+struct Kept {
+    uint8_t *x8, *xe, *z8, *ze;
+};
 
-extern "C" {
-
-kda_status kda_norm_fwd(kda_dtype dt, kda_norm_kind kind, int64_t T, int H, int D, float eps, const void* x,
-                        const float* weight, const float* bias, const void* z, void* y, float* mean, float* rstd,
-                        void* stream) {
+kda_status norm_fwd(kda_dtype dt, kda_norm_kind kind, int64_t T, int H, int D, float eps, const void* x,
+                    const float* weight, const float* bias, const void* z, void* y, float* mean, float* rstd,
+                    const Kept& kept, void* stream) {
     if (!norm_sizes_ok(dt, T, H, D) || !kind_ok(kind) || !(eps >= 0.f)) return KDA_ERR_INVALID_ARGUMENT;
     if (D > 16384) return KDA_ERR_UNSUPPORTED;
     if (!weight || (T > 0 && (!x || !y))) return KDA_ERR_INVALID_ARGUMENT;
@@ -669,25 +710,24 @@ kda_status kda_norm_fwd(kda_dtype dt, kda_norm_kind kind, int64_t T, int H, int 
     a.y = y;
     a.mean = mean;
     a.rstd = rstd;
+    a.x8 = kept.x8;
+    a.xe = kept.xe;
+    a.z8 = kept.z8;
+    a.ze = kept.ze;
     a.stream = stream;
     return launched([&] { return kda::launch_norm(a); });
 }
 
-size_t kda_norm_bwd_workspace_size(kda_dtype dt, int64_t T, int H, int D) {
-    if (!norm_sizes_ok(dt, T, H, D) || D > 16384) return 0;
-    return 2 * round_up((size_t)norm_slots(dt, T, H, D) * D * 4, 256);
-}
-
-kda_status kda_norm_bwd(kda_dtype dt, kda_norm_kind kind, int64_t T, int H, int D, const void* x, const float* weight,
-                        const float* bias, const void* z, const float* mean, const float* rstd, const void* dy,
-                        void* dx, float* dweight, float* dbias, void* dz, void* workspace, size_t workspace_bytes,
-                        void* stream) {
+kda_status norm_bwd(kda_dtype dt, kda_norm_kind kind, int64_t T, int H, int D, const void* x, const float* weight,
+                    const float* bias, const void* z, const float* mean, const float* rstd, const void* dy,
+                    void* dx, float* dweight, float* dbias, void* dz, void* workspace, size_t workspace_bytes,
+                    const Kept& kept, void* stream) {
     if (!norm_sizes_ok(dt, T, H, D) || !kind_ok(kind)) return KDA_ERR_INVALID_ARGUMENT;
     if (D > 16384) return KDA_ERR_UNSUPPORTED;
     if (!weight || !dweight || !workspace) return KDA_ERR_INVALID_ARGUMENT;
-    if (T > 0 && (!x || !rstd || !dy || !dx || (kind == KDA_NORM_LAYER && !mean))) return KDA_ERR_INVALID_ARGUMENT;
+    if (T > 0 && ((!x && !kept.x8) || !rstd || !dy || !dx || (kind == KDA_NORM_LAYER && !mean))) return KDA_ERR_INVALID_ARGUMENT;
     if (kind == KDA_NORM_RMS && mean) return KDA_ERR_INVALID_ARGUMENT;
-    if ((z != nullptr) != (dz != nullptr) && T > 0) return KDA_ERR_INVALID_ARGUMENT;
+    if ((z != nullptr || kept.z8 != nullptr) != (dz != nullptr) && T > 0) return KDA_ERR_INVALID_ARGUMENT;
     const size_t e = elt(dt);
     if (!aligned(x, e) || !aligned(dy, e) || !aligned(dx, e) || !aligned(z, e) || !aligned(dz, e) ||
         !aligned(weight, 4) || !aligned(bias, 4) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(dweight, 4) ||
@@ -715,8 +755,55 @@ kda_status kda_norm_bwd(kda_dtype dt, kda_norm_kind kind, int64_t T, int H, int 
     a.dwp = part<float>(workspace, 0);
     a.dbp = dbias ? part<float>(workspace, half) : nullptr;
     a.slots = norm_slots(dt, T, H, D);
+    a.x8 = kept.x8;
+    a.xe = kept.xe;
+    a.z8 = kept.z8;
+    a.ze = kept.ze;
     a.stream = stream;
     return launched([&] { return kda::launch_norm(a); });
+}
+
+}  // namespace
+
+extern "C" {
+
+kda_status kda_norm_fwd(kda_dtype dt, kda_norm_kind kind, int64_t T, int H, int D, float eps, const void* x,
+                        const float* weight, const float* bias, const void* z, void* y, float* mean, float* rstd,
+                        void* stream) {
+    return norm_fwd(dt, kind, T, H, D, eps, x, weight, bias, z, y, mean, rstd, Kept{}, stream);
+}
+
+kda_status kda_norm_fwd_kept(kda_dtype dt, kda_norm_kind kind, int64_t T, int H, int D, float eps, const void* x,
+                             const float* weight, const float* bias, const void* z, void* y, float* mean, float* rstd,
+                             void* x8, uint8_t* x_exp, void* z8, uint8_t* z_exp, void* stream) {
+    if (T > 0 && (!x8 || !x_exp || (z != nullptr) != (z8 != nullptr) || (z != nullptr) != (z_exp != nullptr)))
+        return KDA_ERR_INVALID_ARGUMENT;
+    return norm_fwd(dt, kind, T, H, D, eps, x, weight, bias, z, y, mean, rstd,
+                    Kept{(uint8_t*)x8, x_exp, (uint8_t*)z8, z_exp}, stream);
+}
+
+size_t kda_norm_bwd_workspace_size(kda_dtype dt, int64_t T, int H, int D) {
+    if (!norm_sizes_ok(dt, T, H, D) || D > 16384) return 0;
+    return 2 * round_up((size_t)norm_slots(dt, T, H, D) * D * 4, 256);
+}
+
+kda_status kda_norm_bwd(kda_dtype dt, kda_norm_kind kind, int64_t T, int H, int D, const void* x, const float* weight,
+                        const float* bias, const void* z, const float* mean, const float* rstd, const void* dy,
+                        void* dx, float* dweight, float* dbias, void* dz, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+    return norm_bwd(dt, kind, T, H, D, x, weight, bias, z, mean, rstd, dy, dx, dweight, dbias, dz, workspace,
+                    workspace_bytes, Kept{}, stream);
+}
+
+kda_status kda_norm_bwd_kept(kda_dtype dt, kda_norm_kind kind, int64_t T, int H, int D, const void* x8,
+                             const uint8_t* x_exp, const float* weight, const float* bias, const void* z8,
+                             const uint8_t* z_exp, const float* mean, const float* rstd, const void* dy, void* dx,
+                             float* dweight, float* dbias, void* dz, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+    if (T > 0 && (!x8 || !x_exp || (z8 != nullptr) != (z_exp != nullptr))) return KDA_ERR_INVALID_ARGUMENT;
+    return norm_bwd(dt, kind, T, H, D, nullptr, weight, bias, nullptr, mean, rstd, dy, dx, dweight, dbias, dz, workspace,
+                    workspace_bytes,
+                    Kept{(uint8_t*)x8, const_cast<uint8_t*>(x_exp), (uint8_t*)z8, const_cast<uint8_t*>(z_exp)}, stream);
 }
 
 }  // extern "C"

@@ -4,6 +4,9 @@
 // with b's sign of the sine reversed for the inverse (the gradient: the turn's
 // matrix is orthogonal up to m).  Pairs are (i, i + rot/2) or (2i, 2i + 1).
 //
+// With several axes (time, height, width) each pair has the axis whose position
+// turns it: all that differs is which position a table entry takes.
+//
 // The angle of a far position needs more than fp32 (at 10^6 positions an fp32
 // angle is off by 0.06): the product is taken in fp64 in turns (radians / 2 pi),
 // its fraction is exact, and only that goes to fp32.  A workgroup's tokens share
@@ -29,7 +32,8 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, int tpb) {
     const int nt = (int)(a.T - t0 < tpb ? a.T - t0 : tpb);
     float* sn = cs + tpb * n;
     for (int i = threadIdx.x; i < nt * n; i += 256) {
-        const double turns = (double)a.positions[t0 + i / n] * (a.inv_freq[i % n] * kInv2Pi);
+        const int64_t axis = !a.pair_axis ? 0 : a.pair_axis[i % n] < a.axes ? a.pair_axis[i % n] : a.axes - 1;
+        const double turns = (double)a.positions[axis * a.T + t0 + i / n] * (a.inv_freq[i % n] * kInv2Pi);
         float s, c;
         sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
         cs[i] = a.mscale * c;

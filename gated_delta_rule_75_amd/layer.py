@@ -23,6 +23,7 @@ from . import KDAError, _check, _dt, _need, _need_workspace, lib
 
 _LAYOUT = {"half": 0, "interleaved": 1}
 _SCALING = {None: 0, "linear": 1, "ntk": 2, "yarn": 3}
+_ORDER = {"runs": 0, "turns": 1}
 _KIND = {"layer": 0, "rms": 1}
 
 
@@ -346,13 +347,19 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: Optional[str] = N
     return freq, m.value
 
 
-def rope(q, k, positions, inv_freq, layout: str = "half", inverse: bool = False, mscale: float = 1.0,
-         q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None):
-    """Turns the first 2 * len(inv_freq) channels of every head of q [T, Hq, d]
-    and k [T, Hk, d] (or None) by positions (int32 [T]) times inv_freq (float64,
-    on the device); inverse turns back, which is the gradient.  layout "half"
-    pairs channels (i, i + rot/2), "interleaved" (2i, 2i + 1).  Outputs may be
-    the inputs.  Returns (q_out, k_out)."""
+def rope_pair_axes(sections, order: str = "runs") -> torch.Tensor:
+    """The axis of each rotated pair as a uint8 CPU tensor, sections[x] pairs for axis
+    x: "runs", all pairs of an axis side by side, or "turns", a pair of each axis in
+    turn while it has pairs left."""
+    if order not in _ORDER:
+        raise ValueError("order must be 'runs' or 'turns'")
+    n = torch.tensor(list(sections), dtype=torch.int32)
+    out = torch.empty(max(int(n.clamp(min=0).sum()), 1), dtype=torch.uint8)
+    _check("kda_rope_pair_axes", lib().kda_rope_pair_axes(n.numel(), _p(n), _ORDER[order], _p(out)))
+    return out
+
+
+def _rope(fn, q, k, axes, positions, pair_axis, inv_freq, layout, inverse, mscale, q_out, k_out):
     dt = _dt(q)
     if q.dim() != 3:
         raise ValueError("q must be [T, Hq, d]")
@@ -368,37 +375,59 @@ def rope(q, k, positions, inv_freq, layout: str = "half", inverse: bool = False,
         raise ValueError("k_out given without k")
     if layout not in _LAYOUT:
         raise ValueError("layout must be 'half' or 'interleaved'")
-    _buf("positions", positions, (T,), torch.int32)
+    _buf("positions", positions, (T,) if axes is None else (axes, T), torch.int32)
     if inv_freq.dim() != 1:
         raise ValueError("inv_freq must be 1-D")
     _buf("inv_freq", inv_freq, inv_freq.shape, torch.float64)
+    _buf("pair_axis", pair_axis, inv_freq.shape, torch.uint8)
     _need("q_out", q_out, q.shape, q.dtype)
     _need("k_out", k_out, None if k is None else k.shape, q.dtype)
-    dev = _device(q, k, positions, inv_freq, q_out, k_out)
+    dev = _device(q, k, positions, pair_axis, inv_freq, q_out, k_out)
     if q_out is None:
         q_out = torch.empty(T, Hq, d, dtype=q.dtype, device=dev)
     if k is not None and k_out is None:
         k_out = torch.empty(T, Hk, d, dtype=q.dtype, device=dev)
     ks, kos = (_rows("k", k), _rows("k_out", k_out)) if k is not None else (0, 0)
-    _call(dev, lib().kda_rope, "kda_rope", dt, T, Hq, Hk, d, 2 * inv_freq.shape[0], _LAYOUT[layout], int(inverse),
-          mscale, _p(positions), _p(inv_freq), _p(q), _rows("q", q), _p(k), ks, _p(q_out), _rows("q_out", q_out),
-          _p(k_out), kos)
+    where = (_p(positions),) if axes is None else (axes, _p(positions), _p(pair_axis))
+    _call(dev, getattr(lib(), fn), fn, dt, T, Hq, Hk, d, 2 * inv_freq.shape[0], _LAYOUT[layout], int(inverse), mscale,
+          *where, _p(inv_freq), _p(q), _rows("q", q), _p(k), ks, _p(q_out), _rows("q_out", q_out), _p(k_out), kos)
     return q_out, k_out
 
 
-def _norm_args(x, weight, bias, z, kind):
+def rope(q, k, positions, inv_freq, layout: str = "half", inverse: bool = False, mscale: float = 1.0,
+         q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None):
+    """Turns the first 2 * len(inv_freq) channels of every head of q [T, Hq, d]
+    and k [T, Hk, d] (or None) by positions (int32 [T]) times inv_freq (float64,
+    on the device); inverse turns back, which is the gradient.  layout "half"
+    pairs channels (i, i + rot/2), "interleaved" (2i, 2i + 1).  Outputs may be
+    the inputs.  Returns (q_out, k_out)."""
+    return _rope("kda_rope", q, k, None, positions, None, inv_freq, layout, inverse, mscale, q_out, k_out)
+
+
+def rope_axes(q, k, positions, pair_axis, inv_freq, layout: str = "half", inverse: bool = False, mscale: float = 1.0,
+              q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None):
+    """rope with several positions a token (time, height, width): positions int32
+    [axes, T], and pair i is turned by those of axis pair_axis[i] (uint8 on the
+    device, as rope_pair_axes makes them).  Returns (q_out, k_out)."""
+    if positions is None or positions.dim() != 2 or pair_axis is None:
+        raise ValueError("positions must be [axes, T], and pair_axis is required")
+    return _rope("kda_rope_axes", q, k, positions.shape[0], positions, pair_axis, inv_freq, layout, inverse, mscale,
+                 q_out, k_out)
+
+
+def _norm_args(x, weight, bias, z, kind, name="x"):
     dt = _dt(x)
     if kind not in _KIND:
         raise ValueError("kind must be 'layer' or 'rms'")
     if x.dim() != 3:
-        raise ValueError("x must be [T, H, D]")
+        raise ValueError(f"{name} must be [T, H, D]")
     T, H, D = x.shape
     if weight is None:
         raise ValueError("weight is required")
     _buf("weight", weight, (H, D), torch.float32)
     _buf("bias", bias, (H, D), torch.float32)
     _buf("z", z, x.shape, x.dtype)
-    _buf("x", x, x.shape, x.dtype)
+    _buf(name, x, x.shape, x.dtype)
     return dt, T, H, D
 
 
@@ -421,6 +450,31 @@ def norm_fwd(x, weight, bias=None, z=None, eps: float = 1e-5, kind: str = "layer
     _call(dev, lib().kda_norm_fwd, "kda_norm_fwd", dt, _KIND[kind], T, H, D, eps, _p(x), _p(weight), _p(bias),
           _p(z), _p(y), _p(mean), _p(rstd))
     return y, mean, rstd
+
+
+def _kept_shapes(T, H, D):
+    return (T, H, D), (T, H, (D + 127) // 128)
+
+
+def norm_fwd_kept(x, weight, bias=None, z=None, eps: float = 1e-5, kind: str = "layer",
+                  y: Optional[torch.Tensor] = None):
+    """norm_fwd that also keeps x and z in 8 bits for norm_bwd_kept.  Returns (y, mean,
+    rstd, kept) with kept = (x8, x_exp, z8, z_exp): float8_e4m3fn [T, H, D], and for
+    each 128 elements of a row 127 plus the exponent of the power of two they are
+    multiplied by, uint8 [T, H, ceil(D / 128)] (z8 and z_exp None without z)."""
+    dt, T, H, D = _norm_args(x, weight, bias, z, kind)
+    _buf("y", y, x.shape, x.dtype)
+    dev = _device(x, weight, bias, z, y)
+    if y is None:
+        y = torch.empty_like(x)
+    rstd = torch.empty(T, H, dtype=torch.float32, device=dev)
+    mean = torch.empty_like(rstd) if kind == "layer" else None
+    values, exps = _kept_shapes(T, H, D)
+    x8, xe = torch.empty(values, dtype=torch.float8_e4m3fn, device=dev), torch.empty(exps, dtype=torch.uint8, device=dev)
+    z8, ze = (None, None) if z is None else (torch.empty_like(x8), torch.empty_like(xe))
+    _call(dev, lib().kda_norm_fwd_kept, "kda_norm_fwd_kept", dt, _KIND[kind], T, H, D, eps, _p(x), _p(weight), _p(bias),
+          _p(z), _p(y), _p(mean), _p(rstd), _p(x8), _p(xe), _p(z8), _p(ze))
+    return y, mean, rstd, (x8, xe, z8, ze)
 
 
 def norm_bwd_workspace_size(dtype: int, T: int, H: int, D: int) -> int:
@@ -449,4 +503,35 @@ def norm_bwd(dy, x, weight, mean, rstd, bias=None, z=None, kind: str = "layer",
     workspace = _workspace("kda_norm_bwd", L.kda_norm_bwd_workspace_size(dt, T, H, D), workspace, dev)
     _call(dev, L.kda_norm_bwd, "kda_norm_bwd", dt, _KIND[kind], T, H, D, _p(x), _p(weight), _p(bias), _p(z),
           _p(mean), _p(rstd), _p(dy), _p(dx), _p(dw), _p(db), _p(dz), _p(workspace), workspace.numel())
+    return dx, dw, db, dz
+
+
+def norm_bwd_kept(dy, kept, weight, mean, rstd, bias=None, kind: str = "layer",
+                  workspace: Optional[torch.Tensor] = None):
+    """The gradient of norm_fwd_kept from the mean, rstd and kept that it returned: at
+    the kept values of x and z.  Returns (dx, dweight, dbias, dz) in dy's dtype (the
+    weight's gradients fp32); dbias and dz are None where bias and z were."""
+    x8, xe, z8, ze = kept
+    dt, T, H, D = _norm_args(dy, weight, bias, None, kind, "dy")
+    if x8 is None or xe is None or (z8 is None) != (ze is None):
+        raise ValueError("kept must be (x8, x_exp, z8, z_exp) as norm_fwd_kept returns them")
+    values, exps = _kept_shapes(T, H, D)
+    for name, t, e in (("x", x8, xe), ("z", z8, ze)):
+        _buf(name + "8", t, values, torch.float8_e4m3fn)
+        _buf(name + "_exp", e, exps, torch.uint8)
+    if rstd is None or (mean is None) != (kind == "rms"):
+        raise ValueError("rstd is required, and mean exactly for kind 'layer'")
+    _buf("mean", mean, (T, H), torch.float32)
+    _buf("rstd", rstd, (T, H), torch.float32)
+    _need_workspace(workspace)
+    _contiguous(workspace=workspace)
+    dev = _device(dy, x8, xe, z8, ze, weight, mean, rstd, bias, workspace)
+    L = lib()
+    dx = torch.empty_like(dy)
+    dz = None if z8 is None else torch.empty_like(dy)
+    dw = torch.empty_like(weight)
+    db = None if bias is None else torch.empty_like(bias)
+    workspace = _workspace("kda_norm_bwd", L.kda_norm_bwd_workspace_size(dt, T, H, D), workspace, dev)
+    _call(dev, L.kda_norm_bwd_kept, "kda_norm_bwd_kept", dt, _KIND[kind], T, H, D, _p(x8), _p(xe), _p(weight), _p(bias),
+          _p(z8), _p(ze), _p(mean), _p(rstd), _p(dy), _p(dx), _p(dw), _p(db), _p(dz), _p(workspace), workspace.numel())
     return dx, dw, db, dz

@@ -584,6 +584,33 @@ kda_status kda_rope(kda_dtype dt, int64_t T, int Hq, int Hk, int d, int rot, kda
                     int64_t k_out_stride, void* stream);
 
 typedef enum {
+    KDA_ROPE_RUNS = 0,    /* all pairs of the first axis, then of the second, ... */
+    KDA_ROPE_TURNS = 1    /* a pair of each axis in turn, while it has pairs left */
+} kda_rope_order;
+
+/*
+ * kda_rope_pair_axes -- host only: the axis of each pair for positions with
+ * several axes (time, height and width of images and video), sections[x] pairs for
+ * axis x, at most 512 in all.  pair_axis is host memory of that many bytes; the
+ * caller copies it to the device for kda_rope_axes.
+ */
+kda_status kda_rope_pair_axes(int axes, const int32_t* sections, kda_rope_order order, uint8_t* pair_axis);
+
+/*
+ * kda_rope_axes -- kda_rope with several positions a token: pair i is turned by
+ * positions[pair_axis[i]][t] * inv_freq[i].
+ *
+ *   axes             1 to 255.
+ *   positions        device int32 [axes, T], any values.
+ *   pair_axis        device bytes [rot / 2]; axes - 1 stands for those above it.
+ *   all other arguments: as kda_rope.
+ */
+kda_status kda_rope_axes(kda_dtype dt, int64_t T, int Hq, int Hk, int d, int rot, kda_rope_layout layout, int inverse,
+                         float mscale, int axes, const int32_t* positions, const uint8_t* pair_axis,
+                         const double* inv_freq, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                         void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* stream);
+
+typedef enum {
     KDA_NORM_LAYER = 0,   /* mean and variance */
     KDA_NORM_RMS = 1      /* mean square only */
 } kda_norm_kind;
@@ -625,6 +652,39 @@ kda_status kda_norm_bwd(kda_dtype dt, kda_norm_kind kind, int64_t T, int H, int 
                         const float* bias, const void* z, const float* mean, const float* rstd, const void* dy,
                         void* dx, float* dweight, float* dbias, void* dz, void* workspace, size_t workspace_bytes,
                         void* stream);
+
+/*
+ * kda_norm_fwd_kept -- kda_norm_fwd that also keeps its inputs in 8 bits for the
+ * gradient: half the bytes of bf16 between the two passes, written in the same
+ * pass over x and z.
+ *
+ *   x8, z8           bytes [T, H, D]: 4-bit-exponent, 3-bit-mantissa floating
+ *                    point (e4m3, no infinities); z8 given exactly where z is.
+ *   x_exp, z_exp     bytes [T, H, ceil(D / 128)]: for each 128 elements of a row,
+ *                    127 plus the exponent of the power of two that their values
+ *                    are multiplied by: the smallest (from -126 on) at which the
+ *                    largest is at most 448.  Values are rounded to the nearest,
+ *                    ties to even; NaN stays NaN, infinities become NaN.
+ *                    None of the four may overlap any other argument.
+ *   all other arguments: as kda_norm_fwd (y may be x or z).
+ */
+kda_status kda_norm_fwd_kept(kda_dtype dt, kda_norm_kind kind, int64_t T, int H, int D, float eps, const void* x,
+                             const float* weight, const float* bias, const void* z, void* y, float* mean, float* rstd,
+                             void* x8, uint8_t* x_exp, void* z8, uint8_t* z_exp, void* stream);
+
+/*
+ * kda_norm_bwd_kept -- kda_norm_bwd from what kda_norm_fwd_kept kept: the gradient at
+ * the kept values of x and z, with the mean and rstd of the full ones.
+ *
+ *   dt               dtype of dy, dx and dz.
+ *   dz               given exactly where z8 is.
+ *   workspace        kda_norm_bwd_workspace_size bytes.
+ */
+kda_status kda_norm_bwd_kept(kda_dtype dt, kda_norm_kind kind, int64_t T, int H, int D, const void* x8,
+                             const uint8_t* x_exp, const float* weight, const float* bias, const void* z8,
+                             const uint8_t* z_exp, const float* mean, const float* rstd, const void* dy, void* dx,
+                             float* dweight, float* dbias, void* dz, void* workspace, size_t workspace_bytes,
+                             void* stream);
 
 #ifdef __cplusplus
 }
