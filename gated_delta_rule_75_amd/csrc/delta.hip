@@ -154,7 +154,8 @@ __device__ __forceinline__ Frag8<T> cols8(const T* t, int s, int h, int s2, int 
 }
 
 // 2^(difference of two sums), each as integer and fraction.
-struct Sums {
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+struct __attribute__((aligned(16))) Sums {
     float frac[C];
     int whole[C];
     __device__ __forceinline__ void set(int lane, double G, bool valid) {
@@ -162,8 +163,33 @@ struct Sums {
         frac[lane] = (float)(G - w);
         whole[lane] = valid ? (int)w : -(1 << 20);   // a row without a token reads nothing
     }
-    __device__ __forceinline__ float ratio(int i, int j) const {
-        return __builtin_amdgcn_ldexpf(exp2_fast(frac[i] - frac[j]), whole[i] - whole[j]);
+    // rows i against j .. j + 3, those behind i and (strict) i itself 0; and rows i .. i + 3
+    // against j
+    __device__ __forceinline__ f32x4_t before(int i, int j, bool strict) const {
+        const f32x4_t f = *reinterpret_cast<const f32x4_t*>(frac + j);
+        const i32x4_t w = *reinterpret_cast<const i32x4_t*>(whole + j);
+        const float fi = frac[i];
+        const int wi = whole[i];
+        f32x4_t d;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            d[r] = __builtin_amdgcn_ldexpf(exp2_fast(fi - f[r]), wi - w[r]);
+            d[r] = j + r < i + !strict ? d[r] : 0.f;
+        }
+        return d;
+    }
+    __device__ __forceinline__ f32x4_t behind(int i, int j, bool strict) const {
+        const f32x4_t f = *reinterpret_cast<const f32x4_t*>(frac + i);
+        const i32x4_t w = *reinterpret_cast<const i32x4_t*>(whole + i);
+        const float fj = frac[j];
+        const int wj = whole[j];
+        f32x4_t d;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            d[r] = __builtin_amdgcn_ldexpf(exp2_fast(f[r] - fj), w[r] - wj);
+            d[r] = j < i + r + !strict ? d[r] : 0.f;
+        }
+        return d;
     }
 };
 
@@ -268,6 +294,8 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrArgs a) {
         tab[C + lane] = valid ? exp2_fast((float)(end - G)) : 0.f;
         tab[2 * C + lane] = beta;
         tab[3 * C + lane] = exp2_fast((float)end);
+        tab[4 * C + lane] = sums.frac[lane];
+        tab[5 * C + lane] = __int_as_float(sums.whole[lane]);
     }
     const T* const k = (const T*)a.k.p + bl.start * a.k.stride + (int64_t)(h / a.k.share) * DK;
     const T* const q = (const T*)a.q.p + bl.start * a.q.stride + (int64_t)(h / a.q.share) * DK;
@@ -291,8 +319,7 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrArgs a) {
 #pragma unroll
         for (int s = 0; s < SN; ++s) m = mma(other[s], own[s], m);
         const int i = 16 * wave + lr, j = 16 * tj + 4 * lg;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) m[r] = j + r < i ? m[r] * sums.ratio(i, j + r) : 0.f;
+        m *= sums.before(i, j, true);
         *reinterpret_cast<f32x4_t*>(sx + i * kLd + j) = m * *reinterpret_cast<const f32x4_t*>(s_beta + j);
         if constexpr (GRAD) *reinterpret_cast<f32x4_t*>(sz + i * kLd + j) = m * s_beta[i];
     }
@@ -315,11 +342,10 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrArgs a) {
 #pragma unroll
                 for (int s = 0; s < SN; ++s) d = mma(other[s], own[s], d);
             }
+            const int c = 16 * t + 4 * lg, w = 16 * wave + lr;
+            d *= GRAD ? sums.behind(c, w, false) : sums.before(w, c, false);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int c = 16 * t + 4 * lg + r, w = 16 * wave + lr, i = GRAD ? c : w, j = GRAD ? w : c;
-                x[4 * half + r] = in && j <= i ? d[r] * sums.ratio(i, j) * a.scale : 0.f;
-            }
+            for (int r = 0; r < 4; ++r) x[4 * half + r] = d[r] * a.scale;
         }
         if (some) put_operand<T, GRAD ? kThree<T> : kTwo<T>>(p, GRAD ? tri_piece_t(wave, s2) : tri_piece(wave, s2), lane, x);
     }
@@ -359,7 +385,7 @@ enum : int { kGdrOut = 0, kGdrStates = 1, kGdrBack = 2 };
 // then copied while this one is worked on).
 template <typename T, int DK, int MODE> constexpr int walk_bytes() {
     return C * DK * (int)sizeof(T) * (MODE == kGdrStates ? 1 : 2) + C * 64 * (int)sizeof(T) +
-           kTri<T, kThree<T>> + (MODE == kGdrStates ? 0 : MODE == kGdrOut ? kTri<T, kTwo<T>> : kTri<T, kThree<T>>) + kGdrTab * 4;
+           kTri<T, kThree<T>> + (MODE == kGdrStates ? 0 : MODE == kGdrOut ? kTri<T, kTwo<T>> : kTri<T, kThree<T>>) + 1024;
 }
 template <typename T, int DK, int MODE> constexpr int walk_bufs() { return 2 * walk_bytes<T, DK, MODE>() <= 160 * 1024 ? 2 : 1; }
 
@@ -664,285 +690,330 @@ __global__ __launch_bounds__(256, 1) void gdr_walk_kernel(GdrArgs a) {
 }
 
 // dQ, dK, dV in the inputs' type, dbeta and the tokens' terms of dg of a (chunk,
-// key head): the value heads that share the key head one after another, their
-// sums in registers.  A wave has DK / 4 channels of dQ and dK.
-template <typename T, int DK> constexpr int grad_bytes() { return 2 * C * DK * (int)sizeof(T) + 4 * kTri<T, kTwo<T>>; }
+// key head), eight waves: the value heads that share the key head one after
+// another, their sums in registers.
+//
+// A head's rows of E, dV = beta U and dY are read once, and kept in LDS as operands
+// in parts; a wave has 16 channels of dQ and dK (and half of the tokens where dk is
+// 64), whose rows of the two states are operands as they lie in memory.  Four waves
+// make the rows i of W and Y, four the rows j; these then take the place of E and dV.
+template <typename T, int DK, int DV>
+struct GradLds {
+    static constexpr int SZ = (int)sizeof(T), N2 = kTwo<T>, N3 = kThree<T>, TRI = kTri<T, N2>;
+    static constexpr int k = 0, rest = C * DK * SZ;
+    static constexpr int e = rest, x = e + N3 * C * DV * SZ, y = x + N2 * C * DV * SZ, first = y + C * DV * SZ;
+    static constexpr int w = rest, q = w + 4 * TRI, second = q + C * DK * SZ;      // over the rows, once they are read
+    static constexpr int dq = rest, dk = dq + C * DK * SZ, third = dk + C * DK * SZ;   // over all of that, at the end
+    static constexpr int most = first > second ? first : second, bytes = most > third ? most : third;
+};
 
 template <typename T, int DK, int DV>
-__global__ __launch_bounds__(256, 1) void gdr_grad_kernel(GdrArgs a) {
-    constexpr int SV = DV / 32, SK = DK / 32, NT = DK / 64, N2 = kTwo<T>, N3 = kThree<T>, EP = 16 / (int)sizeof(T);
-    constexpr int TRI = kTri<T, N2>;
+__global__ __launch_bounds__(512, 2) void gdr_grad_kernel(GdrArgs a) {
+    typedef GradLds<T, DK, DV> Lds;
+    typedef Tile<T, DV> TV;
+    typedef Tile<T, DK> TK;
+    constexpr int SV = DV / 32, SK = DK / 32, N2 = kTwo<T>, N3 = kThree<T>, EP = 16 / (int)sizeof(T), TRI = kTri<T, N2>;
+    constexpr int NCT = DK / 16, TN = NCT / 2;          // channel tiles; token tiles of a wave (4 or 2)
+    constexpr int TPR = DV / 8, NS = C * TPR / 512;     // staging: threads a row, runs of 8 a thread
+    constexpr int NQ = C * DK / EP / 512;               // runs of 16 bytes of a thread, of k and of q
     extern __shared__ __attribute__((aligned(16))) char smem[];
-    T* const sk = reinterpret_cast<T*>(smem);
-    T* const sq = sk + C * DK;
-    char* const w1 = reinterpret_cast<char*>(sq + C * DK);   // W beta and Y beta, rows i, then rows j
-    char* const y1 = w1 + TRI;
-    char* const w2 = y1 + TRI;
-    char* const y2 = w2 + TRI;
+    T* const sk = reinterpret_cast<T*>(smem + Lds::k);
+    T* const se = reinterpret_cast<T*>(smem + Lds::e);
+    T* const sx = reinterpret_cast<T*>(smem + Lds::x);
+    T* const sy = reinterpret_cast<T*>(smem + Lds::y);
+    T* const sq = reinterpret_cast<T*>(smem + Lds::q);
+    char* const wy = smem + Lds::w;                     // W beta and Y beta, rows i, then rows j
     __shared__ Sums sums;
-    __shared__ __attribute__((aligned(16))) float tab[kGdrTab];
-    __shared__ float part_s[4][C], part_p[C], part_v[C];
-    const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6), lr = lane & 15, lg = lane >> 4;
+    __shared__ __attribute__((aligned(16))) float tab[3 * C];
+    __shared__ float part_s[8][C], part_p[C], part_v[C];
+    int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lg = lane >> 4;
+    const int wave = uni(tid >> 6);
     const int H = a.at.H, r_heads = a.k.share, Hk = H / r_heads;
     const int b = uni(blockIdx.x / Hk), hk = blockIdx.x - b * Hk;
     const Block bl = find_block(a.at, b);
     if (bl.n < 0 || bl.cnt == 0) return;
     const int cnt = bl.cnt;
-    for (int i = tid; i < C * DK / EP; i += 256) {
-        const int row = i / (DK / EP), col = i % (DK / EP) * EP;
+    u32x4_t rq[NQ];
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+        const int u = i * 512 + tid, row = u / (DK / EP), col = u % (DK / EP) * EP;
         const int64_t tok = bl.start + (row < cnt ? row : cnt - 1);
-        *reinterpret_cast<u32x4_t*>(sk + Tile<T, DK>::off(row, col)) =
+        rq[i] = *reinterpret_cast<const u32x4_t*>((const T*)a.q.p + tok * a.q.stride + (int64_t)hk * DK + col);
+        *reinterpret_cast<u32x4_t*>(sk + TK::off(row, col)) =
             *reinterpret_cast<const u32x4_t*>((const T*)a.k.p + tok * a.k.stride + (int64_t)hk * DK + col);
-        *reinterpret_cast<u32x4_t*>(sq + Tile<T, DK>::off(row, col)) =
-            *reinterpret_cast<const u32x4_t*>((const T*)a.q.p + tok * a.q.stride + (int64_t)hk * DK + col);
     }
     const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
-    f32x4_t dq[4][NT], dk[4][NT];
+    const int ch0 = 16 * (wave % NCT), t0 = wave / NCT * TN;
+    f32x4_t dq[TN], dk[TN];
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) dq[t][n] = dk[t][n] = zero;
-    const int ch0 = wave * (DK / 4);
+    for (int t = 0; t < TN; ++t) dq[t] = dk[t] = zero;
     for (int m = 0; m < r_heads; ++m) {
         const int h = hk * r_heads + m;
+        // LDS addresses are formed anew for each head: kept across the loop they spill
+        asm volatile("" : "+v"(tid));
+        lane = tid & 63;
+        lr = lane & 15;
+        lg = lane >> 4;
         const int64_t slot = (int64_t)b * H + h;
-        const float* const E = a.errors + slot * C * DV;
-        const float* const U = a.u + slot * C * DV;
-        const T* const dy = (const T*)a.dy + (bl.start * H + h) * DV;
-        __syncthreads();
-        tab[tid] = a.tab[slot * kGdrTab + tid];
-        if (wave == 0) {
-            const bool valid = lane < cnt;
-            sums.set(lane, decay_scan(valid && a.g ? a.g[(bl.start + lane) * H + h] : 0.f), valid);
+        // the wave's rows of the states: on their way while the rows are laid out
+        float s_in[SV][8], r_in[SV][8];
+#pragma unroll
+        for (int s = 0; s < SV; ++s) {
+            const int64_t at = slot * DK * DV + (int64_t)(ch0 + lr) * DV + 32 * s + 8 * lg;
+            load8(a.states + at, s_in[s]);
+            load8(a.rstates + at, r_in[s]);
+        }
+        const float* const gtab = a.tab + slot * kGdrTab;
+        if (m > 0) __syncthreads();
+        if (tid < 3 * C) tab[tid] = gtab[tid];
+        if (tid < C) {
+            sums.frac[tid] = gtab[4 * C + tid];
+            sums.whole[tid] = __float_as_int(gtab[5 * C + tid]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        // rows of E, dV and dY to LDS; dv; e.u and v.dv by tokens
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            const int u = i * 512 + tid, row = u / TPR, col = u % TPR * 8;
+            const bool in = row < cnt;
+            const int64_t tok = bl.start + (in ? row : cnt - 1), at = slot * C * DV + row * DV + col;
+            float e[8], x[8], v[8];
+            load8(a.errors + at, e);
+            load8(a.u + at, x);
+            const T* const pv = (const T*)a.v.p + tok * a.v.stride + (int64_t)h * DV + col;
+            const T* const py = (const T*)a.dy + (tok * H + h) * DV + col;
+            const float be = gtab[2 * C + row];
+            float eu = 0.f, vx = 0.f;
+#pragma unroll
+            for (int c = 0; c < 8; c += EP) {
+                float w[EP];
+                load_vec<T, EP>(pv + c, w);
+                *reinterpret_cast<u32x4_t*>(sy + TV::off(row, col + c)) = *reinterpret_cast<const u32x4_t*>(py + c);
+#pragma unroll
+                for (int j = 0; j < EP; ++j) v[c + j] = w[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                eu += e[j] * x[j];
+                x[j] *= be;
+                vx += v[j] * x[j];
+            }
+            Frag8<T> f3[N3], f2[N2];
+            split(e, f3);
+            split(x, f2);
+            if constexpr (sizeof(T) == 2) {
+#pragma unroll
+                for (int p = 0; p < N3; ++p) *reinterpret_cast<bf16x8_t*>(se + p * C * DV + TV::off(row, col)) = f3[p].v;
+#pragma unroll
+                for (int p = 0; p < N2; ++p) *reinterpret_cast<bf16x8_t*>(sx + p * C * DV + TV::off(row, col)) = f2[p].v;
+            } else {
+#pragma unroll
+                for (int c = 0; c < 8; c += 4) {
+                    *reinterpret_cast<f32x4_t*>(se + TV::off(row, col + c)) = f32x4_t{e[c], e[c + 1], e[c + 2], e[c + 3]};
+                    *reinterpret_cast<f32x4_t*>(sx + TV::off(row, col + c)) = f32x4_t{x[c], x[c + 1], x[c + 2], x[c + 3]};
+                }
+            }
+            if (in) {
+                T* const o = (T*)a.dv_out + (tok * H + h) * DV + col;
+#pragma unroll
+                for (int c = 0; c < 8; c += EP) {
+                    float w[EP];
+#pragma unroll
+                    for (int j = 0; j < EP; ++j) w[j] = x[c + j];
+                    store_vec<T, EP>(o + c, w);
+                }
+            }
+            // over the threads of a row: 16, or 8
+            eu += dpp_mov<0xB1>(eu);
+            vx += dpp_mov<0xB1>(vx);
+            eu += dpp_mov<0x4E>(eu);
+            vx += dpp_mov<0x4E>(vx);
+            eu += dpp_mov<0x141>(eu);
+            vx += dpp_mov<0x141>(vx);
+            if constexpr (TPR == 16) {
+                eu += dpp_mov<0x140>(eu);
+                vx += dpp_mov<0x140>(vx);
+            }
+            if (tid % TPR == 0) {
+                part_v[row] = vx;
+                if (in) a.dbeta[tok * H + h] = eu;
+            }
         }
         __syncthreads();
-        auto dy_at = [&](int t, int s) {
-            const int row = 16 * t + lr < cnt ? 16 * t + lr : cnt - 1;
-            return frag_at(dy + (int64_t)row * H * DV + 32 * s + 8 * lg);
-        };
-        auto read_dy = [&](int t, Frag8<T> (&f)[SV][1]) {
+        // rows in parts, 8 consecutive columns a lane
+        auto rows_of = [&](const T* base, int t, int s, auto& f) {
+            constexpr int N = sizeof(f) / sizeof(f[0]);
 #pragma unroll
-            for (int s = 0; s < SV; ++s) f[s][0] = dy_at(t, s);
+            for (int p = 0; p < N; ++p) f[p] = TV::rows8(base + p * C * DV, 16 * t, s, lane);
         };
-        // rows of E, or of dV = beta U
-        auto part_at = [&](const float* p, int t, int s, bool scaled, auto& f) {
-            float x[8];
-            load8(p + (16 * t + lr) * DV + 32 * s + 8 * lg, x);
-            if (scaled) {
-                const float be = tab[2 * C + 16 * t + lr];
+        // W and Y: rows i of the wave against all before, or its rows j against all behind
+        const int own = wave & 3;
+        f32x4_t w[4], y[4];
+        if (wave < 4) {
+            Frag8<T> fy[SV][1], fx[SV][N2], fq[SK];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] *= be;
+            for (int s = 0; s < SV; ++s) {
+                rows_of(sy, own, s, fy[s]);
+                rows_of(sx, own, s, fx[s]);
             }
-            split(x, f);
-        };
-        // W and Y: rows i of the wave against all before, then its rows j against all behind
-        {
-            Frag8<T> fy[SV][1], fx[SV][N2];
-            read_dy(wave, fy);
+            const int i = 16 * own + lr;
+            const T* const q = (const T*)a.q.p + (bl.start + (i < cnt ? i : cnt - 1)) * a.q.stride + (int64_t)hk * DK;
 #pragma unroll
-            for (int s = 0; s < SV; ++s) part_at(U, wave, s, true, fx[s]);
-            const int i = 16 * wave + lr;
-            float pairs = 0.f;   // sum over j of W beta q_i.k_j, with the scores' 24 bits: an fp32 output's
+            for (int s = 0; s < SK; ++s) fq[s] = frag_at(q + 32 * s + 8 * lg);
+            float pairs = 0.f;   // sum over j of W beta q_i.k_j, with 24 bits: an fp32 output's
 #pragma unroll
             for (int tj = 0; tj < 4; ++tj) {
-                if (tj > (wave | 1)) continue;
-                f32x4_t w = zero, y = zero, qk = zero;
-                if (tj <= wave) {
+                w[tj] = y[tj] = zero;
+                if (tj > own) continue;
+                f32x4_t qk = zero;
 #pragma unroll
-                    for (int s = 0; s < SV; ++s) {
-                        Frag8<T> e3[N3], e2[N2];
-                        part_at(E, tj, s, false, e3);
-                        w = mma_parts(e3, fy[s], w);
+                for (int s = 0; s < SV; ++s) {
+                    Frag8<T> e3[N3], e2[N2];
+                    rows_of(se, tj, s, e3);
+                    w[tj] = mma_parts(e3, fy[s], w[tj]);
 #pragma unroll
-                        for (int p = 0; p < N2; ++p) e2[p] = e3[p];
-                        y = mma_parts(e2, fx[s], y);
-                    }
-#pragma unroll
-                    for (int s = 0; s < SK; ++s)
-                        qk = mma(Tile<T, DK>::rows8(sk, 16 * tj, s, lane), Tile<T, DK>::rows8(sq, 16 * wave, s, lane), qk);
+                    for (int p = 0; p < N2; ++p) e2[p] = e3[p];
+                    y[tj] = mma_parts(e2, fx[s], y[tj]);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int j = 16 * tj + 4 * lg + r;
-                    const float d = j <= i ? sums.ratio(i, j) * tab[2 * C + j] : 0.f;
-                    w[r] = j <= i ? w[r] * d * a.scale : 0.f;
-                    y[r] = j < i ? -y[r] * d : 0.f;
-                    pairs += w[r] * qk[r];
-                }
-                put_half<T>(w1, tri_piece(wave, tj >> 1), tj & 1, lane, w);
-                put_half<T>(y1, tri_piece(wave, tj >> 1), tj & 1, lane, y);
+                for (int s = 0; s < SK; ++s) qk = mma(TK::rows8(sk, 16 * tj, s, lane), fq[s], qk);
+                const int j = 16 * tj + 4 * lg;
+                const f32x4_t be = *reinterpret_cast<const f32x4_t*>(tab + 2 * C + j);
+                w[tj] *= sums.before(i, j, false) * be * a.scale;
+                y[tj] *= sums.before(i, j, true) * -be;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) pairs += w[tj][r] * qk[r];
             }
             pairs += __shfl_xor(pairs, 16);
             pairs += __shfl_xor(pairs, 32);
             if (lg == 0) part_p[i] = pairs;
+        } else {
             Frag8<T> fe[SV][N2];
 #pragma unroll
-            for (int s = 0; s < SV; ++s) part_at(E, wave, s, false, fe[s]);
-            const int j = 16 * wave + lr;
+            for (int s = 0; s < SV; ++s) rows_of(se, own, s, fe[s]);
+            const int j = 16 * own + lr;
 #pragma unroll
             for (int ti = 0; ti < 4; ++ti) {
-                if (ti < (wave & ~1)) continue;
-                f32x4_t w = zero, y = zero;
-                if (ti >= wave) {
-                    read_dy(ti, fy);
+                w[ti] = y[ti] = zero;
+                if (ti < own) continue;
 #pragma unroll
-                    for (int s = 0; s < SV; ++s) {
-                        part_at(U, ti, s, true, fx[s]);
-                        w = mma_parts(fy[s], fe[s], w);
-                        y = mma_parts(fx[s], fe[s], y);
-                    }
+                for (int s = 0; s < SV; ++s) {
+                    Frag8<T> fy[1], fx[N2];
+                    rows_of(sy, ti, s, fy);
+                    rows_of(sx, ti, s, fx);
+                    w[ti] = mma_parts(fy, fe[s], w[ti]);
+                    y[ti] = mma_parts(fx, fe[s], y[ti]);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int i = 16 * ti + 4 * lg + r;
-                    const float d = j <= i ? sums.ratio(i, j) * tab[2 * C + j] : 0.f;
-                    w[r] = j <= i ? w[r] * d * a.scale : 0.f;
-                    y[r] = j < i ? -y[r] * d : 0.f;
-                }
-                put_half<T>(w2, tri_piece_t(wave, ti >> 1), ti & 1, lane, w);
-                put_half<T>(y2, tri_piece_t(wave, ti >> 1), ti & 1, lane, y);
+                const float be = tab[2 * C + j];
+                w[ti] *= sums.behind(16 * ti + 4 * lg, j, false) * (be * a.scale);
+                y[ti] *= sums.behind(16 * ti + 4 * lg, j, true) * -be;
             }
         }
-        __syncthreads();
-        // the states' parts, the wave's channels
-        f32x4_t sq_[4][NT], sa[4][NT], sb[4][NT];
+        // the states' parts, the wave's channels and tokens
+        f32x4_t ps[TN], pa[TN], pb[TN];
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) sq_[t][n] = sa[t][n] = sb[t][n] = zero;
+        for (int t = 0; t < TN; ++t) ps[t] = pa[t] = pb[t] = zero;
 #pragma unroll
         for (int s = 0; s < SV; ++s) {
-            Frag8<T> s3[NT][N3], s2[NT][N2], r2[NT][N2];
+            Frag8<T> s3[N3], s2[N2], r2[N2];
+            split(s_in[s], s3);
+            split(r_in[s], r2);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int64_t at = slot * DK * DV + (int64_t)(ch0 + 16 * n + lr) * DV + 32 * s + 8 * lg;
-                float x[8];
-                load8(a.states + at, x);
-                split(x, s3[n]);
+            for (int p = 0; p < N2; ++p) s2[p] = s3[p];
 #pragma unroll
-                for (int p = 0; p < N2; ++p) s2[n][p] = s3[n][p];
-                load8(a.rstates + at, x);
-                split(x, r2[n]);
+            for (int t = 0; t < TN; ++t) {
+                Frag8<T> fy[1], fx[N2], fe[N2];
+                rows_of(sy, t0 + t, s, fy);
+                rows_of(sx, t0 + t, s, fx);
+                rows_of(se, t0 + t, s, fe);
+                ps[t] = mma_parts(fy, s3, ps[t]);
+                pa[t] = mma_parts(fx, s2, pa[t]);
+                pb[t] = mma_parts(fe, r2, pb[t]);
             }
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const Frag8<T> fy[1] = {dy_at(t, s)};
-                Frag8<T> fx[N2], fe[N2];
-                part_at(U, t, s, true, fx);
-                part_at(E, t, s, false, fe);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    sq_[t][n] = mma_parts(fy, s3[n], sq_[t][n]);
-                    sa[t][n] = mma_parts(fx, s2[n], sa[t][n]);
-                    sb[t][n] = mma_parts(fe, r2[n], sb[t][n]);
-                }
-            }
+            __builtin_amdgcn_sched_barrier(0);
         }
-        float dot[4][4];   // q . (state's part of dq)
+        __syncthreads();
+        // W and Y over E and dV, q over dY
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            const f32x4_t in = *reinterpret_cast<const f32x4_t*>(tab + 16 * t + 4 * lg);
-            const f32x4_t out = *reinterpret_cast<const f32x4_t*>(tab + C + 16 * t + 4 * lg);
-            const f32x4_t beta = *reinterpret_cast<const f32x4_t*>(tab + 2 * C + 16 * t + 4 * lg);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) dot[t][r] = 0.f;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                sq_[t][n] *= in * a.scale;
-                dq[t][n] += sq_[t][n];
-                dk[t][n] += out * beta * sb[t][n] - in * sa[t][n];
-            }
+            if (wave < 4 ? t > (own | 1) : t < (own & ~1)) continue;
+            char* const at = wy + (wave < 4 ? 0 : 2 * TRI);
+            const int piece = wave < 4 ? tri_piece(own, t >> 1) : tri_piece_t(own, t >> 1);
+            put_half<T>(at, piece, t & 1, lane, w[t]);
+            put_half<T>(at + TRI, piece, t & 1, lane, y[t]);
         }
-        // inside the chunk
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const Frag8<T> fk[2] = {Tile<T, DK>::cols(sk, ch0 + 16 * n, 0, lane), Tile<T, DK>::cols(sk, ch0 + 16 * n, 1, lane)};
-            const Frag8<T> fq[2] = {Tile<T, DK>::cols(sq, ch0 + 16 * n, 0, lane), Tile<T, DK>::cols(sq, ch0 + 16 * n, 1, lane)};
+        for (int i = 0; i < NQ; ++i) {
+            const int u = i * 512 + tid;
+            *reinterpret_cast<u32x4_t*>(sq + TK::off(u / (DK / EP), u % (DK / EP) * EP)) = rq[i];
+        }
+        __syncthreads();
+        {
+            const Frag8<T> fk[2] = {TK::cols(sk, ch0, 0, lane), TK::cols(sk, ch0, 1, lane)};
+            const Frag8<T> fq[2] = {TK::cols(sq, ch0, 0, lane), TK::cols(sq, ch0, 1, lane)};
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
+            for (int tt = 0; tt < TN; ++tt) {
+                const int t = t0 + tt;
+                const f32x4_t in = *reinterpret_cast<const f32x4_t*>(tab + 16 * t + 4 * lg);
+                const f32x4_t out = *reinterpret_cast<const f32x4_t*>(tab + C + 16 * t + 4 * lg);
+                const f32x4_t beta = *reinterpret_cast<const f32x4_t*>(tab + 2 * C + 16 * t + 4 * lg);
+                ps[tt] *= in * a.scale;
+                dq[tt] += ps[tt];
+                dk[tt] += out * beta * pb[tt] - in * pa[tt];
+                // q . (state's part of dq)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) dot[t][r] += fq[t >> 1].get(4 * (t & 1) + r) * sq_[t][n][r];
+                for (int r = 0; r < 4; ++r) {
+                    const float qv = t & 2 ? fq[1].get(4 * (t & 1) + r) : fq[0].get(4 * (t & 1) + r);
+                    const float u = row16_sum(qv * ps[tt][r]);
+                    if (lr == 0) part_s[wave % NCT][16 * t + 4 * lg + r] = u;
+                }
 #pragma unroll
                 for (int s2 = 0; s2 < 2; ++s2) {
                     const Frag8<T> bk[1] = {fk[s2]}, bq[1] = {fq[s2]};
                     Frag8<T> f[N2];
                     if (2 * s2 <= t) {
-                        get_operand<T, N2>(w1, tri_piece(t, s2), lane, f);
-                        dq[t][n] = mma_parts(f, bk, dq[t][n]);
-                        get_operand<T, N2>(y1, tri_piece(t, s2), lane, f);
-                        dk[t][n] = mma_parts(f, bk, dk[t][n]);
+                        get_operand<T, N2>(wy, tri_piece(t, s2), lane, f);
+                        dq[tt] = mma_parts(f, bk, dq[tt]);
+                        get_operand<T, N2>(wy + TRI, tri_piece(t, s2), lane, f);
+                        dk[tt] = mma_parts(f, bk, dk[tt]);
                     }
                     if (2 * s2 + 1 >= t) {
-                        get_operand<T, N2>(w2, tri_piece_t(t, s2), lane, f);
-                        dk[t][n] = mma_parts(f, bq, dk[t][n]);
-                        get_operand<T, N2>(y2, tri_piece_t(t, s2), lane, f);
-                        dk[t][n] = mma_parts(f, bk, dk[t][n]);
+                        get_operand<T, N2>(wy + 2 * TRI, tri_piece_t(t, s2), lane, f);
+                        dk[tt] = mma_parts(f, bq, dk[tt]);
+                        get_operand<T, N2>(wy + 3 * TRI, tri_piece_t(t, s2), lane, f);
+                        dk[tt] = mma_parts(f, bk, dk[tt]);
                     }
                 }
-            }
-        }
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float u = row16_sum(dot[t][r]);
-                if (lr == 0) part_s[wave][16 * t + 4 * lg + r] = u;
-            }
-        // dv = beta u, v.dv and e.u by tokens: 4 threads a token
-        {
-            const int row = tid >> 2, c0 = (tid & 3) * (DV / 4);
-            float s = 0.f, eu = 0.f;
-            if (row < cnt) {
-                const int64_t tok = bl.start + row;
-                const T* const v = (const T*)a.v.p + tok * a.v.stride + (int64_t)h * DV + c0;
-                T* const o = (T*)a.dv_out + (tok * H + h) * DV + c0;
-                const float be = tab[2 * C + row];
-#pragma unroll
-                for (int c = 0; c < DV / 4; c += 8) {
-                    float x[8], z[8];
-                    load8(U + row * DV + c0 + c, x);
-                    load8(E + row * DV + c0 + c, z);
-#pragma unroll
-                    for (int e = 0; e < 8; e += EP) {
-                        float u[EP], w[EP];
-                        load_vec<T, EP>(v + c + e, u);
-#pragma unroll
-                        for (int i = 0; i < EP; ++i) {
-                            eu += z[e + i] * x[e + i];
-                            w[i] = be * x[e + i];
-                            s += u[i] * w[i];
-                        }
-                        store_vec<T, EP>(o + c + e, w);
-                    }
-                }
-            }
-            s += dpp_mov<0xB1>(s);
-            s += dpp_mov<0x4E>(s);
-            eu += dpp_mov<0xB1>(eu);
-            eu += dpp_mov<0x4E>(eu);
-            if ((tid & 3) == 0) {
-                part_v[row] = s;
-                if (row < cnt) a.dbeta[(bl.start + row) * H + h] = eu;
             }
         }
         __syncthreads();
-        if (tid < cnt && a.dg)
-            a.terms[slot * C + tid] = ((part_s[0][tid] + part_s[1][tid]) + (part_s[2][tid] + part_s[3][tid])) +
-                                      (part_p[tid] - part_v[tid]);
-    }
+        if (tid < cnt && a.dg) {
+            float d = 0.f;
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = 16 * t + 4 * lg + r;
-            if (row >= cnt) continue;
-            const int64_t at = ((bl.start + row) * Hk + hk) * DK + ch0 + lr;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                gstore((T*)a.dq + at + 16 * n, dq[t][n][r]);
-                gstore((T*)a.dk + at + 16 * n, dk[t][n][r]);
-            }
+            for (int c = 0; c < NCT; ++c) d += part_s[c][tid];
+            a.terms[slot * C + tid] = d + (part_p[tid] - part_v[tid]);
         }
+    }
+    // whole rows of dq and dk through LDS
+#pragma unroll
+    for (int o = 0; o < 2; ++o) {
+        T* const to = reinterpret_cast<T*>(smem + (o ? Lds::dk : Lds::dq));
+#pragma unroll
+        for (int t = 0; t < TN; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) to[TK::off(16 * (t0 + t) + 4 * lg + r, ch0 + lr)] = from_f32<T>(o ? dk[t][r] : dq[t][r]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+        const int u = i * 512 + tid, row = u / (DK / EP), col = u % (DK / EP) * EP;
+        if (row >= cnt) continue;
+        const int64_t at = ((bl.start + row) * Hk + hk) * DK + col;
+        *reinterpret_cast<u32x4_t*>((T*)a.dq + at) = *reinterpret_cast<const u32x4_t*>(smem + Lds::dq + TK::off(row, col) * sizeof(T));
+        *reinterpret_cast<u32x4_t*>((T*)a.dk + at) = *reinterpret_cast<const u32x4_t*>(smem + Lds::dk + TK::off(row, col) * sizeof(T));
+    }
 }
 
 // dg of a block of kBlock chunks of a (sequence, head): the sum of the terms from
@@ -1026,12 +1097,13 @@ hipError_t walk_t(const GdrArgs& a) {
 template <typename T, int DK, int DV>
 hipError_t grad_t(const GdrArgs& a) {
     if (a.at.T_total == 0) return hipSuccess;
-    constexpr int lds = grad_bytes<T, DK>();
+    constexpr int lds = GradLds<T, DK, DV>::bytes;
+    static_assert(lds <= 152 * 1024, "LDS");
     const void* kern = reinterpret_cast<const void*>(&gdr_grad_kernel<T, DK, DV>);
     const hipError_t e = ensure_lds_limit(kern, lds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((gdr_grad_kernel<T, DK, DV>), dim3((unsigned)((int64_t)a.at.nblocks * (a.at.H / a.k.share))),
-                       dim3(256), lds, (hipStream_t)a.at.stream, a);
+                       dim3(512), lds, (hipStream_t)a.at.stream, a);
     return hipGetLastError();
 }
 

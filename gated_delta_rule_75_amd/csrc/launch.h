@@ -252,7 +252,7 @@ hipError_t launch_linattn_decode(const LinDecodeArgs& a);
 // The gated delta rule.  Per (chunk of 64 tokens, head) the workspace holds
 // operand tiles of 64 x 64 lower triangles (kTriBytes each) and the tables.
 constexpr int kTriBytes = 18 * 1024;
-constexpr int kGdrTab = 256;     // floats: decays from the chunk's start, to its end, beta, (the whole chunk's)
+constexpr int kGdrTab = 384;     // floats: decays from the chunk's start, to its end, beta, the whole chunk's; its sums
 struct GdrArgs {
     LinArgs at;                  // sizes, offsets, clear, stream
     LinRows q, k, v;
