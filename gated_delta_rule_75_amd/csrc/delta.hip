@@ -476,18 +476,31 @@ __global__ __launch_bounds__(256, 1) void gdr_walk_kernel(GdrArgs a) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) S[i][r] = s0 ? s0[(int64_t)channel(i, r) * DV] : 0.f;
     }
-    // stores of a chunk, issued behind the copies of the next one
-    constexpr int NST = NB == 1 ? 0 : MODE == kGdrOut ? 4 : KT * 4 + 16;
-    if (nch > 0) fetch(kBack ? nch - 1 : 0);
+    // A chunk's operands are read from LDS a phase before they are multiplied: a wave
+    // has its SIMD to itself, and nothing else hides the reads.  All of them are in
+    // registers when the chunk's barrier comes, so that its buffer takes the copies of
+    // the chunk after the next behind it, and the next one's rows of k are read.
+    Frag8<T> kr[4][SN];
+    auto read_k = [&](const Buf& f) {
+#pragma unroll
+        for (int s = 0; s < SN; ++s)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) kr[t][s] = Tile<T, DK>::rows8(f.k, 16 * t, s, lane);
+    };
+    auto chunk_at = [&](int step) { return kBack ? nch - 1 - step : step; };
+    // stores between the copies of a chunk and the wait for them
+    constexpr int NST = MODE == kGdrOut ? 4 : KT * 4 + 16;
+    static_assert(NST < 64, "vmcnt");
+    if (nch > 0) fetch(chunk_at(0));
     wait_vmcnt<0>();
-    for (int step = 0; step < nch; ++step) {
-        const int c = kBack ? nch - 1 - step : step, m0 = c * C;
-        const bool more = step + 1 < nch;
-        const int next = kBack ? c - 1 : c + 1;
-        // the chunk's copies are there; the chunk before is read
-        if (step > 0) wait_vmcnt<NST>();
+    if (nch > 0) {
         barrier_keep_loads();
-        if (NB == 2 && more) fetch(next);
+        read_k(buf(chunk_at(0)));
+        if (NB == 2 && nch > 1) fetch(chunk_at(1));
+    }
+    for (int step = 0; step < nch; ++step) {
+        const int c = chunk_at(step), m0 = c * C;
+        const bool more = step + 1 < nch;
         const Buf f = buf(c);
         const int64_t slot = (int64_t)(fb + c) * H + h;
         const float end = unif(f.tab[3 * C]);
@@ -518,8 +531,23 @@ __global__ __launch_bounds__(256, 1) void gdr_walk_kernel(GdrArgs a) {
                     __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[i][r]), rsrc,
                                                           (unsigned)((channel(i, r) * DV + lr) * 4), 0, 0);
         }
-        // K S (or K R), a lane 4 tokens of a column
-        Frag8<T> fs[SN][N3];
+        // A: K S (or K R), a lane 4 tokens of a column; X (Z), P^T, the tables and v (dy) come
+        Frag8<T> fx[6][N3], fp[6][NPP], fs[SN][N3];
+#pragma unroll
+        for (int i = 0; i < 6; ++i) get_operand<T, N3>(f.x, i, lane, fx[i]);
+        if constexpr (kBack) {
+#pragma unroll
+            for (int i = 0; i < 6; ++i) get_operand<T, NPP>(f.p, i, lane, fp[i]);
+        }
+        f32x4_t in[4], out[4], beta[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            in[t] = *reinterpret_cast<const f32x4_t*>(f.tab + 16 * t + 4 * lg);
+            out[t] = *reinterpret_cast<const f32x4_t*>(f.tab + C + 16 * t + 4 * lg);
+            beta[t] = *reinterpret_cast<const f32x4_t*>(f.tab + 2 * C + 16 * t + 4 * lg);
+        }
+        // the wave's columns of v (or dy), a lane 4 tokens of each tile
+        const Frag8<T> fv[2] = {Tile<T, 64>::cols(f.v, wcol, 0, lane), Tile<T, 64>::cols(f.v, wcol, 1, lane)};
         f32x4_t ks[4] = {zero, zero, zero, zero};
 #pragma unroll
         for (int s = 0; s < SN; ++s) {
@@ -531,20 +559,33 @@ __global__ __launch_bounds__(256, 1) void gdr_walk_kernel(GdrArgs a) {
             }
             split(x, fs[s]);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const Frag8<T> fk[1] = {Tile<T, DK>::rows8(f.k, 16 * t, s, lane)};
-                ks[t] = mma_parts(fk, fs[s], ks[t]);
-            }
-        }
-        f32x4_t in[4], out[4], beta[4];
+            for (int p = N3 - 1; p >= 0; --p)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            in[t] = *reinterpret_cast<const f32x4_t*>(f.tab + 16 * t + 4 * lg);
-            out[t] = *reinterpret_cast<const f32x4_t*>(f.tab + C + 16 * t + 4 * lg);
-            beta[t] = *reinterpret_cast<const f32x4_t*>(f.tab + 2 * C + 16 * t + 4 * lg);
+                for (int t = 0; t < 4; ++t) ks[t] = mma(kr[t][s], fs[s][p], ks[t]);
         }
-        // the wave's columns of v (or dy), a lane 4 tokens of each tile
-        const Frag8<T> fv[2] = {Tile<T, 64>::cols(f.v, wcol, 0, lane), Tile<T, 64>::cols(f.v, wcol, 1, lane)};
+        if (end == 0.f) {
+#pragma unroll
+            for (int i = 0; i < KT; ++i) S[i] = zero;
+        } else {
+#pragma unroll
+            for (int i = 0; i < KT; ++i) S[i] *= end;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        // B: V - exp(G) K S, or P^T dY + exp(G_63 - G) K R; rows of q come (backwards: its columns)
+        Frag8<T> fq[kBack ? KT : 4][kBack ? 2 : SN];
+        if constexpr (MODE == kGdrOut) {
+#pragma unroll
+            for (int s = 0; s < SN; ++s)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) fq[t][s] = Tile<T, DK>::rows8(f.q, 16 * t, s, lane);
+#pragma unroll
+            for (int i = 0; i < 6; ++i) get_operand<T, NPP>(f.p, i, lane, fp[i]);
+        } else if constexpr (kBack) {
+#pragma unroll
+            for (int s2 = 0; s2 < 2; ++s2)
+#pragma unroll
+                for (int i = 0; i < KT; ++i) fq[i][s2] = cols8<T, DK>(f.q, i >> 1, i & 1, s2, lane);
+        }
         // two 16-token tiles as an operand in parts
         auto operand = [&](const f32x4_t& lo, const f32x4_t& hi, auto& o) {
             float x[8];
@@ -555,7 +596,7 @@ __global__ __launch_bounds__(256, 1) void gdr_walk_kernel(GdrArgs a) {
             }
             split(x, o);
         };
-        f32x4_t e[4];      // V - exp(G) K S, then E; backwards P^T dY + exp(G_63 - G) K R, then U
+        f32x4_t e[4];
         Frag8<T> fe[2][N3];
         if constexpr (!kBack) {
 #pragma unroll
@@ -564,29 +605,65 @@ __global__ __launch_bounds__(256, 1) void gdr_walk_kernel(GdrArgs a) {
                 for (int r = 0; r < 4; ++r) e[t][r] = fv[t >> 1].get(4 * (t & 1) + r) - in[t][r] * ks[t][r];
         } else {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                e[t] = out[t] * ks[t];
+            for (int t = 0; t < 4; ++t) e[t] = out[t] * ks[t];
 #pragma unroll
-                for (int s2 = 0; s2 < 2; ++s2) {
-                    if (2 * s2 + 1 < t) continue;
-                    Frag8<T> fp[NPP];
-                    get_operand<T, NPP>(f.p, tri_piece_t(t, s2), lane, fp);
-                    const Frag8<T> d[1] = {fv[s2]};
-                    e[t] = mma_parts(fp, d, e[t]);
-                }
-            }
+            for (int s2 = 0; s2 < 2; ++s2)
+#pragma unroll
+                for (int p = NPP - 1; p >= 0; --p)
+#pragma unroll
+                    for (int t = 0; t < 2 * s2 + 2; ++t) e[t] = mma(fp[tri_piece_t(t, s2)][p], fv[s2], e[t]);
         }
 #pragma unroll
         for (int s2 = 0; s2 < 2; ++s2) operand(e[2 * s2], e[2 * s2 + 1], fe[s2]);
+        __builtin_amdgcn_sched_barrier(0);
+        // C: E (or U); the columns of k come.  Beside it what does not wait for E: y's part of
+        // the entering state, transposed tiles, a lane 4 columns of token 16 t + l % 16; or dY's
+        // part of R
+        Frag8<T> fk[KT][2];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            e[t] = zero;
+        for (int s2 = 0; s2 < 2; ++s2)
+#pragma unroll
+            for (int i = 0; i < KT; ++i) fk[i][s2] = cols8<T, DK>(f.k, i >> 1, i & 1, s2, lane);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) e[t] = zero;
+#pragma unroll
+        for (int s = N3 - 1; s >= 0; --s)
+#pragma unroll
+            for (int i = 0; i <= s; ++i)
+#pragma unroll
+                for (int s2 = 0; s2 < 2; ++s2)
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        if (kBack ? 2 * s2 + 1 >= t : 2 * s2 <= t)
+                            e[t] = mma(fx[kBack ? tri_piece_t(t, s2) : tri_piece(t, s2)][i], fe[s2][s - i], e[t]);
+        f32x4_t y[4] = {zero, zero, zero, zero};
+        float into[4];
+        if constexpr (MODE == kGdrOut) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) into[t] = f.tab[16 * t + lr];
+            // the state's leading 16 bits
+#pragma unroll
+            for (int s = 0; s < SN; ++s)
+#pragma unroll
+                for (int p = NPP - 1; p >= 0; --p)
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) y[t] = mma(fs[s][p], fq[t][s], y[t]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) y[t] *= into[t] * scale;
+        } else if constexpr (kBack) {
 #pragma unroll
             for (int s2 = 0; s2 < 2; ++s2) {
-                if (kBack ? 2 * s2 + 1 < t : 2 * s2 > t) continue;
-                Frag8<T> fx[N3];
-                get_operand<T, N3>(f.x, kBack ? tri_piece_t(t, s2) : tri_piece(t, s2), lane, fx);
-                e[t] = mma_parts(fx, fe[s2], e[t]);
+                Frag8<T> u[N3];
+                f32x4_t d[2];
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) d[half][r] = fv[s2].get(4 * half + r) * (in[2 * s2 + half][r] * scale);
+                operand(d[0], d[1], u);
+#pragma unroll
+                for (int p = N3 - 1; p >= 0; --p)
+#pragma unroll
+                    for (int i = 0; i < KT; ++i) S[i] = mma(fq[i][s2], u[p], S[i]);
             }
         }
         if constexpr (MODE != kGdrOut) {
@@ -599,84 +676,74 @@ __global__ __launch_bounds__(256, 1) void gdr_walk_kernel(GdrArgs a) {
                     __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(e[t][r]), rsrc,
                                                           (unsigned)(((16 * t + 4 * lg + r) * DV + lr) * 4), 0, 0);
         }
+        // the next chunk's copies are there, this one's operands in registers
+        if (NB == 2) {
+            if (MODE == kGdrOut && step == 0) wait_vmcnt<0>();
+            else wait_vmcnt<NST>();
+        }
+        barrier_keep_loads();
+        if (NB == 2) {
+            if (step + 2 < nch) fetch(chunk_at(step + 2));
+            if (more) read_k(buf(chunk_at(step + 1)));
+        } else if (more) {
+            fetch(chunk_at(step + 1));
+        }
+        // D: the chunk's own part of y, and of the state behind it (or of the gradient before it)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) e[t] *= beta[t];
         if constexpr (MODE == kGdrOut) {
-            // y, transposed tiles: a lane 4 columns of token 16 t + l % 16
-            f32x4_t y[4];
             Frag8<T> fb[2][NPP];
 #pragma unroll
-            for (int s2 = 0; s2 < 2; ++s2) operand(beta[2 * s2] * e[2 * s2], beta[2 * s2 + 1] * e[2 * s2 + 1], fb[s2]);
+            for (int s2 = 0; s2 < 2; ++s2) operand(e[2 * s2], e[2 * s2 + 1], fb[s2]);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                y[t] = zero;
+            for (int s = NPP - 1; s >= 0; --s)
 #pragma unroll
-                for (int s = 0; s < SN; ++s) {
-                    // the state's leading 16 bits
-                    const Frag8<T> fq[1] = {Tile<T, DK>::rows8(f.q, 16 * t, s, lane)};
-                    Frag8<T> f2[NPP];
+                for (int i = 0; i <= s; ++i)
 #pragma unroll
-                    for (int p = 0; p < NPP; ++p) f2[p] = fs[s][p];
-                    y[t] = mma_parts(f2, fq, y[t]);
-                }
-                y[t] *= f.tab[16 * t + lr] * scale;
+                    for (int s2 = 0; s2 < 2; ++s2)
 #pragma unroll
-                for (int s2 = 0; s2 < 2; ++s2) {
-                    if (2 * s2 > t) continue;
-                    Frag8<T> fp[NPP];
-                    get_operand<T, NPP>(f.p, tri_piece(t, s2), lane, fp);
-                    y[t] = mma_parts(fb[s2], fp, y[t]);
-                }
-                if (lost) {
+                        for (int t = 2 * s2; t < 4; ++t) y[t] = mma(fb[s2][i], fp[tri_piece(t, s2)][s - i], y[t]);
+        }
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if ((lost >> (4 * lg + r) & 1) && f.tab[16 * t + lr] != 0.f) y[t][r] = __builtin_nanf("");
-                }
-            }
+        for (int s2 = 0; s2 < 2; ++s2) {
+            Frag8<T> u[N3];
+            if constexpr (!kBack) operand(out[2 * s2] * e[2 * s2], out[2 * s2 + 1] * e[2 * s2 + 1], u);
+            else operand(-(in[2 * s2] * e[2 * s2]), -(in[2 * s2 + 1] * e[2 * s2 + 1]), u);
+#pragma unroll
+            for (int p = N3 - 1; p >= 0; --p)
+#pragma unroll
+                for (int i = 0; i < KT; ++i) S[i] = mma(fk[i][s2], u[p], S[i]);
+        }
+        if constexpr (MODE == kGdrOut) {
             // rows without a token lie behind the bound and are dropped
             const unsigned step_o = xo.step;
             const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(xo.token(m0)), 0,
                                                                 uni((unsigned)(rows.tokens(m0) - 1) * step_o + 64 * SZ), 0x00027000);
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
+            auto store = [&](int t, const f32x4_t& v) {
                 const unsigned at = (unsigned)(16 * t + lr) * step_o + (unsigned)((wcol + 4 * lg) * SZ);
                 if constexpr (SZ == 4) {
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, y[t]), rsrc, at, 0, 0);
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), rsrc, at, 0, 0);
                 } else {
-                    const u32x2_t o = {cvt2(y[t][0], y[t][1]), cvt2(y[t][2], y[t][3])};
+                    const u32x2_t o = {cvt2(v[0], v[1]), cvt2(v[2], v[3])};
                     __builtin_amdgcn_raw_buffer_store_b64(o, rsrc, at, 0, 0);
                 }
-            }
-        }
-        // the state behind the chunk (or the gradient before it)
+            };
 #pragma unroll
-        for (int i = 0; i < KT; ++i) S[i] = end == 0.f ? zero : S[i] * end;
+            for (int t = 0; t < 4; ++t) store(t, y[t]);
+            if (lost) {   // once more, with what the lost state has made of the tokens before its end
 #pragma unroll
-        for (int s2 = 0; s2 < 2; ++s2) {
-            Frag8<T> u[N3];
-            if constexpr (!kBack) {
-                operand(out[2 * s2] * beta[2 * s2] * e[2 * s2], out[2 * s2 + 1] * beta[2 * s2 + 1] * e[2 * s2 + 1], u);
-            } else {
-                f32x4_t d[2];
+                for (int t = 0; t < 4; ++t) {
 #pragma unroll
-                for (int half = 0; half < 2; ++half)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) d[half][r] = fv[s2].get(4 * half + r) * (in[2 * s2 + half][r] * scale);
-                operand(d[0], d[1], u);
-#pragma unroll
-                for (int i = 0; i < KT; ++i) {
-                    const Frag8<T> fq[1] = {cols8<T, DK>(f.q, i >> 1, i & 1, s2, lane)};
-                    S[i] = mma_parts(fq, u, S[i]);
+                    for (int r = 0; r < 4; ++r)
+                        if ((lost >> (4 * lg + r) & 1) && into[t] != 0.f) y[t][r] = __builtin_nanf("");
+                    store(t, y[t]);
                 }
-                operand(-(in[2 * s2] * beta[2 * s2] * e[2 * s2]), -(in[2 * s2 + 1] * beta[2 * s2 + 1] * e[2 * s2 + 1]), u);
-            }
-#pragma unroll
-            for (int i = 0; i < KT; ++i) {
-                const Frag8<T> fk[1] = {cols8<T, DK>(f.k, i >> 1, i & 1, s2, lane)};
-                S[i] = mma_parts(fk, u, S[i]);
             }
         }
         if (NB == 1 && more) {
+            wait_vmcnt<0>();
             barrier_keep_loads();
-            fetch(next);
+            read_k(buf(0));
         }
     }
     float* dst = kBack ? a.d_initial : a.final;
