@@ -378,14 +378,19 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrArgs a) {
     }
 }
 
-enum : int { kGdrOut = 0, kGdrStates = 1, kGdrBack = 2 };
+// Walks: outputs, or (for the gradient) states and errors; backwards; and forwards
+// and backwards over the segments of cut sequences, from zero (or, forwards, from the
+// unit matrix), for what a segment does to a state alone.
+enum : int { kGdrOut = 0, kGdrStates = 1, kGdrBack = 2, kGdrSeg = 3, kGdrBackSeg = 4 };
+constexpr bool back_mode(int m) { return m == kGdrBack || m == kGdrBackSeg; }
+constexpr bool reads_q(int m) { return m == kGdrOut || back_mode(m); }
 
 // LDS of the walks: rows of k and q, 64 columns of v or dy, operand tiles of the
 // inverse and the scores, the tables; twice where two fit (the next chunk's are
 // then copied while this one is worked on).
 template <typename T, int DK, int MODE> constexpr int walk_bytes() {
-    return C * DK * (int)sizeof(T) * (MODE == kGdrStates ? 1 : 2) + C * 64 * (int)sizeof(T) +
-           kTri<T, kThree<T>> + (MODE == kGdrStates ? 0 : MODE == kGdrOut ? kTri<T, kTwo<T>> : kTri<T, kThree<T>>) + 1024;
+    return C * DK * (int)sizeof(T) * (reads_q(MODE) ? 2 : 1) + C * 64 * (int)sizeof(T) + kTri<T, kThree<T>> +
+           (!reads_q(MODE) ? 0 : MODE == kGdrOut ? kTri<T, kTwo<T>> : kTri<T, kThree<T>>) + 1024;
 }
 template <typename T, int DK, int MODE> constexpr int walk_bufs() { return 2 * walk_bytes<T, DK, MODE>() <= 160 * 1024 ? 2 : 1; }
 
@@ -403,30 +408,37 @@ __device__ __forceinline__ void copy_flat(char* lds, const char* src, int wave, 
 template <typename T, int DK, int MODE>
 __global__ __launch_bounds__(256, 1) void gdr_walk_kernel(GdrArgs a) {
     constexpr int SN = DK / 32, KT = DK / 16, N3 = kThree<T>, NPP = MODE == kGdrOut ? kTwo<T> : N3, NB = walk_bufs<T, DK, MODE>(), SZ = (int)sizeof(T);
-    constexpr bool kBack = MODE == kGdrBack, kQ = MODE != kGdrStates;
+    constexpr bool kBack = back_mode(MODE), kQ = reads_q(MODE), kKeep = MODE == kGdrStates || MODE == kGdrBack;
     extern __shared__ __attribute__((aligned(16))) char smem[];
     const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6), lr = lane & 15, lg = lane >> 4;
-    const int H = a.at.H, DV = a.head_v, slices = DV / 64, chains = a.at.num_seqs * H;
+    const int H = a.at.H, DV = a.head_v, slices = DV / 64 + (MODE == kGdrSeg ? DK / 64 : 0), chains = a.seg.nblocks * H;
     // the slices of a head read the same rows: 8 heads apart in the launch, so
     // that they run on one XCD
     const int group = uni(blockIdx.x / (8 * slices)), rem = blockIdx.x - group * 8 * slices;
     const int width = chains - group * 8 < 8 ? chains - group * 8 : 8;
     const int slice = uni(rem / width), chain = group * 8 + rem - slice * width;
-    const int n = uni(chain / H), h = chain - n * H;
-    const int64_t begin = uni64(seq_at(a.at, n)), end_at = uni64(seq_at(a.at, n + 1));
-    const int cnt = (int)(end_at > begin ? end_at - begin : 0);
-    const int fb = uni(first_block(a.at, n));
+    const int sgm = uni(chain / H), h = chain - sgm * H;
+    const Block sb = find_block(a.seg, sgm);
+    if (sb.n < 0) return;
+    const bool first = sb.j == 0, last = sb.j == sb.nb - 1;
+    const bool unit = MODE == kGdrSeg && slice * 64 >= DV;   // columns of the transition, not of values
+    if (MODE == kGdrSeg && (sb.nb == 1 || (last && !(unit && a.seg_mt)))) return;
+    if (MODE == kGdrBackSeg && first) return;
+    // (uni: else the compiler takes addresses for different in each lane)
+    const int n = uni(sb.n), cnt = uni(sb.cnt);
+    const int64_t begin = uni64(sb.start);
+    const int fb = uni(first_block(a.at, n) + sb.j * (int)(a.seg.L / C));
     int nch = (cnt + C - 1) / C;
-    nch = nch < a.at.nblocks - fb ? nch : a.at.nblocks - fb;   // offsets out of order: stay inside the workspace
+    nch = uni(nch < a.at.nblocks - fb ? nch : a.at.nblocks - fb);   // offsets out of order: stay inside the workspace
     const Rows rows{cnt, nch * C, false};
-    const int col0 = slice * 64, wcol = 16 * wave;
+    const int col0 = unit ? slice * 64 - DV : slice * 64, wcol = 16 * wave;
     const int64_t DKV = (int64_t)DK * DV;
 
     Src xk, xq, xv, xo;
     xk.set((const T*)a.k.p, begin * a.k.stride + (int64_t)(h / a.k.share) * DK, a.k.stride);
     xq.set((const T*)a.q.p, begin * a.q.stride + (int64_t)(h / a.q.share) * DK, a.q.stride);
     if constexpr (kBack) xv.set((const T*)a.dy, (begin * H + h) * DV + col0, (int64_t)H * DV);
-    else xv.set((const T*)a.v.p, begin * a.v.stride + (int64_t)h * DV + col0, a.v.stride);
+    else xv.set((const T*)a.v.p, begin * a.v.stride + (int64_t)h * DV + (unit ? 0 : col0), a.v.stride);
     if constexpr (MODE == kGdrOut) xo.set((const T*)a.y, (begin * H + h) * DV + col0, (int64_t)H * DV);
     const float scale = pin(a.scale);
 
@@ -469,12 +481,18 @@ __global__ __launch_bounds__(256, 1) void gdr_walk_kernel(GdrArgs a) {
 
     f32x4_t S[KT];
     {
-        const float* s0 = kBack ? a.d_final : a.initial;
-        if (s0) s0 += ((int64_t)n * H + h) * DKV + col0 + wcol + lr;
+        const float* s0 = nullptr;
+        if (MODE == kGdrOut || kKeep) {
+            s0 = kBack ? a.seg_r : a.seg_s;
+            if (s0) s0 += ((int64_t)sgm * H + h) * DKV;
+            else if ((s0 = kBack ? a.d_final : a.initial)) s0 += ((int64_t)n * H + h) * DKV;
+            if (s0) s0 += col0 + wcol + lr;
+        }
 #pragma unroll
         for (int i = 0; i < KT; ++i)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) S[i][r] = s0 ? s0[(int64_t)channel(i, r) * DV] : 0.f;
+            for (int r = 0; r < 4; ++r)
+                S[i][r] = s0 ? s0[(int64_t)channel(i, r) * DV] : unit && channel(i, r) == col0 + wcol + lr ? 1.f : 0.f;
     }
     // A chunk's operands are read from LDS a phase before they are multiplied: a wave
     // has its SIMD to itself, and nothing else hides the reads.  All of them are in
@@ -489,7 +507,7 @@ __global__ __launch_bounds__(256, 1) void gdr_walk_kernel(GdrArgs a) {
     };
     auto chunk_at = [&](int step) { return kBack ? nch - 1 - step : step; };
     // stores between the copies of a chunk and the wait for them
-    constexpr int NST = MODE == kGdrOut ? 4 : KT * 4 + 16;
+    constexpr int NST = MODE == kGdrOut ? 4 : kKeep ? KT * 4 + 16 : 0;
     static_assert(NST < 64, "vmcnt");
     if (nch > 0) fetch(chunk_at(0));
     wait_vmcnt<0>();
@@ -520,7 +538,7 @@ __global__ __launch_bounds__(256, 1) void gdr_walk_kernel(GdrArgs a) {
                 for (int i = 0; i < KT; ++i) S[i] = zero;
             }
         }
-        if constexpr (MODE != kGdrOut) {
+        if constexpr (kKeep) {
             // the state before the chunk, or the gradient behind it
             float* const dst = (kBack ? a.rstates : a.states) + slot * DKV + col0 + wcol;
             const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(dst, 0, (unsigned)(DKV * 4), 0x00027000);
@@ -547,7 +565,14 @@ __global__ __launch_bounds__(256, 1) void gdr_walk_kernel(GdrArgs a) {
             beta[t] = *reinterpret_cast<const f32x4_t*>(f.tab + 2 * C + 16 * t + 4 * lg);
         }
         // the wave's columns of v (or dy), a lane 4 tokens of each tile
-        const Frag8<T> fv[2] = {Tile<T, 64>::cols(f.v, wcol, 0, lane), Tile<T, 64>::cols(f.v, wcol, 1, lane)};
+        Frag8<T> fv[2] = {Tile<T, 64>::cols(f.v, wcol, 0, lane), Tile<T, 64>::cols(f.v, wcol, 1, lane)};
+        if (unit) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                fv[0].set(j, 0.f);
+                fv[1].set(j, 0.f);
+            }
+        }
         f32x4_t ks[4] = {zero, zero, zero, zero};
 #pragma unroll
         for (int s = 0; s < SN; ++s) {
@@ -666,7 +691,7 @@ __global__ __launch_bounds__(256, 1) void gdr_walk_kernel(GdrArgs a) {
                     for (int i = 0; i < KT; ++i) S[i] = mma(fq[i][s2], u[p], S[i]);
             }
         }
-        if constexpr (MODE != kGdrOut) {
+        if constexpr (kKeep) {
             float* const dst = (kBack ? a.u : a.errors) + slot * C * DV + col0 + wcol;
             const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(dst, 0, (unsigned)(C * DV * 4), 0x00027000);
 #pragma unroll
@@ -678,7 +703,7 @@ __global__ __launch_bounds__(256, 1) void gdr_walk_kernel(GdrArgs a) {
         }
         // the next chunk's copies are there, this one's operands in registers
         if (NB == 2) {
-            if (MODE == kGdrOut && step == 0) wait_vmcnt<0>();
+            if (!kKeep && step == 0) wait_vmcnt<0>();
             else wait_vmcnt<NST>();
         }
         barrier_keep_loads();
@@ -746,13 +771,111 @@ __global__ __launch_bounds__(256, 1) void gdr_walk_kernel(GdrArgs a) {
             read_k(buf(0));
         }
     }
-    float* dst = kBack ? a.d_initial : a.final;
+    if (unit) {
+        const int col = col0 + wcol + lr;
+        const int64_t at = ((int64_t)sgm * H + h) * DK * DK;
+#pragma unroll
+        for (int i = 0; i < KT; ++i) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) a.seg_m[at + channel(i, r) * DK + col] = S[i][r];
+            if (a.seg_mt) *reinterpret_cast<f32x4_t*>(a.seg_mt + at + col * DK + channel(i, 0)) = S[i];
+        }
+        return;
+    }
+    float* dst = nullptr;
+    if (MODE == kGdrSeg || MODE == kGdrBackSeg) dst = (kBack ? a.seg_r : a.seg_s) + ((int64_t)sgm * H + h) * DKV;
+    else if (kBack ? first : last) dst = kBack ? a.d_initial : a.final;
     if (dst) {
-        dst += ((int64_t)n * H + h) * DKV + col0 + wcol + lr;
+        if (MODE != kGdrSeg && MODE != kGdrBackSeg) dst += ((int64_t)n * H + h) * DKV;
+        dst += col0 + wcol + lr;
 #pragma unroll
         for (int i = 0; i < KT; ++i)
 #pragma unroll
             for (int r = 0; r < 4; ++r) dst[(int64_t)channel(i, r) * DV] = S[i][r];
+    }
+}
+
+// The states that enter the segments of a (sequence, head), 64 columns, in place of
+// the segments' own ones: S_{j+1} = M_j S_j + own_j from the sequence's initial state
+// (backwards R_{j-1} = M_j^T R_j + own_j).  A wave has 16 columns; matrices and
+// states enter the products with 24 bits.
+template <int DK>
+__global__ __launch_bounds__(256, 1) void gdr_join_kernel(GdrArgs a, int backwards) {
+    constexpr int SN = DK / 32, KT = DK / 16;
+    const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6), lr = lane & 15, lg = lane >> 4;
+    const int H = a.at.H, DV = a.head_v, n = uni(blockIdx.x / H), h = blockIdx.x - n * H;
+    const int64_t DKV = (int64_t)DK * DV;
+    const int col = blockIdx.y * 64 + 16 * wave + lr;
+    const int b0 = uni(first_block(a.seg, n));
+    int nb = uni(blocks_of(a.seg, seq_at(a.seg, n + 1) - seq_at(a.seg, n)));
+    nb = nb < a.seg.nblocks - b0 ? nb : a.seg.nblocks - b0;   // offsets out of order: stay inside the arrays
+    const float* const m = backwards ? a.seg_mt : a.seg_m;
+    float* const own = backwards ? a.seg_r : a.seg_s;
+    auto channel = [&](int i, int r) { return 32 * (i >> 1) + 8 * lg + 4 * (i & 1) + r; };
+    f32x4_t S[KT];
+    const float* s0 = backwards ? a.d_final : a.initial;
+#pragma unroll
+    for (int i = 0; i < KT; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) S[i][r] = s0 ? s0[((int64_t)n * H + h) * DKV + (int64_t)channel(i, r) * DV + col] : 0.f;
+    for (int step = 0; step < nb; ++step) {
+        const int64_t slot = (int64_t)(b0 + (backwards ? nb - 1 - step : step)) * H + h;
+        const bool more = step + 1 < nb;
+        float* const p = own + slot * DKV + col;
+        f32x4_t next[KT];
+#pragma unroll
+        for (int i = 0; i < KT; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int64_t at = (int64_t)channel(i, r) * DV;
+                next[i][r] = more ? p[at] : 0.f;
+                p[at] = S[i][r];
+            }
+        if (!more) break;
+        float sick = 0.f;
+#pragma unroll
+        for (int i = 0; i < KT; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sick += S[i][r] * 0.f;
+        if (__any(!(sick == 0.f))) {
+            // a state that is not finite ends where a decay of 0 made the segment's matrix zero
+            unsigned bits = 0;
+            for (int e = 4 * lane; e < DK * DK; e += 256) {
+                const u32x4_t v = *reinterpret_cast<const u32x4_t*>(m + slot * DK * DK + e);
+                bits |= (v[0] | v[1] | v[2] | v[3]) << 1;
+            }
+            if (!__any(bits != 0)) {
+#pragma unroll
+                for (int i = 0; i < KT; ++i) S[i] = next[i];
+                continue;
+            }
+        }
+        Frag8<__bf16> fs[SN][3];
+#pragma unroll
+        for (int s = 0; s < SN; ++s) {
+            float x[8];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                x[r] = S[2 * s][r];
+                x[4 + r] = S[2 * s + 1][r];
+            }
+            split(x, fs[s]);
+        }
+        // a tile's rows are its channels
+#pragma unroll
+        for (int i = 0; i < KT; ++i) {
+            const int row = 32 * (i >> 1) + 8 * (lr >> 2) + 4 * (i & 1) + (lr & 3);
+#pragma unroll
+            for (int s = 0; s < SN; ++s) {
+                float x[8];
+                load8(m + slot * DK * DK + row * DK + 32 * s + 8 * lg, x);
+                Frag8<__bf16> f[3];
+                split(x, f);
+                next[i] = mma_parts(f, fs[s], next[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < KT; ++i) S[i] = next[i];
     }
 }
 
@@ -1156,8 +1279,15 @@ hipError_t walk_t(const GdrArgs& a) {
     const void* kern = reinterpret_cast<const void*>(&gdr_walk_kernel<T, DK, MODE>);
     const hipError_t e = ensure_lds_limit(kern, lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((gdr_walk_kernel<T, DK, MODE>), dim3((unsigned)((int64_t)a.at.num_seqs * a.at.H * (a.head_v / 64))),
+    hipLaunchKernelGGL((gdr_walk_kernel<T, DK, MODE>), dim3((unsigned)((int64_t)a.seg.nblocks * a.at.H * (a.head_v / 64 + (MODE == kGdrSeg ? DK / 64 : 0)))),
                        dim3(256), lds, (hipStream_t)a.at.stream, a);
+    return hipGetLastError();
+}
+
+template <int DK>
+hipError_t join(const GdrArgs& a, int backwards) {
+    hipLaunchKernelGGL((gdr_join_kernel<DK>), dim3((unsigned)(a.at.num_seqs * a.at.H), (unsigned)(a.head_v / 64)), dim3(256),
+                       0, (hipStream_t)a.at.stream, a, backwards);
     return hipGetLastError();
 }
 
@@ -1176,14 +1306,25 @@ hipError_t grad_t(const GdrArgs& a) {
 
 template <typename T, int DK>
 hipError_t fwd_t(const GdrArgs& a) {
-    const hipError_t e = prep_t<T, DK, false>(a);
-    return e != hipSuccess ? e : walk_t<T, DK, kGdrOut>(a);
+    hipError_t e = prep_t<T, DK, false>(a);
+    if (e != hipSuccess) return e;
+    if (a.seg_s) {
+        if ((e = walk_t<T, DK, kGdrSeg>(a)) != hipSuccess) return e;
+        if ((e = join<DK>(a, 0)) != hipSuccess) return e;
+    }
+    return walk_t<T, DK, kGdrOut>(a);
 }
 
 template <typename T, int DK>
 hipError_t bwd_t(const GdrArgs& a) {
     hipError_t e = prep_t<T, DK, true>(a);
     if (e != hipSuccess) return e;
+    if (a.seg_s) {
+        if ((e = walk_t<T, DK, kGdrSeg>(a)) != hipSuccess) return e;
+        if ((e = walk_t<T, DK, kGdrBackSeg>(a)) != hipSuccess) return e;
+        if ((e = join<DK>(a, 0)) != hipSuccess) return e;
+        if ((e = join<DK>(a, 1)) != hipSuccess) return e;
+    }
     if (a.at.T_total > 0 && (e = walk_t<T, DK, kGdrStates>(a)) != hipSuccess) return e;
     if ((a.at.T_total > 0 || a.d_initial) && (e = walk_t<T, DK, kGdrBack>(a)) != hipSuccess) return e;
     if ((e = a.head_v == 64 ? grad_t<T, DK, 64>(a) : grad_t<T, DK, 128>(a)) != hipSuccess) return e;

@@ -267,6 +267,10 @@ struct GdrArgs {
     // gradient, by chunk and head: states before it, errors of prediction; the
     // state's gradient behind it, dv / beta; the tokens' terms of dg
     float *states, *errors, *rstates, *u, *terms;
+    // long sequences of few heads: segments, their transitions (and transposes), and
+    // their own states, then those that enter them (NULL: not cut)
+    LinArgs seg;
+    float *seg_m, *seg_mt, *seg_s, *seg_r;
     const float* d_final;
     float* d_initial;
     void *dq, *dk, *dv_out;

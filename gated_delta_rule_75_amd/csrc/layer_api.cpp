@@ -458,10 +458,31 @@ bool gdr_sizes_ok(kda_dtype dt, int H, int Hk, int dk, int dv, int num_seqs, int
            head_ok(dk) && head_ok(dv) && (T / 64 + num_seqs) * (int64_t)H < kMaxChunks;
 }
 
-struct GdrLayout { size_t x, p, z, tab, states, rstates, errors, u, terms, s_end, plan, total; int64_t chunks; };
+// Tokens of a segment.  A walk takes about 4 us a chunk and a CU has one workgroup of
+// it, so long sequences of few heads are cut: the segments' own effects side by side
+// (value columns and the columns of their transitions, about what 256 CUs hold at
+// once), a product of matrices a segment to join them (about 4 us), then the walk over
+// all segments at once.  Fewer than three segments gain nothing, nor do
+// a few chunks (1277 ragged tokens of 8 heads, gradient: 148 us uncut, 164 in segments of
+// 256).  The rule is of tokens and head sizes alone.
+int64_t gdr_segment(int H, int dk, int dv, int num_seqs, int64_t T) {
+    const int64_t all = T < 64 ? 64 : (T + 63) / 64 * 64, chunks = all / 64;
+    int64_t m = (chunks * H * ((dk + dv) / 64) + 255) / 256;
+    const int64_t least = (int64_t)std::ceil(std::sqrt(chunks / 2.0));
+    if (m < least) m = least;
+    if (m < 4) m = 4;
+    return 3 * m > chunks || chunks < 32 || num_seqs > kPlanSeqs ? all : 64 * m;
+}
+
+struct GdrLayout {
+    size_t x, p, z, tab, states, rstates, errors, u, terms, s_end, plan, seg_m, seg_mt, seg_s, seg_r, total;
+    int64_t chunks, L, segments;
+};
 GdrLayout gdr_layout(bool grad, int H, int dk, int dv, int num_seqs, int64_t T) {
     GdrLayout l{};
     l.chunks = T > 64 ? T / 64 + num_seqs : num_seqs;
+    l.L = gdr_segment(H, dk, dv, num_seqs, T);
+    l.segments = l.L < T ? T / l.L + num_seqs : num_seqs;
     Parts p;
     if (T > 0) {
         const size_t n = (size_t)l.chunks * H;
@@ -478,6 +499,13 @@ GdrLayout gdr_layout(bool grad, int H, int dk, int dv, int num_seqs, int64_t T) 
             l.s_end = p.take((size_t)num_seqs * H * dk * dv * 4);
         }
         l.plan = p.take(T > 64 ? plan_bytes(num_seqs) : 0);
+        if (l.L < T) {
+            const size_t m = (size_t)l.segments * H;
+            l.seg_m = p.take(m * dk * dk * 4);
+            l.seg_mt = p.take(grad ? m * dk * dk * 4 : 0);
+            l.seg_s = p.take(m * dk * dv * 4);
+            l.seg_r = p.take(grad ? m * dk * dv * 4 : 0);
+        }
     }
     l.total = p.at ? p.at : 256;
     return l;
@@ -507,6 +535,18 @@ kda_status gdr_args(bool grad, kda_dtype dt, int H, int Hk, int dk, int dv, floa
     a.at.nblocks = (int)l.chunks;
     a.at.stream = stream;
     if (num_seqs > kPlanSeqs && T_total > 64) a.at.first = part<int32_t>(workspace, l.plan);
+    a.seg = a.at;
+    a.seg.L = l.L;
+    a.seg.nblocks = (int)l.segments;
+    a.seg.first = nullptr;
+    if (l.L < T_total) {
+        a.seg_m = part<float>(workspace, l.seg_m);
+        a.seg_s = part<float>(workspace, l.seg_s);
+        if (grad) {
+            a.seg_mt = part<float>(workspace, l.seg_mt);
+            a.seg_r = part<float>(workspace, l.seg_r);
+        }
+    }
     a.q = rows(q, q_stride, H / Hk);
     a.k = rows(k, k_stride, H / Hk);
     a.v = rows(v, v_stride, 1);

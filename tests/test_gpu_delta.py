@@ -150,6 +150,50 @@ def test_nearly_equal_keys(kda, dtype):
         ref.check(f"equal keys {dtype} {n}", a, b, tol(n, dtype))
 
 
+LONG = [([2100], (1, 1, 128, 128)), ([700, 0, 65, 1300], (2, 1, 64, 128)), ([1150, 900], (1, 1, 128, 64)),
+        ([2049], (3, 3, 64, 64))]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,shape", LONG, ids=str)
+def test_long_sequences_of_few_heads(kda, lens, shape, dtype):
+    """Cut into segments that run side by side; decays of every kind pass from one to the next."""
+    for i, decay in enumerate(("token", "reset", "none")):
+        x = make(dtype, lens, *shape, seed=90 + i, decay=decay, state=i < 2)
+        if decay == "token":
+            x["g"] = x["g"] * 0.02       # memories of several segments
+        if decay == "none":
+            x["beta"] = 0.05 * x["beta"]
+        y, s = fwd(kda, x)
+        yr, sr, _ = want_fwd(x)
+        name = f"long {dtype} {lens} {shape} {decay}"
+        ref.check(name + " y", y, yr, ref.TOL[dtype])
+        ref.check(name + " state", s, sr, delta.TOL_STATE)
+        for n, a, b in zip(NAMES, bwd(kda, x), want_bwd(x)):
+            if b is not None:
+                ref.check(f"{name} {n}", a, b, tol(n, dtype))
+
+
+@pytest.mark.parametrize("lens,H", [([130], 2), ([2100], 1)], ids=str)
+def test_a_decay_of_zero_ends_a_state_that_is_not_finite(kda, lens, H):
+    """Infinities and NaN in the initial state are in what comes before a decay of zero, and in nothing behind it;
+    a column of the state that is finite is not touched by the others."""
+    x = make("bf16", lens, H, H, 64, 64, seed=6)
+    at = lens[0] // 2 + 3
+    x["g"][at] = -float("inf")
+    good, sg = fwd(kda, x)
+    x["s0"][:, :, 5, 7], x["s0"][:, :, 9, 40] = float("nan"), float("inf")
+    y, s = fwd(kda, x)
+    assert torch.equal(y[at:], good[at:]) and torch.equal(s, sg)
+    rest = [c for c in range(64) if c not in (7, 40)]
+    assert torch.equal(y[:at][..., rest], good[:at][..., rest])
+    assert not bool(torch.isfinite(y[0, :, [7, 40]]).any())
+    c = cuda({n: (v[:1] if n in ("q", "k", "v", "beta") else v) for n, v in x.items()})
+    state = c["s0"].clone()
+    y1 = kda.gdr_decode_step(c["q"], c["k"], c["v"], torch.full((1, H), -float("inf")).cuda(), c["beta"], state)
+    assert bool(torch.isfinite(y1).all()) and bool(torch.isfinite(state).all())
+
+
 def test_prompt_then_tokens(kda):
     """A prompt's state carried on by single tokens, as one sequence."""
     x = make("bf16", [90], 4, 2, 128, 128, seed=8, state=False)
