@@ -257,9 +257,21 @@ __device__ __forceinline__ void invert(float* sx, int wave, int lane) {
 }
 
 // Tables, scores and inverse of a (chunk, head).  GRAD: X, Z and P^T.
+// LDS: the rows of k (GRAD: and q), then the matrices in their place.
+template <typename T, int DK, bool GRAD> constexpr int prep_bytes() {
+    constexpr int rows = C * DK * (int)sizeof(T) * (GRAD ? 2 : 1), m = C * kLd * 4 * (GRAD ? 2 : 1);
+    return rows > m ? rows : m;
+}
+
 template <typename T, int DK, bool GRAD>
 __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrArgs a) {
-    __shared__ __attribute__((aligned(16))) float sx[C * kLd], sz[GRAD ? C * kLd : 4];
+    typedef Tile<T, DK> TK;
+    constexpr int SN = DK / 32, EP = 16 / (int)sizeof(T), NR = C * DK / EP / 256;
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    T* const sk = reinterpret_cast<T*>(smem);
+    T* const sq = sk + C * DK;
+    float* const sx = reinterpret_cast<float*>(smem);
+    float* const sz = sx + C * kLd;
     __shared__ Sums sums;
     __shared__ __attribute__((aligned(16))) float s_beta[C];
     const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6), lr = lane & 15, lg = lane >> 4;
@@ -281,12 +293,31 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrArgs a) {
     }
     const Block bl = find_block(a.at, b);
     if (bl.n < 0 || bl.cnt == 0) return;
-    const int64_t slot = (int64_t)b * H + h;
+    const int cnt = uni(bl.cnt);
+    const int64_t start = uni64(bl.start), slot = (int64_t)b * H + h;
+    // all of the chunk's reads at once; rows without a token: the last one's
+    const T* const k = (const T*)a.k.p + start * a.k.stride + (int64_t)(h / a.k.share) * DK;
+    const T* const q = (const T*)a.q.p + start * a.q.stride + (int64_t)(h / a.q.share) * DK;
+    const int own = GRAD ? wave : 3 - wave;   // rows i (GRAD: j) of the scores that the wave makes: as many tiles as of M in all
+    u32x4_t rk[NR], rq[GRAD ? NR : 1];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        const int u = i * 256 + tid, row = u / (DK / EP), col = u % (DK / EP) * EP;
+        const int64_t tok = row < cnt ? row : cnt - 1;
+        rk[i] = *reinterpret_cast<const u32x4_t*>(k + tok * a.k.stride + col);
+        if constexpr (GRAD) rq[i] = *reinterpret_cast<const u32x4_t*>(q + tok * a.q.stride + col);
+    }
+    Frag8<T> mine[SN];
+    if constexpr (!GRAD) {
+        const int row = 16 * own + lr < cnt ? 16 * own + lr : cnt - 1;
+#pragma unroll
+        for (int s = 0; s < SN; ++s) mine[s] = frag_at(q + row * a.q.stride + 32 * s + 8 * lg);
+    }
     if (wave == 0) {
-        const bool valid = lane < bl.cnt;
-        const int64_t at = (bl.start + lane) * H + h;
-        const double G = decay_scan(valid && a.g ? a.g[at] : 0.f), end = lane_d(G, 63);
+        const bool valid = lane < cnt;
+        const int64_t at = (start + lane) * H + h;
         const float beta = valid ? a.beta[at] : 0.f;
+        const double G = decay_scan(valid && a.g ? a.g[at] : 0.f), end = lane_d(G, 63);
         sums.set(lane, G, valid);
         s_beta[lane] = beta;
         float* const tab = a.tab + slot * kGdrTab;
@@ -297,57 +328,59 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrArgs a) {
         tab[4 * C + lane] = sums.frac[lane];
         tab[5 * C + lane] = __int_as_float(sums.whole[lane]);
     }
-    const T* const k = (const T*)a.k.p + bl.start * a.k.stride + (int64_t)(h / a.k.share) * DK;
-    const T* const q = (const T*)a.q.p + bl.start * a.q.stride + (int64_t)(h / a.q.share) * DK;
-    auto row = [&](int t) { return 16 * t + lr < bl.cnt ? 16 * t + lr : bl.cnt - 1; };   // rows without a token: the last one's
-    constexpr int SN = DK / 32;
-    auto read = [&](Frag8<T> (&f)[SN], const T* p, int64_t stride, int t) {
 #pragma unroll
-        for (int s = 0; s < SN; ++s) f[s] = frag_at(p + row(t) * stride + 32 * s + 8 * lg);
-    };
+    for (int i = 0; i < NR; ++i) {
+        const int u = i * 256 + tid, at = TK::off(u / (DK / EP), u % (DK / EP) * EP);
+        *reinterpret_cast<u32x4_t*>(sk + at) = rk[i];
+        if constexpr (GRAD) *reinterpret_cast<u32x4_t*>(sq + at) = rq[i];
+    }
     __syncthreads();
     const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
-    Frag8<T> own[SN];
-    // keys of the wave's rows against all before: M beta, rows i in lanes
-    read(own, k, a.k.stride, wave);
+    auto product = [&](const T* rows, int t, const Frag8<T> (&f)[SN]) {
+        f32x4_t d = zero;
 #pragma unroll
-    for (int tj = 0; tj < 4; ++tj) {
-        if (tj > wave) continue;
-        Frag8<T> other[SN];
-        read(other, k, a.k.stride, tj);
-        f32x4_t m = zero;
-#pragma unroll
-        for (int s = 0; s < SN; ++s) m = mma(other[s], own[s], m);
-        const int i = 16 * wave + lr, j = 16 * tj + 4 * lg;
-        m *= sums.before(i, j, true);
-        *reinterpret_cast<f32x4_t*>(sx + i * kLd + j) = m * *reinterpret_cast<const f32x4_t*>(s_beta + j);
-        if constexpr (GRAD) *reinterpret_cast<f32x4_t*>(sz + i * kLd + j) = m * s_beta[i];
-    }
-    // scores, as operands: rows i of the wave, or (transposed) its rows j
+        for (int s = 0; s < SN; ++s) d = mma(TK::rows8(rows, 16 * t, s, lane), f[s], d);
+        return d;
+    };
+    // scores, as operands: the wave's rows i, or (transposed) its rows j
     char* const p = a.p + slot * kTriBytes;
-    if constexpr (!GRAD) read(own, q, a.q.stride, wave);
+    if constexpr (GRAD) {
+#pragma unroll
+        for (int s = 0; s < SN; ++s) mine[s] = TK::rows8(sk, 16 * own, s, lane);
+    }
 #pragma unroll
     for (int s2 = 0; s2 < 2; ++s2) {
+        if (GRAD ? 2 * s2 + 1 < own : 2 * s2 > own) continue;
         float x[8];
-        bool some = false;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int t = 2 * s2 + half;
-            const bool in = GRAD ? t >= wave : t <= wave;
-            some |= in;
             f32x4_t d = zero;
-            if (in) {
-                Frag8<T> other[SN];
-                read(other, GRAD ? q : k, GRAD ? a.q.stride : a.k.stride, t);
-#pragma unroll
-                for (int s = 0; s < SN; ++s) d = mma(other[s], own[s], d);
+            if (GRAD ? t >= own : t <= own) {
+                const int c = 16 * t + 4 * lg, w = 16 * own + lr;
+                d = product(GRAD ? sq : sk, t, mine) * (GRAD ? sums.behind(c, w, false) : sums.before(w, c, false)) * a.scale;
             }
-            const int c = 16 * t + 4 * lg, w = 16 * wave + lr;
-            d *= GRAD ? sums.behind(c, w, false) : sums.before(w, c, false);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) x[4 * half + r] = d[r] * a.scale;
+            for (int r = 0; r < 4; ++r) x[4 * half + r] = d[r];
         }
-        if (some) put_operand<T, GRAD ? kThree<T> : kTwo<T>>(p, GRAD ? tri_piece_t(wave, s2) : tri_piece(wave, s2), lane, x);
+        put_operand<T, GRAD ? kThree<T> : kTwo<T>>(p, GRAD ? tri_piece_t(own, s2) : tri_piece(own, s2), lane, x);
+    }
+    // keys of the wave's rows against all before: M
+    if constexpr (!GRAD) {
+#pragma unroll
+        for (int s = 0; s < SN; ++s) mine[s] = TK::rows8(sk, 16 * wave, s, lane);
+    }
+    f32x4_t m[4];
+#pragma unroll
+    for (int tj = 0; tj < 4; ++tj)
+        if (tj <= wave) m[tj] = product(sk, tj, mine) * sums.before(16 * wave + lr, 16 * tj + 4 * lg, true);
+    __syncthreads();
+#pragma unroll
+    for (int tj = 0; tj < 4; ++tj) {
+        if (tj > wave) continue;
+        const int i = 16 * wave + lr, j = 16 * tj + 4 * lg;
+        *reinterpret_cast<f32x4_t*>(sx + i * kLd + j) = m[tj] * *reinterpret_cast<const f32x4_t*>(s_beta + j);
+        if constexpr (GRAD) *reinterpret_cast<f32x4_t*>(sz + i * kLd + j) = m[tj] * s_beta[i];
     }
     __syncthreads();
     invert(sx, wave, lane);
@@ -1267,7 +1300,11 @@ __global__ __launch_bounds__(256) void gdr_decay_kernel(GdrArgs a, int size) {
 template <typename T, int DK, bool GRAD>
 hipError_t prep_t(const GdrArgs& a) {
     if (a.at.T_total == 0) return hipSuccess;
-    hipLaunchKernelGGL((gdr_prep_kernel<T, DK, GRAD>), dim3((unsigned)((int64_t)a.at.nblocks * a.at.H)), dim3(256), 0,
+    constexpr int lds = prep_bytes<T, DK, GRAD>();
+    const void* kern = reinterpret_cast<const void*>(&gdr_prep_kernel<T, DK, GRAD>);
+    const hipError_t e = ensure_lds_limit(kern, lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((gdr_prep_kernel<T, DK, GRAD>), dim3((unsigned)((int64_t)a.at.nblocks * a.at.H)), dim3(256), lds,
                        (hipStream_t)a.at.stream, a);
     return hipGetLastError();
 }
