@@ -912,330 +912,420 @@ __global__ __launch_bounds__(256, 1) void gdr_join_kernel(GdrArgs a, int backwar
     }
 }
 
-// dQ, dK, dV in the inputs' type, dbeta and the tokens' terms of dg of a (chunk,
-// key head), eight waves: the value heads that share the key head one after
-// another, their sums in registers.
+// dQ, dK, dV in the inputs' type (dQ and dK of shared key heads: each value head's
+// part in fp32), dbeta and the tokens' terms of dg of a (chunk, head).
 //
-// A head's rows of E, dV = beta U and dY are read once, and kept in LDS as operands
-// in parts; a wave has 16 channels of dQ and dK (and half of the tokens where dk is
-// 64), whose rows of the two states are operands as they lie in memory.  Four waves
-// make the rows i of W and Y, four the rows j; these then take the place of E and dV.
-template <typename T, int DK, int DV>
+// 64 value columns at a time the rows of E, dV = beta U and dY are laid out in LDS as
+// operands in parts; each wave adds to its tiles of W and Y (rows i = its own against
+// all before, and all behind against its own as j) and, for its DK / 4 channels, to
+// the states' parts, whose rows are operands as they lie in memory.  W and Y then
+// take the rows' place, and q that of k.  In bf16 two workgroups share a CU: one
+// loads while the other multiplies.
+template <typename T, int DK>
 struct GradLds {
-    static constexpr int SZ = (int)sizeof(T), N2 = kTwo<T>, N3 = kThree<T>, TRI = kTri<T, N2>;
+    static constexpr int SZ = (int)sizeof(T), N2 = kTwo<T>, N3 = kThree<T>, TRI = kTri<T, N2>, ROWS = C * 64 * SZ;
     static constexpr int k = 0, rest = C * DK * SZ;
-    static constexpr int e = rest, x = e + N3 * C * DV * SZ, y = x + N2 * C * DV * SZ, first = y + C * DV * SZ;
-    static constexpr int w = rest, q = w + 4 * TRI, second = q + C * DK * SZ;      // over the rows, once they are read
-    static constexpr int dq = rest, dk = dq + C * DK * SZ, third = dk + C * DK * SZ;   // over all of that, at the end
+    static constexpr int e = rest, x = e + N3 * ROWS, y = x + N2 * ROWS, first = y + ROWS;
+    static constexpr int w = rest, second = w + 4 * TRI;                              // over the rows, once they are read
+    static constexpr int dq = rest, dk = dq + C * DK * SZ, third = dk + C * DK * SZ;   // over those, at the end
     static constexpr int most = first > second ? first : second, bytes = most > third ? most : third;
 };
 
 template <typename T, int DK, int DV>
-__global__ __launch_bounds__(512, 2) void gdr_grad_kernel(GdrArgs a) {
-    typedef GradLds<T, DK, DV> Lds;
-    typedef Tile<T, DV> TV;
+__global__ __launch_bounds__(256, sizeof(T) == 2 || DK == 64 ? 2 : 1) void gdr_grad_kernel(GdrArgs a) {
+    typedef GradLds<T, DK> Lds;
+    typedef Tile<T, 64> TV;
     typedef Tile<T, DK> TK;
-    constexpr int SV = DV / 32, SK = DK / 32, N2 = kTwo<T>, N3 = kThree<T>, EP = 16 / (int)sizeof(T), TRI = kTri<T, N2>;
-    constexpr int NCT = DK / 16, TN = NCT / 2;          // channel tiles; token tiles of a wave (4 or 2)
-    constexpr int TPR = DV / 8, NS = C * TPR / 512;     // staging: threads a row, runs of 8 a thread
-    constexpr int NQ = C * DK / EP / 512;               // runs of 16 bytes of a thread, of k and of q
+    constexpr int SK = DK / 32, NT = DK / 64, N2 = kTwo<T>, N3 = kThree<T>, EP = 16 / (int)sizeof(T), TRI = kTri<T, N2>;
+    constexpr int NQ = C * DK / EP / 256;               // runs of 16 bytes of a thread, of k and of q
     extern __shared__ __attribute__((aligned(16))) char smem[];
     T* const sk = reinterpret_cast<T*>(smem + Lds::k);
     T* const se = reinterpret_cast<T*>(smem + Lds::e);
     T* const sx = reinterpret_cast<T*>(smem + Lds::x);
     T* const sy = reinterpret_cast<T*>(smem + Lds::y);
-    T* const sq = reinterpret_cast<T*>(smem + Lds::q);
     char* const wy = smem + Lds::w;                     // W beta and Y beta, rows i, then rows j
     __shared__ Sums sums;
     __shared__ __attribute__((aligned(16))) float tab[3 * C];
-    __shared__ float part_s[8][C], part_p[C], part_v[C];
+    __shared__ float part_s[4][C], part_p[C], part_v[C];
     int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lg = lane >> 4;
     const int wave = uni(tid >> 6);
-    const int H = a.at.H, r_heads = a.k.share, Hk = H / r_heads;
-    const int b = uni(blockIdx.x / Hk), hk = blockIdx.x - b * Hk;
-    const Block bl = find_block(a.at, b);
-    if (bl.n < 0 || bl.cnt == 0) return;
-    const int cnt = bl.cnt;
-    u32x4_t rq[NQ];
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-        const int u = i * 512 + tid, row = u / (DK / EP), col = u % (DK / EP) * EP;
-        const int64_t tok = bl.start + (row < cnt ? row : cnt - 1);
-        rq[i] = *reinterpret_cast<const u32x4_t*>((const T*)a.q.p + tok * a.q.stride + (int64_t)hk * DK + col);
-        *reinterpret_cast<u32x4_t*>(sk + TK::off(row, col)) =
-            *reinterpret_cast<const u32x4_t*>((const T*)a.k.p + tok * a.k.stride + (int64_t)hk * DK + col);
-    }
-    const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
-    const int ch0 = 16 * (wave % NCT), t0 = wave / NCT * TN;
-    f32x4_t dq[TN], dk[TN];
-#pragma unroll
-    for (int t = 0; t < TN; ++t) dq[t] = dk[t] = zero;
-    for (int m = 0; m < r_heads; ++m) {
-        const int h = hk * r_heads + m;
-        // LDS addresses are formed anew for each head: kept across the loop they spill
+    // LDS addresses are formed anew in each part: kept from part to part they spill
+    auto anew = [&] {
+        __builtin_amdgcn_sched_barrier(0);
         asm volatile("" : "+v"(tid));
         lane = tid & 63;
         lr = lane & 15;
         lg = lane >> 4;
-        const int64_t slot = (int64_t)b * H + h;
-        // the wave's rows of the states: on their way while the rows are laid out
-        float s_in[SV][8], r_in[SV][8];
+    };
+    const int H = a.at.H, r_heads = a.k.share, b = uni(blockIdx.x / H), h = blockIdx.x - b * H, hk = uni(h / r_heads);
+    const Block bl = find_block(a.at, b);
+    if (bl.n < 0 || bl.cnt == 0) return;
+    const int cnt = uni(bl.cnt);
+    const int64_t start = uni64(bl.start), slot = (int64_t)b * H + h;
+    const T* const gk = (const T*)a.k.p + start * a.k.stride + (int64_t)hk * DK;
+    const T* const gq = (const T*)a.q.p + start * a.q.stride + (int64_t)hk * DK;
+    auto row_of = [&](int row) { return row < cnt ? row : cnt - 1; };   // rows without a token: the last one's
 #pragma unroll
-        for (int s = 0; s < SV; ++s) {
-            const int64_t at = slot * DK * DV + (int64_t)(ch0 + lr) * DV + 32 * s + 8 * lg;
-            load8(a.states + at, s_in[s]);
-            load8(a.rstates + at, r_in[s]);
-        }
-        const float* const gtab = a.tab + slot * kGdrTab;
-        if (m > 0) __syncthreads();
-        if (tid < 3 * C) tab[tid] = gtab[tid];
-        if (tid < C) {
-            sums.frac[tid] = gtab[4 * C + tid];
-            sums.whole[tid] = __float_as_int(gtab[5 * C + tid]);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        // rows of E, dV and dY to LDS; dv; e.u and v.dv by tokens
+    for (int i = 0; i < NQ; ++i) {
+        const int u = i * 256 + tid, row = u / (DK / EP), col = u % (DK / EP) * EP;
+        *reinterpret_cast<u32x4_t*>(sk + TK::off(row, col)) =
+            *reinterpret_cast<const u32x4_t*>(gk + (int64_t)row_of(row) * a.k.stride + col);
+    }
+    const float* const gtab = a.tab + slot * kGdrTab;
+    if (tid < 3 * C) tab[tid] = gtab[tid];
+    if (tid < C) {
+        sums.frac[tid] = gtab[4 * C + tid];
+        sums.whole[tid] = __float_as_int(gtab[5 * C + tid]);
+    }
+    const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+    // tiles of W and Y: wave + 1 with its rows as i, 4 - wave with them as j
+    f32x4_t w[5], y[5];
 #pragma unroll
-        for (int i = 0; i < NS; ++i) {
-            const int u = i * 512 + tid, row = u / TPR, col = u % TPR * 8;
-            const bool in = row < cnt;
-            const int64_t tok = bl.start + (in ? row : cnt - 1), at = slot * C * DV + row * DV + col;
+    for (int m = 0; m < 5; ++m) w[m] = y[m] = zero;
+    f32x4_t ps[4][NT], pa[4][NT], pb[4][NT];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) ps[t][n] = pa[t][n] = pb[t][n] = zero;
+    const int ch0 = wave * (DK / 4);
+    float eu[2] = {0.f, 0.f}, vx[2] = {0.f, 0.f};
+    auto rows_of = [&](const T* base, int t, int s, auto& f) {   // 8 consecutive columns a lane, in parts
+        constexpr int N = sizeof(f) / sizeof(f[0]);
+#pragma unroll
+        for (int p = 0; p < N; ++p) f[p] = TV::rows8(base + p * C * 64, 16 * t, s, lane);
+    };
+#pragma unroll 1
+    for (int v0 = 0; v0 < DV; v0 += 64) {
+        if (v0 > 0) __syncthreads();
+        anew();
+        // rows to LDS, and dv; e.u and v.dv by tokens
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int u = i * 256 + tid, row = u / 8, lc = u % 8 * 8, col = v0 + lc;
+            const int64_t tok = start + row_of(row), at = slot * C * DV + row * DV + col;
             float e[8], x[8], v[8];
             load8(a.errors + at, e);
             load8(a.u + at, x);
             const T* const pv = (const T*)a.v.p + tok * a.v.stride + (int64_t)h * DV + col;
             const T* const py = (const T*)a.dy + (tok * H + h) * DV + col;
             const float be = gtab[2 * C + row];
-            float eu = 0.f, vx = 0.f;
 #pragma unroll
             for (int c = 0; c < 8; c += EP) {
-                float w[EP];
-                load_vec<T, EP>(pv + c, w);
-                *reinterpret_cast<u32x4_t*>(sy + TV::off(row, col + c)) = *reinterpret_cast<const u32x4_t*>(py + c);
+                float o[EP];
+                load_vec<T, EP>(pv + c, o);
+                *reinterpret_cast<u32x4_t*>(sy + TV::off(row, lc + c)) = *reinterpret_cast<const u32x4_t*>(py + c);
 #pragma unroll
-                for (int j = 0; j < EP; ++j) v[c + j] = w[j];
+                for (int j = 0; j < EP; ++j) v[c + j] = o[j];
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                eu += e[j] * x[j];
+                eu[i] += e[j] * x[j];
                 x[j] *= be;
-                vx += v[j] * x[j];
+                vx[i] += v[j] * x[j];
             }
-            Frag8<T> f3[N3], f2[N2];
-            split(e, f3);
-            split(x, f2);
             if constexpr (sizeof(T) == 2) {
+                Frag8<T> f3[N3], f2[N2];
+                split(e, f3);
+                split(x, f2);
 #pragma unroll
-                for (int p = 0; p < N3; ++p) *reinterpret_cast<bf16x8_t*>(se + p * C * DV + TV::off(row, col)) = f3[p].v;
+                for (int p = 0; p < N3; ++p) *reinterpret_cast<bf16x8_t*>(se + p * C * 64 + TV::off(row, lc)) = f3[p].v;
 #pragma unroll
-                for (int p = 0; p < N2; ++p) *reinterpret_cast<bf16x8_t*>(sx + p * C * DV + TV::off(row, col)) = f2[p].v;
+                for (int p = 0; p < N2; ++p) *reinterpret_cast<bf16x8_t*>(sx + p * C * 64 + TV::off(row, lc)) = f2[p].v;
             } else {
 #pragma unroll
                 for (int c = 0; c < 8; c += 4) {
-                    *reinterpret_cast<f32x4_t*>(se + TV::off(row, col + c)) = f32x4_t{e[c], e[c + 1], e[c + 2], e[c + 3]};
-                    *reinterpret_cast<f32x4_t*>(sx + TV::off(row, col + c)) = f32x4_t{x[c], x[c + 1], x[c + 2], x[c + 3]};
+                    *reinterpret_cast<f32x4_t*>(se + TV::off(row, lc + c)) = f32x4_t{e[c], e[c + 1], e[c + 2], e[c + 3]};
+                    *reinterpret_cast<f32x4_t*>(sx + TV::off(row, lc + c)) = f32x4_t{x[c], x[c + 1], x[c + 2], x[c + 3]};
                 }
             }
-            if (in) {
+            if (row < cnt) {
                 T* const o = (T*)a.dv_out + (tok * H + h) * DV + col;
 #pragma unroll
                 for (int c = 0; c < 8; c += EP) {
-                    float w[EP];
+                    float f[EP];
 #pragma unroll
-                    for (int j = 0; j < EP; ++j) w[j] = x[c + j];
-                    store_vec<T, EP>(o + c, w);
+                    for (int j = 0; j < EP; ++j) f[j] = x[c + j];
+                    store_vec<T, EP>(o + c, f);
                 }
-            }
-            // over the threads of a row: 16, or 8
-            eu += dpp_mov<0xB1>(eu);
-            vx += dpp_mov<0xB1>(vx);
-            eu += dpp_mov<0x4E>(eu);
-            vx += dpp_mov<0x4E>(vx);
-            eu += dpp_mov<0x141>(eu);
-            vx += dpp_mov<0x141>(vx);
-            if constexpr (TPR == 16) {
-                eu += dpp_mov<0x140>(eu);
-                vx += dpp_mov<0x140>(vx);
-            }
-            if (tid % TPR == 0) {
-                part_v[row] = vx;
-                if (in) a.dbeta[tok * H + h] = eu;
             }
         }
         __syncthreads();
-        // rows in parts, 8 consecutive columns a lane
-        auto rows_of = [&](const T* base, int t, int s, auto& f) {
-            constexpr int N = sizeof(f) / sizeof(f[0]);
+        anew();
+        {
+            // the wave's rows, as i and as j
+            Frag8<T> fy[2][1], fx[2][N2], fe[2][N2];
 #pragma unroll
-            for (int p = 0; p < N; ++p) f[p] = TV::rows8(base + p * C * DV, 16 * t, s, lane);
-        };
-        // W and Y: rows i of the wave against all before, or its rows j against all behind
-        const int own = wave & 3;
-        f32x4_t w[4], y[4];
-        if (wave < 4) {
-            Frag8<T> fy[SV][1], fx[SV][N2], fq[SK];
-#pragma unroll
-            for (int s = 0; s < SV; ++s) {
-                rows_of(sy, own, s, fy[s]);
-                rows_of(sx, own, s, fx[s]);
+            for (int s = 0; s < 2; ++s) {
+                rows_of(sy, wave, s, fy[s]);
+                rows_of(sx, wave, s, fx[s]);
+                rows_of(se, wave, s, fe[s]);
             }
-            const int i = 16 * own + lr;
-            const T* const q = (const T*)a.q.p + (bl.start + (i < cnt ? i : cnt - 1)) * a.q.stride + (int64_t)hk * DK;
 #pragma unroll
-            for (int s = 0; s < SK; ++s) fq[s] = frag_at(q + 32 * s + 8 * lg);
-            float pairs = 0.f;   // sum over j of W beta q_i.k_j, with 24 bits: an fp32 output's
+            for (int m = 0; m < 5; ++m) {
+                if (m <= wave) {
 #pragma unroll
-            for (int tj = 0; tj < 4; ++tj) {
-                w[tj] = y[tj] = zero;
-                if (tj > own) continue;
+                    for (int s = 0; s < 2; ++s) {
+                        Frag8<T> e3[N3], e2[N2];
+                        rows_of(se, m, s, e3);
+                        w[m] = mma_parts(e3, fy[s], w[m]);
+#pragma unroll
+                        for (int p = 0; p < N2; ++p) e2[p] = e3[p];
+                        y[m] = mma_parts(e2, fx[s], y[m]);
+                    }
+                } else {
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        Frag8<T> y1[1], x2[N2];
+                        rows_of(sy, m - 1, s, y1);
+                        rows_of(sx, m - 1, s, x2);
+                        w[m] = mma_parts(y1, fe[s], w[m]);
+                        y[m] = mma_parts(x2, fe[s], y[m]);
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        // the states' parts, the wave's channels
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            anew();
+            Frag8<T> s3[NT][N3], s2[NT][N2], r2[NT][N2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int64_t at = slot * DK * DV + (int64_t)(ch0 + 16 * n + lr) * DV + v0 + 32 * s + 8 * lg;
+                float x[8], z[8];
+                load8(a.states + at, x);
+                load8(a.rstates + at, z);
+                split(x, s3[n]);
+                split(z, r2[n]);
+#pragma unroll
+                for (int p = 0; p < N2; ++p) s2[n][p] = s3[n][p];
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                Frag8<T> fy[1], fx[N2], fe[N2];
+                rows_of(sy, t, s, fy);
+                rows_of(sx, t, s, fx);
+                rows_of(se, t, s, fe);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    ps[t][n] = mma_parts(fy, s3[n], ps[t][n]);
+                    pa[t][n] = mma_parts(fx, s2[n], pa[t][n]);
+                    pb[t][n] = mma_parts(fe, r2[n], pb[t][n]);
+                }
+            }
+        }
+    }
+    anew();
+    // W and Y: decays, beta; the sum over j of W beta q_i.k_j with 24 bits (an fp32 output's)
+    {
+        const int own = 16 * wave + lr;
+        float pairs = 0.f;
+        Frag8<T> fq[SK];
+#pragma unroll
+        for (int s = 0; s < SK; ++s) fq[s] = frag_at(gq + (int64_t)row_of(own) * a.q.stride + 32 * s + 8 * lg);
+#pragma unroll
+        for (int m = 0; m < 5; ++m) {
+            if (m <= wave) {
+                const int j = 16 * m + 4 * lg;
+                const f32x4_t be = *reinterpret_cast<const f32x4_t*>(tab + 2 * C + j);
                 f32x4_t qk = zero;
 #pragma unroll
-                for (int s = 0; s < SV; ++s) {
-                    Frag8<T> e3[N3], e2[N2];
-                    rows_of(se, tj, s, e3);
-                    w[tj] = mma_parts(e3, fy[s], w[tj]);
+                for (int s = 0; s < SK; ++s) qk = mma(TK::rows8(sk, 16 * m, s, lane), fq[s], qk);
+                w[m] *= sums.before(own, j, false) * be * a.scale;
+                y[m] *= sums.before(own, j, true) * -be;
 #pragma unroll
-                    for (int p = 0; p < N2; ++p) e2[p] = e3[p];
-                    y[tj] = mma_parts(e2, fx[s], y[tj]);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-#pragma unroll
-                for (int s = 0; s < SK; ++s) qk = mma(TK::rows8(sk, 16 * tj, s, lane), fq[s], qk);
-                const int j = 16 * tj + 4 * lg;
-                const f32x4_t be = *reinterpret_cast<const f32x4_t*>(tab + 2 * C + j);
-                w[tj] *= sums.before(i, j, false) * be * a.scale;
-                y[tj] *= sums.before(i, j, true) * -be;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) pairs += w[tj][r] * qk[r];
-            }
-            pairs += __shfl_xor(pairs, 16);
-            pairs += __shfl_xor(pairs, 32);
-            if (lg == 0) part_p[i] = pairs;
-        } else {
-            Frag8<T> fe[SV][N2];
-#pragma unroll
-            for (int s = 0; s < SV; ++s) rows_of(se, own, s, fe[s]);
-            const int j = 16 * own + lr;
-#pragma unroll
-            for (int ti = 0; ti < 4; ++ti) {
-                w[ti] = y[ti] = zero;
-                if (ti < own) continue;
-#pragma unroll
-                for (int s = 0; s < SV; ++s) {
-                    Frag8<T> fy[1], fx[N2];
-                    rows_of(sy, ti, s, fy);
-                    rows_of(sx, ti, s, fx);
-                    w[ti] = mma_parts(fy, fe[s], w[ti]);
-                    y[ti] = mma_parts(fx, fe[s], y[ti]);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-                const float be = tab[2 * C + j];
-                w[ti] *= sums.behind(16 * ti + 4 * lg, j, false) * (be * a.scale);
-                y[ti] *= sums.behind(16 * ti + 4 * lg, j, true) * -be;
+                for (int r = 0; r < 4; ++r) pairs += w[m][r] * qk[r];
+            } else {
+                const float be = tab[2 * C + own];
+                w[m] *= sums.behind(16 * (m - 1) + 4 * lg, own, false) * (be * a.scale);
+                y[m] *= sums.behind(16 * (m - 1) + 4 * lg, own, true) * -be;
             }
         }
-        // the states' parts, the wave's channels and tokens
-        f32x4_t ps[TN], pa[TN], pb[TN];
+        pairs += __shfl_xor(pairs, 16);
+        pairs += __shfl_xor(pairs, 32);
+        if (lg == 0) part_p[own] = pairs;
+    }
+    // over the 8 threads of a row
 #pragma unroll
-        for (int t = 0; t < TN; ++t) ps[t] = pa[t] = pb[t] = zero;
-#pragma unroll
-        for (int s = 0; s < SV; ++s) {
-            Frag8<T> s3[N3], s2[N2], r2[N2];
-            split(s_in[s], s3);
-            split(r_in[s], r2);
-#pragma unroll
-            for (int p = 0; p < N2; ++p) s2[p] = s3[p];
-#pragma unroll
-            for (int t = 0; t < TN; ++t) {
-                Frag8<T> fy[1], fx[N2], fe[N2];
-                rows_of(sy, t0 + t, s, fy);
-                rows_of(sx, t0 + t, s, fx);
-                rows_of(se, t0 + t, s, fe);
-                ps[t] = mma_parts(fy, s3, ps[t]);
-                pa[t] = mma_parts(fx, s2, pa[t]);
-                pb[t] = mma_parts(fe, r2, pb[t]);
-            }
-            __builtin_amdgcn_sched_barrier(0);
+    for (int i = 0; i < 2; ++i) {
+        const int row = (i * 256 + tid) / 8;
+        eu[i] += dpp_mov<0xB1>(eu[i]);
+        vx[i] += dpp_mov<0xB1>(vx[i]);
+        eu[i] += dpp_mov<0x4E>(eu[i]);
+        vx[i] += dpp_mov<0x4E>(vx[i]);
+        eu[i] += dpp_mov<0x141>(eu[i]);
+        vx[i] += dpp_mov<0x141>(vx[i]);
+        if (tid % 8 == 0) {
+            part_v[row] = vx[i];
+            if (row < cnt) a.dbeta[(start + row) * H + h] = eu[i];
         }
-        __syncthreads();
-        // W and Y over E and dV, q over dY
+    }
+    anew();
+    u32x4_t rq[NQ];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            if (wave < 4 ? t > (own | 1) : t < (own & ~1)) continue;
-            char* const at = wy + (wave < 4 ? 0 : 2 * TRI);
-            const int piece = wave < 4 ? tri_piece(own, t >> 1) : tri_piece_t(own, t >> 1);
-            put_half<T>(at, piece, t & 1, lane, w[t]);
-            put_half<T>(at + TRI, piece, t & 1, lane, y[t]);
+    for (int i = 0; i < NQ; ++i) {
+        const int u = i * 256 + tid, row = u / (DK / EP), col = u % (DK / EP) * EP;
+        rq[i] = *reinterpret_cast<const u32x4_t*>(gq + (int64_t)row_of(row) * a.q.stride + col);
+    }
+    __syncthreads();
+    // W and Y over the rows, each piece's other half zeros where it lies beyond the diagonal
+#pragma unroll
+    for (int m = 0; m < 5; ++m) {
+        const bool before = m <= wave;
+        char* const at = wy + (before ? 0 : 2 * TRI);
+        const int t = before ? m : m - 1, piece = before ? tri_piece(wave, t >> 1) : tri_piece_t(wave, t >> 1);
+        put_half<T>(at, piece, t & 1, lane, w[m]);
+        put_half<T>(at + TRI, piece, t & 1, lane, y[m]);
+    }
+    {
+        char* const at = wy + (wave & 1 ? 2 * TRI : 0);
+        const int piece = wave & 1 ? tri_piece_t(wave, wave >> 1) : tri_piece(wave, wave >> 1);
+        put_half<T>(at, piece, !(wave & 1), lane, zero);
+        put_half<T>(at + TRI, piece, !(wave & 1), lane, zero);
+    }
+    Frag8<T> fk[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int s2 = 0; s2 < 2; ++s2) fk[n][s2] = TK::cols(sk, ch0 + 16 * n, s2, lane);
+    __syncthreads();
+    // q over k
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+        const int u = i * 256 + tid;
+        *reinterpret_cast<u32x4_t*>(sk + TK::off(u / (DK / EP), u % (DK / EP) * EP)) = rq[i];
+    }
+    anew();
+    f32x4_t dk[4][NT];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const f32x4_t in = *reinterpret_cast<const f32x4_t*>(tab + 16 * t + 4 * lg);
+        const f32x4_t out = *reinterpret_cast<const f32x4_t*>(tab + C + 16 * t + 4 * lg);
+        const f32x4_t beta = *reinterpret_cast<const f32x4_t*>(tab + 2 * C + 16 * t + 4 * lg);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            ps[t][n] *= in * a.scale;
+            dk[t][n] = out * beta * pb[t][n] - in * pa[t][n];
         }
 #pragma unroll
-        for (int i = 0; i < NQ; ++i) {
-            const int u = i * 512 + tid;
-            *reinterpret_cast<u32x4_t*>(sq + TK::off(u / (DK / EP), u % (DK / EP) * EP)) = rq[i];
-        }
-        __syncthreads();
-        {
-            const Frag8<T> fk[2] = {TK::cols(sk, ch0, 0, lane), TK::cols(sk, ch0, 1, lane)};
-            const Frag8<T> fq[2] = {TK::cols(sq, ch0, 0, lane), TK::cols(sq, ch0, 1, lane)};
+        for (int s2 = 0; s2 < 2; ++s2) {
+            Frag8<T> f[N2];
+            if (2 * s2 <= t) {
+                get_operand<T, N2>(wy + TRI, tri_piece(t, s2), lane, f);
 #pragma unroll
-            for (int tt = 0; tt < TN; ++tt) {
-                const int t = t0 + tt;
-                const f32x4_t in = *reinterpret_cast<const f32x4_t*>(tab + 16 * t + 4 * lg);
-                const f32x4_t out = *reinterpret_cast<const f32x4_t*>(tab + C + 16 * t + 4 * lg);
-                const f32x4_t beta = *reinterpret_cast<const f32x4_t*>(tab + 2 * C + 16 * t + 4 * lg);
-                ps[tt] *= in * a.scale;
-                dq[tt] += ps[tt];
-                dk[tt] += out * beta * pb[tt] - in * pa[tt];
-                // q . (state's part of dq)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float qv = t & 2 ? fq[1].get(4 * (t & 1) + r) : fq[0].get(4 * (t & 1) + r);
-                    const float u = row16_sum(qv * ps[tt][r]);
-                    if (lr == 0) part_s[wave % NCT][16 * t + 4 * lg + r] = u;
+                for (int n = 0; n < NT; ++n) {
+                    const Frag8<T> bk[1] = {fk[n][s2]};
+                    dk[t][n] = mma_parts(f, bk, dk[t][n]);
                 }
+            }
+            if (2 * s2 + 1 >= t) {
+                get_operand<T, N2>(wy + 3 * TRI, tri_piece_t(t, s2), lane, f);
 #pragma unroll
-                for (int s2 = 0; s2 < 2; ++s2) {
-                    const Frag8<T> bk[1] = {fk[s2]}, bq[1] = {fq[s2]};
-                    Frag8<T> f[N2];
-                    if (2 * s2 <= t) {
-                        get_operand<T, N2>(wy, tri_piece(t, s2), lane, f);
-                        dq[tt] = mma_parts(f, bk, dq[tt]);
-                        get_operand<T, N2>(wy + TRI, tri_piece(t, s2), lane, f);
-                        dk[tt] = mma_parts(f, bk, dk[tt]);
-                    }
-                    if (2 * s2 + 1 >= t) {
-                        get_operand<T, N2>(wy + 2 * TRI, tri_piece_t(t, s2), lane, f);
-                        dk[tt] = mma_parts(f, bq, dk[tt]);
-                        get_operand<T, N2>(wy + 3 * TRI, tri_piece_t(t, s2), lane, f);
-                        dk[tt] = mma_parts(f, bk, dk[tt]);
-                    }
+                for (int n = 0; n < NT; ++n) {
+                    const Frag8<T> bk[1] = {fk[n][s2]};
+                    dk[t][n] = mma_parts(f, bk, dk[t][n]);
                 }
             }
         }
-        __syncthreads();
-        if (tid < cnt && a.dg) {
-            float d = 0.f;
+    }
+    __syncthreads();
+    Frag8<T> fq[NT][2];
 #pragma unroll
-            for (int c = 0; c < NCT; ++c) d += part_s[c][tid];
-            a.terms[slot * C + tid] = d + (part_p[tid] - part_v[tid]);
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int s2 = 0; s2 < 2; ++s2) fq[n][s2] = TK::cols(sk, ch0 + 16 * n, s2, lane);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        // q . (state's part of dq)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            float u = 0.f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) u += fq[n][t >> 1].get(4 * (t & 1) + r) * ps[t][n][r];
+            u = row16_sum(u);
+            if (lr == 0) part_s[wave][16 * t + 4 * lg + r] = u;
         }
+#pragma unroll
+        for (int s2 = 0; s2 < 2; ++s2) {
+            Frag8<T> f[N2];
+            if (2 * s2 <= t) {
+                get_operand<T, N2>(wy, tri_piece(t, s2), lane, f);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const Frag8<T> bk[1] = {fk[n][s2]};
+                    ps[t][n] = mma_parts(f, bk, ps[t][n]);
+                }
+            }
+            if (2 * s2 + 1 >= t) {
+                get_operand<T, N2>(wy + 2 * TRI, tri_piece_t(t, s2), lane, f);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const Frag8<T> bq[1] = {fq[n][s2]};
+                    dk[t][n] = mma_parts(f, bq, dk[t][n]);
+                }
+            }
+        }
+    }
+    __syncthreads();
+    if (tid < cnt && a.dg)
+        a.terms[slot * C + tid] = ((part_s[0][tid] + part_s[1][tid]) + (part_s[2][tid] + part_s[3][tid])) +
+                                  (part_p[tid] - part_v[tid]);
+    if (a.parts) {
+        // shared key heads: each value head's part
+        const int64_t all = a.at.T_total * H * DK;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 16 * t + 4 * lg + r;
+                if (row >= cnt) continue;
+                float* const at = a.parts + ((start + row) * H + h) * DK + ch0 + lr;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    at[16 * n] = ps[t][n][r];
+                    at[all + 16 * n] = dk[t][n][r];
+                }
+            }
+        return;
     }
     // whole rows of dq and dk through LDS
+    T* const oq = reinterpret_cast<T*>(smem + Lds::dq);
+    T* const ok = reinterpret_cast<T*>(smem + Lds::dk);
 #pragma unroll
-    for (int o = 0; o < 2; ++o) {
-        T* const to = reinterpret_cast<T*>(smem + (o ? Lds::dk : Lds::dq));
+    for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int t = 0; t < TN; ++t)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) to[TK::off(16 * (t0 + t) + 4 * lg + r, ch0 + lr)] = from_f32<T>(o ? dk[t][r] : dq[t][r]);
-    }
+            for (int r = 0; r < 4; ++r) {
+                const int at = TK::off(16 * t + 4 * lg + r, ch0 + 16 * n + lr);
+                oq[at] = from_f32<T>(ps[t][n][r]);
+                ok[at] = from_f32<T>(dk[t][n][r]);
+            }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
-        const int u = i * 512 + tid, row = u / (DK / EP), col = u % (DK / EP) * EP;
+        const int u = i * 256 + tid, row = u / (DK / EP), col = u % (DK / EP) * EP;
         if (row >= cnt) continue;
-        const int64_t at = ((bl.start + row) * Hk + hk) * DK + col;
-        *reinterpret_cast<u32x4_t*>((T*)a.dq + at) = *reinterpret_cast<const u32x4_t*>(smem + Lds::dq + TK::off(row, col) * sizeof(T));
-        *reinterpret_cast<u32x4_t*>((T*)a.dk + at) = *reinterpret_cast<const u32x4_t*>(smem + Lds::dk + TK::off(row, col) * sizeof(T));
+        const int64_t at = ((start + row) * H + h) * DK + col;
+        *reinterpret_cast<u32x4_t*>((T*)a.dq + at) = *reinterpret_cast<const u32x4_t*>(oq + TK::off(row, col));
+        *reinterpret_cast<u32x4_t*>((T*)a.dk + at) = *reinterpret_cast<const u32x4_t*>(ok + TK::off(row, col));
+    }
+}
+
+// dq and dk of key heads that value heads share: the sums of these heads' parts.
+template <typename T>
+__global__ __launch_bounds__(256) void gdr_share_kernel(GdrArgs a, int D) {
+    const int r = a.k.share, Hk = a.at.H / r, per = Hk * (D / 4);   // runs of 4 of a token
+    const int64_t t0 = seq_at(a.at, 0), t1 = seq_at(a.at, a.at.num_seqs), n4 = a.at.T_total * per, all = a.at.T_total * a.at.H * D;
+    for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < 2 * n4; u += (int64_t)gridDim.x * 256) {
+        const int64_t i = u < n4 ? u : u - n4, tok = i / per;
+        if (tok < t0 || tok >= t1) continue;
+        const float* const p = a.parts + (u < n4 ? 0 : all) + (i / (D / 4)) * r * D + i % (D / 4) * 4;
+        f32x4_t s = *reinterpret_cast<const f32x4_t*>(p);
+        for (int j = 1; j < r; ++j) s += *reinterpret_cast<const f32x4_t*>(p + (int64_t)j * D);
+        const float o[4] = {s[0], s[1], s[2], s[3]};
+        store_vec<T, 4>((T*)(u < n4 ? a.dq : a.dk) + i * 4, o);
     }
 }
 
@@ -1331,13 +1421,18 @@ hipError_t join(const GdrArgs& a, int backwards) {
 template <typename T, int DK, int DV>
 hipError_t grad_t(const GdrArgs& a) {
     if (a.at.T_total == 0) return hipSuccess;
-    constexpr int lds = GradLds<T, DK, DV>::bytes;
+    constexpr int lds = GradLds<T, DK>::bytes;
     static_assert(lds <= 152 * 1024, "LDS");
     const void* kern = reinterpret_cast<const void*>(&gdr_grad_kernel<T, DK, DV>);
     const hipError_t e = ensure_lds_limit(kern, lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((gdr_grad_kernel<T, DK, DV>), dim3((unsigned)((int64_t)a.at.nblocks * (a.at.H / a.k.share))),
-                       dim3(512), lds, (hipStream_t)a.at.stream, a);
+    hipLaunchKernelGGL((gdr_grad_kernel<T, DK, DV>), dim3((unsigned)((int64_t)a.at.nblocks * a.at.H)), dim3(256), lds,
+                       (hipStream_t)a.at.stream, a);
+    hipError_t st = hipGetLastError();
+    if (st != hipSuccess || !a.parts) return st;
+    const int64_t runs = a.at.T_total * (a.at.H / a.k.share) * (DK / 2), groups = (runs + 1023) / 1024;   // four a thread
+    hipLaunchKernelGGL((gdr_share_kernel<T>), dim3((unsigned)(groups < 65536 ? groups : 65536)), dim3(256), 0,
+                       (hipStream_t)a.at.stream, a, DK);
     return hipGetLastError();
 }
 

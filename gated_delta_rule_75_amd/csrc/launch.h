@@ -267,6 +267,7 @@ struct GdrArgs {
     // gradient, by chunk and head: states before it, errors of prediction; the
     // state's gradient behind it, dv / beta; the tokens' terms of dg
     float *states, *errors, *rstates, *u, *terms;
+    float* parts;                // shared key heads: dq's and dk's, [2][T][H][dk]; else NULL
     // long sequences of few heads: segments, their transitions (and transposes), and
     // their own states, then those that enter them (NULL: not cut)
     LinArgs seg;

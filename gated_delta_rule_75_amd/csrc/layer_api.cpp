@@ -449,8 +449,8 @@ kda_status kda_rope_axes(kda_dtype dt, int64_t T, int Hq, int Hk, int d, int rot
 
 namespace {
 
-// Chunks of 64 tokens: (chunk, head) pairs as workgroups of 256 threads, 512 for
-// a key head, two a head of a sequence, on an axis of less than 2^32 threads.
+// Chunks of 64 tokens: (chunk, head) pairs as workgroups of 256 threads, and two a
+// head of a sequence, on an axis of less than 2^32 threads.
 constexpr int64_t kMaxChunks = int64_t(1) << 23;
 
 bool gdr_sizes_ok(kda_dtype dt, int H, int Hk, int dk, int dv, int num_seqs, int64_t T) {
@@ -475,10 +475,10 @@ int64_t gdr_segment(int H, int dk, int dv, int num_seqs, int64_t T) {
 }
 
 struct GdrLayout {
-    size_t x, p, z, tab, states, rstates, errors, u, terms, s_end, plan, seg_m, seg_mt, seg_s, seg_r, total;
+    size_t x, p, z, tab, states, rstates, errors, u, terms, s_end, share, plan, seg_m, seg_mt, seg_s, seg_r, total;
     int64_t chunks, L, segments;
 };
-GdrLayout gdr_layout(bool grad, int H, int dk, int dv, int num_seqs, int64_t T) {
+GdrLayout gdr_layout(bool grad, int H, int Hk, int dk, int dv, int num_seqs, int64_t T) {
     GdrLayout l{};
     l.chunks = T > 64 ? T / 64 + num_seqs : num_seqs;
     l.L = gdr_segment(H, dk, dv, num_seqs, T);
@@ -497,6 +497,7 @@ GdrLayout gdr_layout(bool grad, int H, int dk, int dv, int num_seqs, int64_t T) 
             l.u = p.take(n * 64 * dv * 4);
             l.terms = p.take(n * 64 * 4);
             l.s_end = p.take((size_t)num_seqs * H * dk * dv * 4);
+            l.share = p.take(Hk < H ? 2 * (size_t)T * H * dk * 4 : 0);
         }
         l.plan = p.take(T > 64 ? plan_bytes(num_seqs) : 0);
         if (l.L < T) {
@@ -525,7 +526,7 @@ kda_status gdr_args(bool grad, kda_dtype dt, int H, int Hk, int dk, int dv, floa
         (int64_t)H * dv > kMaxStride || !aligned(g, 4) || !aligned(beta, 4) || !aligned(cu_seqlens, 4) ||
         !aligned(initial_state, 16) || !aligned(workspace, 256) || !workspace)
         return KDA_ERR_INVALID_ARGUMENT;
-    const GdrLayout l = gdr_layout(grad, H, dk, dv, num_seqs, T_total);
+    const GdrLayout l = gdr_layout(grad, H, Hk, dk, dv, num_seqs, T_total);
     if (workspace_bytes < l.total) return KDA_ERR_WORKSPACE_TOO_SMALL;
     a.at.H = H;
     a.at.num_seqs = num_seqs;
@@ -564,6 +565,7 @@ kda_status gdr_args(bool grad, kda_dtype dt, int H, int Hk, int dk, int dv, floa
         a.errors = part<float>(workspace, l.errors);
         a.u = part<float>(workspace, l.u);
         a.terms = part<float>(workspace, l.terms);
+        if (Hk < H) a.parts = part<float>(workspace, l.share);
         a.final = part<float>(workspace, l.s_end);
     }
     a.dtype = (int)dt;
@@ -620,11 +622,11 @@ kda_status gdr_bwd(bool clear, kda_dtype dt, int H, int Hk, int dk, int dv, floa
 extern "C" {
 
 size_t kda_gdr_fwd_workspace_size(kda_dtype dt, int H, int Hk, int dk, int dv, int num_seqs, int64_t T_total) {
-    return gdr_sizes_ok(dt, H, Hk, dk, dv, num_seqs, T_total) ? gdr_layout(false, H, dk, dv, num_seqs, T_total).total : 0;
+    return gdr_sizes_ok(dt, H, Hk, dk, dv, num_seqs, T_total) ? gdr_layout(false, H, Hk, dk, dv, num_seqs, T_total).total : 0;
 }
 
 size_t kda_gdr_bwd_workspace_size(kda_dtype dt, int H, int Hk, int dk, int dv, int num_seqs, int64_t T_total) {
-    return gdr_sizes_ok(dt, H, Hk, dk, dv, num_seqs, T_total) ? gdr_layout(true, H, dk, dv, num_seqs, T_total).total : 0;
+    return gdr_sizes_ok(dt, H, Hk, dk, dv, num_seqs, T_total) ? gdr_layout(true, H, Hk, dk, dv, num_seqs, T_total).total : 0;
 }
 
 kda_status kda_gdr_fwd(kda_dtype dt, int H, int Hk, int dk, int dv, float scale, int num_seqs, int64_t T_total,
