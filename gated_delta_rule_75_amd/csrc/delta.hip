@@ -436,14 +436,17 @@ __device__ __forceinline__ void copy_flat(char* lds, const char* src, int wave, 
             copy16(uni(lds_addr(lds) + wave * 1024 + i * 4096), src, (unsigned)(wave * 1024 + i * 4096 + lane * 16));
 }
 
-// A walk over a sequence's chunks: a workgroup has 64 value columns of a head, a
-// wave 16 of them, the state (or its gradient) in its accumulators.
+// A walk over a sequence's chunks: a workgroup has 64 value columns of a head, each of
+// four waves 16 of them, the state (or its gradient) in its accumulators.  Four more
+// waves copy the next chunk's rows and operands to LDS: a wave stalls on a copy while
+// the memory pipe is full, and in the waves that multiply that cost 1 us a chunk.
 template <typename T, int DK, int MODE>
-__global__ __launch_bounds__(256, 1) void gdr_walk_kernel(GdrArgs a) {
+__global__ __launch_bounds__(512, 2) void gdr_walk_kernel(GdrArgs a) {
     constexpr int SN = DK / 32, KT = DK / 16, N3 = kThree<T>, NPP = MODE == kGdrOut ? kTwo<T> : N3, NB = walk_bufs<T, DK, MODE>(), SZ = (int)sizeof(T);
     constexpr bool kBack = back_mode(MODE), kQ = reads_q(MODE), kKeep = MODE == kGdrStates || MODE == kGdrBack;
     extern __shared__ __attribute__((aligned(16))) char smem[];
-    const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6), lr = lane & 15, lg = lane >> 4;
+    const int lane0 = threadIdx.x & 63, w8 = uni(threadIdx.x >> 6), wave = w8 & 3;
+    int lane = lane0, lr = lane & 15, lg = lane >> 4;
     const int H = a.at.H, DV = a.head_v, slices = DV / 64 + (MODE == kGdrSeg ? DK / 64 : 0), chains = a.seg.nblocks * H;
     // the slices of a head read the same rows: 8 heads apart in the launch, so
     // that they run on one XCD
@@ -509,6 +512,17 @@ __global__ __launch_bounds__(256, 1) void gdr_walk_kernel(GdrArgs a) {
         }
         if (wave == 3) copy16(uni(lds_addr(f.tab)), a.tab + slot * kGdrTab, (unsigned)lane * 16);
     };
+    auto chunk_at = [&](int step) { return kBack ? nch - 1 - step : step; };
+    if (w8 >= 4) {
+        for (int step = 0; step < nch; ++step) {
+            if (NB == 1 || step == 0) fetch(chunk_at(step));
+            wait_vmcnt<0>();
+            barrier_keep_loads();                   // the chunk is there (two buffers: and the one before read)
+            if (NB == 2 && step + 1 < nch) fetch(chunk_at(step + 1));
+            if (NB == 1) barrier_keep_loads();      // it is read
+        }
+        return;
+    }
     // channel of the state's tile i, row r of this lane
     auto channel = [&](int i, int r) { return 32 * (i >> 1) + 8 * lg + 4 * (i & 1) + r; };
 
@@ -527,31 +541,14 @@ __global__ __launch_bounds__(256, 1) void gdr_walk_kernel(GdrArgs a) {
             for (int r = 0; r < 4; ++r)
                 S[i][r] = s0 ? s0[(int64_t)channel(i, r) * DV] : unit && channel(i, r) == col0 + wcol + lr ? 1.f : 0.f;
     }
-    // A chunk's operands are read from LDS a phase before they are multiplied: a wave
-    // has its SIMD to itself, and nothing else hides the reads.  All of them are in
-    // registers when the chunk's barrier comes, so that its buffer takes the copies of
-    // the chunk after the next behind it, and the next one's rows of k are read.
-    Frag8<T> kr[4][SN];
-    auto read_k = [&](const Buf& f) {
-#pragma unroll
-        for (int s = 0; s < SN; ++s)
-#pragma unroll
-            for (int t = 0; t < 4; ++t) kr[t][s] = Tile<T, DK, 1>::rows8(f.k, 16 * t, s, lane);
-    };
-    auto chunk_at = [&](int step) { return kBack ? nch - 1 - step : step; };
-    // stores between the copies of a chunk and the wait for them
-    constexpr int NST = MODE == kGdrOut ? 4 : kKeep ? KT * 4 + 16 : 0;
-    static_assert(NST < 64, "vmcnt");
-    if (nch > 0) fetch(chunk_at(0));
-    wait_vmcnt<0>();
-    if (nch > 0) {
-        barrier_keep_loads();
-        read_k(buf(chunk_at(0)));
-        if (NB == 2 && nch > 1) fetch(chunk_at(1));
-    }
     for (int step = 0; step < nch; ++step) {
         const int c = chunk_at(step), m0 = c * C;
-        const bool more = step + 1 < nch;
+        barrier_keep_loads();
+        // LDS addresses are formed anew in each chunk: kept across the loop they spill
+        lane = lane0;
+        asm volatile("" : "+v"(lane));
+        lr = lane & 15;
+        lg = lane >> 4;
         const Buf f = buf(c);
         const int64_t slot = (int64_t)(fb + c) * H + h;
         const float end = unif(f.tab[3 * C]);
@@ -582,14 +579,8 @@ __global__ __launch_bounds__(256, 1) void gdr_walk_kernel(GdrArgs a) {
                     __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[i][r]), rsrc,
                                                           (unsigned)((channel(i, r) * DV + lr) * 4), 0, 0);
         }
-        // A: K S (or K R), a lane 4 tokens of a column; X (Z), P^T, the tables and v (dy) come
-        Frag8<T> fx[6][N3], fp[6][NPP], fs[SN][N3];
-#pragma unroll
-        for (int i = 0; i < 6; ++i) get_operand<T, N3>(f.x, i, lane, fx[i]);
-        if constexpr (kBack) {
-#pragma unroll
-            for (int i = 0; i < 6; ++i) get_operand<T, NPP>(f.p, i, lane, fp[i]);
-        }
+        // A: K S (or K R), a lane 4 tokens of a column; the tables and v (dy) come
+        Frag8<T> fs[SN][N3];
         f32x4_t in[4], out[4], beta[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -615,11 +606,14 @@ __global__ __launch_bounds__(256, 1) void gdr_walk_kernel(GdrArgs a) {
                 x[r] = S[2 * s][r];
                 x[4 + r] = S[2 * s + 1][r];
             }
+            Frag8<T> kr[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) kr[t] = Tile<T, DK, 1>::rows8(f.k, 16 * t, s, lane);
             split(x, fs[s]);
 #pragma unroll
             for (int p = N3 - 1; p >= 0; --p)
 #pragma unroll
-                for (int t = 0; t < 4; ++t) ks[t] = mma(kr[t][s], fs[s][p], ks[t]);
+                for (int t = 0; t < 4; ++t) ks[t] = mma(kr[t], fs[s][p], ks[t]);
         }
         if (end == 0.f) {
 #pragma unroll
@@ -628,22 +622,7 @@ __global__ __launch_bounds__(256, 1) void gdr_walk_kernel(GdrArgs a) {
 #pragma unroll
             for (int i = 0; i < KT; ++i) S[i] *= end;
         }
-        __builtin_amdgcn_sched_barrier(0);
-        // B: V - exp(G) K S, or P^T dY + exp(G_63 - G) K R; rows of q come (backwards: its columns)
-        Frag8<T> fq[kBack ? KT : 4][kBack ? 2 : SN];
-        if constexpr (MODE == kGdrOut) {
-#pragma unroll
-            for (int s = 0; s < SN; ++s)
-#pragma unroll
-                for (int t = 0; t < 4; ++t) fq[t][s] = Tile<T, DK, 1>::rows8(f.q, 16 * t, s, lane);
-#pragma unroll
-            for (int i = 0; i < 6; ++i) get_operand<T, NPP>(f.p, i, lane, fp[i]);
-        } else if constexpr (kBack) {
-#pragma unroll
-            for (int s2 = 0; s2 < 2; ++s2)
-#pragma unroll
-                for (int i = 0; i < KT; ++i) fq[i][s2] = cols8<T, DK>(f.q, i >> 1, i & 1, s2, lane);
-        }
+        // B: V - exp(G) K S, or P^T dY + exp(G_63 - G) K R
         // two 16-token tiles as an operand in parts
         auto operand = [&](const f32x4_t& lo, const f32x4_t& hi, auto& o) {
             float x[8];
@@ -667,33 +646,31 @@ __global__ __launch_bounds__(256, 1) void gdr_walk_kernel(GdrArgs a) {
 #pragma unroll
             for (int s2 = 0; s2 < 2; ++s2)
 #pragma unroll
-                for (int p = NPP - 1; p >= 0; --p)
+                for (int t = 0; t < 2 * s2 + 2; ++t) {
+                    Frag8<T> fp[NPP];
+                    get_operand<T, NPP>(f.p, tri_piece_t(t, s2), lane, fp);
 #pragma unroll
-                    for (int t = 0; t < 2 * s2 + 2; ++t) e[t] = mma(fp[tri_piece_t(t, s2)][p], fv[s2], e[t]);
+                    for (int p = NPP - 1; p >= 0; --p) e[t] = mma(fp[p], fv[s2], e[t]);
+                }
         }
 #pragma unroll
         for (int s2 = 0; s2 < 2; ++s2) operand(e[2 * s2], e[2 * s2 + 1], fe[s2]);
-        __builtin_amdgcn_sched_barrier(0);
-        // C: E (or U); the columns of k come.  Beside it what does not wait for E: y's part of
-        // the entering state, transposed tiles, a lane 4 columns of token 16 t + l % 16; or dY's
-        // part of R
-        Frag8<T> fk[KT][2];
-#pragma unroll
-        for (int s2 = 0; s2 < 2; ++s2)
-#pragma unroll
-            for (int i = 0; i < KT; ++i) fk[i][s2] = cols8<T, DK>(f.k, i >> 1, i & 1, s2, lane);
+        // C: E (or U).  Beside it what does not wait for E: y's part of the entering state,
+        // transposed tiles, a lane 4 columns of token 16 t + l % 16; or dY's part of R
 #pragma unroll
         for (int t = 0; t < 4; ++t) e[t] = zero;
 #pragma unroll
-        for (int s = N3 - 1; s >= 0; --s)
+        for (int s2 = 0; s2 < 2; ++s2)
 #pragma unroll
-            for (int i = 0; i <= s; ++i)
+            for (int t = 0; t < 4; ++t) {
+                if (kBack ? 2 * s2 + 1 < t : 2 * s2 > t) continue;
+                Frag8<T> fx[N3];
+                get_operand<T, N3>(f.x, kBack ? tri_piece_t(t, s2) : tri_piece(t, s2), lane, fx);
 #pragma unroll
-                for (int s2 = 0; s2 < 2; ++s2)
+                for (int s = N3 - 1; s >= 0; --s)
 #pragma unroll
-                    for (int t = 0; t < 4; ++t)
-                        if (kBack ? 2 * s2 + 1 >= t : 2 * s2 <= t)
-                            e[t] = mma(fx[kBack ? tri_piece_t(t, s2) : tri_piece(t, s2)][i], fe[s2][s - i], e[t]);
+                    for (int i = 0; i <= s; ++i) e[t] = mma(fx[i], fe[s2][s - i], e[t]);
+            }
         f32x4_t y[4] = {zero, zero, zero, zero};
         float into[4];
         if constexpr (MODE == kGdrOut) {
@@ -701,11 +678,15 @@ __global__ __launch_bounds__(256, 1) void gdr_walk_kernel(GdrArgs a) {
             for (int t = 0; t < 4; ++t) into[t] = f.tab[16 * t + lr];
             // the state's leading 16 bits
 #pragma unroll
-            for (int s = 0; s < SN; ++s)
+            for (int s = 0; s < SN; ++s) {
+                Frag8<T> fq[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) fq[t] = Tile<T, DK, 1>::rows8(f.q, 16 * t, s, lane);
 #pragma unroll
                 for (int p = NPP - 1; p >= 0; --p)
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) y[t] = mma(fs[s][p], fq[t][s], y[t]);
+                    for (int t = 0; t < 4; ++t) y[t] = mma(fs[s][p], fq[t], y[t]);
+            }
 #pragma unroll
             for (int t = 0; t < 4; ++t) y[t] *= into[t] * scale;
         } else if constexpr (kBack) {
@@ -718,10 +699,13 @@ __global__ __launch_bounds__(256, 1) void gdr_walk_kernel(GdrArgs a) {
 #pragma unroll
                     for (int r = 0; r < 4; ++r) d[half][r] = fv[s2].get(4 * half + r) * (in[2 * s2 + half][r] * scale);
                 operand(d[0], d[1], u);
+                Frag8<T> fq[KT];
+#pragma unroll
+                for (int i = 0; i < KT; ++i) fq[i] = cols8<T, DK>(f.q, i >> 1, i & 1, s2, lane);
 #pragma unroll
                 for (int p = N3 - 1; p >= 0; --p)
 #pragma unroll
-                    for (int i = 0; i < KT; ++i) S[i] = mma(fq[i][s2], u[p], S[i]);
+                    for (int i = 0; i < KT; ++i) S[i] = mma(fq[i], u[p], S[i]);
             }
         }
         if constexpr (kKeep) {
@@ -734,18 +718,6 @@ __global__ __launch_bounds__(256, 1) void gdr_walk_kernel(GdrArgs a) {
                     __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(e[t][r]), rsrc,
                                                           (unsigned)(((16 * t + 4 * lg + r) * DV + lr) * 4), 0, 0);
         }
-        // the next chunk's copies are there, this one's operands in registers
-        if (NB == 2) {
-            if (!kKeep && step == 0) wait_vmcnt<0>();
-            else wait_vmcnt<NST>();
-        }
-        barrier_keep_loads();
-        if (NB == 2) {
-            if (step + 2 < nch) fetch(chunk_at(step + 2));
-            if (more) read_k(buf(chunk_at(step + 1)));
-        } else if (more) {
-            fetch(chunk_at(step + 1));
-        }
         // D: the chunk's own part of y, and of the state behind it (or of the gradient before it)
 #pragma unroll
         for (int t = 0; t < 4; ++t) e[t] *= beta[t];
@@ -754,23 +726,29 @@ __global__ __launch_bounds__(256, 1) void gdr_walk_kernel(GdrArgs a) {
 #pragma unroll
             for (int s2 = 0; s2 < 2; ++s2) operand(e[2 * s2], e[2 * s2 + 1], fb[s2]);
 #pragma unroll
-            for (int s = NPP - 1; s >= 0; --s)
+            for (int s2 = 0; s2 < 2; ++s2)
 #pragma unroll
-                for (int i = 0; i <= s; ++i)
+                for (int t = 2 * s2; t < 4; ++t) {
+                    Frag8<T> fp[NPP];
+                    get_operand<T, NPP>(f.p, tri_piece(t, s2), lane, fp);
 #pragma unroll
-                    for (int s2 = 0; s2 < 2; ++s2)
+                    for (int s = NPP - 1; s >= 0; --s)
 #pragma unroll
-                        for (int t = 2 * s2; t < 4; ++t) y[t] = mma(fb[s2][i], fp[tri_piece(t, s2)][s - i], y[t]);
+                        for (int i = 0; i <= s; ++i) y[t] = mma(fb[s2][i], fp[s - i], y[t]);
+                }
         }
 #pragma unroll
         for (int s2 = 0; s2 < 2; ++s2) {
             Frag8<T> u[N3];
             if constexpr (!kBack) operand(out[2 * s2] * e[2 * s2], out[2 * s2 + 1] * e[2 * s2 + 1], u);
             else operand(-(in[2 * s2] * e[2 * s2]), -(in[2 * s2 + 1] * e[2 * s2 + 1]), u);
+            Frag8<T> fk[KT];
+#pragma unroll
+            for (int i = 0; i < KT; ++i) fk[i] = cols8<T, DK>(f.k, i >> 1, i & 1, s2, lane);
 #pragma unroll
             for (int p = N3 - 1; p >= 0; --p)
 #pragma unroll
-                for (int i = 0; i < KT; ++i) S[i] = mma(fk[i][s2], u[p], S[i]);
+                for (int i = 0; i < KT; ++i) S[i] = mma(fk[i], u[p], S[i]);
         }
         if constexpr (MODE == kGdrOut) {
             // rows without a token lie behind the bound and are dropped
@@ -798,11 +776,7 @@ __global__ __launch_bounds__(256, 1) void gdr_walk_kernel(GdrArgs a) {
                 }
             }
         }
-        if (NB == 1 && more) {
-            wait_vmcnt<0>();
-            barrier_keep_loads();
-            read_k(buf(0));
-        }
+        if (NB == 1) barrier_keep_loads();
     }
     if (unit) {
         const int col = col0 + wcol + lr;
@@ -1407,7 +1381,7 @@ hipError_t walk_t(const GdrArgs& a) {
     const hipError_t e = ensure_lds_limit(kern, lds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((gdr_walk_kernel<T, DK, MODE>), dim3((unsigned)((int64_t)a.seg.nblocks * a.at.H * (a.head_v / 64 + (MODE == kGdrSeg ? DK / 64 : 0)))),
-                       dim3(256), lds, (hipStream_t)a.at.stream, a);
+                       dim3(512), lds, (hipStream_t)a.at.stream, a);
     return hipGetLastError();
 }
 
