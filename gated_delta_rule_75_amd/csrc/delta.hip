@@ -427,6 +427,8 @@ template <typename T, int DK, int MODE> constexpr int walk_bytes() {
 }
 template <typename T, int DK, int MODE> constexpr int walk_bufs() { return 2 * walk_bytes<T, DK, MODE>() <= 160 * 1024 ? 2 : 1; }
 
+constexpr int walk_threads(int m) { return m == kGdrOut ? 512 : 256; }
+
 template <int BYTES>
 __device__ __forceinline__ void copy_flat(char* lds, const char* src, int wave, int lane) {
     static_assert(BYTES % 1024 == 0, "whole copies");
@@ -437,15 +439,20 @@ __device__ __forceinline__ void copy_flat(char* lds, const char* src, int wave, 
 }
 
 // A walk over a sequence's chunks: a workgroup has 64 value columns of a head, each of
-// four waves 16 of them, the state (or its gradient) in its accumulators.  Four more
-// waves copy the next chunk's rows and operands to LDS: a wave stalls on a copy while
-// the memory pipe is full, and in the waves that multiply that cost 1 us a chunk.
+// four waves 16 of them, the state (or its gradient) in its accumulators.  The walk
+// that writes outputs has four more waves, which copy the next chunk's rows and
+// operands to LDS: a wave stalls on a copy while the memory pipe is full.  It then
+// reads operands where they are multiplied, for two waves of a SIMD have half the
+// registers each (8192 tokens of 96 heads: 587 -> 492 us).  The others wait for their
+// stores as well; there the four waves copy themselves, and read ahead (4 x 2048 tokens
+// of 32 heads, with waves that copy: states 148 -> 165 us, backwards 210 -> 229).
 template <typename T, int DK, int MODE>
-__global__ __launch_bounds__(512, 2) void gdr_walk_kernel(GdrArgs a) {
+__global__ __launch_bounds__(walk_threads(MODE), walk_threads(MODE) / 256) void gdr_walk_kernel(GdrArgs a) {
     constexpr int SN = DK / 32, KT = DK / 16, N3 = kThree<T>, NPP = MODE == kGdrOut ? kTwo<T> : N3, NB = walk_bufs<T, DK, MODE>(), SZ = (int)sizeof(T);
     constexpr bool kBack = back_mode(MODE), kQ = reads_q(MODE), kKeep = MODE == kGdrStates || MODE == kGdrBack;
+    constexpr bool kCopiers = walk_threads(MODE) == 512;
     extern __shared__ __attribute__((aligned(16))) char smem[];
-    const int lane0 = threadIdx.x & 63, w8 = uni(threadIdx.x >> 6), wave = w8 & 3;
+    const int lane0 = threadIdx.x & 63, wave = uni(threadIdx.x >> 6) & 3;
     int lane = lane0, lr = lane & 15, lg = lane >> 4;
     const int H = a.at.H, DV = a.head_v, slices = DV / 64 + (MODE == kGdrSeg ? DK / 64 : 0), chains = a.seg.nblocks * H;
     // the slices of a head read the same rows: 8 heads apart in the launch, so
@@ -513,7 +520,7 @@ __global__ __launch_bounds__(512, 2) void gdr_walk_kernel(GdrArgs a) {
         if (wave == 3) copy16(uni(lds_addr(f.tab)), a.tab + slot * kGdrTab, (unsigned)lane * 16);
     };
     auto chunk_at = [&](int step) { return kBack ? nch - 1 - step : step; };
-    if (w8 >= 4) {
+    if (kCopiers && threadIdx.x >= 256) {
         for (int step = 0; step < nch; ++step) {
             if (NB == 1 || step == 0) fetch(chunk_at(step));
             wait_vmcnt<0>();
@@ -541,15 +548,39 @@ __global__ __launch_bounds__(512, 2) void gdr_walk_kernel(GdrArgs a) {
             for (int r = 0; r < 4; ++r)
                 S[i][r] = s0 ? s0[(int64_t)channel(i, r) * DV] : unit && channel(i, r) == col0 + wcol + lr ? 1.f : 0.f;
     }
+    // Without copiers a chunk's operands are read from LDS a phase before they are
+    // multiplied: a wave has its SIMD to itself, and nothing else hides the reads.  All of them are in
+    // registers when the chunk's barrier comes, so that its buffer takes the copies of
+    // the chunk after the next behind it, and the next one's rows of k are read.
+    Frag8<T> kr[4][SN];
+    auto read_k = [&](const Buf& f) {
+#pragma unroll
+        for (int s = 0; s < SN; ++s)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) kr[t][s] = Tile<T, DK, 1>::rows8(f.k, 16 * t, s, lane);
+    };
+    // stores between the copies of a chunk and the wait for them
+    constexpr int NST = MODE == kGdrOut ? 4 : kKeep ? KT * 4 + 16 : 0;
+    static_assert(NST < 64, "vmcnt");
+    if (!kCopiers && nch > 0) {
+        fetch(chunk_at(0));
+        wait_vmcnt<0>();
+        barrier_keep_loads();
+        read_k(buf(chunk_at(0)));
+        if (NB == 2 && nch > 1) fetch(chunk_at(1));
+    }
     for (int step = 0; step < nch; ++step) {
         const int c = chunk_at(step), m0 = c * C;
-        barrier_keep_loads();
-        // LDS addresses are formed anew in each chunk: kept across the loop they spill
-        lane = lane0;
-        asm volatile("" : "+v"(lane));
-        lr = lane & 15;
-        lg = lane >> 4;
+        const bool more = step + 1 < nch;
         const Buf f = buf(c);
+        if constexpr (kCopiers) {
+            barrier_keep_loads();
+            // LDS addresses are formed anew in each chunk: kept across the loop they spill
+            lane = lane0;
+            asm volatile("" : "+v"(lane));
+            lr = lane & 15;
+            lg = lane >> 4;
+        }
         const int64_t slot = (int64_t)(fb + c) * H + h;
         const float end = unif(f.tab[3 * C]);
         const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
@@ -579,8 +610,17 @@ __global__ __launch_bounds__(512, 2) void gdr_walk_kernel(GdrArgs a) {
                     __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[i][r]), rsrc,
                                                           (unsigned)((channel(i, r) * DV + lr) * 4), 0, 0);
         }
-        // A: K S (or K R), a lane 4 tokens of a column; the tables and v (dy) come
-        Frag8<T> fs[SN][N3];
+        // A: K S (or K R), a lane 4 tokens of a column; X (Z), P^T, the tables and v (dy) come
+        Frag8<T> fx[6][N3], fp[6][NPP], fs[SN][N3];
+        auto read_x = [&]() __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < 6; ++i) get_operand<T, N3>(f.x, i, lane, fx[i]);
+        };
+        if constexpr (!kCopiers) read_x();
+        if constexpr (kBack) {
+#pragma unroll
+            for (int i = 0; i < 6; ++i) get_operand<T, NPP>(f.p, i, lane, fp[i]);
+        }
         f32x4_t in[4], out[4], beta[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -606,14 +646,15 @@ __global__ __launch_bounds__(512, 2) void gdr_walk_kernel(GdrArgs a) {
                 x[r] = S[2 * s][r];
                 x[4 + r] = S[2 * s + 1][r];
             }
-            Frag8<T> kr[4];
+            if constexpr (kCopiers) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) kr[t] = Tile<T, DK, 1>::rows8(f.k, 16 * t, s, lane);
+                for (int t = 0; t < 4; ++t) kr[t][s] = Tile<T, DK, 1>::rows8(f.k, 16 * t, s, lane);
+            }
             split(x, fs[s]);
 #pragma unroll
             for (int p = N3 - 1; p >= 0; --p)
 #pragma unroll
-                for (int t = 0; t < 4; ++t) ks[t] = mma(kr[t], fs[s][p], ks[t]);
+                for (int t = 0; t < 4; ++t) ks[t] = mma(kr[t][s], fs[s][p], ks[t]);
         }
         if (end == 0.f) {
 #pragma unroll
@@ -622,7 +663,15 @@ __global__ __launch_bounds__(512, 2) void gdr_walk_kernel(GdrArgs a) {
 #pragma unroll
             for (int i = 0; i < KT; ++i) S[i] *= end;
         }
-        // B: V - exp(G) K S, or P^T dY + exp(G_63 - G) K R
+        if constexpr (!kCopiers) __builtin_amdgcn_sched_barrier(0);
+        // B: V - exp(G) K S, or P^T dY + exp(G_63 - G) K R; rows of q come (backwards: its columns)
+        Frag8<T> fq[kBack ? KT : 4][kBack ? 2 : SN];
+        if constexpr (kBack) {
+#pragma unroll
+            for (int s2 = 0; s2 < 2; ++s2)
+#pragma unroll
+                for (int i = 0; i < KT; ++i) fq[i][s2] = cols8<T, DK>(f.q, i >> 1, i & 1, s2, lane);
+        }
         // two 16-token tiles as an operand in parts
         auto operand = [&](const f32x4_t& lo, const f32x4_t& hi, auto& o) {
             float x[8];
@@ -646,31 +695,39 @@ __global__ __launch_bounds__(512, 2) void gdr_walk_kernel(GdrArgs a) {
 #pragma unroll
             for (int s2 = 0; s2 < 2; ++s2)
 #pragma unroll
-                for (int t = 0; t < 2 * s2 + 2; ++t) {
-                    Frag8<T> fp[NPP];
-                    get_operand<T, NPP>(f.p, tri_piece_t(t, s2), lane, fp);
+                for (int p = NPP - 1; p >= 0; --p)
 #pragma unroll
-                    for (int p = NPP - 1; p >= 0; --p) e[t] = mma(fp[p], fv[s2], e[t]);
-                }
+                    for (int t = 0; t < 2 * s2 + 2; ++t) e[t] = mma(fp[tri_piece_t(t, s2)][p], fv[s2], e[t]);
         }
 #pragma unroll
         for (int s2 = 0; s2 < 2; ++s2) operand(e[2 * s2], e[2 * s2 + 1], fe[s2]);
-        // C: E (or U).  Beside it what does not wait for E: y's part of the entering state,
-        // transposed tiles, a lane 4 columns of token 16 t + l % 16; or dY's part of R
+        if constexpr (!kCopiers) __builtin_amdgcn_sched_barrier(0);
+        // C: E (or U); the columns of k come.  Beside it what does not wait for E: y's part of
+        // the entering state, transposed tiles, a lane 4 columns of token 16 t + l % 16; or dY's
+        // part of R
+        Frag8<T> fk[KT][2];
+        auto read_cols = [&](int s2) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < KT; ++i) fk[i][s2] = cols8<T, DK>(f.k, i >> 1, i & 1, s2, lane);
+        };
+        if constexpr (kCopiers) {
+            read_x();
+        } else {
+            read_cols(0);
+            read_cols(1);
+        }
 #pragma unroll
         for (int t = 0; t < 4; ++t) e[t] = zero;
 #pragma unroll
-        for (int s2 = 0; s2 < 2; ++s2)
+        for (int s = N3 - 1; s >= 0; --s)
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                if (kBack ? 2 * s2 + 1 < t : 2 * s2 > t) continue;
-                Frag8<T> fx[N3];
-                get_operand<T, N3>(f.x, kBack ? tri_piece_t(t, s2) : tri_piece(t, s2), lane, fx);
+            for (int i = 0; i <= s; ++i)
 #pragma unroll
-                for (int s = N3 - 1; s >= 0; --s)
+                for (int s2 = 0; s2 < 2; ++s2)
 #pragma unroll
-                    for (int i = 0; i <= s; ++i) e[t] = mma(fx[i], fe[s2][s - i], e[t]);
-            }
+                    for (int t = 0; t < 4; ++t)
+                        if (kBack ? 2 * s2 + 1 >= t : 2 * s2 <= t)
+                            e[t] = mma(fx[kBack ? tri_piece_t(t, s2) : tri_piece(t, s2)][i], fe[s2][s - i], e[t]);
         f32x4_t y[4] = {zero, zero, zero, zero};
         float into[4];
         if constexpr (MODE == kGdrOut) {
@@ -679,13 +736,12 @@ __global__ __launch_bounds__(512, 2) void gdr_walk_kernel(GdrArgs a) {
             // the state's leading 16 bits
 #pragma unroll
             for (int s = 0; s < SN; ++s) {
-                Frag8<T> fq[4];
 #pragma unroll
-                for (int t = 0; t < 4; ++t) fq[t] = Tile<T, DK, 1>::rows8(f.q, 16 * t, s, lane);
+                for (int t = 0; t < 4; ++t) fq[t][s] = Tile<T, DK, 1>::rows8(f.q, 16 * t, s, lane);
 #pragma unroll
                 for (int p = NPP - 1; p >= 0; --p)
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) y[t] = mma(fs[s][p], fq[t], y[t]);
+                    for (int t = 0; t < 4; ++t) y[t] = mma(fs[s][p], fq[t][s], y[t]);
             }
 #pragma unroll
             for (int t = 0; t < 4; ++t) y[t] *= into[t] * scale;
@@ -699,13 +755,10 @@ __global__ __launch_bounds__(512, 2) void gdr_walk_kernel(GdrArgs a) {
 #pragma unroll
                     for (int r = 0; r < 4; ++r) d[half][r] = fv[s2].get(4 * half + r) * (in[2 * s2 + half][r] * scale);
                 operand(d[0], d[1], u);
-                Frag8<T> fq[KT];
-#pragma unroll
-                for (int i = 0; i < KT; ++i) fq[i] = cols8<T, DK>(f.q, i >> 1, i & 1, s2, lane);
 #pragma unroll
                 for (int p = N3 - 1; p >= 0; --p)
 #pragma unroll
-                    for (int i = 0; i < KT; ++i) S[i] = mma(fq[i], u[p], S[i]);
+                    for (int i = 0; i < KT; ++i) S[i] = mma(fq[i][s2], u[p], S[i]);
             }
         }
         if constexpr (kKeep) {
@@ -718,6 +771,20 @@ __global__ __launch_bounds__(512, 2) void gdr_walk_kernel(GdrArgs a) {
                     __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(e[t][r]), rsrc,
                                                           (unsigned)(((16 * t + 4 * lg + r) * DV + lr) * 4), 0, 0);
         }
+        if constexpr (!kCopiers) {
+            // the next chunk's copies are there, this one's operands in registers
+            if (NB == 2) {
+                if (!kKeep && step == 0) wait_vmcnt<0>();
+                else wait_vmcnt<NST>();
+            }
+            barrier_keep_loads();
+            if (NB == 2) {
+                if (step + 2 < nch) fetch(chunk_at(step + 2));
+                if (more) read_k(buf(chunk_at(step + 1)));
+            } else if (more) {
+                fetch(chunk_at(step + 1));
+            }
+        }
         // D: the chunk's own part of y, and of the state behind it (or of the gradient before it)
 #pragma unroll
         for (int t = 0; t < 4; ++t) e[t] *= beta[t];
@@ -726,29 +793,26 @@ __global__ __launch_bounds__(512, 2) void gdr_walk_kernel(GdrArgs a) {
 #pragma unroll
             for (int s2 = 0; s2 < 2; ++s2) operand(e[2 * s2], e[2 * s2 + 1], fb[s2]);
 #pragma unroll
-            for (int s2 = 0; s2 < 2; ++s2)
+            for (int i = 0; i < 6; ++i) get_operand<T, NPP>(f.p, i, lane, fp[i]);
 #pragma unroll
-                for (int t = 2 * s2; t < 4; ++t) {
-                    Frag8<T> fp[NPP];
-                    get_operand<T, NPP>(f.p, tri_piece(t, s2), lane, fp);
+            for (int s = NPP - 1; s >= 0; --s)
 #pragma unroll
-                    for (int s = NPP - 1; s >= 0; --s)
+                for (int i = 0; i <= s; ++i)
 #pragma unroll
-                        for (int i = 0; i <= s; ++i) y[t] = mma(fb[s2][i], fp[s - i], y[t]);
-                }
+                    for (int s2 = 0; s2 < 2; ++s2)
+#pragma unroll
+                        for (int t = 2 * s2; t < 4; ++t) y[t] = mma(fb[s2][i], fp[tri_piece(t, s2)][s - i], y[t]);
         }
 #pragma unroll
         for (int s2 = 0; s2 < 2; ++s2) {
             Frag8<T> u[N3];
+            if constexpr (kCopiers) read_cols(s2);
             if constexpr (!kBack) operand(out[2 * s2] * e[2 * s2], out[2 * s2 + 1] * e[2 * s2 + 1], u);
             else operand(-(in[2 * s2] * e[2 * s2]), -(in[2 * s2 + 1] * e[2 * s2 + 1]), u);
-            Frag8<T> fk[KT];
-#pragma unroll
-            for (int i = 0; i < KT; ++i) fk[i] = cols8<T, DK>(f.k, i >> 1, i & 1, s2, lane);
 #pragma unroll
             for (int p = N3 - 1; p >= 0; --p)
 #pragma unroll
-                for (int i = 0; i < KT; ++i) S[i] = mma(fk[i], u[p], S[i]);
+                for (int i = 0; i < KT; ++i) S[i] = mma(fk[i][s2], u[p], S[i]);
         }
         if constexpr (MODE == kGdrOut) {
             // rows without a token lie behind the bound and are dropped
@@ -776,7 +840,12 @@ __global__ __launch_bounds__(512, 2) void gdr_walk_kernel(GdrArgs a) {
                 }
             }
         }
-        if (NB == 1) barrier_keep_loads();
+        if (kCopiers && NB == 1) barrier_keep_loads();
+        if (!kCopiers && NB == 1 && more) {
+            wait_vmcnt<0>();
+            barrier_keep_loads();
+            read_k(buf(0));
+        }
     }
     if (unit) {
         const int col = col0 + wcol + lr;
@@ -1381,7 +1450,7 @@ hipError_t walk_t(const GdrArgs& a) {
     const hipError_t e = ensure_lds_limit(kern, lds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((gdr_walk_kernel<T, DK, MODE>), dim3((unsigned)((int64_t)a.seg.nblocks * a.at.H * (a.head_v / 64 + (MODE == kGdrSeg ? DK / 64 : 0)))),
-                       dim3(512), lds, (hipStream_t)a.at.stream, a);
+                       dim3(walk_threads(MODE)), lds, (hipStream_t)a.at.stream, a);
     return hipGetLastError();
 }
 
