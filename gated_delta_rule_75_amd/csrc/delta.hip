@@ -432,7 +432,7 @@ template <typename T, int DK, int MODE> constexpr int walk_bytes() {
 }
 template <typename T, int DK, int MODE> constexpr int walk_bufs() { return 2 * walk_bytes<T, DK, MODE>() <= 160 * 1024 ? 2 : 1; }
 
-constexpr int walk_threads(int m) { return m == kGdrOut ? 512 : 256; }
+template <typename T, int DK> constexpr int walk_threads(int m) { return m == kGdrOut || (sizeof(T) == 4 && DK == 128) ? 512 : 256; }
 
 template <int BYTES>
 __device__ __forceinline__ void copy_flat(char* lds, const char* src, int wave, int lane) {
@@ -450,12 +450,14 @@ __device__ __forceinline__ void copy_flat(char* lds, const char* src, int wave, 
 // reads operands where they are multiplied, for two waves of a SIMD have half the
 // registers each (8192 tokens of 96 heads: 587 -> 492 us).  The others wait for their
 // stores as well; there the four waves copy themselves, and read ahead (4 x 2048 tokens
-// of 32 heads, with waves that copy: states 148 -> 165 us, backwards 210 -> 229).
+// of 32 heads, with waves that copy: states 148 -> 165 us, backwards 210 -> 229),
+// unless what they read ahead overfills the registers, in fp32 with 128 channels (the
+// gradient of the same sizes: 3225 -> 1658 us).
 template <typename T, int DK, int MODE>
-__global__ __launch_bounds__(walk_threads(MODE), walk_threads(MODE) / 256) void gdr_walk_kernel(GdrArgs a) {
+__global__ __launch_bounds__((walk_threads<T, DK>(MODE)), (walk_threads<T, DK>(MODE) / 256)) void gdr_walk_kernel(GdrArgs a) {
     constexpr int SN = DK / 32, KT = DK / 16, N3 = kThree<T>, NPP = MODE == kGdrOut ? kTwo<T> : N3, NB = walk_bufs<T, DK, MODE>(), SZ = (int)sizeof(T);
     constexpr bool kBack = back_mode(MODE), kQ = reads_q(MODE), kKeep = MODE == kGdrStates || MODE == kGdrBack;
-    constexpr bool kCopiers = walk_threads(MODE) == 512;
+    constexpr bool kCopiers = walk_threads<T, DK>(MODE) == 512;
     extern __shared__ __attribute__((aligned(16))) char smem[];
     const int lane0 = threadIdx.x & 63, wave = uni(threadIdx.x >> 6) & 3;
     int lane = lane0, lr = lane & 15, lg = lane >> 4;
@@ -1452,7 +1454,7 @@ hipError_t walk_t(const GdrArgs& a) {
     const hipError_t e = ensure_lds_limit(kern, lds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((gdr_walk_kernel<T, DK, MODE>), dim3((unsigned)((int64_t)a.seg.nblocks * a.at.H * (a.head_v / 64 + (MODE == kGdrSeg ? DK / 64 : 0)))),
-                       dim3(walk_threads(MODE)), lds, (hipStream_t)a.at.stream, a);
+                       dim3((walk_threads<T, DK>(MODE))), lds, (hipStream_t)a.at.stream, a);
     return hipGetLastError();
 }
 
