@@ -262,7 +262,12 @@ __device__ __forceinline__ void invert(float* sx, int wave, int lane) {
 }
 
 // Tables, scores and inverse of a (chunk, head).  GRAD: X, Z and P^T.
-// LDS: the rows of k (GRAD: and q), then the matrices in their place.
+// LDS: the rows of k (GRAD: and q), then the matrices in their place.  For a chunk of
+// its own, since nothing here waits for the state: it fills the card where the walk
+// cannot.  A workgroup asks for all that it reads at once, and the matrices take the
+// rows' place in LDS (8192 tokens of 96 heads: 246 -> 158 us).  Bound by the
+// chain of the 16 x 16 substitutions and by what it writes, 396 MB of operands, 3.9
+// TB/s with what it reads.
 template <typename T, int DK, bool GRAD> constexpr int prep_bytes() {
     constexpr int rows = C * DK * (int)sizeof(T) * (GRAD ? 2 : 1), m = C * kLd * 4 * (GRAD ? 2 : 1);
     return rows > m ? rows : m;
@@ -453,6 +458,11 @@ __device__ __forceinline__ void copy_flat(char* lds, const char* src, int wave, 
 // of 32 heads, with waves that copy: states 148 -> 165 us, backwards 210 -> 229),
 // unless what they read ahead overfills the registers, in fp32 with 128 channels (the
 // gradient of the same sizes: 3225 -> 1658 us).
+//
+// What bounds it: a chunk's products follow one another (K S, E, the state), 182 of
+// them a wave in 16 cycles each beside 580 other vector operations, most to split
+// operands, in 6800 cycles: 3.4 us at 2 GHz.  Copies cost nothing of that any more.
+// Those that keep states are bound by the 411 MB they write (3.1 TB/s).
 template <typename T, int DK, int MODE>
 __global__ __launch_bounds__((walk_threads<T, DK>(MODE)), (walk_threads<T, DK>(MODE) / 256)) void gdr_walk_kernel(GdrArgs a) {
     constexpr int SN = DK / 32, KT = DK / 16, N3 = kThree<T>, NPP = MODE == kGdrOut ? kTwo<T> : N3, NB = walk_bufs<T, DK, MODE>(), SZ = (int)sizeof(T);
@@ -881,7 +891,8 @@ __global__ __launch_bounds__((walk_threads<T, DK>(MODE)), (walk_threads<T, DK>(M
 // The states that enter the segments of a (sequence, head), 64 columns, in place of
 // the segments' own ones: S_{j+1} = M_j S_j + own_j from the sequence's initial state
 // (backwards R_{j-1} = M_j^T R_j + own_j).  A wave has 16 columns; matrices and
-// states enter the products with 24 bits.
+// states enter the products with 24 bits.  About 4 us a segment, latency: a segment's
+// matrix is read while the one before is multiplied.
 template <int DK>
 __global__ __launch_bounds__(256, 1) void gdr_join_kernel(GdrArgs a, int backwards) {
     constexpr int SN = DK / 32, KT = DK / 16;
@@ -970,7 +981,9 @@ __global__ __launch_bounds__(256, 1) void gdr_join_kernel(GdrArgs a, int backwar
 // all before, and all behind against its own as j) and, for its DK / 4 channels, to
 // the states' parts, whose rows are operands as they lie in memory.  W and Y then
 // take the rows' place, and q that of k.  In bf16 two workgroups share a CU: one
-// loads while the other multiplies.
+// loads while the other multiplies (4 x 2048 tokens of 32 heads: 430 us with all value
+// columns at once and one workgroup a CU, 295 so).  It moves 798 MB, 2.7 TB/s, with
+// matrix instructions 19 % and vector ones 32 % of the time: latency between its parts.
 template <typename T, int DK>
 struct GradLds {
     static constexpr int SZ = (int)sizeof(T), N2 = kTwo<T>, N3 = kThree<T>, TRI = kTri<T, N2>, ROWS = C * 64 * SZ;
@@ -1382,7 +1395,7 @@ __global__ __launch_bounds__(256) void gdr_share_kernel(GdrArgs a, int D) {
 // dg of a block of kBlock chunks of a (sequence, head): the sum of the terms from
 // each token to the block's end, and the product of the state there with its
 // gradient, which stands for all that is behind.  In fp64: where decays are
-// strong the tokens take nearly all of the product away again.
+// strong the tokens take nearly all of the product away again.  A wave a chunk.
 template <typename T>
 __global__ __launch_bounds__(256) void gdr_decay_kernel(GdrArgs a, int size) {
     __shared__ double part[5];
@@ -1530,38 +1543,37 @@ hipError_t launch_gdr_bwd(const GdrArgs& a) {
 }
 
 // One token a request against the resident fp32 state [N, H, dk, dv], updated in
-// place.  Columns of a state are independent: a workgroup takes COLS of them, all
-// or narrow slices to spread few states over the CUs.  S^T k and S^T q are summed
-// in one pass over the state in registers (S' ^T q = exp(g) S^T q + beta (k.q) e), so
-// it crosses memory once each way, which bounds the step.
+// place.  A workgroup takes a state whole: in slices of 16 columns, to spread few
+// states over the CUs, 16 states of 128 x 128 take 4.3 us against 4.0, and 256 take
+// 13.4 against 6.3.  S^T k and S^T q are summed in one pass over the state in
+// registers (S'^T q = exp(g) S^T q + beta (k.q) e), so it crosses memory once each
+// way, which bounds the step: 128 requests of 96 heads (1.62 GB) 274 us, 5.9 TB/s.
 namespace {
 
-template <typename T, int DK, int COLS>
+template <typename T, int DK, int DV>
 __global__ __launch_bounds__(256) void gdr_decode_kernel(GdrDecodeArgs a) {
-    constexpr int CG = COLS / 4, RG = 256 / CG, RPT = DK / RG;
+    constexpr int CG = DV / 4, RG = 256 / CG, RPT = DK / RG;
     static_assert(RG * CG == 256 && RPT * RG == DK, "decode tiling");
-    __shared__ float s_k[DK], s_q[DK], s_e[COLS], s_kq[RG];
-    __shared__ float s_p[RG][COLS + 4], s_o[RG][COLS + 4];
+    __shared__ float s_k[DK], s_q[DK], s_e[DV], s_kq[RG];
+    __shared__ float s_p[RG][DV + 4], s_o[RG][DV + 4];
     const int tid = threadIdx.x, cg = tid % CG, rg = tid / CG;
-    const int slices = a.dv / COLS;
-    // whole states: each XCD takes them in runs of two (workgroups i, i + 8,
-    // ... share one), as the KDA decode step does
-    int id = blockIdx.x;
-    if (slices == 1 && gridDim.x % 16 == 0) id = id / 16 * 16 + id % 8 * 2 + id / 8 % 2;
-    const int nh = id / slices, col0 = (id % slices) * COLS;
+    // each XCD takes states in runs of two (workgroups i, i + 8, ... share one), as
+    // the KDA decode step does
+    int nh = blockIdx.x;
+    if (gridDim.x % 16 == 0) nh = nh / 16 * 16 + nh % 8 * 2 + nh / 8 % 2;
     const int n = nh / a.H, h = nh % a.H;
-    float* st = a.state + (int64_t)nh * DK * a.dv + col0 + 4 * cg;
+    float* st = a.state + (int64_t)nh * DK * DV + 4 * cg;
     f32x4_t S[RPT];
 #pragma unroll
-    for (int r = 0; r < RPT; ++r) S[r] = __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(st + (int64_t)(r * RG + rg) * a.dv));
+    for (int r = 0; r < RPT; ++r) S[r] = __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(st + (int64_t)(r * RG + rg) * DV));
     const T* q = (const T*)a.q.p + (int64_t)n * a.q.stride + (int64_t)(h / a.q.share) * DK;
     const T* k = (const T*)a.k.p + (int64_t)n * a.k.stride + (int64_t)(h / a.k.share) * DK;
-    const T* v = (const T*)a.v.p + (int64_t)n * a.v.stride + (int64_t)h * a.dv + col0;
+    const T* v = (const T*)a.v.p + (int64_t)n * a.v.stride + (int64_t)h * DV;
     for (int c = tid; c < DK; c += 256) {
         s_k[c] = gload(k + c);
         s_q[c] = gload(q + c);
     }
-    const float vt = tid < COLS ? gload(v + tid) : 0.f;
+    const float vt = tid < DV ? gload(v + tid) : 0.f;
     const float decay = a.g ? expf(a.g[nh]) : 1.f, beta = a.beta[nh];
     if (decay == 0.f) {   // anew, whatever the state holds
 #pragma unroll
@@ -1585,7 +1597,7 @@ __global__ __launch_bounds__(256) void gdr_decode_kernel(GdrDecodeArgs a) {
         s_o[rg][4 * cg + i] = o[i];
     }
     __syncthreads();
-    if (tid < COLS) {
+    if (tid < DV) {
         float x = 0.f, y = 0.f, z = 0.f;
 #pragma unroll
         for (int r = 0; r < RG; ++r) {
@@ -1595,27 +1607,26 @@ __global__ __launch_bounds__(256) void gdr_decode_kernel(GdrDecodeArgs a) {
         }
         const float e = beta * (vt - x);
         s_e[tid] = e;
-        gstore((T*)a.y + (int64_t)nh * a.dv + col0 + tid, a.scale * (y + z * e));
+        gstore((T*)a.y + (int64_t)nh * DV + tid, a.scale * (y + z * e));
     }
     __syncthreads();
     const f32x4_t e = {s_e[4 * cg], s_e[4 * cg + 1], s_e[4 * cg + 2], s_e[4 * cg + 3]};
 #pragma unroll
     for (int r = 0; r < RPT; ++r) {
         const int row = r * RG + rg;
-        __builtin_nontemporal_store(S[r] + s_k[row] * e, reinterpret_cast<f32x4_t*>(st + (int64_t)row * a.dv));
+        __builtin_nontemporal_store(S[r] + s_k[row] * e, reinterpret_cast<f32x4_t*>(st + (int64_t)row * DV));
     }
 }
 
-template <typename T, int DK, int COLS>
+template <typename T, int DK, int DV>
 hipError_t decode_t(const GdrDecodeArgs& a) {
-    hipLaunchKernelGGL((gdr_decode_kernel<T, DK, COLS>), dim3((unsigned)((int64_t)a.N * a.H * (a.dv / COLS))), dim3(256),
-                       0, (hipStream_t)a.stream, a);
+    hipLaunchKernelGGL((gdr_decode_kernel<T, DK, DV>), dim3((unsigned)((int64_t)a.N * a.H)), dim3(256), 0,
+                       (hipStream_t)a.stream, a);
     return hipGetLastError();
 }
 
 template <typename T, int DK>
 hipError_t decode_c(const GdrDecodeArgs& a) {
-    if (a.N * (int64_t)a.H < 512) return decode_t<T, DK, 16>(a);
     return a.dv == 64 ? decode_t<T, DK, 64>(a) : decode_t<T, DK, 128>(a);
 }
 

@@ -26,7 +26,9 @@
 // Measured: 8192 x 96 heads of 128 with the gate (bf16, 607 MB) 105 us, 5.8 TB/s
 // (a large copy reaches 6.2); its gradient for 4096 x 32 heads (168 MB) 38 us a
 // call, 29 and 4 in the two kernels; for 4099 rows of 2047 (fp32, layer, 101 MB)
-// 30, 21 and 6 in the kernels.
+// 30, 21 and 6 in the kernels.  Keeping: the first 144 us, 5.6 TB/s (805 MB, of
+// which 203 are kept), its gradient 33 a call, 27 and 4 in the kernels (134 MB),
+// the last 26, 22 and 5 (76 MB; its rows of odd bytes are read word by word).
 #include "launch.h"
 #include "vec.h"
 
