@@ -1,16 +1,18 @@
 """The operators around the recurrence: linear attention with a decay for each
-head (prompt, gradient, single token), rotary positions, and the norm of a
-mixer's output with its gate.  The same kind of binding as the recurrence's:
+head and the gated delta rule with one (prompt, gradient, single token), rotary
+positions of one or several axes, and the norm of a mixer's output with its gate,
+also keeping its inputs in 8 bits.  The same kind of binding as the recurrence's:
 checks on the host, outputs from torch, everything else in libkda.so.
 
-Rows q, k, v of linear attention and of rotary positions may be slices of one
+Rows q, k, v of the two mixers and of rotary positions may be slices of one
 projection's output: [T, heads, d] views whose heads are contiguous within a
 token (any stride from token to token).  A call runs on its tensors' device, on
 that device's current stream.
 
 Nothing here is recorded for autograd, also where an input requires a gradient:
-a training step calls the gradients itself (linattn_bwd, norm_bwd, rope with
-inverse), as from the two halves of a torch.autograd.Function.
+a training step calls the gradients itself (linattn_bwd, gdr_bwd, norm_bwd,
+norm_bwd_kept, rope or rope_axes with inverse), as from the two halves of a
+torch.autograd.Function.
 """
 from __future__ import annotations
 
