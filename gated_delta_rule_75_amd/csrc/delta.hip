@@ -577,18 +577,18 @@ __global__ __launch_bounds__((walk_threads<T, DK>(MODE)), (walk_threads<T, DK>(M
             for (int t = 0; t < 4; ++t) kr[t][s] = Tile<T, DK, 1>::rows8(f.k, 16 * t, s, lane);
     };
     // stores between the copies of a chunk and the wait for them
-    constexpr int NST = MODE == kGdrOut ? 4 : kKeep ? KT * 4 + 16 : 0;
+    constexpr int NST = kKeep ? KT * 4 + 16 : 0;
     static_assert(NST < 64, "vmcnt");
+    static_assert(kCopiers || NB == 2, "without copiers the chunk after the next needs a buffer");
     if (!kCopiers && nch > 0) {
         fetch(chunk_at(0));
         wait_vmcnt<0>();
         barrier_keep_loads();
         read_k(buf(chunk_at(0)));
-        if (NB == 2 && nch > 1) fetch(chunk_at(1));
+        if (nch > 1) fetch(chunk_at(1));
     }
     for (int step = 0; step < nch; ++step) {
         const int c = chunk_at(step), m0 = c * C;
-        const bool more = step + 1 < nch;
         const Buf f = buf(c);
         if constexpr (kCopiers) {
             barrier_keep_loads();
@@ -790,17 +790,10 @@ __global__ __launch_bounds__((walk_threads<T, DK>(MODE)), (walk_threads<T, DK>(M
         }
         if constexpr (!kCopiers) {
             // the next chunk's copies are there, this one's operands in registers
-            if (NB == 2) {
-                if (!kKeep && step == 0) wait_vmcnt<0>();
-                else wait_vmcnt<NST>();
-            }
+            wait_vmcnt<NST>();
             barrier_keep_loads();
-            if (NB == 2) {
-                if (step + 2 < nch) fetch(chunk_at(step + 2));
-                if (more) read_k(buf(chunk_at(step + 1)));
-            } else if (more) {
-                fetch(chunk_at(step + 1));
-            }
+            if (step + 2 < nch) fetch(chunk_at(step + 2));
+            if (step + 1 < nch) read_k(buf(chunk_at(step + 1)));
         }
         // D: the chunk's own part of y, and of the state behind it (or of the gradient before it)
 #pragma unroll
@@ -858,11 +851,6 @@ __global__ __launch_bounds__((walk_threads<T, DK>(MODE)), (walk_threads<T, DK>(M
             }
         }
         if (kCopiers && NB == 1) barrier_keep_loads();
-        if (!kCopiers && NB == 1 && more) {
-            wait_vmcnt<0>();
-            barrier_keep_loads();
-            read_k(buf(0));
-        }
     }
     if (unit) {
         const int col = col0 + wcol + lr;

@@ -65,9 +65,12 @@ def test_gdr_workspaces():
     chunks = 8192 // 64 + 1
     assert f(BF16, 4, 2, 128, 64, 1, 8192) >= chunks * 4 * 2 * 64 * 64 * 4 // 2
     assert b(BF16, 4, 2, 128, 64, 1, 8192) >= chunks * 4 * (2 * 128 * 64 + 2 * 64 * 64) * 4
-    # from 257 sequences on, a table of their first chunks
-    at = [f(BF16, 1, 1, 64, 64, n, 100000) for n in (255, 256, 257)]
+    # from 257 sequences on, a table of their first chunks (so few are not cut into segments)
+    at = [f(BF16, 1, 1, 64, 64, n, 1900) for n in (255, 256, 257)]
     assert at[2] - at[1] - (at[1] - at[0]) == (258 * 4 + 255) // 256 * 256
+    # segments: their transitions and states beside that, up to 256 sequences
+    m = [f(BF16, 1, 1, 64, 64, n, 100000) for n in (255, 256, 257)]
+    assert m[1] - m[2] > 256 * 2 * 64 * 64 * 4 and m[1] > m[0]
 
 
 def z(*shape, dtype=torch.bfloat16):
