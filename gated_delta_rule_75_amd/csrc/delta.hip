@@ -1432,6 +1432,8 @@ __global__ __launch_bounds__(256) void gdr_decay_kernel(GdrArgs a, int size) {
     __syncthreads();
     double v = carry + d;
     for (int w = wave + 1; w < 4; ++w) v += part[w];
+    // a sequence's first token decays nothing where no state comes in: exactly 0, not the sum's rounding
+    if (!a.initial && mine == b - bl.j && lane == 0) v = 0.0;
     if (in) a.dg[(bl.start + (int64_t)(mine - b) * C + lane) * H + h] = (float)v;
 }
 

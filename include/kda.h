@@ -500,8 +500,8 @@ kda_status kda_gdr_fwd_padded(kda_dtype dt, int H, int Hk, int dk, int dv, float
  *   dv_out           [T_total, H, dv] in dtype dt.
  *   dg, dbeta        fp32 [T_total, H]; dg given exactly where g is.  Sums of
  *                    terms of both signs, accurate to a few 1e-6 of the sum of
- *                    their sizes.  Where g is below -200 its gradient is taken at
- *                    -200.
+ *                    their sizes; 0 at a sequence's first token without an initial
+ *                    state.  Where g is below -200 its gradient is taken at -200.
  *   d_initial_state  fp32 [num_seqs, H, dk, dv] or NULL.
  *                    No output may overlap an input or another output.
  *   workspace        at least kda_gdr_bwd_workspace_size bytes, 256-byte aligned:

@@ -119,6 +119,18 @@ def test_many_sequences(kda, dtype):
         ref.check(f"many {dtype} {n}", a, b, tol(n, dtype))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_first_token_without_a_state_decays_nothing(kda, dtype):
+    lens = [1, 0, 1, 70, 600]
+    x = make(dtype, lens, 4, 2, 128, 64, seed=37, state=False)
+    dg = bwd(kda, x)[3]
+    first = torch.tensor([c for c, n in zip(x["cu"], lens) if n], device="cuda")
+    assert not bool(dg[first].any())
+    rest = torch.ones(sum(lens), dtype=torch.bool, device="cuda")
+    rest[first] = False
+    assert bool(dg[rest].all())
+
+
 def test_offsets_beyond_32_bits(kda):
     """A stride of 2^20 elements from token to token, and outputs of more than 2^31 elements."""
     x = make("bf16", [2100, 64], 1, 1, 64, 64, seed=36)
