@@ -14,16 +14,24 @@
 //   W = scale dY E^T . D,   Y = -(strictly lower part of dV E^T . D)
 //   dQ = W diag(beta) K + scale exp(G) dY S^T
 //   dK = Y diag(beta) K - exp(G) dV S^T + diag(beta) (W^T Q + Y^T K + exp(G_63 - G) E R^T)
-//   dbeta_t = e_t.u_t,   dg_t = sum over tokens s >= t of (q.dq - v.dv)_s,
-// the last sum begun anew from the product of state and gradient where a block of
-// kBlock chunks ends.
+//   dbeta_t = e_t.u_t
+// and the decay's gradient as the sum of all that crosses token t, from what entered the
+// state before it to what reads it from t on:
+//   dg_t = sum_{j >= t > i} N_ji + sum_{j >= t} a_j + sum_{i < t} b_i + exp(G_63) <S, R>
+//   N = (W . Q K^T + Y . K K^T) diag(beta)      pairs of the chunk, j behind i
+//   a_j = exp(G_j) (scale q_j.S dy_j - k_j.S dv_j)   of the state that enters
+//   b_i = exp(G_63 - G_i) beta_i k_i.R e_i           into the state behind the chunk
+// Each of these holds the decay of t as a factor, so that dg keeps its digits where
+// decays are strong, and is 0 where one is 0 and at a first token without a state.  (As
+// the sum over s >= t of q.dq - v.dv it would be a small difference of large terms:
+// 1 % off at g = -10, all of it at -20.)
 //
 // A first kernel makes what does not involve the state (X, Z, P and P^T as operands,
 // the tables of decays) for all chunks at once.  A second walks a sequence's chunks
 // with the state in its accumulators, a workgroup for 64 value columns of a head.
 // The gradient walks twice, forwards (keeping each chunk's state and E) and
-// backwards (its R and U); then a kernel makes dQ, dK, dV, dbeta and the tokens'
-// terms of dg for all chunks at once, and a small one sums those.
+// backwards (its R and U); then a kernel makes dQ, dK, dV, dbeta and dg for all chunks
+// at once.
 //
 // bf16 inputs enter products as they are.  What is computed enters as a sum of
 // bf16 values: of three, 24 bits, on the way to fp32 outputs (states, E, U, X, Z,
@@ -38,12 +46,6 @@ namespace {
 // Parts of a computed operand: for outputs in T, and for fp32 ones.
 template <typename T> constexpr int kTwo = sizeof(T) == 2 ? 2 : 1;
 template <typename T> constexpr int kThree = sizeof(T) == 2 ? 3 : 1;
-// Chunks between two anchors of the decay's gradient.  dg takes the rounding of a
-// block's terms, so its error grows with the block; an anchor reads two states of
-// fp32.  With 8, 4, 2 chunks dg is off by 1.5e-6, 1.1e-6, 9e-7 at worst in fp32, whose
-// products round, and by 9e-7, 7e-7, 4e-7 from bf16, whose products are exact; the
-// kernel that reads the anchors takes 32, 36, 62 us (4 x 2048 tokens of 32 heads).
-template <typename T> constexpr int kBlock = sizeof(T) == 2 ? 4 : 2;
 
 // c += a b for operands in parts, the smallest products first (those beyond the
 // finer operand's own bits are left out).
@@ -962,7 +964,7 @@ __global__ __launch_bounds__(256, 1) void gdr_join_kernel(GdrArgs a, int backwar
 }
 
 // dQ, dK, dV in the inputs' type (dQ and dK of shared key heads: each value head's
-// part in fp32), dbeta and the tokens' terms of dg of a (chunk, head).
+// part in fp32), dbeta and dg of a (chunk, head).
 //
 // 64 value columns at a time the rows of E, dV = beta U and dY are laid out in LDS as
 // operands in parts; each wave adds to its tiles of W and Y (rows i = its own against
@@ -976,7 +978,7 @@ template <typename T, int DK>
 struct GradLds {
     static constexpr int SZ = (int)sizeof(T), N2 = kTwo<T>, N3 = kThree<T>, TRI = kTri<T, N2>, ROWS = C * 64 * SZ;
     static constexpr int k = 0, rest = C * DK * SZ;
-    static constexpr int e = rest, x = e + N3 * ROWS, y = x + N2 * ROWS, first = y + ROWS;
+    static constexpr int e = rest, x = e + N3 * ROWS, y = x + N3 * ROWS, first = y + ROWS;
     static constexpr int w = rest, second = w + 4 * TRI;                              // over the rows, once they are read
     static constexpr int dq = rest, dk = dq + C * DK * SZ, third = dk + C * DK * SZ;   // over those, at the end
     static constexpr int most = first > second ? first : second, bytes = most > third ? most : third;
@@ -997,7 +999,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 || DK == 64 ? 2 : 1) void gdr_g
     char* const wy = smem + Lds::w;                     // W beta and Y beta, rows i, then rows j
     __shared__ Sums sums;
     __shared__ __attribute__((aligned(16))) float tab[3 * C];
-    __shared__ float part_s[4][C], part_p[C], part_v[C];
+    __shared__ float part_q[4][C], part_k[4][C], part_b[4][C], part_n[4][C];   // of a wave: q.S dy, k.S dv, k.R e; pairs
+    __shared__ double part_c[4];                                                // <S, R>
     int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lg = lane >> 4;
     const int wave = uni(tid >> 6);
     // LDS addresses are formed anew in each part: kept from part to part they spill
@@ -1039,49 +1042,47 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 || DK == 64 ? 2 : 1) void gdr_g
 #pragma unroll
         for (int n = 0; n < NT; ++n) ps[t][n] = pa[t][n] = pb[t][n] = zero;
     const int ch0 = wave * (DK / 4);
-    float eu[2] = {0.f, 0.f}, vx[2] = {0.f, 0.f};
+    float eu[2] = {0.f, 0.f};
+    double across = 0.0;
     auto rows_of = [&](const T* base, int t, int s, auto& f) {   // 8 consecutive columns a lane, in parts
         constexpr int N = sizeof(f) / sizeof(f[0]);
 #pragma unroll
         for (int p = 0; p < N; ++p) f[p] = TV::rows8(base + p * C * 64, 16 * t, s, lane);
     };
+    // (a loop also where it runs once: unrolled, all of its loads are asked for at the start, and spill)
+    int columns = DV;
+    if constexpr (DV == 64) asm volatile("" : "+s"(columns));
 #pragma unroll 1
-    for (int v0 = 0; v0 < DV; v0 += 64) {
+    for (int v0 = 0; v0 < columns; v0 += 64) {
         if (v0 > 0) __syncthreads();
         anew();
-        // rows to LDS, and dv; e.u and v.dv by tokens
+        // rows to LDS, and dv; e.u by tokens
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int u = i * 256 + tid, row = u / 8, lc = u % 8 * 8, col = v0 + lc;
             const int64_t tok = start + row_of(row), at = slot * C * DV + row * DV + col;
-            float e[8], x[8], v[8];
+            float e[8], x[8];
             load8(a.errors + at, e);
             load8(a.u + at, x);
-            const T* const pv = (const T*)a.v.p + tok * a.v.stride + (int64_t)h * DV + col;
             const T* const py = (const T*)a.dy + (tok * H + h) * DV + col;
             const float be = gtab[2 * C + row];
 #pragma unroll
-            for (int c = 0; c < 8; c += EP) {
-                float o[EP];
-                load_vec<T, EP>(pv + c, o);
+            for (int c = 0; c < 8; c += EP)
                 *reinterpret_cast<u32x4_t*>(sy + TV::off(row, lc + c)) = *reinterpret_cast<const u32x4_t*>(py + c);
-#pragma unroll
-                for (int j = 0; j < EP; ++j) v[c + j] = o[j];
-            }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 eu[i] += e[j] * x[j];
                 x[j] *= be;
-                vx[i] += v[j] * x[j];
             }
             if constexpr (sizeof(T) == 2) {
-                Frag8<T> f3[N3], f2[N2];
-                split(e, f3);
-                split(x, f2);
+                Frag8<T> fe[N3], fx[N3];
+                split(e, fe);
+                split(x, fx);
 #pragma unroll
-                for (int p = 0; p < N3; ++p) *reinterpret_cast<bf16x8_t*>(se + p * C * 64 + TV::off(row, lc)) = f3[p].v;
-#pragma unroll
-                for (int p = 0; p < N2; ++p) *reinterpret_cast<bf16x8_t*>(sx + p * C * 64 + TV::off(row, lc)) = f2[p].v;
+                for (int p = 0; p < N3; ++p) {
+                    *reinterpret_cast<bf16x8_t*>(se + p * C * 64 + TV::off(row, lc)) = fe[p].v;
+                    *reinterpret_cast<bf16x8_t*>(sx + p * C * 64 + TV::off(row, lc)) = fx[p].v;
+                }
             } else {
 #pragma unroll
                 for (int c = 0; c < 8; c += 4) {
@@ -1103,8 +1104,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 || DK == 64 ? 2 : 1) void gdr_g
         __syncthreads();
         anew();
         {
-            // the wave's rows, as i and as j
-            Frag8<T> fy[2][1], fx[2][N2], fe[2][N2];
+            // the wave's rows, as i (these make dg's pairs too, an fp32 output's) and as j
+            Frag8<T> fy[2][1], fx[2][N3], fe[2][N2];
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 rows_of(sy, wave, s, fy[s]);
@@ -1116,12 +1117,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 || DK == 64 ? 2 : 1) void gdr_g
                 if (m <= wave) {
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
-                        Frag8<T> e3[N3], e2[N2];
+                        Frag8<T> e3[N3];
                         rows_of(se, m, s, e3);
                         w[m] = mma_parts(e3, fy[s], w[m]);
-#pragma unroll
-                        for (int p = 0; p < N2; ++p) e2[p] = e3[p];
-                        y[m] = mma_parts(e2, fx[s], y[m]);
+                        y[m] = mma_parts(e3, fx[s], y[m]);
                     }
                 } else {
 #pragma unroll
@@ -1140,77 +1139,103 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 || DK == 64 ? 2 : 1) void gdr_g
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             anew();
-            Frag8<T> s3[NT][N3], s2[NT][N2], r2[NT][N2];
+            float z[NT][8];
+            Frag8<T> f[NT][N3];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const int64_t at = slot * DK * DV + (int64_t)(ch0 + 16 * n + lr) * DV + v0 + 32 * s + 8 * lg;
-                float x[8], z[8];
+                float x[8];
                 load8(a.states + at, x);
-                load8(a.rstates + at, z);
-                split(x, s3[n]);
-                split(z, r2[n]);
+                load8(a.rstates + at, z[n]);
 #pragma unroll
-                for (int p = 0; p < N2; ++p) s2[n][p] = s3[n][p];
+                for (int j = 0; j < 8; ++j) across += (double)x[j] * (double)z[n][j];
+                split(x, f[n]);
             }
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                Frag8<T> fy[1], fx[N2], fe[N2];
+                Frag8<T> fy[1], fx[N3];
                 rows_of(sy, t, s, fy);
                 rows_of(sx, t, s, fx);
-                rows_of(se, t, s, fe);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    ps[t][n] = mma_parts(fy, s3[n], ps[t][n]);
-                    pa[t][n] = mma_parts(fx, s2[n], pa[t][n]);
-                    pb[t][n] = mma_parts(fe, r2[n], pb[t][n]);
+                    ps[t][n] = mma_parts(fy, f[n], ps[t][n]);
+                    pa[t][n] = mma_parts(fx, f[n], pa[t][n]);
                 }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) split(z[n], f[n]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                Frag8<T> fe[N3];
+                rows_of(se, t, s, fe);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) pb[t][n] = mma_parts(fe, f[n], pb[t][n]);
             }
         }
     }
     anew();
-    // W and Y: decays, beta; the sum over j of W beta q_i.k_j with 24 bits (an fp32 output's)
+    // W and Y: decays, beta; what the pairs of the wave's rows j carry across each token t: the
+    // sums of N_ji over i < t, for t <= j, then over the rows.  Sums only ever grow towards
+    // the nearer, larger pairs: nothing is taken away again
     {
         const int own = 16 * wave + lr;
-        float pairs = 0.f;
-        Frag8<T> fq[SK];
+        float before = 0.f;
+        Frag8<T> fq[SK], fo[SK];
 #pragma unroll
-        for (int s = 0; s < SK; ++s) fq[s] = frag_at(gq + (int64_t)row_of(own) * a.q.stride + 32 * s + 8 * lg);
+        for (int s = 0; s < SK; ++s) {
+            fq[s] = frag_at(gq + (int64_t)row_of(own) * a.q.stride + 32 * s + 8 * lg);
+            fo[s] = TK::rows8(sk, 16 * wave, s, lane);
+        }
 #pragma unroll
         for (int m = 0; m < 5; ++m) {
             if (m <= wave) {
                 const int j = 16 * m + 4 * lg;
                 const f32x4_t be = *reinterpret_cast<const f32x4_t*>(tab + 2 * C + j);
-                f32x4_t qk = zero;
+                f32x4_t qk = zero, kk = zero;
 #pragma unroll
-                for (int s = 0; s < SK; ++s) qk = mma(TK::rows8(sk, 16 * m, s, lane), fq[s], qk);
+                for (int s = 0; s < SK; ++s) {
+                    const Frag8<T> f = TK::rows8(sk, 16 * m, s, lane);
+                    qk = mma(f, fq[s], qk);
+                    kk = mma(f, fo[s], kk);
+                }
                 w[m] *= sums.before(own, j, false) * be * a.scale;
                 y[m] *= sums.before(own, j, true) * -be;
+                const f32x4_t n = w[m] * qk + y[m] * kk;
+                // of the lane groups before this one, and of all four
+                float upto = (n[0] + n[1]) + (n[2] + n[3]);
+                float x = __shfl_up(upto, 16);
+                upto += lg >= 1 ? x : 0.f;
+                x = __shfl_up(upto, 32);
+                upto += lg >= 2 ? x : 0.f;
+                x = __shfl_up(upto, 16);
+                f32x4_t p;
+                p[0] = before + (lg >= 1 ? x : 0.f);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) pairs += w[m][r] * qk[r];
+                for (int r = 1; r < 4; ++r) p[r] = p[r - 1] + n[r - 1];
+                before += __shfl(upto, 48 + lr);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float u = row16_sum(j + r <= own ? p[r] : 0.f);
+                    if (lr == 0) part_n[wave][j + r] = u;
+                }
             } else {
                 const float be = tab[2 * C + own];
                 w[m] *= sums.behind(16 * (m - 1) + 4 * lg, own, false) * (be * a.scale);
                 y[m] *= sums.behind(16 * (m - 1) + 4 * lg, own, true) * -be;
             }
         }
-        pairs += __shfl_xor(pairs, 16);
-        pairs += __shfl_xor(pairs, 32);
-        if (lg == 0) part_p[own] = pairs;
     }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) across += shfl_d(across, lane ^ d);
+    if (lane == 0) part_c[wave] = across * (double)gtab[3 * C];
     // over the 8 threads of a row
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int row = (i * 256 + tid) / 8;
         eu[i] += dpp_mov<0xB1>(eu[i]);
-        vx[i] += dpp_mov<0xB1>(vx[i]);
         eu[i] += dpp_mov<0x4E>(eu[i]);
-        vx[i] += dpp_mov<0x4E>(vx[i]);
         eu[i] += dpp_mov<0x141>(eu[i]);
-        vx[i] += dpp_mov<0x141>(vx[i]);
-        if (tid % 8 == 0) {
-            part_v[row] = vx[i];
-            if (row < cnt) a.dbeta[(start + row) * H + h] = eu[i];
-        }
+        if (tid % 8 == 0 && row < cnt) a.dbeta[(start + row) * H + h] = eu[i];
     }
     anew();
     u32x4_t rq[NQ];
@@ -1257,7 +1282,26 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 || DK == 64 ? 2 : 1) void gdr_g
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             ps[t][n] *= in * a.scale;
-            dk[t][n] = out * beta * pb[t][n] - in * pa[t][n];
+            pa[t][n] *= in;
+            pb[t][n] *= out * beta;
+            dk[t][n] = pb[t][n] - pa[t][n];
+        }
+        // k . (state's parts of dk)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            float u = 0.f, v = 0.f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float f = fk[n][t >> 1].get(4 * (t & 1) + r);
+                u += f * pa[t][n][r];
+                v += f * pb[t][n][r];
+            }
+            u = row16_sum(u);
+            v = row16_sum(v);
+            if (lr == 0) {
+                part_k[wave][16 * t + 4 * lg + r] = u;
+                part_b[wave][16 * t + 4 * lg + r] = v;
+            }
         }
 #pragma unroll
         for (int s2 = 0; s2 < 2; ++s2) {
@@ -1295,7 +1339,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 || DK == 64 ? 2 : 1) void gdr_g
 #pragma unroll
             for (int n = 0; n < NT; ++n) u += fq[n][t >> 1].get(4 * (t & 1) + r) * ps[t][n][r];
             u = row16_sum(u);
-            if (lr == 0) part_s[wave][16 * t + 4 * lg + r] = u;
+            if (lr == 0) part_q[wave][16 * t + 4 * lg + r] = u;
         }
 #pragma unroll
         for (int s2 = 0; s2 < 2; ++s2) {
@@ -1319,9 +1363,28 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 || DK == 64 ? 2 : 1) void gdr_g
         }
     }
     __syncthreads();
-    if (tid < cnt && a.dg)
-        a.terms[slot * C + tid] = ((part_s[0][tid] + part_s[1][tid]) + (part_s[2][tid] + part_s[3][tid])) +
-                                  (part_p[tid] - part_v[tid]);
+    if (wave == 0 && a.dg) {
+        // a token a lane: what enters with the state and is read from here on, what was written before
+        // and goes on behind the chunk, the pairs, and what passes the whole chunk
+        const int t = lane;
+        double from = 0.0, until = 0.0, n = 0.0;
+#pragma unroll
+        for (int w4 = 0; w4 < 4; ++w4) {
+            from += (double)part_q[w4][t] - (double)part_k[w4][t];
+            until += (double)part_b[w4][t];
+            if (16 * w4 + 15 >= t) n += (double)part_n[w4][t];
+        }
+#pragma unroll
+        for (int d = 1; d < kWave; d <<= 1) {
+            const double x = shfl_d(from, t + d < kWave ? t + d : t), y = shfl_d(until, t >= d ? t - d : t);
+            if (t + d < kWave) from += x;
+            if (t >= d) until += y;
+        }
+        until = shfl_d(until, t > 0 ? t - 1 : 0);
+        if (t == 0) until = 0.0;
+        const double all = (part_c[0] + part_c[1]) + (part_c[2] + part_c[3]);
+        if (t < cnt) a.dg[(start + t) * H + h] = (float)((n + from) + (until + all));
+    }
     if (a.parts) {
         // shared key heads: each value head's part
         const int64_t all = a.at.T_total * H * DK;
@@ -1378,63 +1441,6 @@ __global__ __launch_bounds__(256) void gdr_share_kernel(GdrArgs a, int D) {
         const float o[4] = {s[0], s[1], s[2], s[3]};
         store_vec<T, 4>((T*)(u < n4 ? a.dq : a.dk) + i * 4, o);
     }
-}
-
-// dg of a block of kBlock chunks of a (sequence, head): the sum of the terms from
-// each token to the block's end, and the product of the state there with its
-// gradient, which stands for all that is behind.  In fp64: where decays are
-// strong the tokens take nearly all of the product away again.  A wave a chunk.
-template <typename T>
-__global__ __launch_bounds__(256) void gdr_decay_kernel(GdrArgs a, int size) {
-    __shared__ double part[5];
-    double& carry = part[4];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int H = a.at.H, b = uni(blockIdx.x / H), h = blockIdx.x - b * H;
-    const Block bl = find_block(a.at, b);   // the block's last chunk, or none
-    if (bl.n < 0 || bl.cnt == 0) return;
-    const bool last = bl.j == bl.nb - 1;
-    if (!last && bl.j % kBlock<T> != kBlock<T> - 1) return;
-    const int first = b - bl.j % kBlock<T>;
-    const float *S = nullptr, *R = nullptr;
-    if (!last && b + 1 < a.at.nblocks) {
-        S = a.states + ((int64_t)(b + 1) * H + h) * size;
-        R = a.rstates + ((int64_t)b * H + h) * size;
-    } else if (a.d_final) {
-        S = a.final + ((int64_t)bl.n * H + h) * size;
-        R = a.d_final + ((int64_t)bl.n * H + h) * size;
-    }
-    double e = 0.0;
-    if (S) {
-#pragma unroll 8
-        for (int i = tid * 4; i < size; i += 1024) {
-            const f32x4_t u = *reinterpret_cast<const f32x4_t*>(S + i), v = *reinterpret_cast<const f32x4_t*>(R + i);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) e += (double)u[r] * (double)v[r];
-        }
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1) e += shfl_d(e, lane ^ d);
-    }
-    if (lane == 0) part[wave] = e;
-    __syncthreads();
-    if (tid == 0) carry = (part[0] + part[1]) + (part[2] + part[3]);
-    __syncthreads();
-    // a wave a chunk, the last one wave 3
-    static_assert(kBlock<T> <= 4, "waves");
-    const int mine = b - (3 - wave);
-    const bool in = mine >= first && (mine < b || lane < bl.cnt);
-    double d = in ? (double)a.terms[((int64_t)mine * H + h) * C + lane] : 0.0;
-#pragma unroll
-    for (int k = 1; k < kWave; k <<= 1) {
-        const double o = shfl_d(d, lane + k < kWave ? lane + k : lane);
-        if (lane + k < kWave) d += o;
-    }
-    if (lane == 0) part[wave] = d;
-    __syncthreads();
-    double v = carry + d;
-    for (int w = wave + 1; w < 4; ++w) v += part[w];
-    // a sequence's first token decays nothing where no state comes in: exactly 0, not the sum's rounding
-    if (!a.initial && mine == b - bl.j && lane == 0) v = 0.0;
-    if (in) a.dg[(bl.start + (int64_t)(mine - b) * C + lane) * H + h] = (float)v;
 }
 
 template <typename T, int DK, bool GRAD>
@@ -1509,11 +1515,7 @@ hipError_t bwd_t(const GdrArgs& a) {
     }
     if (a.at.T_total > 0 && (e = walk_t<T, DK, kGdrStates>(a)) != hipSuccess) return e;
     if ((a.at.T_total > 0 || a.d_initial) && (e = walk_t<T, DK, kGdrBack>(a)) != hipSuccess) return e;
-    if ((e = a.head_v == 64 ? grad_t<T, DK, 64>(a) : grad_t<T, DK, 128>(a)) != hipSuccess) return e;
-    if (!a.dg || a.at.T_total == 0) return hipSuccess;
-    hipLaunchKernelGGL((gdr_decay_kernel<T>), dim3((unsigned)((int64_t)a.at.nblocks * a.at.H)), dim3(256), 0,
-                       (hipStream_t)a.at.stream, a, a.head_k * a.head_v);
-    return hipGetLastError();
+    return a.head_v == 64 ? grad_t<T, DK, 64>(a) : grad_t<T, DK, 128>(a);
 }
 
 }  // namespace

@@ -262,11 +262,11 @@ struct GdrArgs {
     char *x, *z, *p;             // inverses (z: backwards) and scores
     float* tab;
     const float* initial;
-    float* final;                // gradient: in the workspace, or NULL
+    float* final;                // the gradient has none
     void* y;
     // gradient, by chunk and head: states before it, errors of prediction; the
-    // state's gradient behind it, dv / beta; the tokens' terms of dg
-    float *states, *errors, *rstates, *u, *terms;
+    // state's gradient behind it, dv / beta
+    float *states, *errors, *rstates, *u;
     float* parts;                // shared key heads: dq's and dk's, [2][T][H][dk]; else NULL
     // long sequences of few heads: segments, their transitions (and transposes), and
     // their own states, then those that enter them (NULL: not cut)

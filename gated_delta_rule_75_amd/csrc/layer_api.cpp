@@ -475,7 +475,7 @@ int64_t gdr_segment(int H, int dk, int dv, int num_seqs, int64_t T) {
 }
 
 struct GdrLayout {
-    size_t x, p, z, tab, states, rstates, errors, u, terms, s_end, share, plan, seg_m, seg_mt, seg_s, seg_r, total;
+    size_t x, p, z, tab, states, rstates, errors, u, share, plan, seg_m, seg_mt, seg_s, seg_r, total;
     int64_t chunks, L, segments;
 };
 GdrLayout gdr_layout(bool grad, int H, int Hk, int dk, int dv, int num_seqs, int64_t T) {
@@ -495,8 +495,6 @@ GdrLayout gdr_layout(bool grad, int H, int Hk, int dk, int dv, int num_seqs, int
             l.rstates = p.take(n * dk * dv * 4);
             l.errors = p.take(n * 64 * dv * 4);
             l.u = p.take(n * 64 * dv * 4);
-            l.terms = p.take(n * 64 * 4);
-            l.s_end = p.take((size_t)num_seqs * H * dk * dv * 4);
             l.share = p.take(Hk < H ? 2 * (size_t)T * H * dk * 4 : 0);
         }
         l.plan = p.take(T > 64 ? plan_bytes(num_seqs) : 0);
@@ -564,9 +562,7 @@ kda_status gdr_args(bool grad, kda_dtype dt, int H, int Hk, int dk, int dv, floa
         a.rstates = part<float>(workspace, l.rstates);
         a.errors = part<float>(workspace, l.errors);
         a.u = part<float>(workspace, l.u);
-        a.terms = part<float>(workspace, l.terms);
         if (Hk < H) a.parts = part<float>(workspace, l.share);
-        a.final = part<float>(workspace, l.s_end);
     }
     a.dtype = (int)dt;
     a.head_k = dk;
@@ -606,7 +602,6 @@ kda_status gdr_bwd(bool clear, kda_dtype dt, int H, int Hk, int dk, int dv, floa
     if (st != KDA_OK) return st;
     a.at.clear = clear;
     a.dy = dy;
-    if (!d_final_state) a.final = nullptr;
     a.d_final = d_final_state;
     a.d_initial = d_initial_state;
     a.dq = dq;

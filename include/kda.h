@@ -499,9 +499,11 @@ kda_status kda_gdr_fwd_padded(kda_dtype dt, int H, int Hk, int dk, int dv, float
  *                    that share a key head (in fp32, rounded once).
  *   dv_out           [T_total, H, dv] in dtype dt.
  *   dg, dbeta        fp32 [T_total, H]; dg given exactly where g is.  Sums of
- *                    terms of both signs, accurate to a few 1e-6 of the sum of
- *                    their sizes; 0 at a sequence's first token without an initial
- *                    state.  Where g is below -200 its gradient is taken at -200.
+ *                    terms of both signs: dg, which is the product of a token's
+ *                    decayed state with its gradient, is off by about 1e-6 of the
+ *                    product of their norms, however strong the decay.  It is 0
+ *                    where exp(g) is 0 in fp32, and at a sequence's first token
+ *                    without an initial state.
  *   d_initial_state  fp32 [num_seqs, H, dk, dv] or NULL.
  *                    No output may overlap an input or another output.
  *   workspace        at least kda_gdr_bwd_workspace_size bytes, 256-byte aligned:
