@@ -476,7 +476,9 @@ __global__ __launch_bounds__((walk_threads<T, DK>(MODE)), (walk_threads<T, DK>(M
     const int H = a.at.H, DV = a.head_v, slices = DV / 64 + (MODE == kGdrSeg ? DK / 64 : 0), chains = a.seg.nblocks * H;
     // the slices of a head read the same rows: 8 heads apart in the launch, so
     // that they run on one XCD
-    const int group = uni(blockIdx.x / (8 * slices)), rem = blockIdx.x - group * 8 * slices;
+    const int wg = uni((int)(blockIdx.y * gridDim.x + blockIdx.x));
+    if (wg >= chains * slices) return;
+    const int group = uni(wg / (8 * slices)), rem = wg - group * 8 * slices;
     const int width = chains - group * 8 < 8 ? chains - group * 8 : 8;
     const int slice = uni(rem / width), chain = group * 8 + rem - slice * width;
     const int sgm = uni(chain / H), h = chain - sgm * H;
@@ -1462,8 +1464,9 @@ hipError_t walk_t(const GdrArgs& a) {
     const void* kern = reinterpret_cast<const void*>(&gdr_walk_kernel<T, DK, MODE>);
     const hipError_t e = ensure_lds_limit(kern, lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((gdr_walk_kernel<T, DK, MODE>), dim3((unsigned)((int64_t)a.seg.nblocks * a.at.H * (a.head_v / 64 + (MODE == kGdrSeg ? DK / 64 : 0)))),
-                       dim3((walk_threads<T, DK>(MODE))), lds, (hipStream_t)a.at.stream, a);
+    const int64_t groups = (int64_t)a.seg.nblocks * a.at.H * (a.head_v / 64 + (MODE == kGdrSeg ? DK / 64 : 0));
+    hipLaunchKernelGGL((gdr_walk_kernel<T, DK, MODE>), folded_grid(groups), dim3((walk_threads<T, DK>(MODE))), lds,
+                       (hipStream_t)a.at.stream, a);
     return hipGetLastError();
 }
 

@@ -449,8 +449,9 @@ kda_status kda_rope_axes(kda_dtype dt, int64_t T, int Hq, int Hk, int d, int rot
 
 namespace {
 
-// Chunks of 64 tokens: (chunk, head) pairs as workgroups of 256 threads, and two a
-// head of a sequence, on an axis of less than 2^32 threads.
+// Chunks of 64 tokens: (chunk, head) pairs as workgroups of 256 threads on an axis of
+// less than 2^32 threads.  (The walks, of up to 512 threads and two a head of a sequence
+// or more, fold their grid.)
 constexpr int64_t kMaxChunks = int64_t(1) << 23;
 
 bool gdr_sizes_ok(kda_dtype dt, int H, int Hk, int dk, int dv, int num_seqs, int64_t T) {
