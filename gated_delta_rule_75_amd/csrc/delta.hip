@@ -473,7 +473,9 @@ __global__ __launch_bounds__((walk_threads<T, DK>(MODE)), (walk_threads<T, DK>(M
     extern __shared__ __attribute__((aligned(16))) char smem[];
     const int lane0 = threadIdx.x & 63, wave = uni(threadIdx.x >> 6) & 3;
     int lane = lane0, lr = lane & 15, lg = lane >> 4;
-    const int H = a.at.H, DV = a.head_v, slices = DV / 64 + (MODE == kGdrSeg ? DK / 64 : 0), chains = a.seg.nblocks * H;
+    const int H = a.at.H, DV = a.head_v, slices = DV / 64 + (MODE == kGdrSeg ? DK / 64 : 0);
+    constexpr bool kSeg = MODE == kGdrSeg || MODE == kGdrBackSeg;   // of the cut sequences alone
+    const int chains = (kSeg ? a.cuts : a.seg.nblocks) * H;
     // the slices of a head read the same rows: 8 heads apart in the launch, so
     // that they run on one XCD
     const int wg = uni((int)(blockIdx.y * gridDim.x + blockIdx.x));
@@ -481,12 +483,17 @@ __global__ __launch_bounds__((walk_threads<T, DK>(MODE)), (walk_threads<T, DK>(M
     const int group = uni(wg / (8 * slices)), rem = wg - group * 8 * slices;
     const int width = chains - group * 8 < 8 ? chains - group * 8 : 8;
     const int slice = uni(rem / width), chain = group * 8 + rem - slice * width;
-    const int sgm = uni(chain / H), h = chain - sgm * H;
-    const Block sb = find_block(a.seg, sgm);
+    int sgm = uni(chain / H);
+    const int h = chain - sgm * H;
+    const Block sb = find_block<kGdrLeastSegments, kSeg>(a.seg, sgm);
     if (sb.n < 0) return;
+    if constexpr (kSeg) {
+        sgm = uni(first_block<kGdrLeastSegments>(a.seg, sb.n) + sb.j);
+        if (sgm >= a.seg.nblocks) return;   // offsets out of order: stay inside the arrays
+    }
     const bool first = sb.j == 0, last = sb.j == sb.nb - 1;
     const bool unit = MODE == kGdrSeg && slice * 64 >= DV;   // columns of the transition, not of values
-    if (MODE == kGdrSeg && (sb.nb == 1 || (last && !(unit && a.seg_mt)))) return;
+    if (MODE == kGdrSeg && last && !(unit && a.seg_mt)) return;
     if (MODE == kGdrBackSeg && first) return;
     // (uni: else the compiler takes addresses for different in each lane)
     const int n = uni(sb.n), cnt = uni(sb.cnt);
@@ -557,8 +564,8 @@ __global__ __launch_bounds__((walk_threads<T, DK>(MODE)), (walk_threads<T, DK>(M
     f32x4_t S[KT];
     {
         const float* s0 = nullptr;
-        if (MODE == kGdrOut || kKeep) {
-            s0 = kBack ? a.seg_r : a.seg_s;
+        if (!kSeg) {
+            s0 = sb.nb == 1 ? nullptr : kBack ? a.seg_r : a.seg_s;
             if (s0) s0 += ((int64_t)sgm * H + h) * DKV;
             else if ((s0 = kBack ? a.d_final : a.initial)) s0 += ((int64_t)n * H + h) * DKV;
             if (s0) s0 += col0 + wcol + lr;
@@ -868,10 +875,10 @@ __global__ __launch_bounds__((walk_threads<T, DK>(MODE)), (walk_threads<T, DK>(M
         return;
     }
     float* dst = nullptr;
-    if (MODE == kGdrSeg || MODE == kGdrBackSeg) dst = (kBack ? a.seg_r : a.seg_s) + ((int64_t)sgm * H + h) * DKV;
+    if (kSeg) dst = (kBack ? a.seg_r : a.seg_s) + ((int64_t)sgm * H + h) * DKV;
     else if (kBack ? first : last) dst = kBack ? a.d_initial : a.final;
     if (dst) {
-        if (MODE != kGdrSeg && MODE != kGdrBackSeg) dst += ((int64_t)n * H + h) * DKV;
+        if (!kSeg) dst += ((int64_t)n * H + h) * DKV;
         dst += col0 + wcol + lr;
 #pragma unroll
         for (int i = 0; i < KT; ++i)
@@ -892,8 +899,9 @@ __global__ __launch_bounds__(256, 1) void gdr_join_kernel(GdrArgs a, int backwar
     const int H = a.at.H, DV = a.head_v, n = uni(blockIdx.x / H), h = blockIdx.x - n * H;
     const int64_t DKV = (int64_t)DK * DV;
     const int col = blockIdx.y * 64 + 16 * wave + lr;
-    const int b0 = uni(first_block(a.seg, n));
-    int nb = uni(blocks_of(a.seg, seq_at(a.seg, n + 1) - seq_at(a.seg, n)));
+    int nb = uni(blocks_of<kGdrLeastSegments>(a.seg, seq_at(a.seg, n + 1) - seq_at(a.seg, n)));
+    if (nb == 1) return;   // not cut: the walk begins with the sequence's own state
+    const int b0 = uni(first_block<kGdrLeastSegments>(a.seg, n));
     nb = nb < a.seg.nblocks - b0 ? nb : a.seg.nblocks - b0;   // offsets out of order: stay inside the arrays
     const float* const m = backwards ? a.seg_mt : a.seg_m;
     float* const own = backwards ? a.seg_r : a.seg_s;
@@ -1464,7 +1472,8 @@ hipError_t walk_t(const GdrArgs& a) {
     const void* kern = reinterpret_cast<const void*>(&gdr_walk_kernel<T, DK, MODE>);
     const hipError_t e = ensure_lds_limit(kern, lds);
     if (e != hipSuccess) return e;
-    const int64_t groups = (int64_t)a.seg.nblocks * a.at.H * (a.head_v / 64 + (MODE == kGdrSeg ? DK / 64 : 0));
+    const int64_t groups = (int64_t)(MODE == kGdrSeg || MODE == kGdrBackSeg ? a.cuts : a.seg.nblocks) * a.at.H *
+                           (a.head_v / 64 + (MODE == kGdrSeg ? DK / 64 : 0));
     hipLaunchKernelGGL((gdr_walk_kernel<T, DK, MODE>), folded_grid(groups), dim3((walk_threads<T, DK>(MODE))), lds,
                        (hipStream_t)a.at.stream, a);
     return hipGetLastError();

@@ -252,6 +252,7 @@ hipError_t launch_linattn_decode(const LinDecodeArgs& a);
 // The gated delta rule.  Per (chunk of 64 tokens, head) the workspace holds
 // operand tiles of 64 x 64 lower triangles (kTriBytes each) and the tables.
 constexpr int kTriBytes = 18 * 1024;
+constexpr int kGdrLeastSegments = 3;   // a sequence of fewer is not cut
 constexpr int kGdrTab = 384;     // floats: decays from the chunk's start, to its end, beta, the whole chunk's; its sums
 struct GdrArgs {
     LinArgs at;                  // sizes, offsets, clear, stream
@@ -271,6 +272,7 @@ struct GdrArgs {
     // long sequences of few heads: segments, their transitions (and transposes), and
     // their own states, then those that enter them (NULL: not cut)
     LinArgs seg;
+    int cuts;                    // a bound on the segments of sequences that are cut
     float *seg_m, *seg_mt, *seg_s, *seg_r;
     const float* d_final;
     float* d_initial;

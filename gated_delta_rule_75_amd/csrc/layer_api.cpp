@@ -463,16 +463,27 @@ bool gdr_sizes_ok(kda_dtype dt, int H, int Hk, int dk, int dv, int num_seqs, int
 // it, so long sequences of few heads are cut: the segments' own effects side by side
 // (value columns and the columns of their transitions, about what 256 CUs hold at
 // once), a product of matrices a segment to join them (about 4 us), then the walk over
-// all segments at once.  Fewer than three segments gain nothing, nor do
-// a few chunks (1277 ragged tokens of 8 heads, gradient: 148 us uncut, 164 in segments of
-// 256).  The rule is of tokens and head sizes alone.
+// all segments at once.  Times uncut and cut, d = 128, bf16 prompt, its gradient, and the
+// same in fp32 (us):
+//   8192 tokens x 12 heads        394  238   1051  706   1427 550   2803 1500
+//   6000 + 15 x 146 tokens x 8    295  188    799  534   1051 398   2082 1069
+//   2 x 4096 x 12                 211  198    623  624    737 510   1598 1421
+//   3 x 2730 x 8 (3 segments)     148  150    447  474    500 358   1114 1031
+//   4 x 2048 x 8 (2 segments)     116  136    345  409    378 344    863  923
+//   6 x 1365 x 8 (2 segments)      89  138    314  412    276 348    734  909
+// so a sequence of fewer than three segments stays whole; which ones these are the
+// kernels see, the host knows the tokens of all alone.  What is cut nowhere
+// pays for two launches that find nothing to do, and for finding so (16 x 512 x 8: 52 and
+// 58, gradient 207 and 218; 128 x 64 x 12: 139 and 159, 412 and 458).  A few chunks
+// gain nothing (1277 ragged tokens of 8 heads, fp32 gradient: 148 uncut, 164 in segments
+// of 256).  The rule is of tokens and head sizes alone.
 int64_t gdr_segment(int H, int dk, int dv, int num_seqs, int64_t T) {
     const int64_t all = T < 64 ? 64 : (T + 63) / 64 * 64, chunks = all / 64;
     int64_t m = (chunks * H * ((dk + dv) / 64) + 255) / 256;
     const int64_t least = (int64_t)std::ceil(std::sqrt(chunks / 2.0));
     if (m < least) m = least;
     if (m < 4) m = 4;
-    return 3 * m > chunks || chunks < 32 || num_seqs > kPlanSeqs ? all : 64 * m;
+    return kda::kGdrLeastSegments * m > chunks || chunks < 32 || num_seqs > kPlanSeqs ? all : 64 * m;
 }
 
 struct GdrLayout {
@@ -540,6 +551,8 @@ kda_status gdr_args(bool grad, kda_dtype dt, int H, int Hk, int dk, int dv, floa
     a.seg.nblocks = (int)l.segments;
     a.seg.first = nullptr;
     if (l.L < T_total) {
+        // (more than two segments long: at most half as many again as fit)
+        a.cuts = (int)(3 * T_total / (2 * l.L));
         a.seg_m = part<float>(workspace, l.seg_m);
         a.seg_s = part<float>(workspace, l.seg_s);
         if (grad) {

@@ -130,7 +130,9 @@ __device__ __forceinline__ int64_t uni64(int64_t x) {
 }
 
 // The block of tokens of a workgroup: block j of sequence n.  A sequence has
-// max(1, ceil(len / L)) blocks, numbered across the sequences in order.
+// max(1, ceil(len / L)) blocks, numbered across the sequences in order; with LEAST one
+// of fewer than LEAST blocks stays whole, as one block of any length, and with CUT such
+// sequences are passed over in the numbering.
 struct Block {
     int n, j;            // sequence, block in it (n < 0: no such block)
     int nb;              // blocks of the sequence
@@ -146,8 +148,9 @@ __device__ __forceinline__ int64_t seq_at(const LinArgs& a, int n) {
 }
 
 // At most the bound on all blocks: offsets out of order stay inside the arrays.
+template <int LEAST = 1>
 __device__ __forceinline__ int blocks_of(const LinArgs& a, int64_t len) {
-    const int64_t nb = len <= a.L ? 1 : (len + a.L - 1) / a.L;
+    const int64_t nb = len <= (LEAST > 1 ? (LEAST - 1) * a.L : a.L) ? 1 : (len + a.L - 1) / a.L;
     return nb < a.nblocks ? (int)nb : a.nblocks;
 }
 
@@ -167,6 +170,7 @@ __device__ __forceinline__ int64_t shfl_i64(int64_t x, int src) {
 // Every wave finds the block itself.  Uncut sequences are their blocks.  Else by
 // the sequences' first blocks, a 64th of what is left at a step; for up to
 // kPlanSeqs sequences, which have no such table, by counting, 64 at a time.
+template <int LEAST = 1, bool CUT = false>
 __device__ __forceinline__ Block find_block(const LinArgs& a, int b) {
     const int lane = threadIdx.x & 63;
     Block r;
@@ -197,7 +201,8 @@ __device__ __forceinline__ Block find_block(const LinArgs& a, int b) {
             if (n < a.num_seqs) {
                 s = seq_at(a, n);
                 e = seq_at(a, n + 1);
-                nb = blocks_of(a, e - s);
+                nb = blocks_of<LEAST>(a, e - s);
+                if (CUT && nb == 1) nb = 0;
             }
             const int incl = wave_incl_sum(nb, lane);
             const int total = __shfl(incl, kWave - 1);
@@ -225,17 +230,18 @@ __device__ __forceinline__ Block find_block(const LinArgs& a, int b) {
     r.begin = uni64(s);
     r.start = r.begin + (int64_t)r.j * a.L;
     const int64_t left = uni64(e) - r.start;
-    r.cnt = uni((int)(left < 0 ? 0 : left < a.L ? left : a.L));
+    r.cnt = uni((int)(left < 0 ? 0 : left < a.L || (LEAST > 1 && r.nb == 1) ? left : a.L));
     return r;
 }
 
 // Index of sequence n's first block.
+template <int LEAST = 1>
 __device__ __forceinline__ int first_block(const LinArgs& a, int n) {
     if (a.L >= a.T_total) return n;
     if (a.first) return a.first[n];
     const int lane = threadIdx.x & 63;
     int sum = 0;
-    for (int m = lane; m < n; m += kWave) sum += blocks_of(a, seq_at(a, m + 1) - seq_at(a, m));
+    for (int m = lane; m < n; m += kWave) sum += blocks_of<LEAST>(a, seq_at(a, m + 1) - seq_at(a, m));
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
     return sum;
