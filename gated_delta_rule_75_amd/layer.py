@@ -263,7 +263,10 @@ def gdr_fwd(q, k, v, g, beta, cu_seqlens: Optional[torch.Tensor] = None, initial
     anew, whatever it held), or None: no decay; beta fp32 [T, H].  Stable for
     beta |k|^2 <= 2.  cu_seqlens may begin after 0 or end before T: rows of no
     sequence are not read; they are zeros in a y made here, and left as they are
-    in one that is given.  Returns (y, final_state or None)."""
+    in one that is given.  Sums are in fp32; of bf16 inputs, what is computed inside
+    enters products with 24 bits for the states and 16 for y (up to one value in 100
+    is the neighbour of the exact value's rounding; fp32 inputs compute in fp32).
+    Returns (y, final_state or None)."""
     dt, T, H, Hk, dk, dv = _gdr(q, k, v, g, beta)
     N = _seqs(cu_seqlens)
     _need("initial_state", initial_state, (N, H, dk, dv), torch.float32)
@@ -292,7 +295,8 @@ def gdr_bwd(q, k, v, g, beta, dy, cu_seqlens: Optional[torch.Tensor] = None, ini
     d_final_state of the final state.  Returns (dq, dk, dv, dg, dbeta,
     d_initial_state): dq, dk [T, Hk, dk] summed over the value heads that share a
     key head, dg and dbeta [T, H] (dg None where g is); zeros in rows of no
-    sequence."""
+    sequence.  Precision as in gdr_fwd: 16 bits inside for dq and dk in bf16, 24 for
+    all else.  dg keeps its digits however strong the decay, and is 0 where exp(g) is."""
     dt, T, H, Hk, dk, dv = _gdr(q, k, v, g, beta)
     N = _seqs(cu_seqlens)
     _need("dy", dy, (T, H, dv), q.dtype)

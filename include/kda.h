@@ -467,6 +467,12 @@ kda_status kda_linattn_decode_step(kda_dtype dt, int N, int H, int Hk, int dk, i
  *   initial_state, final_state   fp32 [num_seqs, H, dk, dv] or NULL, as
  *                    kda_chunk_fwd; they may be the same buffer.
  *   y                [T_total, H, dv] in dtype dt; must not overlap inputs.
+ *                    Sums are in fp32.  KDA_F32: products too.  KDA_BF16: inputs enter
+ *                    products as they are; what is computed inside enters with 24
+ *                    bits for fp32 outputs (states; dg, dbeta and dv_out of the
+ *                    gradient), with 16 for bf16 ones (y; dq, dk_out): the output's
+ *                    own rounding to 8 is what shows, and up to one value in 100 is
+ *                    the neighbour of the exact value's rounding.
  *   workspace        at least kda_gdr_fwd_workspace_size bytes for the same sizes,
  *                    256-byte aligned.  Calls that may overlap in time need a
  *                    workspace each.
