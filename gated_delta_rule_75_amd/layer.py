@@ -360,7 +360,7 @@ def rope_pair_axes(sections, order: str = "runs") -> torch.Tensor:
     if order not in _ORDER:
         raise ValueError("order must be 'runs' or 'turns'")
     n = torch.tensor(list(sections), dtype=torch.int32)
-    out = torch.empty(max(int(n.clamp(min=0).sum()), 1), dtype=torch.uint8)
+    out = torch.empty(min(max(int(n.clamp(min=0).sum()), 1), 512), dtype=torch.uint8)   # more are refused
     _check("kda_rope_pair_axes", lib().kda_rope_pair_axes(n.numel(), _p(n), _ORDER[order], _p(out)))
     return out
 

@@ -19,3 +19,10 @@ def test_both_sides_of_the_bound(size, call, dv):
     for N, T in ((MOST + 1, 0), (MOST, 64), (MOST - 999, 64000)):
         assert size(BF16, 1, 1, 64, dv, N, T) == 0
         assert call(N=N, T=T, **a) == INVALID
+
+
+def test_axes_of_too_many_pairs_are_refused_before_memory_is_asked_for():
+    for bad in ((513,), ((1 << 31) - 1,) * 255, (500, 13)):
+        with pytest.raises(kda.KDAError):
+            kda.rope_pair_axes(bad)
+    assert kda.rope_pair_axes((500, 12)).tolist() == [0] * 500 + [1] * 12
