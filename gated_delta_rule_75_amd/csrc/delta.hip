@@ -148,15 +148,15 @@ __device__ __forceinline__ Frag8<T> cols8(const T* t, int s, int h, int s2, int 
     Frag8<T> f;
     if constexpr (sizeof(T) == 2) {
         const int row = 32 * s2 + 4 * (lane >> 4) + ((lane & 15) >> 2), col = 32 * s + 8 * (lane & 3) + 4 * h;
-        const bf16x4_t x = __builtin_bit_cast(bf16x4_t, lds_tr(t + Tile<T, D, 1>::off(row, col)));
-        const bf16x4_t y = __builtin_bit_cast(bf16x4_t, lds_tr(t + Tile<T, D, 1>::off(row + 16, col)));
+        const bf16x4_t x = __builtin_bit_cast(bf16x4_t, lds_tr(t + Tile<T, D>::off(row, col)));
+        const bf16x4_t y = __builtin_bit_cast(bf16x4_t, lds_tr(t + Tile<T, D>::off(row + 16, col)));
         f.v = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
     } else {
         const int m = lane & 15, row = 32 * s2 + 4 * (lane >> 4), col = 32 * s + 8 * (m >> 2) + 4 * h + (m & 3);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            f.v[i] = t[Tile<T, D, 1>::off(row + i, col)];
-            f.v[4 + i] = t[Tile<T, D, 1>::off(row + 16 + i, col)];
+            f.v[i] = t[Tile<T, D>::off(row + i, col)];
+            f.v[4 + i] = t[Tile<T, D>::off(row + 16 + i, col)];
         }
     }
     return f;
@@ -279,7 +279,7 @@ template <typename T, int DK, bool GRAD> constexpr int prep_bytes() {
 
 template <typename T, int DK, bool GRAD>
 __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrArgs a) {
-    typedef Tile<T, DK, 1> TK;
+    typedef Tile<T, DK> TK;
     constexpr int SN = DK / 32, EP = 16 / (int)sizeof(T), NR = C * DK / EP / 256;
     extern __shared__ __attribute__((aligned(16))) char smem[];
     T* const sk = reinterpret_cast<T*>(smem);
@@ -540,11 +540,11 @@ __global__ __launch_bounds__((walk_threads<T, DK>(MODE)), (walk_threads<T, DK>(M
         const Buf f = buf(c);
         const int m0 = c * C;
         const int64_t slot = (int64_t)(fb + c) * H + h;
-        copy_tile<T, DK, 1>(f.k, xk, rows, m0, wave, lane);
-        copy_tile<T, 64, 1>(f.v, xv, rows, m0, wave, lane);
+        copy_tile<T, DK>(f.k, xk, rows, m0, wave, lane);
+        copy_tile<T, 64>(f.v, xv, rows, m0, wave, lane);
         copy_flat<kTri<T, N3>>(f.x, (kBack ? a.z : a.x) + slot * kTriBytes, wave, lane);
         if constexpr (kQ) {
-            copy_tile<T, DK, 1>(f.q, xq, rows, m0, wave, lane);
+            copy_tile<T, DK>(f.q, xq, rows, m0, wave, lane);
             copy_flat<kTri<T, NPP>>(f.p, a.p + slot * kTriBytes, wave, lane);
         }
         if (wave == 3) copy16(uni(lds_addr(f.tab)), a.tab + slot * kGdrTab, (unsigned)lane * 16);
@@ -587,7 +587,7 @@ __global__ __launch_bounds__((walk_threads<T, DK>(MODE)), (walk_threads<T, DK>(M
 #pragma unroll
         for (int s = 0; s < SN; ++s)
 #pragma unroll
-            for (int t = 0; t < 4; ++t) kr[t][s] = Tile<T, DK, 1>::rows8(f.k, 16 * t, s, lane);
+            for (int t = 0; t < 4; ++t) kr[t][s] = Tile<T, DK>::rows8(f.k, 16 * t, s, lane);
     };
     // stores between the copies of a chunk and the wait for them
     constexpr int NST = kKeep ? KT * 4 + 16 : 0;
@@ -659,7 +659,7 @@ __global__ __launch_bounds__((walk_threads<T, DK>(MODE)), (walk_threads<T, DK>(M
             beta[t] = *reinterpret_cast<const f32x4_t*>(f.tab + 2 * C + 16 * t + 4 * lg);
         }
         // the wave's columns of v (or dy), a lane 4 tokens of each tile
-        Frag8<T> fv[2] = {Tile<T, 64, 1>::cols(f.v, wcol, 0, lane), Tile<T, 64, 1>::cols(f.v, wcol, 1, lane)};
+        Frag8<T> fv[2] = {Tile<T, 64>::cols(f.v, wcol, 0, lane), Tile<T, 64>::cols(f.v, wcol, 1, lane)};
         if (unit) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -678,7 +678,7 @@ __global__ __launch_bounds__((walk_threads<T, DK>(MODE)), (walk_threads<T, DK>(M
             }
             if constexpr (kCopiers) {
 #pragma unroll
-                for (int t = 0; t < 4; ++t) kr[t][s] = Tile<T, DK, 1>::rows8(f.k, 16 * t, s, lane);
+                for (int t = 0; t < 4; ++t) kr[t][s] = Tile<T, DK>::rows8(f.k, 16 * t, s, lane);
             }
             split(x, fs[s]);
 #pragma unroll
@@ -767,7 +767,7 @@ __global__ __launch_bounds__((walk_threads<T, DK>(MODE)), (walk_threads<T, DK>(M
 #pragma unroll
             for (int s = 0; s < SN; ++s) {
 #pragma unroll
-                for (int t = 0; t < 4; ++t) fq[t][s] = Tile<T, DK, 1>::rows8(f.q, 16 * t, s, lane);
+                for (int t = 0; t < 4; ++t) fq[t][s] = Tile<T, DK>::rows8(f.q, 16 * t, s, lane);
 #pragma unroll
                 for (int p = NPP - 1; p >= 0; --p)
 #pragma unroll
@@ -999,8 +999,8 @@ struct GradLds {
 template <typename T, int DK, int DV>
 __global__ __launch_bounds__(256, sizeof(T) == 2 || DK == 64 ? 2 : 1) void gdr_grad_kernel(GdrArgs a) {
     typedef GradLds<T, DK> Lds;
-    typedef Tile<T, 64, 1> TV;
-    typedef Tile<T, DK, 1> TK;
+    typedef Tile<T, 64> TV;
+    typedef Tile<T, DK> TK;
     constexpr int SK = DK / 32, NT = DK / 64, N2 = kTwo<T>, N3 = kThree<T>, EP = 16 / (int)sizeof(T), TRI = kTri<T, N2>;
     constexpr int NQ = C * DK / EP / 256;               // runs of 16 bytes of a thread, of k and of q
     extern __shared__ __attribute__((aligned(16))) char smem[];

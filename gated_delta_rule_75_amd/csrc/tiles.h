@@ -41,9 +41,8 @@ __device__ __forceinline__ f32x4_t mma(const Frag8<float>& a, const Frag8<float>
     return c;
 }
 
-// A tile of rows of D elements in LDS, 16-byte pieces swizzled by the row.  W: for
-// bf16 column reads whose 16 columns are halves of four pieces, not two whole ones.
-template <typename T, int D, int W = 0>
+// A tile of rows of D elements in LDS, 16-byte pieces swizzled by the row.
+template <typename T, int D>
 struct Tile {
     static constexpr int EP = 16 / (int)sizeof(T);        // elements of a piece
     static constexpr int PIECES = D / EP;
@@ -52,8 +51,6 @@ struct Tile {
     // once.  (bf16 rows of 128 bytes share a line of banks in twos.)
     static __device__ __forceinline__ int swz(int row) {
         if constexpr (sizeof(T) == 4) return row & 15;
-        // four rows in turn differ above the four pieces, eight rows everywhere
-        if constexpr (W == 1) return PIECES == 16 ? ((row & 3) << 2) | ((row >> 2) & 3) : ((row & 2) << 1) | ((row >> 2) & 3);
         if constexpr (PIECES == 16) return ((row << 1) | ((row >> 3) & 1)) & 15;
         return (row & 6) | ((row >> 3) & 1);   // rows in twos: bits 3 2 1 turned to 2 1 3
     }
@@ -355,13 +352,13 @@ __device__ __forceinline__ void copy4(unsigned lds, const void* addr) {
 // wave's copy is 1 KiB of LDS in order, so the swizzle is on the source side.
 // Rows without a token take the last token's: the tables give them no weight.
 template <typename T, int D> constexpr int kCopies = C * D * (int)sizeof(T) / 4096;   // of a wave
-template <typename T, int D, int W = 0>
+template <typename T, int D>
 __device__ __forceinline__ void copy_part(T* t, const Src& x, const Rows& rows, int m0, int wave, int lane, int i) {
-    constexpr int PIECES = Tile<T, D, W>::PIECES, RPW = 64 / PIECES, N = kCopies<T, D>;
+    constexpr int PIECES = Tile<T, D>::PIECES, RPW = 64 / PIECES, N = kCopies<T, D>;
     const int top = rows.tokens(m0) - 1;
     const int row0 = wave * RPW + lane / PIECES, row = 4 * RPW * i + row0;
     const unsigned lds = uni(lds_addr(t) + wave * 1024) + i * 4096;
-    const unsigned piece = (unsigned)((lane % PIECES) ^ Tile<T, D, W>::swz(row)) * 16u;
+    const unsigned piece = (unsigned)((lane % PIECES) ^ Tile<T, D>::swz(row)) * 16u;
     const int64_t base = x.token(rows.low(m0));
     if (top == C - 1) {
         const int64_t at = base + (int64_t)((rows.rev ? N - 1 - i : i) * 4 * RPW) * x.step;
@@ -371,10 +368,10 @@ __device__ __forceinline__ void copy_part(T* t, const Src& x, const Rows& rows, 
         copy16(lds, reinterpret_cast<const void*>(base), (unsigned)(tok < top ? tok : top) * x.step + piece);
     }
 }
-template <typename T, int D, int W = 0>
+template <typename T, int D>
 __device__ __forceinline__ void copy_tile(T* t, const Src& x, const Rows& rows, int m0, int wave, int lane) {
 #pragma unroll
-    for (int i = 0; i < kCopies<T, D>; ++i) copy_part<T, D, W>(t, x, rows, m0, wave, lane, i);
+    for (int i = 0; i < kCopies<T, D>; ++i) copy_part<T, D>(t, x, rows, m0, wave, lane, i);
 }
 
 // Eight values as a sum of NS operands of type T.  One: rounded to nearest.

@@ -462,7 +462,8 @@ kda_status kda_linattn_decode_step(kda_dtype dt, int N, int H, int Hk, int dk, i
  *   g                fp32 [T_total, H], natural log of the decay, <= 0, or NULL: no
  *                    decay.  Below -200 it counts as -200 (a factor of 0):
  *                    -INFINITY starts the head's state anew at that token, also
- *                    where it held infinities or NaN.
+ *                    where it held infinities or NaN.  (So do, in a prompt, decays
+ *                    whose product within a chunk of 64 tokens is 0 in fp32.)
  *   beta             fp32 [T_total, H].
  *   initial_state, final_state   fp32 [num_seqs, H, dk, dv] or NULL, as
  *                    kda_chunk_fwd; they may be the same buffer.
@@ -500,7 +501,8 @@ kda_status kda_gdr_fwd_padded(kda_dtype dt, int H, int Hk, int dk, int dv, float
  *
  *   dy               [T_total, H, dv] in dtype dt, contiguous.
  *   initial_state    as given to the forward call; finite.
- *   d_final_state    fp32 [num_seqs, H, dk, dv], or NULL (zeros).
+ *   d_final_state    fp32 [num_seqs, H, dk, dv], or NULL (zeros); finite, as
+ *                    dy.
  *   dq, dk_out       [T_total, Hk, dk] in dtype dt, summed over the value heads
  *                    that share a key head (in fp32, rounded once).
  *   dv_out           [T_total, H, dv] in dtype dt.
