@@ -461,12 +461,13 @@ __device__ __forceinline__ void copy_flat(char* lds, const char* src, int wave, 
 // stores as well; there the four waves copy themselves, and read ahead (4 x 2048 tokens
 // of 32 heads, with waves that copy: states 148 -> 165 us, backwards 210 -> 229),
 // unless what they read ahead overfills the registers, in fp32 with 128 channels (the
-// gradient of the same sizes: 3225 -> 1658 us).
+// gradient of the same sizes: 3225 -> 1658 us, with all that came later 1606).
 //
 // What bounds it: a chunk's products follow one another (K S, E, the state), 182 of
 // them a wave in 16 cycles each beside 580 other vector operations, most to split
 // operands, in 6800 cycles: 3.4 us at 2 GHz.  Copies cost nothing of that any more.
-// Those that keep states are bound by the 411 MB they write (3.1 TB/s).
+// Those that keep states take 4.2 us a chunk, backwards 6.4, where they write 411 MB
+// at 3.0 and 2.0 TB/s, half of what memory takes and less: the chain again.
 template <typename T, int DK, int MODE>
 __global__ __launch_bounds__((walk_threads<T, DK>(MODE)), (walk_threads<T, DK>(MODE) / 256)) void gdr_walk_kernel(GdrArgs a) {
     constexpr int SN = DK / 32, KT = DK / 16, N3 = kThree<T>, NPP = MODE == kGdrOut ? kTwo<T> : N3, NB = walk_bufs<T, DK, MODE>(), SZ = (int)sizeof(T);
@@ -892,8 +893,8 @@ __global__ __launch_bounds__((walk_threads<T, DK>(MODE)), (walk_threads<T, DK>(M
 // The states that enter the segments of a (sequence, head), 64 columns, in place of
 // the segments' own ones: S_{j+1} = M_j S_j + own_j from the sequence's initial state
 // (backwards R_{j-1} = M_j^T R_j + own_j).  A wave has 16 columns; matrices and
-// states enter the products with 24 bits.  About 4 us a segment, latency: a segment's
-// matrix is read while the one before is multiplied.
+// states enter the products with 24 bits.  A segment takes 13 us with 128 channels, 8
+// with 64: latency, since each wave reads the segment's matrix as it multiplies.
 template <int DK>
 __global__ __launch_bounds__(256, 1) void gdr_join_kernel(GdrArgs a, int backwards) {
     constexpr int SN = DK / 32, KT = DK / 16;
@@ -984,8 +985,10 @@ __global__ __launch_bounds__(256, 1) void gdr_join_kernel(GdrArgs a, int backwar
 // the states' parts, whose rows are operands as they lie in memory.  W and Y then
 // take the rows' place, and q that of k.  In bf16 two workgroups share a CU: one
 // loads while the other multiplies (4 x 2048 tokens of 32 heads: 430 us with all value
-// columns at once and one workgroup a CU, 295 so).  It moves 798 MB, 2.7 TB/s, with
-// matrix instructions 19 % and vector ones 32 % of the time: latency between its parts.
+// columns at once and one workgroup a CU, 295 so; with dg made here, which needs 24 bits
+// in E, dV, S and R, 341, and a kernel of 35 for dg less).  It moves 726 MB, 2.1 TB/s, with
+// matrix instructions 27 % and vector ones 42 % of the time, and waits for 53 % of it:
+// states are asked for right before they are multiplied.
 template <typename T, int DK>
 struct GradLds {
     static constexpr int SZ = (int)sizeof(T), N2 = kTwo<T>, N3 = kThree<T>, TRI = kTri<T, N2>, ROWS = C * 64 * SZ;

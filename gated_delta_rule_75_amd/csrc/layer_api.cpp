@@ -462,8 +462,9 @@ bool gdr_sizes_ok(kda_dtype dt, int H, int Hk, int dk, int dv, int num_seqs, int
 // Tokens of a segment.  A walk takes about 4 us a chunk and a CU has one workgroup of
 // it, so long sequences of few heads are cut: the segments' own effects side by side
 // (value columns and the columns of their transitions, about what 256 CUs hold at
-// once), a product of matrices a segment to join them (about 4 us), then the walk over
-// all segments at once.  Times uncut and cut, d = 128, bf16 prompt, its gradient, and the
+// once), a product of matrices a segment to join them (13 us with 128 channels, 8 with
+// 64), then the walk over all segments at once.  As the joins are a chain too, a segment
+// has sqrt(chunks / 2) chunks at least.  Times uncut and cut, d = 128, bf16 prompt, its gradient, and the
 // same in fp32 (us):
 //   8192 tokens x 12 heads        394  238   1051  706   1427 550   2803 1500
 //   6000 + 15 x 146 tokens x 8    295  188    799  534   1051 398   2082 1069
