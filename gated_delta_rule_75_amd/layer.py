@@ -264,8 +264,8 @@ def gdr_fwd(q, k, v, g, beta, cu_seqlens: Optional[torch.Tensor] = None, initial
     beta |k|^2 <= 2.  cu_seqlens may begin after 0 or end before T: rows of no
     sequence are not read; they are zeros in a y made here, and left as they are
     in one that is given.  Sums are in fp32; of bf16 inputs, what is computed inside
-    enters products with 24 bits for the states and 16 for y (up to one value in 100
-    is the neighbour of the exact value's rounding; fp32 inputs compute in fp32).
+    enters products with 24 bits for the states and 16 for y (about 2^-17 of the size
+    of a value's terms, beside its own rounding; fp32 inputs compute in fp32).
     Returns (y, final_state or None)."""
     dt, T, H, Hk, dk, dv = _gdr(q, k, v, g, beta)
     N = _seqs(cu_seqlens)

@@ -471,9 +471,10 @@ kda_status kda_linattn_decode_step(kda_dtype dt, int N, int H, int Hk, int dk, i
  *                    Sums are in fp32.  KDA_F32: products too.  KDA_BF16: inputs enter
  *                    products as they are; what is computed inside enters with 24
  *                    bits for fp32 outputs (states; dg, dbeta and dv_out of the
- *                    gradient), with 16 for bf16 ones (y; dq, dk_out): the output's
- *                    own rounding to 8 is what shows, and up to one value in 100 is
- *                    the neighbour of the exact value's rounding.
+ *                    gradient), with 16 for bf16 ones (y; dq, dk_out): about 2^-17
+ *                    of the size of the terms that make a value, beside its own
+ *                    rounding to 8 bits, by which up to one value in 100 is rounded
+ *                    the other way.
  *   workspace        at least kda_gdr_fwd_workspace_size bytes for the same sizes,
  *                    256-byte aligned.  Calls that may overlap in time need a
  *                    workspace each.
